@@ -47,6 +47,25 @@
  * Token position t of a sequence lives in physical block
  * block_tables[seq][t / block_size] at offset t % block_size.
  * A slot is physical_block * block_size + offset.
+ *
+ * Integer-coded pools (PKV_INT8, PKV_INT4).  A row (one token of one head) x of
+ * D values is held as unsigned codes of b = 8 or 4 bits with a binary32 scale
+ * and zero of its own: lo = min x, hi = max x, scale = (hi - lo) / (2^b - 1) (0
+ * where that is below 2^-126), zero = lo, code = min(rint((x - lo) * (1 /
+ * scale)), 2^b - 1), each step one IEEE binary32 operation; the value held is
+ * zero + scale * code.  hi - lo must be finite.  The tile of one block and KV
+ * head is, instead of 16 * D elements, 16 * RB code bytes (RB = D * b / 8) and
+ * then 16 pairs (scale, zero): 16 * (RB + 8) bytes, so a pool is
+ * [num_blocks][num_kv_heads][16 * (RB + 8)] bytes (pkv_cache_block_bytes).  Byte
+ * k of token t's row holds element k, or for 4 bits elements 2k (low half) and
+ * 2k + 1, and lies, in a key tile, at (k / 64) * 16 * W + t * W + k % 64 with
+ * W = min(RB, 64); in a value tile, with x = (k / 2) * 4 + (t % 2) * 2 + k % 2,
+ * at (x / 32) * 256 + (t / 2) * 32 + x % 32.  k_scale and v_scale are ignored.
+ * Served by pkv_paged_kv_append, pkv_paged_kv_read, pkv_copy_blocks,
+ * pkv_swap_blocks, pkv_paged_attention_decode (and _noalloc),
+ * pkv_paged_attention_decode_sparse, pkv_paged_key_bounds, pkv_select_blocks and
+ * pkv_paged_attention_prefill; pkv_paged_attention_decode_append and _cascade
+ * return PKV_ERR_UNSUPPORTED.
  */
 #ifndef PAGEDKV_H
 #define PAGEDKV_H
@@ -71,7 +90,9 @@ typedef enum {
 typedef enum {
     PKV_F16 = 0,       /* IEEE binary16 */
     PKV_BF16 = 1,      /* bfloat16 */
-    PKV_FP8_E4M3 = 2   /* OCP E4M3FN, per-tensor scale: value = code * scale */
+    PKV_FP8_E4M3 = 2,  /* OCP E4M3FN, per-tensor scale: value = code * scale */
+    PKV_INT8 = 3,      /* pools only: 8-bit codes, a scale and a zero per row (see below) */
+    PKV_INT4 = 4       /* pools only: 4-bit codes, a scale and a zero per row */
 } pkv_dtype;
 
 /* Bits of the device error word (pkv_get_device_error). */
@@ -106,7 +127,11 @@ typedef struct {
  *   Token t is written to block slot / b at offset slot % b of every KV
  *   head.  For an fp8 cache each element is stored as the E4M3 code nearest
  *   (ties to even, saturating at +-448) to binary32(x) / k_scale (v_scale).
- *   Two tokens with the same slot race (which one lands is unspecified).
+ *   For an integer-coded pool in_dtype is PKV_BF16 or PKV_F16 and each row is
+ *   encoded as described above; two blocks' tokens may be appended in any
+ *   order and by concurrent calls.
+ *   Two tokens with the same slot race (which one lands is unspecified; in an
+ *   integer-coded pool the codes of one may meet the scale of the other).
  * k_cache, v_cache: device pools in the layout above, written in place.
  * A slot >= num_blocks * b sets PKV_DEVERR_SLOT and that token is skipped.
  * num_tokens == 0 is a no-op.
@@ -114,6 +139,27 @@ typedef struct {
 pkv_status pkv_paged_kv_append(const void* k, const void* v, int32_t in_dtype, int32_t num_tokens,
                                const int64_t* slot_mapping, void* k_cache, void* v_cache,
                                const pkv_cache_desc* desc, void* stream);
+
+/* Bytes of one block (all KV heads) of one pool of this description; 0 for a
+ * description that is not supported. */
+size_t pkv_cache_block_bytes(const pkv_cache_desc* desc);
+
+/*
+ * Cached rows read back by slot, as 16-bit values: the inverse of
+ * pkv_paged_kv_append.  The pages have no counterpart: it serves what needs
+ * the cached keys and values outside the attention kernels (recomputing part
+ * of a prompt, moving a sequence to another pool type, inspection).
+ *
+ * slot_mapping: device int64 [num_tokens].  Row t of k_out and v_out (device
+ *   [num_tokens][num_kv_heads][head_size], out_dtype) receives slot
+ *   slot_mapping[t]'s keys and values; a negative slot leaves its rows as they
+ *   were; a slot >= num_blocks * b sets PKV_DEVERR_SLOT and is skipped.
+ * out_dtype: PKV_F16 or PKV_BF16, the pool's own type for a 16-bit pool.  Codes
+ *   are scaled in binary32 (k_scale / v_scale for fp8) and rounded once.
+ */
+pkv_status pkv_paged_kv_read(const int64_t* slot_mapping, int32_t num_tokens, const void* k_cache,
+                             const void* v_cache, const pkv_cache_desc* desc, void* k_out, void* v_out,
+                             int32_t out_dtype, void* stream);
 
 /*
  * Block copy behind copy-on-write ([P4] "Prefix Caching 与 Copy-on-Write":
@@ -194,7 +240,8 @@ size_t pkv_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t
  *   max_seq_len, partition_tokens) bytes (may be NULL when that is 0);
  *   otherwise PKV_ERR_WORKSPACE.
  * Implemented: block_size 16; head_size 64 or 128; num_q_heads / num_kv_heads
- *   in {1, 2, 4, 8}; pools f16, bf16 or fp8 E4M3.
+ *   in {1, 2, 4, 8}; pools f16, bf16, fp8 E4M3, or integer-coded (q f16 or
+ *   bf16; one tensor-core kernel, which pkv_set_decode_path does not change).
  */
 pkv_status pkv_paged_attention_decode(const void* q, int32_t q_dtype, int32_t num_seqs,
                                       int32_t num_q_heads, const void* k_cache, const void* v_cache,
@@ -363,6 +410,94 @@ size_t pkv_decode_cascade_staging_bytes(int32_t kv_dtype, int32_t num_seqs, int3
                                         int32_t head_size);
 
 /*
+ * Sparse decode: attention over a choice of blocks instead of the whole
+ * context, in three calls.  pkv_paged_key_bounds keeps, for each block and KV
+ * head, the channelwise minimum and maximum of its keys; pkv_select_blocks
+ * scores every block of a sequence by the highest value that a query's score
+ * could take on it and keeps the best; pkv_paged_attention_decode_sparse
+ * attends to those.  A decode step appends, updates the bounds of the blocks
+ * that received tokens, selects and attends.  A block that copy-on-write
+ * copied gets its bounds with the append that caused the copy; after
+ * pkv_swap_blocks the bounds of the blocks swapped in have to be made anew
+ * (new_lens NULL).  The pages name long contexts ([P2] partitions) but no
+ * such scheme.
+ *
+ * pkv_paged_key_bounds
+ * bounds: device [num_blocks][num_kv_heads][2][head_size] in bounds_dtype, row 0
+ *   the minimum and row 1 the maximum over the block's tokens inside the
+ *   sequence, of the keys as they are held (scaled codes, formed in binary32);
+ *   16-bit bounds of scaled codes are rounded outwards.  NaN keys are passed
+ *   over.
+ * new_lens: device int32 [num_seqs]: the last new_lens[s] tokens of sequence s
+ *   are new, and the bounds of every block that holds one of them are
+ *   computed from the block's tokens (0: none).  NULL: all its tokens are.
+ *   max_new_len (host): at least every entry (for NULL, every length).  Other
+ *   blocks' bounds stay as they are.  An entry below 0, above the sequence's
+ *   length or above max_new_len, or a length outside the block table, sets
+ *   PKV_DEVERR_SEQ_LEN and that sequence is skipped.
+ * bounds_dtype: PKV_F16 or PKV_BF16, the pool's own type for a 16-bit pool.
+ * Sequences that share a block write the same bounds to it.
+ */
+pkv_status pkv_paged_key_bounds(const void* k_cache, const pkv_cache_desc* desc, const int32_t* block_tables,
+                                int32_t max_blocks_per_seq, const int32_t* seq_lens, const int32_t* new_lens,
+                                int32_t max_new_len, int32_t num_seqs, void* bounds, int32_t bounds_dtype,
+                                void* stream);
+
+/* Workspace bytes of pkv_select_blocks (0 on invalid sizes). */
+size_t pkv_select_blocks_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len);
+
+/*
+ * Block selection.  The score of block j of sequence s for KV head h is
+ *     max over the query heads g of h of  sum_d max(q_gd lo_d, q_gd hi_d)
+ * with (lo, hi) the block's bounds, taken exactly (as real numbers; a NaN score
+ * counts as the lowest).  Row (s, h) of selected, device int32 [num_seqs]
+ * [num_kv_heads][num_selected], receives logical block numbers in ascending
+ * order: the first sink_blocks and the last recent_blocks blocks of the
+ * sequence and those of the highest scores among the others, ties to the
+ * lowest number; every block when there are at most num_selected; the rest
+ * of the row is -1.  sink_blocks + recent_blocks <= num_selected.
+ * q: device [num_seqs][num_q_heads][head_size]; bounds as pkv_paged_key_bounds
+ *   writes them, in q_dtype (for a 16-bit pool the pool's type).
+ * max_seq_len (host) must be >= every length; a length below 0, above it
+ *   (rounded up to 256 tokens) or above the block table sets
+ *   PKV_DEVERR_SEQ_LEN and is clamped.  A block id outside the pool sets
+ *   PKV_DEVERR_BLOCK_ID and scores lowest.
+ * workspace: pkv_select_blocks_workspace_bytes(...) bytes (else
+ *   PKV_ERR_WORKSPACE), in use until the call's kernels have finished.
+ */
+pkv_status pkv_select_blocks(const void* q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                             const void* bounds, const pkv_cache_desc* desc, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len,
+                             int32_t num_selected, int32_t sink_blocks, int32_t recent_blocks, int32_t* selected,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes of pkv_paged_attention_decode_sparse (0 on invalid sizes or
+ * where one partition holds a list; partition_blocks = 0 sizes for the
+ * automatic choice's largest case). */
+size_t pkv_decode_sparse_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t head_size,
+                                         int32_t num_selected, int32_t partition_blocks);
+
+/*
+ * Decode attention over selected blocks: pkv_paged_attention_decode with the
+ * sum and the softmax of row (s, query head i) taken over the tokens, inside
+ * the sequence, of the logical blocks that selected[s][i / (num_q_heads /
+ * num_kv_heads)][0 .. num_selected) lists.  A negative entry names no block; an
+ * entry at or past the sequence's last block + 1 sets PKV_DEVERR_BLOCK_ID and
+ * is skipped; a block listed twice is attended to twice.  A row whose list
+ * names no token gives zeros.  Pools of every type; q, out, tables and errors as for
+ * pkv_paged_attention_decode.
+ * partition_blocks: list entries per split-K partition, or 0 to let the
+ *   library choose.  workspace: pkv_decode_sparse_workspace_bytes(...) bytes
+ *   (may be NULL when that is 0).
+ */
+pkv_status pkv_paged_attention_decode_sparse(const void* q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                                             const void* k_cache, const void* v_cache, const pkv_cache_desc* desc,
+                                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                             const int32_t* seq_lens, const int32_t* selected, int32_t num_selected,
+                                             float scale, void* out, void* workspace, size_t workspace_bytes,
+                                             int32_t partition_blocks, void* stream);
+
+/*
  * Paged (chunked) prefill attention, causal, on the tensor cores.  Prefill
  * processes a prompt's tokens together; chunked prefill cuts a long prompt
  * into chunks that run in successive iterations, each attending to the KV
@@ -383,8 +518,8 @@ size_t pkv_decode_cascade_staging_bytes(int32_t kv_dtype, int32_t num_seqs, int3
  *   PKV_DEVERR_SEQ_LEN and its rows past the bound may be left unwritten.
  * Rows of out outside every sequence's range are not written.
  * scale must be finite and > 0 (else PKV_ERR_INVALID).
- * Implemented for f16 / bf16 pools with q of the same type, fp8 E4M3 pools
- * with f16 or bf16 q, head_size 64 or 128, num_q_heads / num_kv_heads in
+ * Implemented for f16 / bf16 pools with q of the same type, fp8 E4M3 and
+ * integer-coded pools with f16 or bf16 q, head_size 64 or 128, num_q_heads / num_kv_heads in
  * {1, 2, 4, 8}, and at most 2^31 - 1 CTAs (ceil(max_query_len * G / 256) *
  * num_kv_heads * num_seqs, G = num_q_heads / num_kv_heads); others return
  * PKV_ERR_UNSUPPORTED.  out has q's type.
@@ -394,6 +529,9 @@ size_t pkv_decode_cascade_staging_bytes(int32_t kv_dtype, int32_t num_seqs, int3
  * ceil(seq_lens[s] / 16) entries of each block-table row) into 16-bit
  * blocks of q's type in the workspace -- exact, since every E4M3 value is an
  * f16 and a bf16 value -- and the attention pass reads that copy.
+ * Integer-coded pools: the first kernel rounds each value held once to q's
+ * type (zeros past a sequence's end), in the same workspace layout; the
+ * attention is that of those 16-bit values.
  * workspace, workspace_bytes: device memory of at least
  * pkv_prefill_workspace_bytes(desc->kv_dtype, num_seqs, num_kv_heads,
  * head_size, max_blocks_per_seq) bytes, 16-byte aligned, owned by the
@@ -418,7 +556,7 @@ size_t pkv_decode_cascade_staging_bytes(int32_t kv_dtype, int32_t num_seqs, int3
  * Inconsistent query_start / seq_lens (n_s < 0,
  * n_s > seq_lens[s], past num_tokens or the block table) set
  * PKV_DEVERR_SEQ_LEN and the sequence is skipped; a block id outside the pool
- * sets PKV_DEVERR_BLOCK_ID (for an fp8 pool the block reads as zeros).
+ * sets PKV_DEVERR_BLOCK_ID (in a staged copy the block reads as zeros).
  */
 pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype, int32_t num_tokens, int32_t num_q_heads,
                                        int32_t num_seqs, const int32_t* query_start, int32_t max_query_len,
@@ -430,7 +568,7 @@ pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype, int32_t n
 
 /*
  * Workspace bytes pkv_paged_attention_prefill needs: 0 for an f16 / bf16
- * pool; for an fp8 E4M3 pool 2 * 2 * num_seqs * max_blocks_per_seq *
+ * pool; for an fp8 E4M3 or integer-coded pool 2 * 2 * num_seqs * max_blocks_per_seq *
  * num_kv_heads * 16 * head_size bytes of 16-bit block copies plus a 4-byte
  * block-table entry per (sequence, block), each part rounded up to 256 bytes.
  * Returns 0 for a negative count or a non-positive num_kv_heads / head_size.

@@ -276,7 +276,7 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
         return PKV_ERR_INVALID;
     if (d->num_blocks <= 0 || d->num_kv_heads <= 0 || d->head_size <= 0 || d->block_size <= 0)
         return PKV_ERR_INVALID;
-    if (d->kv_dtype < PKV_F16 || d->kv_dtype > PKV_FP8_E4M3) return PKV_ERR_INVALID;
+    if (!known_kv_dtype(d->kv_dtype)) return PKV_ERR_INVALID;
     if (q_dtype != PKV_F16 && q_dtype != PKV_BF16) return PKV_ERR_INVALID;
     if (num_q_heads % d->num_kv_heads) return PKV_ERR_INVALID;
     if (!(scale == scale)) return PKV_ERR_INVALID;
@@ -284,7 +284,9 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
     if (static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_blocks_per_seq) * d->block_size)
         return PKV_ERR_INVALID;
     if (partition_tokens % kBlockSize) return PKV_ERR_INVALID;
-    if (d->kv_dtype != PKV_FP8_E4M3 && q_dtype != d->kv_dtype) return PKV_ERR_UNSUPPORTED;
+    const bool int_pool = is_int_pool(d->kv_dtype);
+    if (d->kv_dtype != PKV_FP8_E4M3 && !int_pool && q_dtype != d->kv_dtype) return PKV_ERR_UNSUPPORTED;
+    if (int_pool && app) return PKV_ERR_UNSUPPORTED;
     if (d->block_size != kBlockSize || (d->head_size != 64 && d->head_size != 128)) return PKV_ERR_UNSUPPORTED;
     const int G = num_q_heads / d->num_kv_heads;
     if (G != 1 && G != 2 && G != 4 && G != 8) return PKV_ERR_UNSUPPORTED;
@@ -351,13 +353,15 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
     // cores otherwise (one query row per KV head is not a dense tile).
     const int64_t pool_rows = static_cast<int64_t>(d->num_blocks) * d->num_kv_heads * kBlockSize;
     const bool mma_ok = d->head_size == 128 && G >= 2 && pool_rows <= 0x7fffffff;
-    const int path = g_decode_path.load();
+    const int path = int_pool ? 0 : g_decode_path.load();  // integer-coded pools have one kernel
     if (path == 2 && !mma_ok) return PKV_ERR_UNSUPPORTED;
-    const bool use_mma = mma_ok && path != 1;
+    const bool use_mma = mma_ok && path != 1 && !int_pool;
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (use_mma) {
+    if (int_pool) {
+        e = d->kv_dtype == PKV_INT8 ? launch_decode_int8(p, G, q_dtype, st) : launch_decode_int4(p, G, q_dtype, st);
+    } else if (use_mma) {
         CUtensorMap tk, tv;
         const int eb = d->kv_dtype == PKV_FP8_E4M3 ? 1 : 2;
         if (!encode_pool_map(&tk, k_cache, eb, pool_rows, d->head_size) ||

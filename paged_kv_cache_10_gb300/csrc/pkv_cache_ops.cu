@@ -134,7 +134,7 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 bool desc_ok(const pkv_cache_desc* d) {
     if (!d) return false;
     if (d->num_blocks <= 0 || d->num_kv_heads <= 0 || d->head_size <= 0 || d->block_size <= 0) return false;
-    if (d->kv_dtype < PKV_F16 || d->kv_dtype > PKV_FP8_E4M3) return false;
+    if (!known_kv_dtype(d->kv_dtype)) return false;
     if (d->kv_dtype == PKV_FP8_E4M3 && !(d->k_scale > 0.f && d->v_scale > 0.f)) return false;
     return true;
 }
@@ -169,10 +169,15 @@ extern "C" pkv_status pkv_paged_kv_append(const void* k, const void* v, int32_t 
         return PKV_ERR_INVALID;
     const bool same = in_dtype == desc->kv_dtype;
     const bool to_fp8 = desc->kv_dtype == PKV_FP8_E4M3 && (in_dtype == PKV_BF16 || in_dtype == PKV_F16);
-    if (!same && !to_fp8) return PKV_ERR_UNSUPPORTED;
+    const bool to_int = is_int_pool(desc->kv_dtype) && (in_dtype == PKV_BF16 || in_dtype == PKV_F16);
+    if (!same && !to_fp8 && !to_int) return PKV_ERR_UNSUPPORTED;
     unsigned int* err = error_word();
     if (!err) return PKV_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (to_int)
+        return launch_append_int(k, v, in_dtype, num_tokens, slot_mapping, k_cache, v_cache, desc, err, st) == cudaSuccess
+                   ? PKV_OK
+                   : PKV_ERR_CUDA;
     const int Hkv = desc->num_kv_heads, D = desc->head_size;
     const int64_t num_slots = static_cast<int64_t>(desc->num_blocks) * kBlockSize;
     if (same) {
@@ -207,8 +212,7 @@ extern "C" pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const pkv_ca
     if (num_pairs > 65535 * 1024) return PKV_ERR_UNSUPPORTED;
     unsigned int* err = error_word();
     if (!err) return PKV_ERR_CUDA;
-    const int64_t block_bytes = static_cast<int64_t>(desc->num_kv_heads) * kBlockSize * desc->head_size *
-                                (desc->kv_dtype == PKV_FP8_E4M3 ? 1 : 2);
+    const int64_t block_bytes = desc->num_kv_heads * tile_bytes(desc->kv_dtype, desc->head_size);
     dim3 grid(num_pairs, kCopySplit, 2);
     copy_blocks_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
         static_cast<unsigned char*>(k_cache), static_cast<unsigned char*>(v_cache), pairs, desc->num_blocks,
@@ -238,8 +242,7 @@ extern "C" pkv_status pkv_swap_blocks(void* k_cache, void* v_cache, const pkv_ca
     if (!aligned16(kd) || !aligned16(vd)) return PKV_ERR_INVALID;
     unsigned int* err = error_word();
     if (!err) return PKV_ERR_CUDA;
-    const int64_t block_bytes = static_cast<int64_t>(desc->num_kv_heads) * kBlockSize * desc->head_size *
-                                (desc->kv_dtype == PKV_FP8_E4M3 ? 1 : 2);
+    const int64_t block_bytes = desc->num_kv_heads * tile_bytes(desc->kv_dtype, desc->head_size);
     dim3 grid(num_pairs, kCopySplit, 2);
     swap_blocks_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(
         static_cast<unsigned char*>(k_cache), static_cast<unsigned char*>(v_cache),

@@ -75,7 +75,8 @@ extern "C" pkv_status pkv_paged_attention_decode_cascade(
         return PKV_ERR_INVALID;
     if (d->num_blocks <= 0 || d->num_kv_heads <= 0 || d->head_size <= 0 || d->block_size <= 0)
         return PKV_ERR_INVALID;
-    if (d->kv_dtype < PKV_F16 || d->kv_dtype > PKV_FP8_E4M3) return PKV_ERR_INVALID;
+    if (!known_kv_dtype(d->kv_dtype)) return PKV_ERR_INVALID;
+    if (is_int_pool(d->kv_dtype)) return PKV_ERR_UNSUPPORTED;
     if (q_dtype != PKV_F16 && q_dtype != PKV_BF16) return PKV_ERR_INVALID;
     if (num_q_heads % d->num_kv_heads || !(scale > 0.f) || scale > 3.0e38f) return PKV_ERR_INVALID;
     if (static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_blocks_per_seq) * d->block_size)

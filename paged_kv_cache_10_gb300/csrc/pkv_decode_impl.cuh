@@ -107,7 +107,30 @@ __device__ __forceinline__ bool decode_unit(const DecodeParams& p, int& part, in
     return true;
 }
 
-template <int D, int G, typename KT, typename QT, int NW, int NST>
+// Sparse decode (SPARSE kernels): the range of list entries of this CTA's
+// partition.  Every row has p.NP partitions, the last ones perhaps empty.
+__device__ __forceinline__ int sparse_range(const DecodeParams& p, int part, int& first) {
+    const int per = p.P / kBlockSize;
+    first = part * per;
+    return max(0, min(per, p.nsel - first));
+}
+
+// One list entry: the physical block (or kNoBlock) and its tokens inside the
+// sequence.  A negative entry names no block; one past the sequence's blocks
+// is reported.
+constexpr int kNoBlock = -2;
+__device__ __forceinline__ int sparse_block(const DecodeParams& p, int s, int logical, int len, int& valid) {
+    valid = 0;
+    if (logical < 0) return kNoBlock;
+    if (logical >= p.MB || logical > (len - 1) / kBlockSize || len <= 0) {
+        report(p.err, PKV_DEVERR_BLOCK_ID);
+        return kNoBlock;
+    }
+    valid = min(kBlockSize, len - logical * kBlockSize);
+    return __ldg(p.block_tables + static_cast<int64_t>(s) * p.MB + logical);
+}
+
+template <int D, int G, typename KT, typename QT, int NW, int NST, bool SPARSE>
 __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
     constexpr int VEC = D / 16;               // elements of a row per lane
     constexpr int VBYTES = VEC * KT::bytes;   // bytes of a row slice per lane
@@ -133,32 +156,43 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
     const int Lcap = p.MB * kBlockSize;
     bool bad = L < 0 || L > Lcap;
     L = L < 0 ? 0 : (L > Lcap ? Lcap : L);
-    const int start = own_start(p.seq_group, p.group_blocks, s, L, &bad);
-    int Lown = L - start;
-    if (Lown > (p.NP - p.part_base) * p.P) {
-        bad = true;
-        Lown = (p.NP - p.part_base) * p.P;
-        L = start + Lown;
+    int nparts, t1, j0, nblk;
+    if constexpr (SPARSE) {
+        if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        nparts = p.NP;
+        t1 = L;
+        nblk = sparse_range(p, part, j0);
+    } else {
+        const int start = own_start(p.seq_group, p.group_blocks, s, L, &bad);
+        int Lown = L - start;
+        if (Lown > (p.NP - p.part_base) * p.P) {
+            bad = true;
+            Lown = (p.NP - p.part_base) * p.P;
+            L = start + Lown;
+        }
+        if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        nparts = Lown > 0 ? (Lown + p.P - 1) / p.P : (p.cascade ? 0 : 1);
+        if (part >= nparts) return;
+        const int t0 = start + part * p.P;
+        t1 = min(L, t0 + p.P);
+        j0 = t0 / kBlockSize;
+        nblk = (t1 + kBlockSize - 1) / kBlockSize - j0;
     }
-    if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
-    const int nparts = Lown > 0 ? (Lown + p.P - 1) / p.P : (p.cascade ? 0 : 1);
-    if (part >= nparts) return;
-    const int t0 = start + part * p.P;
-    const int t1 = min(L, t0 + p.P);
-    const int j0 = t0 / kBlockSize;
-    const int nblk = (t1 + kBlockSize - 1) / kBlockSize - j0;
     const int nb_w = warp < nblk ? (nblk - warp + NW - 1) / NW : 0;
     // fused append: the warp that streams the partition's last block writes
     // the new token's row just before copying that block
-    const bool append_here = p.slots && t1 == L && !bad && nblk > 0 && warp == (nblk - 1) % NW;
+    const bool append_here = !SPARSE && p.slots && t1 == L && !bad && nblk > 0 && warp == (nblk - 1) % NW;
     const FusedRow frow = fused_prefetch(p, s, h, L, append_here);
 
     unsigned char* wbase = smem + warp * NST * STAGE;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBarOffset) + warp * NST;
     volatile int* stage_phys = reinterpret_cast<int*>(smem + SM::kPhysOffset) + warp * NST;
     float* pbuf = reinterpret_cast<float*>(smem + SM::kPOffset) + warp * kBlockSize * G;
+    // sparse: valid tokens of each stage's block, behind everything else
+    volatile int* stage_val = reinterpret_cast<int*>(smem + SM::template bytes<G>()) + warp * NST;
 
-    const int32_t* bt = p.block_tables + static_cast<int64_t>(s) * p.MB + j0 + warp;
+    const int32_t* bt = (SPARSE ? p.selected + (static_cast<int64_t>(s) * p.Hkv + h) * p.nsel
+                                : p.block_tables + static_cast<int64_t>(s) * p.MB) + j0 + warp;
     const unsigned char* kpool = static_cast<const unsigned char*>(p.k_cache);
     const unsigned char* vpool = static_cast<const unsigned char*>(p.v_cache);
     const uint64_t pol = policy_evict_first();
@@ -171,15 +205,20 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
     __syncwarp();
 
     // Lane k of `tbl` holds the block id of this warp's block (window + k).
-    int tbl = -1;
+    int tbl = -1, val = 0;
     int k_issue = 0;
     auto issue_next = [&]() {  // warp-uniform call
         if ((k_issue & 31) == 0) {
             const int k = k_issue + lane;
             tbl = k < nb_w ? __ldg(bt + static_cast<int64_t>(k) * NW) : -1;
+            if constexpr (SPARSE) tbl = sparse_block(p, s, tbl, L, val);
         }
         const int phys = __shfl_sync(kFull, tbl, k_issue & 31);
         const int stage = k_issue % NST;
+        if constexpr (SPARSE) {
+            const int nv = __shfl_sync(kFull, val, k_issue & 31);
+            if (lane == 0) stage_val[stage] = nv;
+        }
         if (append_here && k_issue == nb_w - 1) {
             fused_commit<KT>(p, h, frow);
             __syncwarp();
@@ -192,7 +231,7 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
                 bulk_g2s(wbase + stage * STAGE, kpool + off, TILE, &bars[stage], pol);
                 bulk_g2s(wbase + stage * STAGE + TILE, vpool + off, TILE, &bars[stage], pol);
             } else {
-                report(p.err, PKV_DEVERR_BLOCK_ID);
+                if (!SPARSE || phys != kNoBlock) report(p.err, PKV_DEVERR_BLOCK_ID);
                 mbar_arrive_expect_tx(&bars[stage], 0);
             }
         }
@@ -239,7 +278,7 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
         }
         const int phys = stage_phys[stage];
         const int tok0 = (j0 + warp + k * NW) * kBlockSize;
-        const int nvalid = min(kBlockSize, t1 - tok0);
+        const int nvalid = SPARSE ? stage_val[stage] : min(kBlockSize, t1 - tok0);
         if (phys >= 0 && phys < p.NB) {
             const unsigned char* kt = wbase + stage * STAGE;
             const unsigned char* vt = kt + TILE;
@@ -407,12 +446,12 @@ constexpr int decode_stages() {
     return st < 2 ? 2 : (st > 8 ? 8 : st);
 }
 
-template <int D, int G, typename KT, typename QT>
+template <int D, int G, typename KT, typename QT, bool SPARSE>
 cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t st) {
     constexpr int NW = kDecodeWarps;
     constexpr int NST = decode_stages<D, KT>();
-    constexpr int SMEM = DecodeSmem<D, KT, NW, NST>::template bytes<G>();
-    auto kern = decode_kernel<D, G, KT, QT, NW, NST>;
+    constexpr int SMEM = DecodeSmem<D, KT, NW, NST>::template bytes<G>() + (SPARSE ? NW * NST * 4 : 0);
+    auto kern = decode_kernel<D, G, KT, QT, NW, NST, SPARSE>;
     static bool configured[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -428,21 +467,21 @@ cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t st) {
     return launch_maybe_pdl(p.join_primary != 0 && !p.work, kern, grid, dim3(NW * 32), SMEM, st, p);
 }
 
-template <typename KT, typename QT>
+template <typename KT, typename QT, bool SPARSE = false>
 cudaError_t launch_decode_family(const DecodeParams& p, int G, cudaStream_t st) {
     if (p.D == 128) {
         switch (G) {
-        case 1: return launch_decode_t<128, 1, KT, QT>(p, st);
-        case 2: return launch_decode_t<128, 2, KT, QT>(p, st);
-        case 4: return launch_decode_t<128, 4, KT, QT>(p, st);
-        case 8: return launch_decode_t<128, 8, KT, QT>(p, st);
+        case 1: return launch_decode_t<128, 1, KT, QT, SPARSE>(p, st);
+        case 2: return launch_decode_t<128, 2, KT, QT, SPARSE>(p, st);
+        case 4: return launch_decode_t<128, 4, KT, QT, SPARSE>(p, st);
+        case 8: return launch_decode_t<128, 8, KT, QT, SPARSE>(p, st);
         }
     } else if (p.D == 64) {
         switch (G) {
-        case 1: return launch_decode_t<64, 1, KT, QT>(p, st);
-        case 2: return launch_decode_t<64, 2, KT, QT>(p, st);
-        case 4: return launch_decode_t<64, 4, KT, QT>(p, st);
-        case 8: return launch_decode_t<64, 8, KT, QT>(p, st);
+        case 1: return launch_decode_t<64, 1, KT, QT, SPARSE>(p, st);
+        case 2: return launch_decode_t<64, 2, KT, QT, SPARSE>(p, st);
+        case 4: return launch_decode_t<64, 4, KT, QT, SPARSE>(p, st);
+        case 8: return launch_decode_t<64, 8, KT, QT, SPARSE>(p, st);
         }
     }
     return cudaErrorInvalidValue;

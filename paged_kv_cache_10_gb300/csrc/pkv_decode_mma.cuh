@@ -369,7 +369,7 @@ __device__ __forceinline__ void mma_block(unsigned char* kt, int nvalid, const u
     }
 }
 
-template <int G, typename KT, typename QT, int NW, int NST>
+template <int G, typename KT, typename QT, int NW, int NST, bool SPARSE>
 __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
@@ -398,30 +398,41 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     const int Lcap = p.MB * kBlockSize;
     bool bad = L < 0 || L > Lcap;
     L = L < 0 ? 0 : (L > Lcap ? Lcap : L);
-    const int start = own_start(p.seq_group, p.group_blocks, s, L, &bad);
-    int Lown = L - start;
-    if (Lown > (p.NP - p.part_base) * p.P) {
-        bad = true;
-        Lown = (p.NP - p.part_base) * p.P;
-        L = start + Lown;
+    int nparts, t1, j0, nblk;
+    if constexpr (SPARSE) {
+        if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        nparts = p.NP;
+        t1 = L;
+        nblk = sparse_range(p, part, j0);
+    } else {
+        const int start = own_start(p.seq_group, p.group_blocks, s, L, &bad);
+        int Lown = L - start;
+        if (Lown > (p.NP - p.part_base) * p.P) {
+            bad = true;
+            Lown = (p.NP - p.part_base) * p.P;
+            L = start + Lown;
+        }
+        if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        nparts = Lown > 0 ? (Lown + p.P - 1) / p.P : (p.cascade ? 0 : 1);
+        if (part >= nparts) return;
+        const int t0 = start + part * p.P;
+        t1 = min(L, t0 + p.P);
+        j0 = t0 / kBlockSize;
+        nblk = (t1 + kBlockSize - 1) / kBlockSize - j0;
     }
-    if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
-    const int nparts = Lown > 0 ? (Lown + p.P - 1) / p.P : (p.cascade ? 0 : 1);
-    if (part >= nparts) return;
-    const int t0 = start + part * p.P;
-    const int t1 = min(L, t0 + p.P);
-    const int j0 = t0 / kBlockSize;
-    const int nblk = (t1 + kBlockSize - 1) / kBlockSize - j0;
     const int nb_w = warp < nblk ? (nblk - warp + NW - 1) / NW : 0;
     // fused append: the warp that streams the partition's last block writes
     // the new token's row just before copying that block
-    const bool append_here = p.slots && t1 == L && !bad && nblk > 0 && warp == (nblk - 1) % NW;
+    const bool append_here = !SPARSE && p.slots && t1 == L && !bad && nblk > 0 && warp == (nblk - 1) % NW;
     const FusedRow frow = fused_prefetch(p, s, h, L, append_here);
 
     unsigned char* wbase = smem + warp * NST * STAGE;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::kBarOffset) + warp * NST;
     volatile int* stage_phys = reinterpret_cast<int*>(smem + SM::kPhysOffset) + warp * NST;
-    const int32_t* bt = p.block_tables + static_cast<int64_t>(s) * p.MB + j0 + warp;
+    const int32_t* bt = (SPARSE ? p.selected + (static_cast<int64_t>(s) * p.Hkv + h) * p.nsel
+                                : p.block_tables + static_cast<int64_t>(s) * p.MB) + j0 + warp;
+    // sparse: valid tokens of each stage's block, behind everything else
+    volatile int* stage_val = reinterpret_cast<int*>(smem + SM::kBytes - 1024) + warp * NST;
     const uint64_t pol = policy_evict_first();
 
     if (lane == 0) {
@@ -431,14 +442,19 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     }
     __syncwarp();
 
-    int tbl = -1;
+    int tbl = -1, val = 0;
     int k_issue = 0;
     auto issue_next = [&](const int stage) {  // warp-uniform call; stage = k_issue % NST
         if ((k_issue & 31) == 0) {
             const int k = k_issue + lane;
             tbl = k < nb_w ? __ldg(bt + static_cast<int64_t>(k) * NW) : -1;
+            if constexpr (SPARSE) tbl = sparse_block(p, s, tbl, L, val);
         }
         const int phys = __shfl_sync(kFull, tbl, k_issue & 31);
+        if constexpr (SPARSE) {
+            const int nv = __shfl_sync(kFull, val, k_issue & 31);
+            if (lane == 0) stage_val[stage] = nv;
+        }
         if (append_here && k_issue == nb_w - 1) {
             fused_commit<KT>(p, h, frow);
             __syncwarp();
@@ -460,7 +476,7 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
                     tma_load_2d(dst + TILE + 2048, &tmv, 64, y, &bars[stage], pol);
                 }
             } else {
-                report(p.err, PKV_DEVERR_BLOCK_ID);
+                if (!SPARSE || phys != kNoBlock) report(p.err, PKV_DEVERR_BLOCK_ID);
                 mbar_arrive_expect_tx(&bars[stage], 0);
             }
         }
@@ -510,7 +526,7 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
                 break;
             }
             const int phys = stage_phys[st];
-            const int nvalid = min(kBlockSize, t1 - tok0);
+            const int nvalid = SPARSE ? stage_val[st] : min(kBlockSize, t1 - tok0);
             tok0 += NW * kBlockSize;
             if (phys >= 0 && phys < p.NB) {
                 mma_block<G, KT, QT>(wbase + st * STAGE, nvalid, qb, qsm, o, mA, mB, lA, lB, p.qk_scale, koff, voff);
@@ -639,13 +655,13 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
 }
 
 // ------------------------------------------------------------- launchers
-template <int G, typename KT, typename QT>
+template <int G, typename KT, typename QT, bool SPARSE>
 cudaError_t launch_decode_mma_t(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                 cudaStream_t st) {
     constexpr int NW = MmaCfg<KT>::kWarps;
     constexpr int NST = MmaCfg<KT>::kStages;
-    constexpr int SMEM = MmaSmem<KT, NW, NST>::kBytes;
-    auto kern = decode_mma_kernel<G, KT, QT, NW, NST>;
+    constexpr int SMEM = MmaSmem<KT, NW, NST>::kBytes + (SPARSE ? NW * NST * 4 : 0);
+    auto kern = decode_mma_kernel<G, KT, QT, NW, NST, SPARSE>;
     static bool configured[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -661,13 +677,13 @@ cudaError_t launch_decode_mma_t(const DecodeParams& p, const CUtensorMap& tk, co
     return launch_maybe_pdl(p.join_primary != 0 && !p.work, kern, grid, dim3(NW * 32), SMEM, st, p, tk, tv);
 }
 
-template <typename KT, typename QT>
+template <typename KT, typename QT, bool SPARSE = false>
 cudaError_t launch_decode_mma_family(const DecodeParams& p, int G, const CUtensorMap& tk, const CUtensorMap& tv,
                                      cudaStream_t st) {
     switch (G) {
-    case 2: return launch_decode_mma_t<2, KT, QT>(p, tk, tv, st);
-    case 4: return launch_decode_mma_t<4, KT, QT>(p, tk, tv, st);
-    case 8: return launch_decode_mma_t<8, KT, QT>(p, tk, tv, st);
+    case 2: return launch_decode_mma_t<2, KT, QT, SPARSE>(p, tk, tv, st);
+    case 4: return launch_decode_mma_t<4, KT, QT, SPARSE>(p, tk, tv, st);
+    case 8: return launch_decode_mma_t<8, KT, QT, SPARSE>(p, tk, tv, st);
     }
     return cudaErrorInvalidValue;
 }

@@ -1,0 +1,145 @@
+// pkv_int.cuh -- integer-coded KV pools (PKV_INT8, PKV_INT4): the tile layout
+// and the row codec shared by the append, read, staging, key-bounds and
+// decode kernels.
+//
+// A row (one token of one KV head) of D values x is held as unsigned codes of
+// b bits with a binary32 scale and zero taken from the row itself:
+//   lo = min x, hi = max x, scale = (hi - lo) / (2^b - 1), zero = lo,
+//   code = min(rint((x - lo) * (1 / scale)), 2^b - 1),  value = zero + scale * code
+// each step one IEEE binary32 operation, so that the codes are the same on
+// every machine.  A scale below 2^-126 (a constant row) is stored as 0.
+//
+// A tile (16 tokens of one block and KV head, in one pool) is 16 * RB code
+// bytes (RB = D * b / 8) followed by 16 pairs (scale, zero), one contiguous
+// run of 640 to 2176 bytes, a multiple of 128: one 1-D bulk copy brings codes
+// and parameters together, and a block copy or swap moves both without
+// knowing about them.  The code bytes are permuted so that the tensor-core
+// decode reads its MMA fragments from a tile as it lies, free of
+// shared-memory bank conflicts and without a byte shuffle:
+//   keys    byte k of token t: panel k / 64 of [16 tokens][min(RB, 64)] bytes
+//   values  byte k of token t is byte x = (k / 2) * 4 + (t % 2) * 2 + k % 2 of
+//           token pair t / 2: panel x / 32 of [8 pairs][32] bytes
+// (a 32-bit word of a value pair holds two bytes of the even token and the
+// same two of the odd one, so masking it gives f16 pairs along the tokens,
+// the contraction axis of P V).
+#pragma once
+
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+template <int D, int BITS>
+struct IntTile {
+    static_assert((D == 64 || D == 128) && (BITS == 4 || BITS == 8), "");
+    static constexpr int RB = D * BITS / 8;            // code bytes of a row
+    static constexpr int KW = RB < 64 ? RB : 64;       // bytes of a key panel's row
+    static constexpr int kCodes = kBlockSize * RB;     // code bytes of a tile
+    static constexpr int kBytes = kCodes + kBlockSize * 8;
+    static constexpr int kD = D, kBits = BITS;
+    static_assert(kBytes % 128 == 0, "shared-memory stages keep their bank alignment");
+    __host__ __device__ static constexpr int key(int t, int k) { return (k / 64) * (16 * KW) + t * KW + k % 64; }
+    __host__ __device__ static constexpr int val(int t, int k) {
+        const int x = (k / 2) * 4 + (t % 2) * 2 + k % 2;
+        return (x / 32) * 256 + (t / 2) * 32 + x % 32;
+    }
+    __host__ __device__ static constexpr int param(int t) { return kCodes + t * 8; }
+};
+
+// Eight elements 8 * c .. 8 * c + 7 of token t of a tile in global memory.
+template <int D, int BITS>
+__device__ __forceinline__ void int_load8(const unsigned char* tile, bool value, int t, int c, float* f) {
+    using L = IntTile<D, BITS>;
+    const float2 sz = *reinterpret_cast<const float2*>(tile + L::param(t));
+    uint32_t w[BITS / 4];  // the 8 elements' code bytes, in order
+    if (!value) {
+        const unsigned char* p = tile + L::key(t, c * BITS);
+        if constexpr (BITS == 8) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            w[0] = x.x;
+            w[1] = x.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
+    } else {
+        const unsigned char* p = tile + L::val(t, c * BITS);
+#pragma unroll
+        for (int i = 0; i < BITS / 4; ++i) {
+            const uint32_t a = *reinterpret_cast<const uint16_t*>(p + 8 * i);
+            const uint32_t b = *reinterpret_cast<const uint16_t*>(p + 8 * i + 4);
+            w[i] = a | (b << 16);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const uint32_t code = BITS == 8 ? (w[e >> 2] >> (8 * (e & 3))) & 0xffu : (w[0] >> (4 * e)) & 0xfu;
+        f[e] = fmaf(static_cast<float>(code), sz.x, sz.y);
+    }
+}
+
+// Encodes a row held by the D / 8 consecutive lanes of a group, eight
+// elements each: w receives the lane's code bytes in order, (scale, zero) is
+// the row's.  Every lane of the warp takes part in the shuffles.
+template <int D, int BITS>
+__device__ __forceinline__ float2 int_encode8(const float* f, uint32_t* w) {
+    float lo = f[0], hi = f[0];
+#pragma unroll
+    for (int e = 1; e < 8; ++e) {
+        lo = fminf(lo, f[e]);
+        hi = fmaxf(hi, f[e]);
+    }
+#pragma unroll
+    for (int m = 1; m < D / 8; m <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+    }
+    constexpr float top = BITS == 8 ? 255.f : 15.f;
+    float scale = __fdiv_rn(__fsub_rn(hi, lo), top);
+    if (!(scale >= 0x1p-126f)) scale = 0.f;
+    const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+    uint32_t code[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const int r = __float2int_rn(__fmul_rn(__fsub_rn(f[e], lo), inv));
+        code[e] = static_cast<uint32_t>(min(max(r, 0), static_cast<int>(top)));
+    }
+    if constexpr (BITS == 8) {
+        w[0] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
+        w[1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
+    } else {
+        w[0] = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[0] |= code[e] << (4 * e);
+    }
+    return make_float2(scale, lo);
+}
+
+// Stores the lane's code bytes of int_encode8 (elements 8c .. 8c + 7) and, from
+// the group's first lane, the row's parameters.
+template <int D, int BITS>
+__device__ __forceinline__ void int_store8(unsigned char* tile, bool value, int t, int c, const uint32_t* w, float2 sz) {
+    using L = IntTile<D, BITS>;
+    if (!value) {
+        unsigned char* p = tile + L::key(t, c * BITS);
+        if constexpr (BITS == 8)
+            *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        else
+            *reinterpret_cast<uint32_t*>(p) = w[0];
+    } else {
+        unsigned char* p = tile + L::val(t, c * BITS);
+#pragma unroll
+        for (int i = 0; i < BITS / 4; ++i) {
+            *reinterpret_cast<uint16_t*>(p + 8 * i) = static_cast<uint16_t>(w[i]);
+            *reinterpret_cast<uint16_t*>(p + 8 * i + 4) = static_cast<uint16_t>(w[i] >> 16);
+        }
+    }
+    if (c == 0) *reinterpret_cast<float2*>(tile + L::param(t)) = sz;
+}
+
+// Calls fn(IntTile<D, BITS>) for an integer pool type and head size.
+template <typename Fn>
+inline cudaError_t with_int_tile(int kv_dtype, int D, Fn&& fn) {
+    if (kv_dtype == PKV_INT8) return D == 128 ? fn(IntTile<128, 8>{}) : fn(IntTile<64, 8>{});
+    return D == 128 ? fn(IntTile<128, 4>{}) : fn(IntTile<64, 4>{});
+}
+
+}  // namespace pkv

@@ -17,6 +17,19 @@ constexpr int kMaxDevices = 64;
 // Smallest partition the automatic choice uses (sizes the P = 0 workspace).
 constexpr int kAutoMinPartition = 256;
 
+// Integer-coded pools (pkv_int.cuh): a row carries its own scale and zero.
+inline bool is_int_pool(int kv_dtype) { return kv_dtype == PKV_INT8 || kv_dtype == PKV_INT4; }
+inline bool known_kv_dtype(int kv_dtype) { return kv_dtype >= PKV_F16 && kv_dtype <= PKV_INT4; }
+// Bytes of one tile (16 tokens of one block and KV head) of one pool.
+inline int64_t tile_bytes(int kv_dtype, int64_t D) {
+    switch (kv_dtype) {
+    case PKV_FP8_E4M3: return kBlockSize * D;
+    case PKV_INT8: return kBlockSize * (D + 8);
+    case PKV_INT4: return kBlockSize * (D / 2 + 8);
+    default: return kBlockSize * D * 2;
+    }
+}
+
 // Arguments of one decode launch, already validated on the host.
 struct DecodeParams {
     const void* q;
@@ -62,6 +75,12 @@ struct DecodeParams {
     // (0, 0, S) waits for the prefix pass to complete, so this grid completes
     // after it and a programmatic dependent of this grid (the merge) sees both.
     int32_t join_primary = 0;
+    // Sparse decode: row (s, KV head h) attends to the blocks that its list
+    // selected[(s * Hkv + h) * nsel ..] names (logical block numbers of the
+    // sequence, a negative entry none).  P and NP then count list entries (P / 16
+    // of them in a partition), and every row has NP partitions.  Null: dense.
+    const int32_t* selected = nullptr;
+    int32_t nsel = 0;
 };
 
 // Launches kern on st, as a programmatic dependent of the kernel before it
@@ -129,6 +148,28 @@ cudaError_t launch_decode_mma_fp8_f16q(const DecodeParams& p, int G, const CUten
 // (the warp-level MMA kernel).
 cudaError_t launch_decode_gqa(const DecodeParams& p, int G, int kv_dtype, int q_dtype, const CUtensorMap& tk,
                               const CUtensorMap& tv, cudaStream_t st);
+
+// Append of 16-bit rows into an integer-coded pool (pkv_int_cache.cu).
+cudaError_t launch_append_int(const void* k, const void* v, int in_dtype, int64_t num_tokens, const int64_t* slots,
+                              void* k_cache, void* v_cache, const pkv_cache_desc* d, unsigned int* err,
+                              cudaStream_t st);
+// Integer-coded pools: dense and (p.selected) sparse decode, any G in
+// {1, 2, 4, 8}, head_size 64 or 128 (pkv_decode_int.cuh).
+cudaError_t launch_decode_int8(const DecodeParams& p, int G, int q_dtype, cudaStream_t st);
+cudaError_t launch_decode_int4(const DecodeParams& p, int G, int q_dtype, cudaStream_t st);
+// Sparse decode over 16-bit and fp8 pools: the dense kernels walking a list.
+cudaError_t launch_decode_sparse_f16(const DecodeParams& p, int G, const CUtensorMap* tk, const CUtensorMap* tv,
+                                     cudaStream_t st);
+cudaError_t launch_decode_sparse_bf16(const DecodeParams& p, int G, const CUtensorMap* tk, const CUtensorMap* tv,
+                                      cudaStream_t st);
+cudaError_t launch_decode_sparse_fp8(const DecodeParams& p, int G, int q_dtype, const CUtensorMap* tk,
+                                     const CUtensorMap* tv, cudaStream_t st);
+// Copies the blocks a batch reaches out of an integer-coded pool into 16-bit
+// blocks of q's type (prefill): copy block s * MB + j holds sequence s's
+// logical block j, and table_copy says so.
+cudaError_t launch_stage_int(int kv_dtype, int D, int q_dtype, const void* k_cache, const void* v_cache,
+                             const int32_t* block_tables, const int32_t* seq_lens, int S, int MB, int NB, int Hkv,
+                             void* k_copy, void* v_copy, int32_t* table_copy, unsigned int* err, cudaStream_t st);
 
 // Shared-prefix (cascade) decode: the prefix pass over each group's shared
 // leading blocks, kPrefixPartitionBlocks blocks per prefix partition.  Wide

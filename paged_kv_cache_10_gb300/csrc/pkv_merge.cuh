@@ -17,6 +17,11 @@ constexpr unsigned kMergeFull = 0xffffffffu;
 // sequence length.  nparts <= 1 outside cascade decode means the main
 // kernel wrote the row itself.
 __device__ __forceinline__ void merge_row_range(const DecodeParams& p, int64_t row, int& first, int& nparts) {
+    if (p.selected) {  // sparse decode: every partition of the list, empty ones with l = 0
+        first = 0;
+        nparts = p.NP;
+        return;
+    }
     const int s = static_cast<int>(row / p.Hq);
     int L = __ldg(p.seq_lens + s);
     const int Lcap = p.MB * kBlockSize;

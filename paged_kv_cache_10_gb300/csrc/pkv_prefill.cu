@@ -1220,8 +1220,10 @@ extern "C" pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype
     const int D = desc->head_size;
     if ((D != 64 && D != 128) || (G != 1 && G != 2 && G != 4 && G != 8)) return PKV_ERR_UNSUPPORTED;
     const bool fp8 = desc->kv_dtype == PKV_FP8_E4M3;
-    if (desc->kv_dtype != PKV_F16 && desc->kv_dtype != PKV_BF16 && !fp8) return PKV_ERR_UNSUPPORTED;
-    if (fp8 ? (q_dtype != PKV_F16 && q_dtype != PKV_BF16) : q_dtype != desc->kv_dtype) return PKV_ERR_UNSUPPORTED;
+    const bool coded = is_int_pool(desc->kv_dtype);
+    const bool staged = fp8 || coded;
+    if (desc->kv_dtype != PKV_F16 && desc->kv_dtype != PKV_BF16 && !staged) return PKV_ERR_UNSUPPORTED;
+    if (staged ? (q_dtype != PKV_F16 && q_dtype != PKV_BF16) : q_dtype != desc->kv_dtype) return PKV_ERR_UNSUPPORTED;
     if (!(scale > 0.f) || scale > 3.0e38f) return PKV_ERR_INVALID;  // finite, > 0 (max on raw scores)
     if (fp8 && !(desc->k_scale > 0.f && desc->k_scale < 3.0e38f && desc->v_scale > 0.f && desc->v_scale < 3.0e38f))
         return PKV_ERR_INVALID;
@@ -1233,7 +1235,7 @@ extern "C" pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype
     if (num_seqs > 65535 || desc->num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
     if (static_cast<int64_t>(desc->num_blocks) * desc->num_kv_heads * kBlockSize > INT32_MAX) return PKV_ERR_UNSUPPORTED;
     StageLayout lay{};
-    if (fp8) {
+    if (staged) {
         // the copy is a pool of num_seqs * max_blocks_per_seq blocks
         if (static_cast<int64_t>(num_seqs) * max_blocks_per_seq * desc->num_kv_heads * kBlockSize > INT32_MAX)
             return PKV_ERR_UNSUPPORTED;
@@ -1247,7 +1249,7 @@ extern "C" pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype
     const void* k_pool = k_cache;
     const void* v_pool = v_cache;
     int32_t pool_blocks = desc->num_blocks;
-    if (fp8) {
+    if (staged) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         int32_t* table_copy = reinterpret_cast<int32_t*>(ws + lay.table_off);
         uint4* k_copy = reinterpret_cast<uint4*>(ws + lay.k_off);
@@ -1256,7 +1258,12 @@ extern "C" pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype
         const dim3 grid(static_cast<unsigned>(max_blocks_per_seq), static_cast<unsigned>(num_seqs), 2);
         const auto* kc = static_cast<const uint8_t*>(k_cache);
         const auto* vc = static_cast<const uint8_t*>(v_cache);
-        if (q_dtype == PKV_BF16)
+        if (coded) {
+            if (launch_stage_int(desc->kv_dtype, D, q_dtype, k_cache, v_cache, block_tables, seq_lens, num_seqs,
+                                 max_blocks_per_seq, desc->num_blocks, desc->num_kv_heads, k_copy, v_copy, table_copy,
+                                 err, st) != cudaSuccess)
+                return PKV_ERR_CUDA;
+        } else if (q_dtype == PKV_BF16)
             stage_fp8_kernel<BF16, false><<<grid, 256, 0, st>>>(kc, vc, block_tables, seq_lens, max_blocks_per_seq,
                                                                 desc->num_blocks, block_vecs, k_copy, v_copy,
                                                                 table_copy, err, nullptr, nullptr, nullptr, 0, 0);
@@ -1308,6 +1315,6 @@ extern "C" pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype
 extern "C" size_t pkv_prefill_workspace_bytes(int32_t kv_dtype, int32_t num_seqs, int32_t num_kv_heads,
                                               int32_t head_size, int32_t max_blocks_per_seq) {
     if (num_seqs < 0 || num_kv_heads <= 0 || head_size <= 0 || max_blocks_per_seq < 0) return 0;
-    if (kv_dtype != PKV_FP8_E4M3) return 0;  // 16-bit pools are read in place
+    if (kv_dtype != PKV_FP8_E4M3 && !is_int_pool(kv_dtype)) return 0;  // 16-bit pools are read in place
     return static_cast<size_t>(stage_layout(num_seqs, max_blocks_per_seq, num_kv_heads, head_size).bytes);
 }

@@ -1,0 +1,756 @@
+// pkv_select.cu -- block selection for sparse decode: the channelwise key bounds
+// of every block, the blocks whose bounds promise the highest scores, and the
+// entry point of the attention over them.
+//
+// For a block with key bounds lo_d <= k_td <= hi_d no token of it can score
+// above  u_g = sum_d max(q_gd lo_d, q_gd hi_d)  for query head g.  A block's
+// score is max_g u_g over the G query heads of a KV head, and a row (sequence,
+// KV head) keeps the blocks of the highest scores.  With q+ = max(q, 0) and
+// q- = min(q, 0), u_g = q+_g . hi + q-_g . lo: one product of length 2 D with the
+// block's bounds as they are stored, on the warp-level tensor-core MMA with 16
+// blocks on its M rows and the G heads on its N columns.
+#include <algorithm>
+#include <cstdint>
+
+#include "pkv_decode_mma.cuh"
+#include "pkv_int.cuh"
+#include "pkv_pool_row.cuh"
+
+namespace pkv {
+namespace {
+
+// ------------------------------------------------------------- key bounds
+// One CTA per (block in reach of the new tokens, sequence): a thread takes
+// eight channels of one KV head and reads them of the block's (at most 16)
+// tokens, 16 independent loads in flight; lanes of a row read it whole, so
+// no reduction across threads is needed.
+template <int D, int KV, typename OT>
+__global__ void __launch_bounds__(128) key_bounds_kernel(const unsigned char* __restrict__ kc,
+                                                         const int32_t* __restrict__ block_tables, int MB,
+                                                         const int32_t* __restrict__ seq_lens,
+                                                         const int32_t* __restrict__ new_lens, int max_new, int NB,
+                                                         int Hkv, float k_scale, unsigned char* __restrict__ bounds,
+                                                         unsigned int* err) {
+    const int s = blockIdx.y;
+    const int len = __ldg(seq_lens + s);
+    const int fresh = new_lens ? __ldg(new_lens + s) : len;
+    if (len < 0 || len > MB * kBlockSize || fresh < 0 || fresh > len || fresh > max_new) {
+        if (threadIdx.x == 0 && blockIdx.x == 0) report(err, PKV_DEVERR_SEQ_LEN);
+        return;
+    }
+    if (fresh == 0) return;
+    const int j = (len - fresh) / kBlockSize + blockIdx.x;
+    if (j > (len - 1) / kBlockSize) return;
+    const int id = __ldg(block_tables + static_cast<int64_t>(s) * MB + j);
+    if (id < 0 || id >= NB) {
+        if (threadIdx.x == 0) report(err, PKV_DEVERR_BLOCK_ID);
+        return;
+    }
+    const int valid = min(kBlockSize, len - j * kBlockSize);
+    for (int i = threadIdx.x; i < Hkv * (D / 8); i += blockDim.x) {
+        const int h = i / (D / 8), c = i % (D / 8);
+        const int64_t at = static_cast<int64_t>(id) * Hkv + h;
+        const unsigned char* tile = kc + at * PoolRow<D, KV>::kTile;
+        float lo[8], hi[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            lo[e] = INFINITY;
+            hi[e] = -INFINITY;
+        }
+#pragma unroll
+        for (int t = 0; t < kBlockSize; ++t) {
+            if (t < valid) {
+                float f[8];
+                PoolRow<D, KV>::load(tile, false, t, c, k_scale, f);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    lo[e] = fminf(lo[e], f[e]);
+                    hi[e] = fmaxf(hi[e], f[e]);
+                }
+            }
+        }
+        unsigned char* out = bounds + (at * 2 * D + 8 * c) * 2;
+        *reinterpret_cast<uint4*>(out) = pack8_down<OT>(lo);
+        *reinterpret_cast<uint4*>(out + D * 2) = pack8_up<OT>(hi);
+    }
+}
+
+// ----------------------------------------------------------------- scores
+struct SelectParams {
+    const void* q;
+    const unsigned char* bounds;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    int32_t* selected;
+    float* score;   // [S * Hkv][cols]
+    float* top;     // [S * Hkv][cols / 16]  largest |bound| of 16 blocks
+    double* exact;  // [S * Hkv][cols]  64-bit scores of the blocks near the border
+    int S, Hq, Hkv, G, MB, NB, cols, n, sink, recent;
+    int tiles;      // 16-block tiles one warp of the score kernel takes
+    int smem_cols;  // columns of a row that the selection keeps in shared memory
+    unsigned int* err;
+};
+
+// The row's blocks, clamped to what the launch covers.
+__device__ __forceinline__ int row_blocks(const SelectParams& p, int s, bool& bad) {
+    int len = __ldg(p.seq_lens + s);
+    const int cap = min(p.MB, p.cols);
+    bad = len < 0 || (len > 0 && (len - 1) / kBlockSize >= cap);
+    return len <= 0 ? 0 : min((len - 1) / kBlockSize + 1, cap);
+}
+
+// Largest |x| of packed 16-bit pairs: magnitudes order like their bits.
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t x) { return __vmaxu2(m, x & 0x7fff7fffu); }
+
+// One warp per (KV head, run of p.tiles 16-block tiles, sequence): the tile's
+// 16 rows of 2 D bound elements come straight from global memory as MMA
+// fragments.  Lane (g8, qd) reads 16-byte chunks qd, qd + 4, ... of rows g8 and
+// g8 + 8 (four lanes read 64 contiguous bytes of a row), which only permutes the
+// contraction axis; Q's fragments follow the same order.  All loads of a tile
+// are issued before its first product.
+template <int D, typename T>
+__global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) {
+    constexpr bool kBF = std::is_same<T, BF16>::value;
+    constexpr int CH = D / 16;  // 16-byte chunks of a row per lane
+    allow_dependent_launch();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, qd = lane & 3;
+    const int64_t unit = blockIdx.x * 4ll + warp;
+    const int h = static_cast<int>(unit % p.Hkv), s = blockIdx.y;
+    const int first = static_cast<int>(unit / p.Hkv) * p.tiles;
+    bool bad;
+    const int nblk = row_blocks(p, s, bad);
+    if (bad && unit == 0 && lane == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+    if (first * 16 >= nblk || nblk <= p.n) return;  // a row that keeps every block needs no scores
+    // ---- Q's fragments: elements of [q-, q+] of head g8
+    uint32_t qb[2 * CH][2];
+    {
+        const bool live = g8 < p.G;
+        const uint4* row = reinterpret_cast<const uint4*>(static_cast<const unsigned char*>(p.q) +
+                                                          (static_cast<int64_t>(s) * p.Hq + h * p.G + (live ? g8 : 0)) * D * 2);
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            const int c = 4 * j + qd;  // chunk of the 2 D row: the first D / 8 are lo's
+            const bool low = c < D / 8;
+            const uint4 x = live ? __ldg(row + (low ? c : c - D / 8)) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            uint32_t y[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                // keep the elements whose sign bit says q < 0 (lo) or q >= 0 (hi)
+                const uint32_t neg = ((w[i] >> 15) & 0x00010001u) * 0xffffu;
+                y[i] = w[i] & (low ? neg : ~neg);
+            }
+            qb[2 * j][0] = y[0];
+            qb[2 * j][1] = y[1];
+            qb[2 * j + 1][0] = y[2];
+            qb[2 * j + 1][1] = y[3];
+        }
+    }
+    const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.MB;
+    const int64_t out = (static_cast<int64_t>(s) * p.Hkv + h) * p.cols;
+    for (int tile = first; tile < first + p.tiles && tile * 16 < nblk; ++tile) {
+        uint4 a[2][CH];
+        bool ok[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int j = tile * 16 + g8 + 8 * r;
+            const int id = j < nblk ? __ldg(table + j) : -1;
+            ok[r] = id >= 0 && id < p.NB;
+            if (j < nblk && !ok[r] && qd == 0 && h == 0) report(p.err, PKV_DEVERR_BLOCK_ID);
+            const uint4* src = reinterpret_cast<const uint4*>(p.bounds + ((ok[r] ? id : 0) * static_cast<int64_t>(p.Hkv) + h) * (4 * D)) + qd;
+#pragma unroll
+            for (int j4 = 0; j4 < CH; ++j4) a[r][j4] = ok[r] ? __ldg(src + 4 * j4) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+        uint32_t big = 0u;
+#pragma unroll
+        for (int j = 0; j < CH; ++j) {
+            mma16816a<kBF>(sa[0], a[0][j].x, a[1][j].x, a[0][j].y, a[1][j].y, qb[2 * j][0], qb[2 * j][1]);
+            mma16816a<kBF>(sa[1], a[0][j].z, a[1][j].z, a[0][j].w, a[1][j].w, qb[2 * j + 1][0], qb[2 * j + 1][1]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                big = abs_max2(abs_max2(abs_max2(abs_max2(big, a[r][j].x), a[r][j].y), a[r][j].z), a[r][j].w);
+        }
+        float v[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float x = sa[0][2 * r] + sa[1][2 * r], y = sa[0][2 * r + 1] + sa[1][2 * r + 1];
+            float m = -INFINITY;  // NaN scores are dropped: such a block ranks last
+            if (2 * qd < p.G) m = fmaxf(m, x);
+            if (2 * qd + 1 < p.G) m = fmaxf(m, y);
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+            v[r] = ok[r] ? m : -INFINITY;
+        }
+        if (qd == 0) {
+            p.score[out + tile * 16 + g8] = v[0];
+            p.score[out + tile * 16 + g8 + 8] = v[1];
+        }
+        big = __reduce_max_sync(kFull, max(big >> 16, big & 0xffffu));
+        if (lane == 0) {
+            const uint16_t b = static_cast<uint16_t>(big);
+            p.top[out / 16 + tile] = to_float(*reinterpret_cast<const typename T::storage*>(&b));
+        }
+    }
+}
+
+// -------------------------------------------------------------- selection
+constexpr int kSelThreads = 512;
+constexpr int kSelBins = 1024;
+constexpr int kSelNear = 256;  // blocks near the border that are ranked pair by pair
+
+// Sums / extrema over the CTA, the result in every thread.
+template <typename T, typename Op>
+__device__ __forceinline__ T cta_reduce(T v, Op op, T* red) {
+#pragma unroll
+    for (int m = 16; m; m >>= 1) v = op(v, __shfl_xor_sync(kFull, v, m));
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = red[threadIdx.x & (kSelThreads / 32 - 1)];
+#pragma unroll
+    for (int m = kSelThreads / 64; m; m >>= 1) v = op(v, __shfl_xor_sync(kFull, v, m));
+    return v;
+}
+
+// Exclusive sum of v over the CTA's threads in order.
+__device__ __forceinline__ int cta_scan(int v, int* red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int x = v;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, m);
+        if (lane >= m) x += y;
+    }
+    __syncthreads();
+    if (lane == 31) red[warp] = x;
+    __syncthreads();
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < kSelThreads / 32; ++w)
+        if (w < warp) before += red[w];
+    return before + x - v;
+}
+
+// Bits that order like the double they come from.
+__device__ __forceinline__ uint64_t order64(double x) {
+    const int64_t b = __double_as_longlong(x);
+    return static_cast<uint64_t>(b) ^ (b < 0 ? ~0ull : 1ull << 63);
+}
+
+// The score of block j in 64 bits, by one warp: products of 16-bit values are
+// exact, and so, but for extreme ranges, are their sums.
+template <int D, typename T>
+__device__ __forceinline__ double exact_score(const SelectParams& p, int s, int h, int j) {
+    const int lane = threadIdx.x & 31;
+    const int id = __ldg(p.block_tables + static_cast<int64_t>(s) * p.MB + j);
+    if (id < 0 || id >= p.NB) return -HUGE_VAL;
+    using E = typename T::storage;
+    const E* lo = reinterpret_cast<const E*>(p.bounds) + (static_cast<int64_t>(id) * p.Hkv + h) * 2 * D;
+    double best = -HUGE_VAL;
+    for (int g = 0; g < p.G; ++g) {
+        const E* q = reinterpret_cast<const E*>(p.q) + (static_cast<int64_t>(s) * p.Hq + h * p.G + g) * D;
+        double sum = 0.0;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const int d = lane + 32 * i;
+            const float x = to_float(q[d]);
+            sum += static_cast<double>(x) * static_cast<double>(to_float(x < 0.f ? lo[d] : lo[D + d]));
+        }
+#pragma unroll
+        for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(kFull, sum, m);
+        best = fmax(best, sum);
+    }
+    return best;
+}
+
+// One CTA per (KV head, sequence): the n blocks of the highest scores, in
+// ascending order of their numbers, ties to the lowest number.
+//
+// The binary32 scores decide all but a border band.  Every product in them is
+// exact; an MMA adds 16 of them to its accumulator, aligned to the largest
+// addend, with an error of at most 17 * 2^-23 of it, and a score is D / 8 MMAs
+// in two chains of at most 8, so with A = max_g |q_g|_1 * max |bound| it is within
+// 8 * 17 * 2^-23 A + 2^-23 A < 2^-15 A of the true score.  eps = 2^-14 A covers it
+// twice.  A histogram over the scores' range finds the bin that holds the k-th
+// highest, zooming in while the bin is wide and full; with [tl, th] the scores
+// in it, a block above th + 2 eps is in and one below tl - 2 eps is out, and
+// the few between them are scored again in 64 bits and ranked by (score,
+// number).  So the answer is that of exact arithmetic whatever the order of the
+// binary32 sums.
+template <int D, typename T>
+__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
+    extern __shared__ float row_smem[];
+    __shared__ int hist[kSelBins];
+    __shared__ __align__(8) unsigned char red_bytes[(kSelThreads / 32) * 8];
+    __shared__ int near_id[kSelNear];
+    __shared__ double near_y[kSelNear];
+    __shared__ int sh[4];
+    int* redi = reinterpret_cast<int*>(red_bytes);
+    float* redf = reinterpret_cast<float*>(red_bytes);
+    const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = static_cast<int64_t>(s) * p.Hkv + h;
+    int32_t* out = p.selected + row * p.n;
+    bool bad;
+    const int nblk = row_blocks(p, s, bad);
+    if (nblk <= p.n) {  // every block; not waiting for the scores is fine, none are read or written
+        for (int i = tid; i < p.n; i += kSelThreads) out[i] = i < nblk ? i : -1;
+        wait_primary_grid();
+        return;
+    }
+    // the free range [f0, f1) and how many of it to keep: n >= sink + recent and nblk > n
+    const int f0 = p.sink, f1 = nblk - p.recent, m = f1 - f0, k = p.n - p.sink - p.recent;
+    // A: the largest |q_g|_1 while the scores are still being made
+    float q1 = 0.f;
+    for (int g = warp; g < p.G; g += kSelThreads / 32) {
+        const typename T::storage* q =
+            reinterpret_cast<const typename T::storage*>(p.q) + (static_cast<int64_t>(s) * p.Hq + h * p.G + g) * D;
+        float a = 0.f;
+        for (int d = lane; d < D; d += 32) a += fabsf(to_float(q[d]));
+#pragma unroll
+        for (int x = 16; x; x >>= 1) a += __shfl_xor_sync(kFull, a, x);
+        q1 = fmaxf(q1, a);
+    }
+    wait_primary_grid();
+    const auto fmx = [](float a, float b) { return fmaxf(a, b); };
+    const auto fmn = [](float a, float b) { return fminf(a, b); };
+    float* sc = p.score + row * p.cols;
+    if (nblk <= p.smem_cols) {
+        for (int i = tid; i < nblk; i += kSelThreads) row_smem[i] = sc[i];
+        sc = row_smem;
+    }
+    float big = 0.f;
+    for (int i = tid; i < (nblk + 15) / 16; i += kSelThreads) big = fmaxf(big, p.top[row * (p.cols / 16) + i]);
+    q1 = cta_reduce(q1, fmx, redf);
+    big = cta_reduce(big, fmx, redf);
+    const float eps2 = 2.f * 0x1p-14f * q1 * big;
+
+    float thr = INFINITY;  // blocks above it are in
+    if (k > 0) {
+        float a = INFINITY, b = -INFINITY;
+        for (int i = f0 + tid; i < f1; i += kSelThreads) {
+            const float x = sc[i];
+            if (x > -INFINITY) a = fminf(a, x);
+            b = fmaxf(b, x);
+        }
+        a = cta_reduce(a, fmn, redf);
+        b = cta_reduce(b, fmx, redf);
+        if (!(a <= b)) a = b;  // no finite score at all
+        int above = 0;         // blocks known to score over b
+        for (int round = 0; round < 4; ++round) {
+            const float scale = kSelBins / (b - a);
+            if (!(b > a) || !(scale < INFINITY) || !(scale > 0.f)) break;
+            for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+            __syncthreads();
+            const auto bin_of = [&](float x) {  // monotone in x
+                return min(kSelBins - 1, static_cast<int>((x - a) * scale));
+            };
+            for (int i = f0 + tid; i < f1; i += kSelThreads) {
+                const float x = sc[i];
+                if (x >= a && x <= b) atomicAdd(&hist[bin_of(x)], 1);
+            }
+            __syncthreads();
+            // the bin of the k-th highest: scan from the top, two bins a thread
+            const int top_bin = kSelBins - 1 - 2 * tid;
+            const int c0 = hist[top_bin], c1 = hist[top_bin - 1];
+            const int before = above + cta_scan(c0 + c1, redi);
+            if (tid == 0) sh[0] = -1;
+            __syncthreads();
+            if (before < k && before + c0 >= k) {
+                sh[0] = top_bin;
+                sh[1] = before;
+                sh[2] = c0;
+            } else if (before + c0 < k && before + c0 + c1 >= k) {
+                sh[0] = top_bin - 1;
+                sh[1] = before + c0;
+                sh[2] = c1;
+            }
+            __syncthreads();
+            const int t = sh[0], cnt = sh[2];
+            if (t < 0) {  // the k-th is below every finite score
+                b = a;
+                break;
+            }
+            above = sh[1];
+            float na = INFINITY, nb = -INFINITY;
+            for (int i = f0 + tid; i < f1; i += kSelThreads) {
+                const float x = sc[i];
+                if (x >= a && x <= b && bin_of(x) == t) {
+                    na = fminf(na, x);
+                    nb = fmaxf(nb, x);
+                }
+            }
+            a = cta_reduce(na, fmn, redf);
+            b = cta_reduce(nb, fmx, redf);
+            if (cnt <= 16 || b - a <= eps2) break;
+        }
+        // fewer finite scores than k: everything left over is in the band
+        float low = a - eps2;
+        thr = b + eps2;
+        if (!(low > -INFINITY) || !(thr < INFINITY)) {  // no usable bound: all in the band
+            low = -INFINITY;
+            thr = INFINITY;
+        }
+        int sure = 0, band = 0, maybe = 0;
+        for (int i = f0 + tid; i < f1; i += kSelThreads) {
+            const float x = sc[i];
+            sure += x > thr;
+            band += x <= thr && x >= low;
+            maybe += x < low;
+        }
+        const auto add = [](int u, int v) { return u + v; };
+        sure = cta_reduce(sure, add, redi);
+        band = cta_reduce(band, add, redi);
+        if (sure + band < k) {  // blocks without a usable score fill up
+            low = -INFINITY;
+            band = m - sure;
+        }
+        const int want = k - sure;
+        if (band == want) {
+            thr = low;  // all of the band
+            for (int i = f0 + tid; i < f1; i += kSelThreads)
+                if (sc[i] == low) sc[i] = INFINITY;
+        } else {
+            // ---- 64-bit scores of the band
+            if (tid == 0) sh[3] = 0;
+            __syncthreads();
+            const bool few = band <= kSelNear;
+            if (few) {
+                for (int i = f0 + tid; i < f1; i += kSelThreads)
+                    if (sc[i] <= thr && sc[i] >= low) near_id[atomicAdd(&sh[3], 1)] = i;
+                __syncthreads();
+                for (int i = warp; i < band; i += kSelThreads / 32) {
+                    const double y = exact_score<D, T>(p, s, h, near_id[i]);
+                    if (lane == 0) near_y[i] = y;
+                }
+                __syncthreads();
+                for (int i = tid; i < band; i += kSelThreads) {
+                    const double y = near_y[i];
+                    const int id = near_id[i];
+                    int rank = 0;
+                    for (int j = 0; j < band; ++j) rank += near_y[j] > y || (near_y[j] == y && near_id[j] < id);
+                    sc[id] = rank < want ? INFINITY : -INFINITY;
+                }
+            } else {
+                // many near the border (equal scores): radix selection of the want-th
+                // highest 64-bit score, then the lowest numbers among those equal to it
+                double* ex = p.exact + row * p.cols;
+                for (int i = f0 + warp; i < f1; i += kSelThreads / 32) {
+                    const float x = sc[i];
+                    if (!(x <= thr && x >= low)) continue;
+                    const double y = exact_score<D, T>(p, s, h, i);
+                    if (lane == 0) ex[i] = y;
+                }
+                __syncthreads();
+                uint64_t prefix = 0, mask = 0;
+                int left = want;
+                for (int shift = 56; shift >= 0; shift -= 8) {
+                    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
+                    __syncthreads();
+                    for (int i = f0 + tid; i < f1; i += kSelThreads) {
+                        const float x = sc[i];
+                        if (!(x <= thr && x >= low)) continue;
+                        const uint64_t o = order64(ex[i]);
+                        if ((o & mask) == prefix) atomicAdd(&hist[(o >> shift) & 255], 1);
+                    }
+                    __syncthreads();
+                    const int c = tid < 256 ? hist[255 - tid] : 0;
+                    const int before = cta_scan(c, redi);
+                    if (before < left && before + c >= left) {
+                        sh[0] = 255 - tid;
+                        sh[1] = left - before;
+                    }
+                    __syncthreads();
+                    prefix |= static_cast<uint64_t>(sh[0]) << shift;
+                    mask |= 255ull << shift;
+                    left = sh[1];
+                    __syncthreads();
+                }
+                // `left` of the blocks whose score has these bits, lowest numbers first
+                const int per = (m + kSelThreads - 1) / kSelThreads;
+                const int i0 = f0 + tid * per, i1 = min(f1, i0 + per);
+                int same = 0;
+                for (int i = i0; i < i1; ++i) same += sc[i] <= thr && sc[i] >= low && order64(ex[i]) == prefix;
+                int at = cta_scan(same, redi);
+                for (int i = i0; i < i1; ++i) {
+                    const float x = sc[i];
+                    if (!(x <= thr && x >= low)) continue;
+                    const uint64_t o = order64(ex[i]);
+                    const bool in = o > prefix || (o == prefix && at++ < left);
+                    sc[i] = in ? INFINITY : -INFINITY;
+                }
+            }
+        }
+        __syncthreads();
+    }
+    // ---- the kept blocks in ascending order
+    const int per = (nblk + kSelThreads - 1) / kSelThreads;
+    const int i0 = tid * per, i1 = min(nblk, i0 + per);
+    const auto kept = [&](int i) { return i < f0 || i >= f1 || (k > 0 && (sc[i] > thr || sc[i] == INFINITY)); };
+    int mine = 0;
+    for (int i = i0; i < i1; ++i) mine += kept(i);
+    int at = cta_scan(mine, redi);
+    for (int i = i0; i < i1; ++i)
+        if (kept(i) && at < p.n) out[at++] = i;
+}
+
+template <int D, typename T>
+cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
+    const int64_t units = static_cast<int64_t>((p.cols / 16 + p.tiles - 1) / p.tiles) * p.Hkv;
+    block_score_kernel<D, T><<<dim3(static_cast<unsigned>((units + 3) / 4), p.S), 128, 0, st>>>(p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const size_t smem = static_cast<size_t>(p.smem_cols) * 4;
+    if (smem > 32 * 1024) {  // with the static arrays, more than a launch gets unasked
+        e = cudaFuncSetAttribute(select_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+    }
+    return launch_maybe_pdl(true, select_kernel<D, T>, dim3(p.Hkv, p.S), dim3(kSelThreads), smem, st, p);
+}
+
+template <int D, typename OT>
+cudaError_t launch_bounds_of(int kv, dim3 grid, cudaStream_t st, const unsigned char* kc, const int32_t* tables, int MB,
+                             const int32_t* lens, const int32_t* fresh, int max_new, const pkv_cache_desc* d,
+                             unsigned char* bounds, unsigned int* err) {
+    void (*kern)(const unsigned char*, const int32_t*, int, const int32_t*, const int32_t*, int, int, int, float,
+                 unsigned char*, unsigned int*) = nullptr;
+    switch (kv) {
+    case PKV_F16: kern = key_bounds_kernel<D, PKV_F16, F16>; break;
+    case PKV_BF16: kern = key_bounds_kernel<D, PKV_BF16, BF16>; break;
+    case PKV_FP8_E4M3: kern = key_bounds_kernel<D, PKV_FP8_E4M3, OT>; break;
+    case PKV_INT8: kern = key_bounds_kernel<D, PKV_INT8, OT>; break;
+    default: kern = key_bounds_kernel<D, PKV_INT4, OT>; break;
+    }
+    kern<<<grid, 128, 0, st>>>(kc, tables, MB, lens, fresh, max_new, d->num_blocks, d->num_kv_heads, d->k_scale, bounds,
+                               err);
+    return cudaGetLastError();
+}
+
+bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Checks that the three calls share.
+pkv_status check_desc(const pkv_cache_desc* d, int32_t num_seqs, int32_t max_blocks_per_seq) {
+    if (!d || num_seqs < 0 || max_blocks_per_seq <= 0) return PKV_ERR_INVALID;
+    if (d->num_blocks <= 0 || d->num_kv_heads <= 0 || d->head_size <= 0 || d->block_size <= 0) return PKV_ERR_INVALID;
+    if (!known_kv_dtype(d->kv_dtype)) return PKV_ERR_INVALID;
+    if (d->kv_dtype == PKV_FP8_E4M3 && !(d->k_scale > 0.f && d->v_scale > 0.f)) return PKV_ERR_INVALID;
+    if (d->block_size != kBlockSize || (d->head_size != 64 && d->head_size != 128)) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs > 65535 || d->num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if (max_blocks_per_seq > 0x7fffffff / kBlockSize) return PKV_ERR_UNSUPPORTED;  // positions are 32-bit
+    return PKV_OK;
+}
+
+bool group_ok(int32_t num_q_heads, const pkv_cache_desc* d, pkv_status* st) {
+    *st = PKV_ERR_INVALID;
+    if (num_q_heads <= 0 || num_q_heads % d->num_kv_heads) return false;
+    const int G = num_q_heads / d->num_kv_heads;
+    *st = PKV_ERR_UNSUPPORTED;
+    return G == 1 || G == 2 || G == 4 || G == 8;
+}
+
+struct SelectLayout {
+    int64_t cols, top_off, exact_off, bytes;
+};
+SelectLayout select_layout(int64_t S, int64_t Hkv, int64_t max_seq_len) {
+    const auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
+    SelectLayout l{};
+    l.cols = cdiv(max_seq_len > 0 ? cdiv(max_seq_len, kBlockSize) : 1, 16) * 16;
+    const int64_t rows = S * Hkv;
+    l.top_off = up(rows * l.cols * 4);
+    l.exact_off = l.top_off + up(rows * (l.cols / 16) * 4);
+    l.bytes = l.exact_off + up(rows * l.cols * 8);
+    return l;
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" pkv_status pkv_paged_key_bounds(const void* k_cache, const pkv_cache_desc* d, const int32_t* block_tables,
+                                           int32_t max_blocks_per_seq, const int32_t* seq_lens, const int32_t* new_lens,
+                                           int32_t max_new_len, int32_t num_seqs, void* bounds, int32_t bounds_dtype,
+                                           void* stream) {
+    const pkv_status c = check_desc(d, num_seqs, max_blocks_per_seq);
+    if (c != PKV_OK) return c;
+    if (max_new_len < 0 || (bounds_dtype != PKV_F16 && bounds_dtype != PKV_BF16)) return PKV_ERR_INVALID;
+    if ((d->kv_dtype == PKV_F16 || d->kv_dtype == PKV_BF16) && bounds_dtype != d->kv_dtype) return PKV_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(max_new_len) > static_cast<int64_t>(max_blocks_per_seq) * kBlockSize) return PKV_ERR_INVALID;
+    if (num_seqs == 0 || max_new_len == 0) return PKV_OK;
+    if (!k_cache || !block_tables || !seq_lens || !bounds) return PKV_ERR_INVALID;
+    if (!aligned(k_cache, 16) || !aligned(bounds, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+        !aligned(new_lens, 4))
+        return PKV_ERR_INVALID;
+    unsigned int* err = error_word();
+    if (!err) return PKV_ERR_CUDA;
+    // n new tokens reach into at most (n + 14) / 16 + 1 blocks
+    const int64_t reach = (static_cast<int64_t>(max_new_len) + 14) / kBlockSize + 1;
+    const dim3 grid(static_cast<unsigned>(reach < max_blocks_per_seq ? reach : max_blocks_per_seq),
+                    static_cast<unsigned>(num_seqs));
+    const auto* kc = static_cast<const unsigned char*>(k_cache);
+    auto* out = static_cast<unsigned char*>(bounds);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool bf = bounds_dtype == PKV_BF16;
+    cudaError_t e;
+    if (d->head_size == 128)
+        e = bf ? launch_bounds_of<128, BF16>(d->kv_dtype, grid, st, kc, block_tables, max_blocks_per_seq, seq_lens, new_lens,
+                                             max_new_len, d, out, err)
+               : launch_bounds_of<128, F16>(d->kv_dtype, grid, st, kc, block_tables, max_blocks_per_seq, seq_lens, new_lens,
+                                            max_new_len, d, out, err);
+    else
+        e = bf ? launch_bounds_of<64, BF16>(d->kv_dtype, grid, st, kc, block_tables, max_blocks_per_seq, seq_lens, new_lens,
+                                            max_new_len, d, out, err)
+               : launch_bounds_of<64, F16>(d->kv_dtype, grid, st, kc, block_tables, max_blocks_per_seq, seq_lens, new_lens,
+                                           max_new_len, d, out, err);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+extern "C" size_t pkv_select_blocks_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads, int32_t max_seq_len) {
+    if (num_seqs < 0 || num_kv_heads <= 0 || max_seq_len < 0) return 0;
+    return static_cast<size_t>(select_layout(num_seqs, num_kv_heads, max_seq_len).bytes);
+}
+
+extern "C" pkv_status pkv_select_blocks(const void* q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                                        const void* bounds, const pkv_cache_desc* d, const int32_t* block_tables,
+                                        int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len,
+                                        int32_t num_selected, int32_t sink_blocks, int32_t recent_blocks,
+                                        int32_t* selected, void* workspace, size_t workspace_bytes, void* stream) {
+    const pkv_status c = check_desc(d, num_seqs, max_blocks_per_seq);
+    if (c != PKV_OK) return c;
+    if ((q_dtype != PKV_F16 && q_dtype != PKV_BF16) || max_seq_len < 0) return PKV_ERR_INVALID;
+    if (num_selected <= 0 || sink_blocks < 0 || recent_blocks < 0 ||
+        static_cast<int64_t>(sink_blocks) + recent_blocks > num_selected)
+        return PKV_ERR_INVALID;
+    if (static_cast<int64_t>(max_seq_len) > static_cast<int64_t>(max_blocks_per_seq) * kBlockSize) return PKV_ERR_INVALID;
+    pkv_status g;
+    if (!group_ok(num_q_heads, d, &g)) return g;
+    if ((d->kv_dtype == PKV_F16 || d->kv_dtype == PKV_BF16) && q_dtype != d->kv_dtype) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!q || !bounds || !block_tables || !seq_lens || !selected) return PKV_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(block_tables, 4) || !aligned(seq_lens, 4) ||
+        !aligned(selected, 4))
+        return PKV_ERR_INVALID;
+    const SelectLayout l = select_layout(num_seqs, d->num_kv_heads, max_seq_len);
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < static_cast<size_t>(l.bytes)) return PKV_ERR_WORKSPACE;
+    SelectParams p{};
+    p.err = error_word();
+    if (!p.err) return PKV_ERR_CUDA;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    p.q = q;
+    p.bounds = static_cast<const unsigned char*>(bounds);
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.selected = selected;
+    p.score = reinterpret_cast<float*>(ws);
+    p.top = reinterpret_cast<float*>(ws + l.top_off);
+    p.exact = reinterpret_cast<double*>(ws + l.exact_off);
+    p.S = num_seqs;
+    p.Hq = num_q_heads;
+    p.Hkv = d->num_kv_heads;
+    p.G = num_q_heads / d->num_kv_heads;
+    p.MB = max_blocks_per_seq;
+    p.NB = d->num_blocks;
+    p.cols = static_cast<int>(l.cols);
+    p.n = num_selected;
+    p.sink = sink_blocks;
+    p.recent = recent_blocks;
+    // enough warps to fill the SMs a few times; beyond that a warp takes several
+    // tiles and builds Q's fragments once
+    const int64_t warps = static_cast<int64_t>(l.cols / 16) * p.Hkv * p.S;
+    p.tiles = static_cast<int>(std::min<int64_t>(8, std::max<int64_t>(1, warps / (num_sms() * 32))));
+    constexpr int kSmemCols = 16384;  // 64 KiB; longer rows stay in the workspace
+    p.smem_cols = static_cast<int>(std::min<int64_t>(l.cols, kSmemCols));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool bf = q_dtype == PKV_BF16;
+    cudaError_t e;
+    if (d->head_size == 128)
+        e = bf ? launch_select<128, BF16>(p, st) : launch_select<128, F16>(p, st);
+    else
+        e = bf ? launch_select<64, BF16>(p, st) : launch_select<64, F16>(p, st);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+extern "C" size_t pkv_decode_sparse_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t head_size,
+                                                    int32_t num_selected, int32_t partition_blocks) {
+    if (num_seqs < 0 || num_q_heads <= 0 || head_size <= 0 || num_selected <= 0 || partition_blocks < 0) return 0;
+    const int64_t NP = cdiv(num_selected, partition_blocks > 0 ? partition_blocks : kAutoMinPartition / kBlockSize);
+    return NP <= 1 ? 0 : partials_bytes(num_seqs, num_q_heads, head_size, NP);
+}
+
+extern "C" pkv_status pkv_paged_attention_decode_sparse(const void* q, int32_t q_dtype, int32_t num_seqs,
+                                                        int32_t num_q_heads, const void* k_cache, const void* v_cache,
+                                                        const pkv_cache_desc* d, const int32_t* block_tables,
+                                                        int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                                        const int32_t* selected, int32_t num_selected, float scale,
+                                                        void* out, void* workspace, size_t workspace_bytes,
+                                                        int32_t partition_blocks, void* stream) {
+    const pkv_status c = check_desc(d, num_seqs, max_blocks_per_seq);
+    if (c != PKV_OK) return c;
+    if ((q_dtype != PKV_F16 && q_dtype != PKV_BF16) || !(scale == scale)) return PKV_ERR_INVALID;
+    if (num_selected <= 0 || partition_blocks < 0 || partition_blocks > 0x7fffffff / kBlockSize ||
+        num_selected > 0x7fffffff / kBlockSize)
+        return PKV_ERR_INVALID;
+    pkv_status g;
+    if (!group_ok(num_q_heads, d, &g)) return g;
+    if ((d->kv_dtype == PKV_F16 || d->kv_dtype == PKV_BF16) && q_dtype != d->kv_dtype) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !seq_lens || !selected || !out) return PKV_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4))
+        return PKV_ERR_INVALID;
+    const int G = num_q_heads / d->num_kv_heads;
+    const int per = partition_blocks > 0
+                        ? partition_blocks
+                        : auto_partition(num_seqs, d->num_kv_heads, num_selected * kBlockSize, false) / kBlockSize;
+    const int64_t NP = cdiv(num_selected, per);
+    const size_t need = NP > 1 ? partials_bytes(num_seqs, num_q_heads, d->head_size, NP) : 0;
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return PKV_ERR_WORKSPACE;
+    DecodeParams p{};
+    p.err = error_word();
+    if (!p.err) return PKV_ERR_CUDA;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.out = out;
+    p.S = num_seqs;
+    p.Hq = num_q_heads;
+    p.Hkv = d->num_kv_heads;
+    p.D = d->head_size;
+    p.NB = d->num_blocks;
+    p.MB = max_blocks_per_seq;
+    p.P = per * kBlockSize;
+    p.NP = static_cast<int32_t>(NP);
+    const bool fp8 = d->kv_dtype == PKV_FP8_E4M3;
+    p.qk_scale = scale * 1.4426950408889634f * (fp8 ? d->k_scale : 1.f);
+    p.v_scale = fp8 ? d->v_scale : 1.f;
+    p.selected = selected;
+    p.nsel = num_selected;
+    if (need > 0) partials_layout(p, workspace);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (is_int_pool(d->kv_dtype)) {
+        e = d->kv_dtype == PKV_INT8 ? launch_decode_int8(p, G, q_dtype, st) : launch_decode_int4(p, G, q_dtype, st);
+    } else {
+        // the kernel that the dense decode of this shape would use
+        const int64_t pool_rows = static_cast<int64_t>(d->num_blocks) * d->num_kv_heads * kBlockSize;
+        CUtensorMap tk, tv;
+        const bool mma = d->head_size == 128 && G >= 2 && pool_rows <= 0x7fffffff;
+        if (mma && (!encode_pool_map(&tk, k_cache, fp8 ? 1 : 2, pool_rows, d->head_size) ||
+                    !encode_pool_map(&tv, v_cache, fp8 ? 1 : 2, pool_rows, d->head_size)))
+            return PKV_ERR_CUDA;
+        const CUtensorMap* mk = mma ? &tk : nullptr;
+        const CUtensorMap* mv = mma ? &tv : nullptr;
+        if (fp8)
+            e = launch_decode_sparse_fp8(p, G, q_dtype, mk, mv, st);
+        else
+            e = d->kv_dtype == PKV_F16 ? launch_decode_sparse_f16(p, G, mk, mv, st)
+                                       : launch_decode_sparse_bf16(p, G, mk, mv, st);
+    }
+    if (e != cudaSuccess) return PKV_ERR_CUDA;
+    if (NP > 1 && launch_merge(p, q_dtype, st) != cudaSuccess) return PKV_ERR_CUDA;
+    return PKV_OK;
+}

@@ -20,8 +20,8 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpagedkv.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_OOM, ERR_CUDA, ERR_WORKSPACE, ERR_NOT_FOUND = range(7)
-F16, BF16, FP8_E4M3 = 0, 1, 2
-DTYPE_CODE = {"f16": F16, "bf16": BF16, "e4m3": FP8_E4M3}
+F16, BF16, FP8_E4M3, INT8, INT4 = 0, 1, 2, 3, 4
+DTYPE_CODE = {"f16": F16, "bf16": BF16, "e4m3": FP8_E4M3, "int8": INT8, "int4": INT4}
 DEVERR_BLOCK_ID, DEVERR_SEQ_LEN, DEVERR_SLOT, DEVERR_COPY_PAIR, DEVERR_TIMEOUT = 1, 2, 4, 8, 16
 
 EXPORTED = [
@@ -37,7 +37,9 @@ EXPORTED = [
     "pkv_alloc_lookup", "pkv_alloc_seq_new_prefix", "pkv_alloc_commit", "pkv_alloc_num_cached",
     "pkv_alloc_block_hash_of", "pkv_alloc_reset_prefix_cache", "pkv_paged_attention_decode_append",
     "pkv_prefill_plan", "pkv_decode_plan", "pkv_prefill_workspace_bytes", "pkv_check_wait_timeout",
-    "pkv_decode_cascade_staging_bytes",
+    "pkv_decode_cascade_staging_bytes", "pkv_cache_block_bytes", "pkv_paged_kv_read", "pkv_paged_key_bounds",
+    "pkv_select_blocks_workspace_bytes", "pkv_select_blocks", "pkv_decode_sparse_workspace_bytes",
+    "pkv_paged_attention_decode_sparse",
 ]
 
 
@@ -139,6 +141,14 @@ def lib():
                                               ctypes.c_float, P, P, ctypes.c_size_t, P]),
         "pkv_prefill_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32]),
         "pkv_prefill_plan": (i32, [P, P, i32, i32, i32, i32, P, i32, P]),
+        "pkv_cache_block_bytes": (ctypes.c_size_t, [D]),
+        "pkv_paged_kv_read": (i32, [P, i32, P, P, D, P, P, i32, P]),
+        "pkv_paged_key_bounds": (i32, [P, D, P, i32, P, P, i32, i32, P, i32, P]),
+        "pkv_select_blocks_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32]),
+        "pkv_select_blocks": (i32, [P, i32, i32, i32, P, D, P, i32, P, i32, i32, i32, i32, P, P, ctypes.c_size_t, P]),
+        "pkv_decode_sparse_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32]),
+        "pkv_paged_attention_decode_sparse": (i32, [P, i32, i32, i32, P, P, D, P, i32, P, P, i32, ctypes.c_float, P,
+                                                    P, ctypes.c_size_t, i32, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -190,6 +200,32 @@ def _dtype_code(t: torch.Tensor, declared: str | None) -> int:
     return _TORCH_CODE[t.dtype]
 
 
+def _on_current_device(*tensors) -> None:
+    """The launch goes to the current device: a tensor of another one is refused."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.is_cuda and t.device.index != cur:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
+
+
+def _shape(t: torch.Tensor, want: tuple, name: str) -> None:
+    if tuple(t.shape) != want:
+        raise ValueError(f"{name} must have shape {list(want)}, not {list(t.shape)}")
+
+
+def _pool_ptr(t: torch.Tensor, desc: CacheDesc, name: str) -> int:
+    p = _dev_ptr(t, name)
+    if t.numel() * t.element_size() != desc.num_blocks * block_bytes(desc):
+        raise ValueError(f"{name} must hold {desc.num_blocks} blocks of {block_bytes(desc)} bytes")
+    return p
+
+
+def block_bytes(desc: CacheDesc) -> int:
+    """Bytes of one block (every KV head) of one pool, 0 for a description that is not supported.  An
+    int8 / int4 pool is a uint8 tensor [num_blocks, num_kv_heads, tile bytes]."""
+    return int(lib().pkv_cache_block_bytes(ctypes.byref(desc.c())))
+
+
 # ------------------------------------------------------------------- GPU ops
 def paged_kv_append(k, v, slot_mapping, k_cache, v_cache, desc: CacheDesc, in_dtype: str | None = None,
                     stream=None) -> None:
@@ -201,6 +237,25 @@ def paged_kv_append(k, v, slot_mapping, k_cache, v_cache, desc: CacheDesc, in_dt
                                    _dev_ptr(slot_mapping, "slot_mapping"), _dev_ptr(k_cache, "k_cache"),
                                    _dev_ptr(v_cache, "v_cache"), ctypes.byref(desc.c()), _stream(stream))
     _check(st, "paged_kv_append")
+
+
+def paged_kv_read(slot_mapping, k_cache, v_cache, desc: CacheDesc, k_out, v_out, out_dtype: str | None = None,
+                  stream=None) -> None:
+    """Cached rows by slot, as 16-bit values: k_out, v_out [T, Hkv, D]; slot_mapping int64 [T] (device); the
+    output rows of negative slots stay as they are."""
+    T = int(slot_mapping.shape[0])
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    for o, n in ((k_out, "k_out"), (v_out, "v_out")):
+        _shape(o, (T, desc.num_kv_heads, desc.head_size), n)
+    if k_out.element_size() != 2 or v_out.dtype != k_out.dtype:
+        raise TypeError("k_out and v_out must be of one 16-bit type")
+    _on_current_device(slot_mapping, k_cache, v_cache, k_out, v_out)
+    st = lib().pkv_paged_kv_read(_dev_ptr(slot_mapping, "slot_mapping"), T, _pool_ptr(k_cache, desc, "k_cache"),
+                                 _pool_ptr(v_cache, desc, "v_cache"), ctypes.byref(desc.c()),
+                                 _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"), _dtype_code(k_out, out_dtype),
+                                 _stream(stream))
+    _check(st, "paged_kv_read")
 
 
 def copy_blocks(k_cache, v_cache, desc: CacheDesc, pairs, num_pairs: int | None = None, stream=None) -> None:
@@ -353,6 +408,94 @@ def paged_attention_decode_append(k_new, v_new, slot_mapping, q, k_cache, v_cach
         _dev_ptr(work_units, "work_units") if work_units is not None and work_units.numel() else None,
         int(work_units.numel()) if work_units is not None else 0, _stream(stream))
     _check(st, "paged_attention_decode_append")
+
+
+def paged_key_bounds(k_cache, desc: CacheDesc, block_tables, seq_lens, new_lens, max_new_len: int, bounds,
+                     bounds_dtype: str | None = None, stream=None) -> None:
+    """Channelwise minimum and maximum of the keys of every block that holds one of a sequence's last
+    new_lens[s] tokens (int32 [S], device; None: all its tokens): bounds [NB, Hkv, 2, D], row 0 the minimum."""
+    S = int(seq_lens.shape[0])
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        raise TypeError("block_tables and seq_lens must be int32")
+    if new_lens is not None and (new_lens.dtype != torch.int32 or int(new_lens.shape[0]) != S):
+        raise ValueError("new_lens must be int32 with one entry per sequence")
+    if int(block_tables.shape[0]) != S:
+        raise ValueError("block_tables must have one row per sequence")
+    _shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_size), "bounds")
+    if bounds.element_size() != 2:
+        raise TypeError("bounds must be of a 16-bit type")
+    _on_current_device(k_cache, block_tables, seq_lens, new_lens, bounds)
+    st = lib().pkv_paged_key_bounds(_pool_ptr(k_cache, desc, "k_cache"), ctypes.byref(desc.c()),
+                                    _dev_ptr(block_tables, "block_tables"), int(block_tables.shape[1]),
+                                    _dev_ptr(seq_lens, "seq_lens"),
+                                    _dev_ptr(new_lens, "new_lens") if new_lens is not None else None,
+                                    int(max_new_len), S, _dev_ptr(bounds, "bounds"),
+                                    _dtype_code(bounds, bounds_dtype), _stream(stream))
+    _check(st, "paged_key_bounds")
+
+
+def select_blocks_workspace_bytes(num_seqs: int, num_kv_heads: int, max_seq_len: int) -> int:
+    return int(lib().pkv_select_blocks_workspace_bytes(num_seqs, num_kv_heads, max_seq_len))
+
+
+def select_blocks(q, bounds, desc: CacheDesc, block_tables, seq_lens, max_seq_len: int, selected, workspace,
+                  sink_blocks: int = 1, recent_blocks: int = 1, q_dtype: str | None = None, stream=None) -> None:
+    """The blocks each (sequence, KV head) attends to: q [S, Hq, D], bounds [NB, Hkv, 2, D] of q's type,
+    selected int32 [S, Hkv, n] (logical block numbers, ascending, then -1)."""
+    S, Hq = int(q.shape[0]), int(q.shape[1])
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or selected.dtype != torch.int32:
+        raise TypeError("block_tables, seq_lens and selected must be int32")
+    if bounds.dtype != q.dtype:
+        raise TypeError("bounds must have q's type")
+    _shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_size), "bounds")
+    _shape(q, (S, Hq, desc.head_size), "q")
+    if selected.dim() != 3 or tuple(selected.shape[:2]) != (S, desc.num_kv_heads):
+        raise ValueError("selected must have shape [num_seqs, num_kv_heads, n]")
+    if int(block_tables.shape[0]) != S or int(seq_lens.shape[0]) != S:
+        raise ValueError("block_tables and seq_lens must have one row per sequence")
+    _on_current_device(q, bounds, block_tables, seq_lens, selected, workspace)
+    st = lib().pkv_select_blocks(_dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq, _dev_ptr(bounds, "bounds"),
+                                 ctypes.byref(desc.c()), _dev_ptr(block_tables, "block_tables"),
+                                 int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"), int(max_seq_len),
+                                 int(selected.shape[2]), int(sink_blocks), int(recent_blocks),
+                                 _dev_ptr(selected, "selected"), _dev_ptr(workspace, "workspace"),
+                                 workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "select_blocks")
+
+
+def decode_sparse_workspace_bytes(num_seqs: int, num_q_heads: int, head_size: int, num_selected: int,
+                                  partition_blocks: int = 0) -> int:
+    return int(lib().pkv_decode_sparse_workspace_bytes(num_seqs, num_q_heads, head_size, num_selected,
+                                                       partition_blocks))
+
+
+def paged_attention_decode_sparse(q, k_cache, v_cache, desc: CacheDesc, block_tables, seq_lens, selected,
+                                  scale: float, out, workspace=None, partition_blocks: int = 0,
+                                  q_dtype: str | None = None, stream=None) -> None:
+    """Decode attention over the blocks that selected (int32 [S, Hkv, n], as select_blocks writes it) names:
+    q, out [S, Hq, D]."""
+    S, Hq = int(q.shape[0]), int(q.shape[1])
+    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or selected.dtype != torch.int32:
+        raise TypeError("block_tables, seq_lens and selected must be int32")
+    _shape(q, (S, Hq, desc.head_size), "q")
+    _shape(out, (S, Hq, desc.head_size), "out")
+    if out.dtype != q.dtype:
+        raise TypeError("out must have q's type")
+    if selected.dim() != 3 or tuple(selected.shape[:2]) != (S, desc.num_kv_heads):
+        raise ValueError("selected must have shape [num_seqs, num_kv_heads, n]")
+    if int(block_tables.shape[0]) != S or int(seq_lens.shape[0]) != S:
+        raise ValueError("block_tables and seq_lens must have one row per sequence")
+    _on_current_device(q, k_cache, v_cache, block_tables, seq_lens, selected, out, workspace)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_ptr, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    st = lib().pkv_paged_attention_decode_sparse(
+        _dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq, _pool_ptr(k_cache, desc, "k_cache"),
+        _pool_ptr(v_cache, desc, "v_cache"), ctypes.byref(desc.c()), _dev_ptr(block_tables, "block_tables"),
+        int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(selected, "selected"),
+        int(selected.shape[2]), float(scale), _dev_ptr(out, "out"), ws_ptr, ws_bytes, int(partition_blocks),
+        _stream(stream))
+    _check(st, "paged_attention_decode_sparse")
 
 
 def decode_plan(seq_lens, num_kv_heads: int, max_seq_len: int, partition_tokens: int = 0) -> np.ndarray:
