@@ -171,6 +171,7 @@ extern "C" pkv_status pkv_paged_kv_append(const void* k, const void* v, int32_t 
     const bool to_fp8 = desc->kv_dtype == PKV_FP8_E4M3 && (in_dtype == PKV_BF16 || in_dtype == PKV_F16);
     const bool to_int = is_int_pool(desc->kv_dtype) && (in_dtype == PKV_BF16 || in_dtype == PKV_F16);
     if (!same && !to_fp8 && !to_int) return PKV_ERR_UNSUPPORTED;
+    if (to_int && static_cast<int64_t>(num_tokens) * desc->num_kv_heads > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
     unsigned int* err = error_word();
     if (!err) return PKV_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -24,6 +24,8 @@
 // the contraction axis of P V).
 #pragma once
 
+#include <type_traits>
+
 #include "pkv_device.cuh"
 
 namespace pkv {
@@ -44,6 +46,14 @@ struct IntTile {
     }
     __host__ __device__ static constexpr int param(int t) { return kCodes + t * 8; }
 };
+
+// The values of a word's four bytes: a byte under the exponent of 2^23 is that
+// float plus the code, exactly, which spares the integer conversion.
+__device__ __forceinline__ void int_value4(uint32_t w, float2 sz, float* f, int step) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i * step] = fmaf(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | i)) - 8388608.f, sz.x, sz.y);
+}
 
 // Eight elements 8 * c .. 8 * c + 7 of token t of a tile in global memory.
 template <int D, int BITS>
@@ -69,46 +79,58 @@ __device__ __forceinline__ void int_load8(const unsigned char* tile, bool value,
             w[i] = a | (b << 16);
         }
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const uint32_t code = BITS == 8 ? (w[e >> 2] >> (8 * (e & 3))) & 0xffu : (w[0] >> (4 * e)) & 0xfu;
-        f[e] = fmaf(static_cast<float>(code), sz.x, sz.y);
+    if constexpr (BITS == 4) {
+        const uint32_t x = w[0];
+        uint32_t lo = x & 0x0f0f0f0fu, hi = (x >> 4) & 0x0f0f0f0fu;
+        int_value4(lo, sz, f, 2);
+        int_value4(hi, sz, f + 1, 2);
+    } else {
+        int_value4(w[0], sz, f, 1);
+        int_value4(w[1], sz, f + 4, 1);
     }
 }
 
-// Encodes a row held by the D / 8 consecutive lanes of a group, eight
-// elements each: w receives the lane's code bytes in order, (scale, zero) is
-// the row's.  Every lane of the warp takes part in the shuffles.
-template <int D, int BITS>
-__device__ __forceinline__ float2 int_encode8(const float* f, uint32_t* w) {
-    float lo = f[0], hi = f[0];
-#pragma unroll
-    for (int e = 1; e < 8; ++e) {
-        lo = fminf(lo, f[e]);
-        hi = fmaxf(hi, f[e]);
-    }
+// Eight 16-bit elements of a row held by the D / 8 consecutive lanes of a group
+// to code bytes: w receives the lane's, in order; (scale, zero) is the row's.
+// Every lane of the warp takes part in the shuffles.  The extrema are found on
+// 16-bit pairs, (min, -max) in one register from the first shuffle on.
+template <int D, int BITS, typename IT>
+__device__ __forceinline__ float2 int_encode8(uint4 x, uint32_t* w) {
+    using P2 = typename std::conditional<std::is_same<IT, BF16>::value, __nv_bfloat162, __half2>::type;
+    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+    const P2* v = reinterpret_cast<const P2*>(xw);
+    const P2 mn = __hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3]));
+    const P2 mx = __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3]));
+    P2 key;
+    key.x = __hmin(mn.x, mn.y);
+    key.y = __hneg(__hmax(mx.x, mx.y));
 #pragma unroll
     for (int m = 1; m < D / 8; m <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, m));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, m));
+        const uint32_t o = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&key), m);
+        key = __hmin2(key, *reinterpret_cast<const P2*>(&o));
     }
+    const float lo = to_float(key.x), hi = -to_float(key.y);
     constexpr float top = BITS == 8 ? 255.f : 15.f;
     float scale = __fdiv_rn(__fsub_rn(hi, lo), top);
     if (!(scale >= 0x1p-126f)) scale = 0.f;
     const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
-    uint32_t code[8];
+    float f[8];
+    Unpack<IT, 8>::run(xw, f);
+    // rint by adding 2^23 (round to nearest, ties to even, like rint): the code is
+    // the sum's low bits.  (x - lo) * inv <= top (1 + 2^-22), so no code passes top.
+    uint32_t c[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int r = __float2int_rn(__fmul_rn(__fsub_rn(f[e], lo), inv));
-        code[e] = static_cast<uint32_t>(min(max(r, 0), static_cast<int>(top)));
-    }
+    for (int e = 0; e < 8; ++e)
+        c[e] = __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(f[e], lo), inv), 8388608.f));
     if constexpr (BITS == 8) {
-        w[0] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
-        w[1] = code[4] | code[5] << 8 | code[6] << 16 | code[7] << 24;
-    } else {
-        w[0] = 0u;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) w[0] |= code[e] << (4 * e);
+        for (int i = 0; i < 2; ++i)
+            w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040),
+                               0x5410);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = c[2 * i] + (c[2 * i + 1] << 4);  // low byte: both codes
+        w[0] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
     }
     return make_float2(scale, lo);
 }

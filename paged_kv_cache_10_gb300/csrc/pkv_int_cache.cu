@@ -14,45 +14,55 @@
 namespace pkv {
 namespace {
 
+// Quotient of a row number below 2^31 by the number of KV heads, as a product.
+struct RowDiv {
+    uint32_t mul, d;
+    int shift;
+};
+RowDiv row_div(int d) {
+    int s = 0;
+    while ((1ll << s) < d) ++s;
+    return {static_cast<uint32_t>((1ull << (31 + s)) / d + 1), static_cast<uint32_t>(d), 31 + s};
+}
+__device__ __forceinline__ uint32_t quotient(uint32_t n, RowDiv v) {
+    return static_cast<uint32_t>((static_cast<uint64_t>(n) * v.mul) >> v.shift);
+}
+
 // Append into an integer-coded pool: one group of D / 8 lanes per row (t, h),
 // blockIdx.y = 0 keys, 1 values.  Lanes of a warp whose row is padding or out
 // of range still take part in the group's shuffles.
 template <int D, int BITS, typename IT>
 __global__ void __launch_bounds__(256) append_int_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
                                                          const int64_t* __restrict__ slots, unsigned char* kc,
-                                                         unsigned char* vc, int64_t rows, int Hkv, int64_t num_slots,
-                                                         unsigned int* err) {
+                                                         unsigned char* vc, uint32_t rows, RowDiv heads,
+                                                         int64_t num_slots, unsigned int* err) {
     using L = IntTile<D, BITS>;
-    constexpr int LPR = D / 8;  // lanes of a row
+    constexpr int LPR = D / 8, RPC = 256 / LPR;  // lanes of a row, rows of a CTA
     const bool value = blockIdx.y != 0;
     const uint4* src = value ? v : k;
     unsigned char* pool = value ? vc : kc;
     const int c = threadIdx.x % LPR;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * (256 / LPR);
-    const int64_t first = blockIdx.x * static_cast<int64_t>(256 / LPR) + threadIdx.x / LPR;
-    // the loop's end is the same for a warp's lanes: shuffles need all of them
-    const int64_t warp_first = blockIdx.x * static_cast<int64_t>(256 / LPR) + (threadIdx.x & ~31) / LPR;
-    for (int64_t i = 0; warp_first + i * step < rows; ++i) {
-        const int64_t row = first + i * step;
+    // rows < 2^31 and gridDim.x * RPC < 2^20: no overflow.  The loop's end is the same
+    // for a CTA's lanes, since the shuffles need all of them.
+    for (uint32_t base = blockIdx.x * RPC; base < rows; base += gridDim.x * RPC) {
+        const uint32_t row = base + threadIdx.x / LPR;
         int64_t slot = -1;
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        int h = 0;
+        uint32_t h = 0;
         if (row < rows) {
-            const int64_t t = row / Hkv;
-            h = static_cast<int>(row - t * Hkv);
+            const uint32_t t = quotient(row, heads);
+            h = row - t * heads.d;
+            x = __ldg(src + static_cast<int64_t>(row) * LPR + c);
             slot = __ldg(slots + t);
             if (slot >= num_slots) {
                 if (h == 0 && c == 0 && !value) report(err, PKV_DEVERR_SLOT);
                 slot = -1;
             }
-            if (slot >= 0) x = __ldg(src + row * LPR + c);
         }
-        float f[8];
-        Unpack<IT, 8>::run(&x.x, f);
         uint32_t w[2];
-        const float2 sz = int_encode8<D, BITS>(f, w);
+        const float2 sz = int_encode8<D, BITS, IT>(x, w);
         if (slot >= 0) {
-            unsigned char* tile = pool + (slot / kBlockSize * Hkv + h) * L::kBytes;
+            unsigned char* tile = pool + (slot / kBlockSize * heads.d + h) * L::kBytes;
             int_store8<D, BITS>(tile, value, static_cast<int>(slot % kBlockSize), c, w, sz);
         }
     }
@@ -63,28 +73,26 @@ template <int D, int KV, typename OT>
 __global__ void __launch_bounds__(256) read_kernel(const unsigned char* __restrict__ kc,
                                                    const unsigned char* __restrict__ vc,
                                                    const int64_t* __restrict__ slots, uint4* k_out, uint4* v_out,
-                                                   int64_t rows, int Hkv, int64_t num_slots, float k_scale,
+                                                   uint32_t rows, RowDiv heads, int64_t num_slots, float k_scale,
                                                    float v_scale, unsigned int* err) {
-    constexpr int LPR = D / 8;
+    constexpr int LPR = D / 8, RPC = 256 / LPR;
     const bool value = blockIdx.y != 0;
     const unsigned char* pool = value ? vc : kc;
     uint4* out = value ? v_out : k_out;
     const float scale = value ? v_scale : k_scale;
-    const int64_t total = rows * LPR;
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const int c = static_cast<int>(i % LPR);
-        const int64_t row = i / LPR, t = row / Hkv;
-        const int h = static_cast<int>(row - t * Hkv);
+    const int c = threadIdx.x % LPR;
+    for (uint32_t row = blockIdx.x * RPC + threadIdx.x / LPR; row < rows; row += gridDim.x * RPC) {
+        const uint32_t t = quotient(row, heads), h = row - t * heads.d;
         const int64_t slot = __ldg(slots + t);
         if (slot < 0) continue;
         if (slot >= num_slots) {
             if (h == 0 && c == 0 && !value) report(err, PKV_DEVERR_SLOT);
             continue;
         }
-        const unsigned char* tile = pool + (slot / kBlockSize * Hkv + h) * PoolRow<D, KV>::kTile;
+        const unsigned char* tile = pool + (slot / kBlockSize * heads.d + h) * PoolRow<D, KV>::kTile;
         float f[8];
         PoolRow<D, KV>::load(tile, value, static_cast<int>(slot % kBlockSize), c, scale, f);
-        out[i] = pack8<OT>(f);
+        out[static_cast<int64_t>(row) * LPR + c] = pack8<OT>(f);
     }
 }
 
@@ -135,7 +143,7 @@ unsigned row_grid(int64_t rows, int rows_per_cta) {
 template <int D, typename OT>
 cudaError_t launch_read(int kv, const void* kc, const void* vc, const int64_t* slots, void* ko, void* vo, int64_t rows,
                         const pkv_cache_desc* d, unsigned int* err, cudaStream_t st) {
-    void (*kern)(const unsigned char*, const unsigned char*, const int64_t*, uint4*, uint4*, int64_t, int, int64_t,
+    void (*kern)(const unsigned char*, const unsigned char*, const int64_t*, uint4*, uint4*, uint32_t, RowDiv, int64_t,
                  float, float, unsigned int*) = nullptr;
     switch (kv) {
     case PKV_F16: kern = read_kernel<D, PKV_F16, F16>; break;
@@ -146,7 +154,7 @@ cudaError_t launch_read(int kv, const void* kc, const void* vc, const int64_t* s
     }
     kern<<<dim3(row_grid(rows, 256 * 8 / D), 2), 256, 0, st>>>(
         static_cast<const unsigned char*>(kc), static_cast<const unsigned char*>(vc), slots, static_cast<uint4*>(ko),
-        static_cast<uint4*>(vo), rows, d->num_kv_heads, static_cast<int64_t>(d->num_blocks) * kBlockSize, d->k_scale,
+        static_cast<uint4*>(vo), static_cast<uint32_t>(rows), row_div(d->num_kv_heads), static_cast<int64_t>(d->num_blocks) * kBlockSize, d->k_scale,
         d->v_scale, err);
     return cudaGetLastError();
 }
@@ -163,7 +171,7 @@ cudaError_t launch_append_int(const void* k, const void* v, int in_dtype, int64_
         auto kern = in_dtype == PKV_BF16 ? append_int_kernel<D, BITS, BF16> : append_int_kernel<D, BITS, F16>;
         kern<<<dim3(row_grid(rows, 256 * 8 / D), 2), 256, 0, st>>>(
             static_cast<const uint4*>(k), static_cast<const uint4*>(v), slots, static_cast<unsigned char*>(k_cache),
-            static_cast<unsigned char*>(v_cache), rows, d->num_kv_heads,
+            static_cast<unsigned char*>(v_cache), static_cast<uint32_t>(rows), row_div(d->num_kv_heads),
             static_cast<int64_t>(d->num_blocks) * kBlockSize, err);
         return cudaGetLastError();
     });
@@ -211,6 +219,7 @@ extern "C" pkv_status pkv_paged_kv_read(const int64_t* slot_mapping, int32_t num
     unsigned int* err = error_word();
     if (!err) return PKV_ERR_CUDA;
     const int64_t rows = static_cast<int64_t>(num_tokens) * d->num_kv_heads;
+    if (rows > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (d->head_size == 128)

@@ -15,6 +15,9 @@
 #include "pkv_decode_mma.cuh"
 #include "pkv_int.cuh"
 #include "pkv_pool_row.cuh"
+#ifndef PKV_TILES_CAP
+#define PKV_TILES_CAP 16
+#endif
 
 namespace pkv {
 namespace {
@@ -57,16 +60,16 @@ __global__ void __launch_bounds__(128) key_bounds_kernel(const unsigned char* __
             lo[e] = INFINITY;
             hi[e] = -INFINITY;
         }
+        // past the last token the last one again: the loads need no branch between
+        // them, and an extremum does not mind
 #pragma unroll
         for (int t = 0; t < kBlockSize; ++t) {
-            if (t < valid) {
-                float f[8];
-                PoolRow<D, KV>::load(tile, false, t, c, k_scale, f);
+            float f[8];
+            PoolRow<D, KV>::load(tile, false, min(t, valid - 1), c, k_scale, f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    lo[e] = fminf(lo[e], f[e]);
-                    hi[e] = fmaxf(hi[e], f[e]);
-                }
+            for (int e = 0; e < 8; ++e) {
+                lo[e] = fminf(lo[e], f[e]);
+                hi[e] = fmaxf(hi[e], f[e]);
             }
         }
         unsigned char* out = bounds + (at * 2 * D + 8 * c) * 2;
@@ -102,16 +105,35 @@ __device__ __forceinline__ int row_blocks(const SelectParams& p, int s, bool& ba
 // Largest |x| of packed 16-bit pairs: magnitudes order like their bits.
 __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t x) { return __vmaxu2(m, x & 0x7fff7fffu); }
 
-// One warp per (KV head, run of p.tiles 16-block tiles, sequence): the tile's
-// 16 rows of 2 D bound elements come straight from global memory as MMA
-// fragments.  Lane (g8, qd) reads 16-byte chunks qd, qd + 4, ... of rows g8 and
-// g8 + 8 (four lanes read 64 contiguous bytes of a row), which only permutes the
-// contraction axis; Q's fragments follow the same order.  All loads of a tile
-// are issued before its first product.
+// Shared memory of the score kernel: a ring of 16-block tiles per warp.  A
+// block's 2 D bound elements lie at a pitch of 64 bytes modulo 128, so that the
+// eight lanes of a 16-byte read phase (two rows, four chunks) hit all banks.
+template <int D>
+struct ScoreCfg {
+    static constexpr int kWarps = 4;
+    static constexpr int kStages = D == 128 ? 3 : 5;
+    static constexpr int kRow = 4 * D;  // bytes of a block's bounds for one KV head
+    static constexpr int kPitch = kRow + 64;
+    static constexpr int kStage = 16 * kPitch;
+    static constexpr int kBarOffset = kWarps * kStages * kStage;
+    static constexpr int kMaskOffset = kBarOffset + kWarps * kStages * 8;
+    static constexpr int kBytes = kMaskOffset + kWarps * kStages * 4 + 128;
+    static_assert(kPitch % 128 == 64 && 2 * (kBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+};
+
+// One warp per (KV head, run of p.tiles 16-block tiles, sequence).  A tile's 16
+// rows come by one bulk copy each, issued by 16 lanes, kStages tiles ahead, with
+// the ids of the next tiles already in registers.  Lane (g8, qd) reads
+// 16-byte chunks qd, qd + 4, ... of rows g8 and g8 + 8 as MMA fragments, which
+// only permutes the contraction axis; Q's fragments follow the same order.
 template <int D, typename T>
 __global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) {
+    using C = ScoreCfg<D>;
     constexpr bool kBF = std::is_same<T, BF16>::value;
     constexpr int CH = D / 16;  // 16-byte chunks of a row per lane
+    constexpr int NST = C::kStages;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char* smem = smem_raw + ((128 - (smem_addr(smem_raw) & 127)) & 127);
     allow_dependent_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, qd = lane & 3;
     const int64_t unit = blockIdx.x * 4ll + warp;
@@ -121,6 +143,55 @@ __global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) 
     const int nblk = row_blocks(p, s, bad);
     if (bad && unit == 0 && lane == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
     if (first * 16 >= nblk || nblk <= p.n) return;  // a row that keeps every block needs no scores
+    const int tiles = min(p.tiles, (nblk + 15) / 16 - first);
+
+    unsigned char* ring = smem + warp * NST * C::kStage;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset) + warp * NST;
+    volatile uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::kMaskOffset) + warp * NST;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < NST; ++i) mbar_init(&bars[i], 1);
+        mbar_init_fence();
+    }
+    __syncwarp();
+    const uint64_t pol = policy_evict_first();
+    const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.MB;
+    // Lane l of `ids` number k & 1 holds the id of block l of tile pair k (-1 for
+    // none); a pair is loaded two pairs ahead of its use.
+    const auto ids_of = [&](int k) {
+        const int j = (first + 2 * k) * 16 + lane;
+        return 2 * k + (lane >> 4) < tiles && j < nblk ? __ldg(table + j) : -1;
+    };
+    int ids[2] = {ids_of(0), ids_of(1)};
+    const auto issue = [&](int t, int stage) {  // warp-uniform; tiles in order
+        const int src = (lane & 15) + 16 * (t & 1);
+        const int id0 = __shfl_sync(kFull, ids[0], src), id1 = __shfl_sync(kFull, ids[1], src);
+        const int id = lane < 16 ? ((t >> 1) & 1 ? id1 : id0) : -1;
+        const bool in = id >= 0 && id < p.NB;
+        if (!in && lane < 16 && (first + t) * 16 + lane < nblk && h == 0) report(p.err, PKV_DEVERR_BLOCK_ID);
+        const uint32_t mask = __ballot_sync(kFull, in);
+        if (lane == 0) {
+            masks[stage] = mask;
+            mbar_arrive_expect_tx(&bars[stage], __popc(mask) * C::kRow);
+        }
+        __syncwarp();
+        if (in)
+            bulk_g2s(ring + stage * C::kStage + lane * C::kPitch,
+                     p.bounds + (id * static_cast<int64_t>(p.Hkv) + h) * C::kRow, C::kRow, &bars[stage], pol);
+        if (t & 1) {
+            if ((t >> 1) & 1)
+                ids[1] = ids_of((t >> 1) + 2);
+            else
+                ids[0] = ids_of((t >> 1) + 2);
+        }
+    };
+    int issued = 0;
+#pragma unroll
+    for (int i = 0; i < NST; ++i)
+        if (issued < tiles) {
+            issue(issued, i);
+            ++issued;
+        }
     // ---- Q's fragments: elements of [q-, q+] of head g8
     uint32_t qb[2 * CH][2];
     {
@@ -146,50 +217,66 @@ __global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) 
             qb[2 * j + 1][1] = y[3];
         }
     }
-    const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.MB;
-    const int64_t out = (static_cast<int64_t>(s) * p.Hkv + h) * p.cols;
-    for (int tile = first; tile < first + p.tiles && tile * 16 < nblk; ++tile) {
-        uint4 a[2][CH];
-        bool ok[2];
+    const int64_t out = (static_cast<int64_t>(s) * p.Hkv + h) * p.cols + static_cast<int64_t>(first) * 16;
+    bool aborted = false;
+    uint32_t phase = 0;
+    for (int t0 = 0; t0 < tiles && !aborted; t0 += NST) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const int j = tile * 16 + g8 + 8 * r;
-            const int id = j < nblk ? __ldg(table + j) : -1;
-            ok[r] = id >= 0 && id < p.NB;
-            if (j < nblk && !ok[r] && qd == 0 && h == 0) report(p.err, PKV_DEVERR_BLOCK_ID);
-            const uint4* src = reinterpret_cast<const uint4*>(p.bounds + ((ok[r] ? id : 0) * static_cast<int64_t>(p.Hkv) + h) * (4 * D)) + qd;
+        for (int st = 0; st < NST; ++st) {
+            const int t = t0 + st;
+            if (t >= tiles) break;
+            if (!mbar_wait(&bars[st], phase)) {
+                if (lane == 0) report(p.err, PKV_DEVERR_TIMEOUT);
+                aborted = true;
+                break;
+            }
+            const uint32_t mask = masks[st];
+            const uint32_t base = smem_addr(ring + st * C::kStage) + g8 * C::kPitch + qd * 16;
+            float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+            uint32_t big0 = 0u, big1 = 0u;
 #pragma unroll
-            for (int j4 = 0; j4 < CH; ++j4) a[r][j4] = ok[r] ? __ldg(src + 4 * j4) : make_uint4(0u, 0u, 0u, 0u);
+            for (int j = 0; j < CH; ++j) {
+                const uint4 a = lds128(base + 64 * j), b = lds128(base + 8 * C::kPitch + 64 * j);
+                mma16816a<kBF>(sa[0], a.x, b.x, a.y, b.y, qb[2 * j][0], qb[2 * j][1]);
+                mma16816a<kBF>(sa[1], a.z, b.z, a.w, b.w, qb[2 * j + 1][0], qb[2 * j + 1][1]);
+                big0 = abs_max2(abs_max2(abs_max2(abs_max2(big0, a.x), a.y), a.z), a.w);
+                big1 = abs_max2(abs_max2(abs_max2(abs_max2(big1, b.x), b.y), b.z), b.w);
+            }
+            const bool ok[2] = {(mask >> g8 & 1u) != 0u, (mask >> (g8 + 8) & 1u) != 0u};
+            const uint32_t big = abs_max2(ok[0] ? big0 : 0u, ok[1] ? big1 : 0u);
+            float v[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float x = sa[0][2 * r] + sa[1][2 * r], y = sa[0][2 * r + 1] + sa[1][2 * r + 1];
+                float m = -INFINITY;  // NaN scores are dropped: such a block ranks last
+                if (2 * qd < p.G) m = fmaxf(m, x);
+                if (2 * qd + 1 < p.G) m = fmaxf(m, y);
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
+                v[r] = ok[r] ? m : -INFINITY;  // a row without a block holds stale bytes
+            }
+            if (qd == 0) {
+                p.score[out + t * 16 + g8] = v[0];
+                p.score[out + t * 16 + g8 + 8] = v[1];
+            }
+            const uint32_t top = __reduce_max_sync(kFull, max(big >> 16, big & 0xffffu));
+            if (lane == 0) {
+                const uint16_t b = static_cast<uint16_t>(top);
+                p.top[out / 16 + t] = to_float(*reinterpret_cast<const typename T::storage*>(&b));
+            }
+            __syncwarp();
+            if (issued < tiles) {
+                issue(issued, st);
+                ++issued;
+            }
         }
-        float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        uint32_t big = 0u;
-#pragma unroll
-        for (int j = 0; j < CH; ++j) {
-            mma16816a<kBF>(sa[0], a[0][j].x, a[1][j].x, a[0][j].y, a[1][j].y, qb[2 * j][0], qb[2 * j][1]);
-            mma16816a<kBF>(sa[1], a[0][j].z, a[1][j].z, a[0][j].w, a[1][j].w, qb[2 * j + 1][0], qb[2 * j + 1][1]);
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-                big = abs_max2(abs_max2(abs_max2(abs_max2(big, a[r][j].x), a[r][j].y), a[r][j].z), a[r][j].w);
-        }
-        float v[2];
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const float x = sa[0][2 * r] + sa[1][2 * r], y = sa[0][2 * r + 1] + sa[1][2 * r + 1];
-            float m = -INFINITY;  // NaN scores are dropped: such a block ranks last
-            if (2 * qd < p.G) m = fmaxf(m, x);
-            if (2 * qd + 1 < p.G) m = fmaxf(m, y);
-            m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-            v[r] = ok[r] ? m : -INFINITY;
-        }
-        if (qd == 0) {
-            p.score[out + tile * 16 + g8] = v[0];
-            p.score[out + tile * 16 + g8 + 8] = v[1];
-        }
-        big = __reduce_max_sync(kFull, max(big >> 16, big & 0xffffu));
-        if (lane == 0) {
-            const uint16_t b = static_cast<uint16_t>(big);
-            p.top[out / 16 + tile] = to_float(*reinterpret_cast<const typename T::storage*>(&b));
+        phase ^= 1u;
+    }
+    if (aborted) {  // no copy may outlive the CTA
+        for (int k = 0; k < NST; ++k) {
+            const int t = issued - 1 - k;
+            if (t < 0) break;
+            (void)mbar_wait(&bars[t % NST], (t / NST) & 1);
         }
     }
 }
@@ -238,28 +325,35 @@ __device__ __forceinline__ uint64_t order64(double x) {
     return static_cast<uint64_t>(b) ^ (b < 0 ? ~0ull : 1ull << 63);
 }
 
-// The score of block j in 64 bits, by one warp: products of 16-bit values are
-// exact, and so, but for extreme ranges, are their sums.
-template <int D, typename T>
-__device__ __forceinline__ double exact_score(const SelectParams& p, int s, int h, int j) {
+// The score of block j by one warp, in binary32 (A = float) or 64 bits.  Products
+// of 16-bit values are exact in both; in 64 bits so are, but for extreme
+// ranges, their sums; in binary32 an element's sum takes at most D / 32 - 1 + 5
+// = 8 additions, each within 2^-24 of the sum of magnitudes.
+template <int D, typename T, typename A>
+__device__ __forceinline__ A warp_score(const SelectParams& p, int s, int h, int j) {
     const int lane = threadIdx.x & 31;
     const int id = __ldg(p.block_tables + static_cast<int64_t>(s) * p.MB + j);
-    if (id < 0 || id >= p.NB) return -HUGE_VAL;
+    if (id < 0 || id >= p.NB) return static_cast<A>(-INFINITY);
     using E = typename T::storage;
-    const E* lo = reinterpret_cast<const E*>(p.bounds) + (static_cast<int64_t>(id) * p.Hkv + h) * 2 * D;
-    double best = -HUGE_VAL;
+    const E* b = reinterpret_cast<const E*>(p.bounds) + (static_cast<int64_t>(id) * p.Hkv + h) * 2 * D;
+    float lo[D / 32], hi[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+        lo[i] = to_float(b[lane + 32 * i]);
+        hi[i] = to_float(b[D + lane + 32 * i]);
+    }
+    A best = static_cast<A>(-INFINITY);
     for (int g = 0; g < p.G; ++g) {
         const E* q = reinterpret_cast<const E*>(p.q) + (static_cast<int64_t>(s) * p.Hq + h * p.G + g) * D;
-        double sum = 0.0;
+        A sum = 0;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {
-            const int d = lane + 32 * i;
-            const float x = to_float(q[d]);
-            sum += static_cast<double>(x) * static_cast<double>(to_float(x < 0.f ? lo[d] : lo[D + d]));
+            const float x = to_float(q[lane + 32 * i]);
+            sum += static_cast<A>(x) * static_cast<A>(x < 0.f ? lo[i] : hi[i]);
         }
 #pragma unroll
         for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(kFull, sum, m);
-        best = fmax(best, sum);
+        best = best > sum ? best : (sum == sum ? sum : best);  // NaN is dropped
     }
     return best;
 }
@@ -275,7 +369,8 @@ __device__ __forceinline__ double exact_score(const SelectParams& p, int s, int 
 // twice.  A histogram over the scores' range finds the bin that holds the k-th
 // highest, zooming in while the bin is wide and full; with [tl, th] the scores
 // in it, a block above th + 2 eps is in and one below tl - 2 eps is out, and
-// the few between them are scored again in 64 bits and ranked by (score,
+// the few between them are scored again, in binary32 with a far smaller bound
+// and, where that leaves an order open, in 64 bits, and ranked by (score,
 // number).  So the answer is that of exact arithmetic whatever the order of the
 // binary32 sums.
 template <int D, typename T>
@@ -285,6 +380,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     __shared__ __align__(8) unsigned char red_bytes[(kSelThreads / 32) * 8];
     __shared__ int near_id[kSelNear];
     __shared__ double near_y[kSelNear];
+    __shared__ float near_f[kSelNear];
+    __shared__ short tie[kSelNear];
     __shared__ int sh[4];
     int* redi = reinterpret_cast<int*>(red_bytes);
     float* redf = reinterpret_cast<float*>(red_bytes);
@@ -419,17 +516,42 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 for (int i = f0 + tid; i < f1; i += kSelThreads)
                     if (sc[i] <= thr && sc[i] >= low) near_id[atomicAdd(&sh[3], 1)] = i;
                 __syncthreads();
+                // binary32 first, each within 8 * 2^-24 A: twice that and its double is eps2 / 64
                 for (int i = warp; i < band; i += kSelThreads / 32) {
-                    const double y = exact_score<D, T>(p, s, h, near_id[i]);
+                    const float y = warp_score<D, T, float>(p, s, h, near_id[i]);
+                    if (lane == 0) near_f[i] = y;
+                }
+                if (tid == 0) sh[3] = sh[2] = 0;
+                __syncthreads();
+                const float e2 = eps2 * 0x1p-6f;
+                for (int i = tid; i < band; i += kSelThreads) {
+                    const float y = near_f[i];
+                    int over = 0, near_or_over = 0;
+                    for (int j = 0; j < band; ++j) {
+                        over += near_f[j] > y + e2;
+                        near_or_over += !(near_f[j] < y - e2);
+                    }
+                    const bool in = near_or_over <= want && e2 < INFINITY, off = over >= want && e2 < INFINITY;
+                    if (in) atomicAdd(&sh[2], 1);
+                    if (in || off)
+                        sc[near_id[i]] = in ? INFINITY : -INFINITY;
+                    else
+                        tie[atomicAdd(&sh[3], 1)] = i;
+                }
+                __syncthreads();
+                const int ties = sh[3], left = want - sh[2];
+                // the few that binary32 cannot order: 64 bits
+                for (int i = warp; i < ties; i += kSelThreads / 32) {
+                    const double y = warp_score<D, T, double>(p, s, h, near_id[tie[i]]);
                     if (lane == 0) near_y[i] = y;
                 }
                 __syncthreads();
-                for (int i = tid; i < band; i += kSelThreads) {
+                for (int i = tid; i < ties; i += kSelThreads) {
                     const double y = near_y[i];
-                    const int id = near_id[i];
+                    const int at = near_id[tie[i]];
                     int rank = 0;
-                    for (int j = 0; j < band; ++j) rank += near_y[j] > y || (near_y[j] == y && near_id[j] < id);
-                    sc[id] = rank < want ? INFINITY : -INFINITY;
+                    for (int j = 0; j < ties; ++j) rank += near_y[j] > y || (near_y[j] == y && near_id[tie[j]] < at);
+                    sc[at] = rank < left ? INFINITY : -INFINITY;
                 }
             } else {
                 // many near the border (equal scores): radix selection of the want-th
@@ -438,7 +560,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 for (int i = f0 + warp; i < f1; i += kSelThreads / 32) {
                     const float x = sc[i];
                     if (!(x <= thr && x >= low)) continue;
-                    const double y = exact_score<D, T>(p, s, h, i);
+                    const double y = warp_score<D, T, double>(p, s, h, i);
                     if (lane == 0) ex[i] = y;
                 }
                 __syncthreads();
@@ -497,8 +619,11 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 template <int D, typename T>
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
     const int64_t units = static_cast<int64_t>((p.cols / 16 + p.tiles - 1) / p.tiles) * p.Hkv;
-    block_score_kernel<D, T><<<dim3(static_cast<unsigned>((units + 3) / 4), p.S), 128, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
+    constexpr int kScoreSmem = ScoreCfg<D>::kBytes;
+    cudaError_t e = cudaFuncSetAttribute(block_score_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+    if (e != cudaSuccess) return e;
+    block_score_kernel<D, T><<<dim3(static_cast<unsigned>((units + 3) / 4), p.S), 128, kScoreSmem, st>>>(p);
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const size_t smem = static_cast<size_t>(p.smem_cols) * 4;
     if (smem > 32 * 1024) {  // with the static arrays, more than a launch gets unasked
@@ -656,10 +781,10 @@ extern "C" pkv_status pkv_select_blocks(const void* q, int32_t q_dtype, int32_t 
     p.n = num_selected;
     p.sink = sink_blocks;
     p.recent = recent_blocks;
-    // enough warps to fill the SMs a few times; beyond that a warp takes several
-    // tiles and builds Q's fragments once
-    const int64_t warps = static_cast<int64_t>(l.cols / 16) * p.Hkv * p.S;
-    p.tiles = static_cast<int>(std::min<int64_t>(8, std::max<int64_t>(1, warps / (num_sms() * 32))));
+    // eight warps fit an SM: enough units for about two rounds of them, beyond that
+    // a warp takes a run of tiles, which its ring streams
+    const int64_t tiles = static_cast<int64_t>(l.cols / 16) * p.Hkv * p.S;
+    p.tiles = static_cast<int>(std::min<int64_t>(PKV_TILES_CAP, std::max<int64_t>(1, tiles / (num_sms() * 16))));
     constexpr int kSmemCols = 16384;  // 64 KiB; longer rows stay in the workspace
     p.smem_cols = static_cast<int>(std::min<int64_t>(l.cols, kSmemCols));
     cudaStream_t st = static_cast<cudaStream_t>(stream);

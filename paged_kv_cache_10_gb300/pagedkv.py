@@ -183,7 +183,8 @@ def _dev_ptr(t: torch.Tensor, name: str) -> int:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -200,24 +201,37 @@ def _dtype_code(t: torch.Tensor, declared: str | None) -> int:
     return _TORCH_CODE[t.dtype]
 
 
+_descs: dict = {}
+
+
+def _desc(d: CacheDesc):
+    """(reference to the C description, bytes of a pool) of a description's present values, made once."""
+    key = (d.num_blocks, d.num_kv_heads, d.head_size, d.kv_dtype, d.k_scale, d.v_scale, d.block_size)
+    r = _descs.get(key)
+    if r is None:
+        if len(_descs) >= 256:
+            _descs.clear()
+        r = _descs[key] = (ctypes.byref(d.c()), d.num_blocks * block_bytes(d))
+    return r
+
+
 def _on_current_device(*tensors) -> None:
     """The launch goes to the current device: a tensor of another one is refused."""
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.is_cuda and t.device.index != cur:
+        if t is not None and t.get_device() != cur and t.is_cuda:
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
 
 
 def _shape(t: torch.Tensor, want: tuple, name: str) -> None:
-    if tuple(t.shape) != want:
+    if t.shape != want:
         raise ValueError(f"{name} must have shape {list(want)}, not {list(t.shape)}")
 
 
 def _pool_ptr(t: torch.Tensor, desc: CacheDesc, name: str) -> int:
-    p = _dev_ptr(t, name)
-    if t.numel() * t.element_size() != desc.num_blocks * block_bytes(desc):
+    if t.numel() * t.element_size() != _desc(desc)[1]:
         raise ValueError(f"{name} must hold {desc.num_blocks} blocks of {block_bytes(desc)} bytes")
-    return p
+    return _dev_ptr(t, name)
 
 
 def block_bytes(desc: CacheDesc) -> int:
@@ -235,7 +249,7 @@ def paged_kv_append(k, v, slot_mapping, k_cache, v_cache, desc: CacheDesc, in_dt
         raise TypeError("slot_mapping must be int64")
     st = lib().pkv_paged_kv_append(_dev_ptr(k, "k"), _dev_ptr(v, "v"), _dtype_code(k, in_dtype), T,
                                    _dev_ptr(slot_mapping, "slot_mapping"), _dev_ptr(k_cache, "k_cache"),
-                                   _dev_ptr(v_cache, "v_cache"), ctypes.byref(desc.c()), _stream(stream))
+                                   _dev_ptr(v_cache, "v_cache"), _desc(desc)[0], _stream(stream))
     _check(st, "paged_kv_append")
 
 
@@ -252,7 +266,7 @@ def paged_kv_read(slot_mapping, k_cache, v_cache, desc: CacheDesc, k_out, v_out,
         raise TypeError("k_out and v_out must be of one 16-bit type")
     _on_current_device(slot_mapping, k_cache, v_cache, k_out, v_out)
     st = lib().pkv_paged_kv_read(_dev_ptr(slot_mapping, "slot_mapping"), T, _pool_ptr(k_cache, desc, "k_cache"),
-                                 _pool_ptr(v_cache, desc, "v_cache"), ctypes.byref(desc.c()),
+                                 _pool_ptr(v_cache, desc, "v_cache"), _desc(desc)[0],
                                  _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"), _dtype_code(k_out, out_dtype),
                                  _stream(stream))
     _check(st, "paged_kv_read")
@@ -263,7 +277,7 @@ def copy_blocks(k_cache, v_cache, desc: CacheDesc, pairs, num_pairs: int | None 
     n = int(pairs.shape[0]) if num_pairs is None else int(num_pairs)
     if pairs.dtype != torch.int32:
         raise TypeError("pairs must be int32")
-    st = lib().pkv_copy_blocks(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), ctypes.byref(desc.c()),
+    st = lib().pkv_copy_blocks(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _desc(desc)[0],
                                _dev_ptr(pairs, "pairs") if n > 0 else None, n, _stream(stream))
     _check(st, "copy_blocks")
 
@@ -293,7 +307,7 @@ def paged_attention_decode(q, k_cache, v_cache, desc: CacheDesc, block_tables, s
         ws_ptr, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
     st = lib().pkv_paged_attention_decode(_dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq,
                                           _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-                                          ctypes.byref(desc.c()), _dev_ptr(block_tables, "block_tables"),
+                                          _desc(desc)[0], _dev_ptr(block_tables, "block_tables"),
                                           int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"),
                                           int(max_seq_len), float(scale), _dev_ptr(out, "out"), ws_ptr, ws_bytes,
                                           int(partition_tokens), _stream(stream))
@@ -338,7 +352,7 @@ def paged_attention_decode_noalloc(q, k_cache, v_cache, desc: CacheDesc, block_t
         raise TypeError("block_tables and seq_lens must be int32")
     st = lib().pkv_paged_attention_decode_noalloc(_dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq,
                                                   _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-                                                  ctypes.byref(desc.c()), _dev_ptr(block_tables, "block_tables"),
+                                                  _desc(desc)[0], _dev_ptr(block_tables, "block_tables"),
                                                   int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"),
                                                   int(max_seq_len), float(scale), _dev_ptr(out, "out"),
                                                   int(partition_tokens), _stream(stream))
@@ -402,7 +416,7 @@ def paged_attention_decode_append(k_new, v_new, slot_mapping, q, k_cache, v_cach
         _dev_ptr(k_new, "k_new"), _dev_ptr(v_new, "v_new"), _dtype_code(k_new, in_dtype),
         _dev_ptr(slot_mapping, "slot_mapping"), _dev_ptr(cow_src, "cow_src") if cow_src is not None else None,
         _dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq,
-        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), ctypes.byref(desc.c()),
+        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _desc(desc)[0],
         _dev_ptr(block_tables, "block_tables"), int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"),
         int(max_seq_len), float(scale), _dev_ptr(out, "out"), ws_ptr, ws_bytes, int(partition_tokens),
         _dev_ptr(work_units, "work_units") if work_units is not None and work_units.numel() else None,
@@ -425,7 +439,7 @@ def paged_key_bounds(k_cache, desc: CacheDesc, block_tables, seq_lens, new_lens,
     if bounds.element_size() != 2:
         raise TypeError("bounds must be of a 16-bit type")
     _on_current_device(k_cache, block_tables, seq_lens, new_lens, bounds)
-    st = lib().pkv_paged_key_bounds(_pool_ptr(k_cache, desc, "k_cache"), ctypes.byref(desc.c()),
+    st = lib().pkv_paged_key_bounds(_pool_ptr(k_cache, desc, "k_cache"), _desc(desc)[0],
                                     _dev_ptr(block_tables, "block_tables"), int(block_tables.shape[1]),
                                     _dev_ptr(seq_lens, "seq_lens"),
                                     _dev_ptr(new_lens, "new_lens") if new_lens is not None else None,
@@ -455,7 +469,7 @@ def select_blocks(q, bounds, desc: CacheDesc, block_tables, seq_lens, max_seq_le
         raise ValueError("block_tables and seq_lens must have one row per sequence")
     _on_current_device(q, bounds, block_tables, seq_lens, selected, workspace)
     st = lib().pkv_select_blocks(_dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq, _dev_ptr(bounds, "bounds"),
-                                 ctypes.byref(desc.c()), _dev_ptr(block_tables, "block_tables"),
+                                 _desc(desc)[0], _dev_ptr(block_tables, "block_tables"),
                                  int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"), int(max_seq_len),
                                  int(selected.shape[2]), int(sink_blocks), int(recent_blocks),
                                  _dev_ptr(selected, "selected"), _dev_ptr(workspace, "workspace"),
@@ -491,7 +505,7 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, desc: CacheDesc, block_ta
         ws_ptr, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
     st = lib().pkv_paged_attention_decode_sparse(
         _dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq, _pool_ptr(k_cache, desc, "k_cache"),
-        _pool_ptr(v_cache, desc, "v_cache"), ctypes.byref(desc.c()), _dev_ptr(block_tables, "block_tables"),
+        _pool_ptr(v_cache, desc, "v_cache"), _desc(desc)[0], _dev_ptr(block_tables, "block_tables"),
         int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(selected, "selected"),
         int(selected.shape[2]), float(scale), _dev_ptr(out, "out"), ws_ptr, ws_bytes, int(partition_blocks),
         _stream(stream))
@@ -525,7 +539,7 @@ def paged_attention_decode_cascade(q, k_cache, v_cache, desc: CacheDesc, block_t
     ptr = lambda t, n: _dev_ptr(t, n) if t.numel() > 0 else None
     st = lib().pkv_paged_attention_decode_cascade(
         _dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq, _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-        ctypes.byref(desc.c()), _dev_ptr(block_tables, "block_tables"), int(block_tables.shape[1]),
+        _desc(desc)[0], _dev_ptr(block_tables, "block_tables"), int(block_tables.shape[1]),
         _dev_ptr(seq_lens, "seq_lens"), int(max_seq_len), _dev_ptr(seq_group, "seq_group"),
         ptr(group_blocks, "group_blocks"), ptr(group_offsets, "group_offsets"), ptr(group_members, "group_members"),
         ng, int(max_group_members), int(max_group_blocks), float(scale), _dev_ptr(out, "out"),
@@ -552,7 +566,7 @@ def paged_attention_prefill(q, k_cache, v_cache, desc: CacheDesc, query_start, m
         ws_ptr, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
     st = lib().pkv_paged_attention_prefill(
         _dev_ptr(q, "q"), _dtype_code(q, q_dtype), T, Hq, S, _dev_ptr(query_start, "query_start"), int(max_query_len),
-        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), ctypes.byref(desc.c()),
+        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _desc(desc)[0],
         _dev_ptr(block_tables, "block_tables"), int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"),
         wp, nw, float(scale), _dev_ptr(out, "out"), ws_ptr, ws_bytes, _stream(stream))
     _check(st, "paged_attention_prefill")
@@ -616,7 +630,7 @@ def swap_blocks(k_cache, v_cache, desc: CacheDesc, k_host, v_host, pairs, direct
         if t.is_cuda or not t.is_pinned() or not t.is_contiguous():
             raise ValueError(f"{n} must be a contiguous pinned CPU tensor")
     n = int(pairs.shape[0])
-    st = lib().pkv_swap_blocks(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), ctypes.byref(desc.c()),
+    st = lib().pkv_swap_blocks(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _desc(desc)[0],
                                k_host.data_ptr(), v_host.data_ptr(), int(k_host.shape[0]),
                                _dev_ptr(pairs, "pairs") if n else None, n, int(direction), _stream(stream))
     _check(st, "swap_blocks")
