@@ -37,7 +37,8 @@
 
 namespace pkv {
 
-template <int D, int BITS>
+// FOLD: groups of at most four heads, whose columns 4 .. 7 carry the tails.
+template <int D, int BITS, bool FOLD>
 struct IntCfg {
     using L = IntTile<D, BITS>;
     static constexpr int kWarps = 4;
@@ -48,7 +49,8 @@ struct IntCfg {
     static constexpr int kBarOffset = kRing;
     static constexpr int kInfoOffset = kBarOffset + kWarps * kStages * 8;  // valid tokens of a stage's two blocks
     static constexpr int kMergeOffset = kInfoOffset + kWarps * kStages * 8;
-    static constexpr int kBytes = kMergeOffset + (kWarps * 8 + 16) * 4 + 128;  // + alignment slack
+    static constexpr int kQOffset = (kMergeOffset + (kWarps * 16 + 16) * 4 + 15) / 16 * 16;  // Q^T fragments, 8 bytes a lane and k-step
+    static constexpr int kBytes = kQOffset + (D / 16) * 32 * 8 + 128;  // + alignment slack
     static constexpr int kState = (24 + 4 * (D / 16) * 33) * 4;  // a warp's state for the cross-warp merge
     static_assert(kState <= kStages * kStage, "the merge state reuses the warp's ring");
     static_assert(kCtasPerSm * (kBytes + 1024) <= 228 * 1024 || BITS == 8, "residency");
@@ -88,15 +90,16 @@ __device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
     return BITS == 8 ? __byte_perm(w, 0u, 0x4341) : w & 0x00f000f0u;
 }
 
-template <int D, int BITS, bool SPARSE>
-__global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
+template <int D, int BITS, bool FOLD, bool SPARSE>
+__global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, BITS, FOLD>::kCtasPerSm)
     decode_int_kernel(const DecodeParams p, const int G, const int q_bf16) {
-    using C = IntCfg<D, BITS>;
+    using C = IntCfg<D, BITS, FOLD>;
     using L = IntTile<D, BITS>;
     constexpr int NW = C::kWarps, NST = C::kStages, TB = L::kBytes, STAGE = C::kStage;
     constexpr int KS = D / 16;             // k-steps of S = K Q^T and m-tiles of O^T = V^T P^T
     constexpr int WORDS = L::RB / 16;      // code words a lane reads of a row (keys) or half a pair
     constexpr int PER = KS / WORDS;        // MMAs a word feeds: 1 (8 bits) or 2 (4 bits)
+    constexpr int kGroup = 2;
     static_assert(WORDS * PER == KS && (PER == 1 || PER == 2), "fragment split");
 
     extern __shared__ unsigned char smem_raw[];
@@ -106,15 +109,23 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
     allow_dependent_launch();
     const int part = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
 
+    // the first window's table (or list) entries, loaded beside the length
+    const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.MB;
+    const int j0 = part * (p.P / kBlockSize);  // first block (or list entry) of this partition
+    const int32_t* list = SPARSE ? p.selected + (static_cast<int64_t>(s) * p.Hkv + h) * p.nsel + j0 : table + j0;
+    const int list_len = (SPARSE ? p.nsel : p.MB) - j0;
+    const auto entry = [&](int k) {  // lane 2i + u: block u of this warp's step k + i
+        const int j = 2 * (warp + (k + (lane >> 1)) * NW) + (lane & 1);
+        return j < list_len ? __ldg(list + j) : -1;
+    };
+    int next = entry(0);
     int len = __ldg(p.seq_lens + s);
     const int cap = p.MB * kBlockSize;
     bool bad = len < 0 || len > cap;
     len = len < 0 ? 0 : (len > cap ? cap : len);
-    int nblk, j0;  // blocks (or list entries) of this partition, its first
+    int nblk;  // blocks (or list entries) of this partition
     if constexpr (SPARSE) {
-        const int per = p.P / kBlockSize;
-        j0 = part * per;
-        nblk = min(per, p.nsel - j0);
+        nblk = min(p.P / kBlockSize, list_len);
         if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
     } else {
         if (len > p.NP * p.P) {
@@ -124,7 +135,6 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
         if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
         const int nparts = len > 0 ? (len + p.P - 1) / p.P : 1;
         if (part >= nparts) return;
-        j0 = part * (p.P / kBlockSize);
         nblk = (min(len, (part + 1) * p.P) + kBlockSize - 1) / kBlockSize - j0;
     }
     // a step is two blocks; warp w takes steps w, w + NW, ...
@@ -134,8 +144,6 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
     unsigned char* ring = smem + warp * NST * STAGE;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset) + warp * NST;
     volatile int* info = reinterpret_cast<int*>(smem + C::kInfoOffset) + warp * NST * 2;
-    const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.MB;
-    const int32_t* list = SPARSE ? p.selected + (static_cast<int64_t>(s) * p.Hkv + h) * p.nsel + j0 : nullptr;
     const unsigned char* kpool = static_cast<const unsigned char*>(p.k_cache);
     const unsigned char* vpool = static_cast<const unsigned char*>(p.v_cache);
     const uint64_t pol = policy_evict_first();
@@ -153,13 +161,14 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
         if ((k_issue & 15) == 0) {
             const int k = k_issue + (lane >> 1);
             const int j = 2 * (warp + k * NW) + (lane & 1);
+            const int e = next;
             tbl = -1;
             val = 0;
             if (k < ns_w && j < nblk) {
                 if constexpr (SPARSE) {
-                    tbl = sparse_block(p, s, __ldg(list + j), len, val);
+                    tbl = sparse_block(p, s, e, len, val);
                 } else {
-                    tbl = __ldg(table + j0 + j);
+                    tbl = e;
                     val = min(kBlockSize, len - (j0 + j) * kBlockSize);
                 }
                 if (val > 0 && (tbl < 0 || tbl >= p.NB)) {
@@ -167,24 +176,20 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
                     val = 0;
                 }
             }
+            next = entry(k_issue + 16);  // a window ahead
         }
-        const int at = 2 * (k_issue & 15);
-        const int b0 = __shfl_sync(kFull, tbl, at), b1 = __shfl_sync(kFull, tbl, at + 1);
-        const int n0 = __shfl_sync(kFull, val, at), n1 = __shfl_sync(kFull, val, at + 1);
-        if (lane == 0) {
-            info[2 * stage] = n0;
-            info[2 * stage + 1] = n1;
-            unsigned char* dst = ring + stage * STAGE;
-            mbar_arrive_expect_tx(&bars[stage], (n0 > 0 ? 2 * TB : 0) + (n1 > 0 ? 2 * TB : 0));
-            if (n0 > 0) {
-                const int64_t off = (static_cast<int64_t>(b0) * p.Hkv + h) * TB;
+        // the two lanes that hold the step's blocks issue their copies
+        const uint32_t both = __ballot_sync(kFull, val > 0) >> (2 * (k_issue & 15)) & 3u;
+        const int u = lane - 2 * (k_issue & 15);
+        if (u == 0) mbar_arrive_expect_tx(&bars[stage], __popc(both) * 2 * TB);
+        __syncwarp();
+        if (u == 0 || u == 1) {
+            info[2 * stage + u] = val;
+            if (val > 0) {
+                unsigned char* dst = ring + stage * STAGE + u * 2 * TB;
+                const int64_t off = (static_cast<int64_t>(tbl) * p.Hkv + h) * TB;
                 bulk_g2s(dst, kpool + off, TB, &bars[stage], pol);
                 bulk_g2s(dst + TB, vpool + off, TB, &bars[stage], pol);
-            }
-            if (n1 > 0) {
-                const int64_t off = (static_cast<int64_t>(b1) * p.Hkv + h) * TB;
-                bulk_g2s(dst + 2 * TB, kpool + off, TB, &bars[stage], pol);
-                bulk_g2s(dst + 3 * TB, vpool + off, TB, &bars[stage], pol);
             }
         }
         ++k_issue;
@@ -193,65 +198,73 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
     for (int i = 0; i < NST; ++i)
         if (k_issue < ns_w) issue_next(i);
 
-    // ---- B fragments of Q^T (column n = head g8), per-head scale and sum
-    uint32_t qb[KS][2];
+    // ---- B fragments of Q^T (column n = head g8), per-head scale and sum: the
+    // warps share the words, each head's extrema and sums meet in shared memory
+    uint2* qsm = reinterpret_cast<uint2*>(smem + C::kQOffset);
+    float* msc = reinterpret_cast<float*>(smem + C::kMergeOffset);
     float sfA, sfB, qsA, qsB;  // heads 2 qd (A) and 2 qd + 1 (B)
     {
-        float f[KS][4];  // the lane's elements in MMA order: b0 = (0, 1), b1 = (2, 3)
-        const bool live = g8 < G;
+        constexpr int EPW = 32 / BITS;                // elements of a word
+        constexpr int MINE = (WORDS + NW - 1) / NW;   // words a warp takes
+        const int head = FOLD ? g8 & 3 : g8;  // FOLD: columns 4 .. 7 repeat the heads
+        const bool live = head < G;
         const unsigned char* row =
-            static_cast<const unsigned char*>(p.q) + (static_cast<int64_t>(s) * p.Hq + h * G + (live ? g8 : 0)) * D * 2;
+            static_cast<const unsigned char*>(p.q) + (static_cast<int64_t>(s) * p.Hq + h * G + (live ? head : 0)) * D * 2;
+        float e[MINE][EPW];
         float amax = 0.f, sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < WORDS; ++w) {
-            // the 32 / BITS elements of the lane's word w start at d0
+        for (int m = 0; m < MINE; ++m) {
+            const int w = warp + m * NW;
             const int d0 = BITS == 8 ? 64 * (w >> 2) + 16 * qd + 4 * (w & 3) : (D / 4) * qd + 8 * w;
-            float e[32 / BITS];
+            uint32_t x[EPW / 2];
 #pragma unroll
-            for (int i = 0; i < 16 / BITS; ++i) {  // 32-bit words of q
-                const uint32_t x = live ? __ldg(reinterpret_cast<const uint32_t*>(row + d0 * 2) + i) : 0u;
-                if (q_bf16)
-                    Unpack<BF16, 2>::run(&x, e + 2 * i);
-                else
-                    Unpack<F16, 2>::run(&x, e + 2 * i);
-            }
+            for (int i = 0; i < EPW / 2; ++i) x[i] = 0u;
+            if (live && w < WORDS) load_words<EPW * 2>(row + d0 * 2, x);
+            if (q_bf16)
+                Unpack<BF16, EPW>::run(x, e[m]);
+            else
+                Unpack<F16, EPW>::run(x, e[m]);
 #pragma unroll
-            for (int i = 0; i < 32 / BITS; ++i) {
-                amax = fmaxf(amax, fabsf(e[i]));
-                sum += e[i];
-            }
-            if constexpr (BITS == 8) {
-                f[w][0] = e[0]; f[w][1] = e[2]; f[w][2] = e[1]; f[w][3] = e[3];
-            } else {
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    f[2 * w + j][0] = e[2 * j];
-                    f[2 * w + j][1] = e[2 * j + 4];
-                    f[2 * w + j][2] = e[2 * j + 1];
-                    f[2 * w + j][3] = e[2 * j + 5];
-                }
+            for (int i = 0; i < EPW; ++i) {
+                amax = fmaxf(amax, fabsf(e[m][i]));
+                sum += e[m][i];
             }
         }
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, 2));
         sum += __shfl_xor_sync(kFull, sum, 1);
         sum += __shfl_xor_sync(kFull, sum, 2);
-        // 2^e with amax * 2^e in [2^9, 2^10), kept within 2^+-100
-        const int ex = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
-        const int e = min(max(9 - ex, -100), 100);
-        const float up = __int_as_float((e + 127) << 23);
+        if (qd == 0) reinterpret_cast<float2*>(msc)[warp * 8 + g8] = make_float2(amax, sum);
+        __syncthreads();
+        amax = sum = 0.f;
 #pragma unroll
-        for (int i = 0; i < KS; ++i) {
-            const float hi = BITS == 8 ? up : up * 0.0625f;  // odd elements of 4-bit words come times 16
-            qb[i][0] = pack2<false>(f[i][0] * up, f[i][1] * up);
-            qb[i][1] = pack2<false>(f[i][2] * hi, f[i][3] * hi);
+        for (int w = 0; w < NW; ++w) {
+            const float2 v = reinterpret_cast<const float2*>(msc)[w * 8 + g8];
+            amax = fmaxf(amax, v.x);
+            sum += v.y;
         }
-        const float sf = p.qk_scale * (__int_as_float((127 - e) << 23) * 0x1p24f), qs = p.qk_scale * sum;
+        // 2^ex with amax * 2^ex in [2^9, 2^10), kept within 2^+-100
+        const int ex = min(max(9 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), -100), 100);
+        const float up = __int_as_float((ex + 127) << 23);
+        const float hi = BITS == 8 ? up : up * 0.0625f;  // odd elements of 4-bit words come times 16
+#pragma unroll
+        for (int m = 0; m < MINE; ++m) {
+            const int w = warp + m * NW;
+            if (w >= WORDS) break;
+#pragma unroll
+            for (int j = 0; j < PER; ++j) {
+                constexpr int R = BITS == 8 ? 2 : 4;  // element distance of an f16 pair
+                qsm[(w * PER + j) * 32 + lane] = make_uint2(pack2<false>(e[m][2 * j] * up, e[m][2 * j + R] * up),
+                                                            pack2<false>(e[m][2 * j + 1] * hi, e[m][2 * j + 1 + R] * hi));
+            }
+        }
+        const float sf = p.qk_scale * (__int_as_float((127 - ex) << 23) * 0x1p24f), qs = p.qk_scale * sum;
         sfA = __shfl_sync(kFull, sf, 8 * qd);
         sfB = __shfl_sync(kFull, sf, 8 * qd + 4);
         qsA = __shfl_sync(kFull, qs, 8 * qd);
         qsB = __shfl_sync(kFull, qs, 8 * qd + 4);
     }
+    __syncthreads();
 
     float o[KS][4];
 #pragma unroll
@@ -283,42 +296,44 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
                 float sv[2][4];  // (token g8, heads A, B), (token g8 + 8, heads A, B)
                 float vs[2][2];  // value scale of tokens g8, g8 + 8
                 float vz[2][2];
+                {
+                    // the two blocks' products side by side, two accumulators each: four
+                    // independent chains of MMAs, one load of Q for both blocks
+                    float sa[2][2][4];
+                    uint32_t w0[2][WORDS], w1[2][WORDS];
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const uint32_t kt = base + b * 2 * TB;
-                    float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-                    uint32_t w0[WORDS], w1[WORDS];
-                    lds_words<WORDS, 16 * L::KW>(kt + koff, w0);
-                    lds_words<WORDS, 16 * L::KW>(kt + koff + 8 * L::KW, w1);
-                    const uint2 kp0 = lds64(kt + poff), kp1 = lds64(kt + poff + 64);
-                    const uint2 vp0 = lds64(kt + TB + poff), vp1 = lds64(kt + TB + poff + 64);
+                    for (int b = 0; b < 2; ++b) {
+                        const uint32_t kt = base + b * 2 * TB + koff;
+                        lds_words<WORDS, 16 * L::KW>(kt, w0[b]);
+                        lds_words<WORDS, 16 * L::KW>(kt + 8 * L::KW, w1[b]);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) sa[b][c][0] = sa[b][c][1] = sa[b][c][2] = sa[b][c][3] = 0.f;
+                    }
 #pragma unroll
                     for (int w = 0; w < WORDS; ++w)
 #pragma unroll
                         for (int j = 0; j < PER; ++j) {
-                            const uint32_t x = w0[w] >> (8 * j), y = w1[w] >> (8 * j);
-                            mma16816a<false>(sa[(w * PER + j) & 1], codes_lo<BITS>(x), codes_lo<BITS>(y),
-                                             codes_hi<BITS>(x), codes_hi<BITS>(y), qb[w * PER + j][0],
-                                             qb[w * PER + j][1]);
+                            const uint2 qf = qsm[(w * PER + j) * 32 + lane];
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                const uint32_t x = w0[b][w] >> (8 * j), y = w1[b][w] >> (8 * j);
+                                mma16816a<false>(sa[b][(w * PER + j) & 1], codes_lo<BITS>(x), codes_lo<BITS>(y),
+                                                 codes_hi<BITS>(x), codes_hi<BITS>(y), qf.x, qf.y);
+                            }
                         }
-                    const float ks0 = __uint_as_float(kp0.x), ks1 = __uint_as_float(kp1.x);
-                    const float kz0 = __uint_as_float(kp0.y), kz1 = __uint_as_float(kp1.y);
-                    sv[b][0] = fmaf(ks0 * (sa[0][0] + sa[1][0]), sfA, kz0 * qsA);
-                    sv[b][1] = fmaf(ks0 * (sa[0][1] + sa[1][1]), sfB, kz0 * qsB);
-                    sv[b][2] = fmaf(ks1 * (sa[0][2] + sa[1][2]), sfA, kz1 * qsA);
-                    sv[b][3] = fmaf(ks1 * (sa[0][3] + sa[1][3]), sfB, kz1 * qsB);
-                    vs[b][0] = __uint_as_float(vp0.x);
-                    vs[b][1] = __uint_as_float(vp1.x);
-                    vz[b][0] = __uint_as_float(vp0.y);
-                    vz[b][1] = __uint_as_float(vp1.y);
-                    if (!whole) {  // tokens past the end: stale parameters must not get through
-                        if (g8 >= nv[b]) {
-                            sv[b][0] = sv[b][1] = -INFINITY;
-                            vs[b][0] = vz[b][0] = 0.f;
-                        }
-                        if (g8 + 8 >= nv[b]) {
-                            sv[b][2] = sv[b][3] = -INFINITY;
-                            vs[b][1] = vz[b][1] = 0.f;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const uint32_t kp = base + b * 2 * TB + poff;
+                        const uint2 kp0 = lds64(kp), kp1 = lds64(kp + 64);
+                        const float ks0 = __uint_as_float(kp0.x), ks1 = __uint_as_float(kp1.x);
+                        const float kz0 = __uint_as_float(kp0.y), kz1 = __uint_as_float(kp1.y);
+                        sv[b][0] = fmaf(ks0 * (sa[b][0][0] + sa[b][1][0]), sfA, kz0 * qsA);
+                        sv[b][1] = fmaf(ks0 * (sa[b][0][1] + sa[b][1][1]), sfB, kz0 * qsB);
+                        sv[b][2] = fmaf(ks1 * (sa[b][0][2] + sa[b][1][2]), sfA, kz1 * qsA);
+                        sv[b][3] = fmaf(ks1 * (sa[b][0][3] + sa[b][1][3]), sfB, kz1 * qsB);
+                        if (!whole) {  // tokens past the end: stale parameters must not get through
+                            if (g8 >= nv[b]) sv[b][0] = sv[b][1] = -INFINITY;
+                            if (g8 + 8 >= nv[b]) sv[b][2] = sv[b][3] = -INFINITY;
                         }
                     }
                 }
@@ -339,6 +354,18 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
                 lB *= alB;
                 zA *= alA;
                 zB *= alB;
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint2 vp0 = lds64(base + (2 * b + 1) * TB + poff), vp1 = lds64(base + (2 * b + 1) * TB + poff + 64);
+                    vs[b][0] = __uint_as_float(vp0.x);
+                    vs[b][1] = __uint_as_float(vp1.x);
+                    vz[b][0] = __uint_as_float(vp0.y);
+                    vz[b][1] = __uint_as_float(vp1.y);
+                    if (!whole) {
+                        if (g8 >= nv[b]) vs[b][0] = vz[b][0] = 0.f;
+                        if (g8 + 8 >= nv[b]) vs[b][1] = vz[b][1] = 0.f;
+                    }
+                }
                 // the value scales' reference moves only up, by powers of two
                 const uint32_t vmax = __reduce_max_sync(
                     kFull, __float_as_uint(fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]))));
@@ -374,21 +401,40 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
                     uint32_t h01, t01, h23, t23;
                     pack2_split<false>(p0 * u0, p1 * u0, h01, t01);
                     pack2_split<false>(p2 * u1, p3 * u1, h23, t23);
-                    const uint32_t pb0 = movmatrix_t(h01), pt0 = movmatrix_t(t01);  // tokens 0..7
-                    const uint32_t pb1 = movmatrix_t(h23), pt1 = movmatrix_t(t23);  // tokens 8..15
+                    uint32_t pb0, pb1, pt0 = 0u, pt1 = 0u;  // tokens 0 .. 7, tokens 8 .. 15
+                    if constexpr (FOLD) {
+                        // columns 4 .. 7 (lanes qd >= 2) hold the same probabilities: they
+                        // carry the tails, and one MMA does both
+                        pb0 = movmatrix_t(qd < 2 ? h01 : t01);
+                        pb1 = movmatrix_t(qd < 2 ? h23 : t23);
+                    } else {
+                        pb0 = movmatrix_t(h01);
+                        pt0 = movmatrix_t(t01);
+                        pb1 = movmatrix_t(h23);
+                        pt1 = movmatrix_t(t23);
+                    }
                     uint32_t w0[WORDS], w1[WORDS];
                     lds_words<WORDS, 1024>(vt + voff, w0);
                     lds_words<WORDS, 1024>(vt + voff + 128, w1);
+                    // kGroup m-tiles' head products, then their tails: an accumulator's two
+                    // MMAs are not back to back
 #pragma unroll
-                    for (int w = 0; w < WORDS; ++w)
+                    for (int i0 = 0; i0 < KS; i0 += kGroup) {
+                        uint32_t a[kGroup][4];
 #pragma unroll
-                        for (int j = 0; j < PER; ++j) {
+                        for (int i = 0; i < kGroup; ++i) {
+                            const int w = (i0 + i) / PER, j = (i0 + i) % PER;
                             const uint32_t x = w0[w] >> (8 * j), y = w1[w] >> (8 * j);
-                            const uint32_t a0 = codes_lo<BITS>(x), a1 = codes_hi<BITS>(x);
-                            const uint32_t a2 = codes_lo<BITS>(y), a3 = codes_hi<BITS>(y);
-                            mma16816a<false>(o[w * PER + j], a0, a1, a2, a3, pb0, pb1);
-                            mma16816a<false>(o[w * PER + j], a0, a1, a2, a3, pt0, pt1);
+                            a[i][0] = codes_lo<BITS>(x);
+                            a[i][1] = codes_hi<BITS>(x);
+                            a[i][2] = codes_lo<BITS>(y);
+                            a[i][3] = codes_hi<BITS>(y);
+                            mma16816a<false>(o[i0 + i], a[i][0], a[i][1], a[i][2], a[i][3], pb0, pb1);
                         }
+#pragma unroll
+                        for (int i = 0; i < kGroup && !FOLD; ++i)
+                            mma16816a<false>(o[i0 + i], a[i][0], a[i][1], a[i][2], a[i][3], pt0, pt1);
+                    }
                 }
             }
             __syncwarp();
@@ -433,7 +479,7 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
     __syncthreads();
 
     // ---- cross-warp log-sum-exp weights, once per (warp, head)
-    float* msc = reinterpret_cast<float*>(smem + C::kMergeOffset);  // [NW][8]
+    // msc: [NW][8]
     float* minv = msc + NW * 8;
     float* mmax = minv + 8;
     if (threadIdx.x < G) {
@@ -479,8 +525,9 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
             const float* wsw = reinterpret_cast<float*>(smem + w * NST * STAGE);
             const float sc = msc[w * 8 + g];
             if (sc != 0.f) {
-                r0 = fmaf(sc, wsw[frag] + wsw[16 + g], r0);
-                r1 = fmaf(sc, wsw[frag + 66] + wsw[16 + g], r1);
+                // FOLD: the tails' sums are those of column g + 4, two lanes on
+                r0 = fmaf(sc, wsw[frag] + (FOLD ? wsw[frag + 2] : 0.f) + wsw[16 + g], r0);
+                r1 = fmaf(sc, wsw[frag + 66] + (FOLD ? wsw[frag + 68] : 0.f) + wsw[16 + g], r1);
             }
         }
         r0 *= minv[g];
@@ -494,10 +541,10 @@ __global__ void __launch_bounds__(128, IntCfg<D, BITS>::kCtasPerSm)
     }
 }
 
-template <int D, int BITS, bool SPARSE>
+template <int D, int BITS, bool FOLD, bool SPARSE>
 cudaError_t launch_decode_int_t(const DecodeParams& p, int G, int q_dtype, cudaStream_t st) {
-    constexpr int SMEM = IntCfg<D, BITS>::kBytes;
-    auto kern = decode_int_kernel<D, BITS, SPARSE>;
+    constexpr int SMEM = IntCfg<D, BITS, FOLD>::kBytes;
+    auto kern = decode_int_kernel<D, BITS, FOLD, SPARSE>;
     static bool configured[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -508,17 +555,21 @@ cudaError_t launch_decode_int_t(const DecodeParams& p, int G, int q_dtype, cudaS
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    kern<<<dim3(p.NP, p.Hkv, p.S), 128, SMEM, st>>>(p, G, q_dtype == PKV_BF16 ? 1 : 0);
+    kern<<<dim3(p.NP, p.Hkv, p.S), IntCfg<D, BITS, FOLD>::kWarps * 32, SMEM, st>>>(p, G, q_dtype == PKV_BF16 ? 1 : 0);
     return cudaGetLastError();
 }
 
 template <int BITS>
 cudaError_t launch_decode_int(const DecodeParams& p, int G, int q_dtype, cudaStream_t st) {
-    if (p.selected)
-        return p.D == 128 ? launch_decode_int_t<128, BITS, true>(p, G, q_dtype, st)
-                          : launch_decode_int_t<64, BITS, true>(p, G, q_dtype, st);
-    return p.D == 128 ? launch_decode_int_t<128, BITS, false>(p, G, q_dtype, st)
-                      : launch_decode_int_t<64, BITS, false>(p, G, q_dtype, st);
+    const auto run = [&](auto fold) {
+        constexpr bool F = decltype(fold)::value;
+        if (p.selected)
+            return p.D == 128 ? launch_decode_int_t<128, BITS, F, true>(p, G, q_dtype, st)
+                              : launch_decode_int_t<64, BITS, F, true>(p, G, q_dtype, st);
+        return p.D == 128 ? launch_decode_int_t<128, BITS, F, false>(p, G, q_dtype, st)
+                          : launch_decode_int_t<64, BITS, F, false>(p, G, q_dtype, st);
+    };
+    return G <= 4 ? run(std::true_type{}) : run(std::false_type{});
 }
 
 }  // namespace pkv
