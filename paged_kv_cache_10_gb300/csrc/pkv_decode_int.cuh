@@ -79,15 +79,25 @@ __device__ __forceinline__ void lds_words(uint32_t addr, uint32_t* w) {
     }
 }
 
-// f16 pair of codes from a word's even bytes (8 bits) or low halves (4 bits) ...
+// The A operand pairs of code word w for its j-th MMA (j = 0 for 8 bits): lo from
+// the even bytes or, of byte j of each half, the low codes, hi from the odd bytes
+// or the high codes times 16.  The second byte's low codes are what is left of
+// the byte without the high ones: a subtraction, exact on these values, that
+// runs beside the logic operations instead of among them.
 template <int BITS>
-__device__ __forceinline__ uint32_t codes_lo(uint32_t w) {
-    return w & (BITS == 8 ? 0x00ff00ffu : 0x000f000fu);
-}
-// ... and from its odd bytes, or its high halves (there times 16).
-template <int BITS>
-__device__ __forceinline__ uint32_t codes_hi(uint32_t w) {
-    return BITS == 8 ? __byte_perm(w, 0u, 0x4341) : w & 0x00f000f0u;
+__device__ __forceinline__ void code_pairs(uint32_t w, int j, uint32_t& lo, uint32_t& hi) {
+    if constexpr (BITS == 8) {
+        lo = w & 0x00ff00ffu;
+        hi = __byte_perm(w, 0u, 0x4341);
+    } else if (j == 0) {
+        lo = w & 0x000f000fu;
+        hi = w & 0x00f000f0u;
+    } else {
+        const uint32_t x = __byte_perm(w, 0u, 0x4341);
+        hi = x & 0x00f000f0u;
+        const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&hi));
+        lo = *reinterpret_cast<const uint32_t*>(&d);
+    }
 }
 
 template <int D, int BITS, bool FOLD, bool SPARSE>
@@ -316,9 +326,10 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
                             const uint2 qf = qsm[(w * PER + j) * 32 + lane];
 #pragma unroll
                             for (int b = 0; b < 2; ++b) {
-                                const uint32_t x = w0[b][w] >> (8 * j), y = w1[b][w] >> (8 * j);
-                                mma16816a<false>(sa[b][(w * PER + j) & 1], codes_lo<BITS>(x), codes_lo<BITS>(y),
-                                                 codes_hi<BITS>(x), codes_hi<BITS>(y), qf.x, qf.y);
+                                uint32_t a0, a1, a2, a3;
+                                code_pairs<BITS>(w0[b][w], j, a0, a2);
+                                code_pairs<BITS>(w1[b][w], j, a1, a3);
+                                mma16816a<false>(sa[b][(w * PER + j) & 1], a0, a1, a2, a3, qf.x, qf.y);
                             }
                         }
 #pragma unroll
@@ -424,11 +435,8 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
 #pragma unroll
                         for (int i = 0; i < kGroup; ++i) {
                             const int w = (i0 + i) / PER, j = (i0 + i) % PER;
-                            const uint32_t x = w0[w] >> (8 * j), y = w1[w] >> (8 * j);
-                            a[i][0] = codes_lo<BITS>(x);
-                            a[i][1] = codes_hi<BITS>(x);
-                            a[i][2] = codes_lo<BITS>(y);
-                            a[i][3] = codes_hi<BITS>(y);
+                            code_pairs<BITS>(w0[w], j, a[i][0], a[i][1]);
+                            code_pairs<BITS>(w1[w], j, a[i][2], a[i][3]);
                             mma16816a<false>(o[i0 + i], a[i][0], a[i][1], a[i][2], a[i][3], pb0, pb1);
                         }
 #pragma unroll
@@ -481,7 +489,6 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     // ---- cross-warp log-sum-exp weights, once per (warp, head)
     // msc: [NW][8]
     float* minv = msc + NW * 8;
-    float* mmax = minv + 8;
     if (threadIdx.x < G) {
         const int g = threadIdx.x;
         float M = -INFINITY;
@@ -496,7 +503,6 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
             den = fmaf(sc, wsw[8 + g], den);
         }
         minv[g] = den > 0.f ? 1.f / den : (den == den ? 0.f : den);
-        mmax[g] = M;
         const int64_t row = static_cast<int64_t>(s) * p.Hq + h * G + g;
         if (p.NP > 1) {
             p.part_m[row * p.NP + part] = M;
