@@ -15,9 +15,6 @@
 #include "pkv_decode_mma.cuh"
 #include "pkv_int.cuh"
 #include "pkv_pool_row.cuh"
-#ifndef PKV_TILES_CAP
-#define PKV_TILES_CAP 16
-#endif
 
 namespace pkv {
 namespace {
@@ -282,23 +279,11 @@ __global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) 
 }
 
 // -------------------------------------------------------------- selection
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 1024;
 constexpr int kSelNear = 256;  // blocks near the border that are ranked pair by pair
-
-// Sums / extrema over the CTA, the result in every thread.
-template <typename T, typename Op>
-__device__ __forceinline__ T cta_reduce(T v, Op op, T* red) {
-#pragma unroll
-    for (int m = 16; m; m >>= 1) v = op(v, __shfl_xor_sync(kFull, v, m));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = red[threadIdx.x & (kSelThreads / 32 - 1)];
-#pragma unroll
-    for (int m = kSelThreads / 64; m; m >>= 1) v = op(v, __shfl_xor_sync(kFull, v, m));
-    return v;
-}
+constexpr int kSelAtOnce = 4;  // of them that a warp scores at once
 
 // Exclusive sum of v over the CTA's threads in order.
 __device__ __forceinline__ int cta_scan(int v, int* red) {
@@ -314,7 +299,7 @@ __device__ __forceinline__ int cta_scan(int v, int* red) {
     __syncthreads();
     int before = 0;
 #pragma unroll
-    for (int w = 0; w < kSelThreads / 32; ++w)
+    for (int w = 0; w < kSelWarps; ++w)
         if (w < warp) before += red[w];
     return before + x - v;
 }
@@ -325,37 +310,52 @@ __device__ __forceinline__ uint64_t order64(double x) {
     return static_cast<uint64_t>(b) ^ (b < 0 ? ~0ull : 1ull << 63);
 }
 
-// The score of block j by one warp, in binary32 (A = float) or 64 bits.  Products
-// of 16-bit values are exact in both; in 64 bits so are, but for extreme
-// ranges, their sums; in binary32 an element's sum takes at most D / 32 - 1 + 5
-// = 8 additions, each within 2^-24 of the sum of magnitudes.
-template <int D, typename T, typename A>
-__device__ __forceinline__ A warp_score(const SelectParams& p, int s, int h, int j) {
-    const int lane = threadIdx.x & 31;
-    const int id = __ldg(p.block_tables + static_cast<int64_t>(s) * p.MB + j);
-    if (id < 0 || id >= p.NB) return static_cast<A>(-INFINITY);
+// The scores of blocks j[0 .. N) by one warp, in binary32 (A = float) or 64 bits.
+// Products of 16-bit values are exact in both; in 64 bits so are, but for
+// extreme ranges, their sums; in binary32 an element's sum takes at most D / 32 -
+// 1 + 5 = 8 additions, each within 2^-24 of the sum of magnitudes.  q: the G query
+// rows in shared memory.  A negative j gives -inf.
+template <int D, typename T, typename A, int N>
+__device__ __forceinline__ void warp_scores(const SelectParams& p, const float* q, int s, int h, const int (&j)[N],
+                                            A (&best)[N]) {
+    constexpr int V = D / 32;
     using E = typename T::storage;
-    const E* b = reinterpret_cast<const E*>(p.bounds) + (static_cast<int64_t>(id) * p.Hkv + h) * 2 * D;
-    float lo[D / 32], hi[D / 32];
+    const int lane = threadIdx.x & 31;
+    E lo[N][V], hi[N][V];
+    bool ok[N];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-        lo[i] = to_float(b[lane + 32 * i]);
-        hi[i] = to_float(b[D + lane + 32 * i]);
+    for (int n = 0; n < N; ++n) {
+        const int id = j[n] >= 0 ? __ldg(p.block_tables + static_cast<int64_t>(s) * p.MB + j[n]) : -1;
+        ok[n] = id >= 0 && id < p.NB;
+        const E* b = reinterpret_cast<const E*>(p.bounds) + (static_cast<int64_t>(ok[n] ? id : 0) * p.Hkv + h) * 2 * D + lane;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            lo[n][i] = b[32 * i];
+            hi[n][i] = b[D + 32 * i];
+        }
+        best[n] = static_cast<A>(-INFINITY);
     }
-    A best = static_cast<A>(-INFINITY);
     for (int g = 0; g < p.G; ++g) {
-        const E* q = reinterpret_cast<const E*>(p.q) + (static_cast<int64_t>(s) * p.Hq + h * p.G + g) * D;
-        A sum = 0;
+        A sum[N];
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const float x = to_float(q[lane + 32 * i]);
-            sum += static_cast<A>(x) * static_cast<A>(x < 0.f ? lo[i] : hi[i]);
+        for (int n = 0; n < N; ++n) sum[n] = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const float x = q[g * D + lane + 32 * i];
+#pragma unroll
+            for (int n = 0; n < N; ++n)
+                sum[n] += static_cast<A>(x) * static_cast<A>(to_float(x < 0.f ? lo[n][i] : hi[n][i]));
         }
 #pragma unroll
-        for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(kFull, sum, m);
-        best = best > sum ? best : (sum == sum ? sum : best);  // NaN is dropped
+        for (int n = 0; n < N; ++n) {
+#pragma unroll
+            for (int m = 16; m; m >>= 1) sum[n] += __shfl_xor_sync(kFull, sum[n], m);
+            if (sum[n] > best[n]) best[n] = sum[n];  // NaN is dropped
+        }
     }
-    return best;
+#pragma unroll
+    for (int n = 0; n < N; ++n)
+        if (!ok[n]) best[n] = static_cast<A>(-INFINITY);
 }
 
 // One CTA per (KV head, sequence): the n blocks of the highest scores, in
@@ -367,24 +367,24 @@ __device__ __forceinline__ A warp_score(const SelectParams& p, int s, int h, int
 // in two chains of at most 8, so with A = max_g |q_g|_1 * max |bound| it is within
 // 8 * 17 * 2^-23 A + 2^-23 A < 2^-15 A of the true score.  eps = 2^-14 A covers it
 // twice.  A histogram over the scores' range finds the bin that holds the k-th
-// highest, zooming in while the bin is wide and full; with [tl, th] the scores
-// in it, a block above th + 2 eps is in and one below tl - 2 eps is out, and
-// the few between them are scored again, in binary32 with a far smaller bound
-// and, where that leaves an order open, in 64 bits, and ranked by (score,
+// highest, zooming in while the bin is wide and full; with [tl, th] around the
+// scores in it, a block above th + 2 eps is in and one below tl - 2 eps is out,
+// and the few between them are scored again, in binary32 with a far smaller
+// bound and, where that leaves an order open, in 64 bits, and ranked by (score,
 // number).  So the answer is that of exact arithmetic whatever the order of the
 // binary32 sums.
 template <int D, typename T>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
     extern __shared__ float row_smem[];
     __shared__ int hist[kSelBins];
-    __shared__ __align__(8) unsigned char red_bytes[(kSelThreads / 32) * 8];
+    __shared__ float qs[8 * D];
+    __shared__ float redf[4][kSelWarps];
+    __shared__ int redi[kSelWarps];
     __shared__ int near_id[kSelNear];
     __shared__ double near_y[kSelNear];
     __shared__ float near_f[kSelNear];
     __shared__ short tie[kSelNear];
-    __shared__ int sh[4];
-    int* redi = reinterpret_cast<int*>(red_bytes);
-    float* redf = reinterpret_cast<float*>(red_bytes);
+    __shared__ int sh[5];
     const int h = blockIdx.x, s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = static_cast<int64_t>(s) * p.Hkv + h;
     int32_t* out = p.selected + row * p.n;
@@ -397,153 +397,194 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     }
     // the free range [f0, f1) and how many of it to keep: n >= sink + recent and nblk > n
     const int f0 = p.sink, f1 = nblk - p.recent, m = f1 - f0, k = p.n - p.sink - p.recent;
-    // A: the largest |q_g|_1 while the scores are still being made
+    // A: the largest |q_g|_1, while the scores are still being made
     float q1 = 0.f;
-    for (int g = warp; g < p.G; g += kSelThreads / 32) {
+    for (int g = warp; g < p.G; g += kSelWarps) {
         const typename T::storage* q =
             reinterpret_cast<const typename T::storage*>(p.q) + (static_cast<int64_t>(s) * p.Hq + h * p.G + g) * D;
         float a = 0.f;
-        for (int d = lane; d < D; d += 32) a += fabsf(to_float(q[d]));
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const float x = to_float(q[lane + 32 * i]);
+            qs[g * D + lane + 32 * i] = x;
+            a += fabsf(x);
+        }
 #pragma unroll
         for (int x = 16; x; x >>= 1) a += __shfl_xor_sync(kFull, a, x);
         q1 = fmaxf(q1, a);
     }
+    for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+    if (tid == 0) sh[2] = sh[3] = sh[4] = 0;
     wait_primary_grid();
-    const auto fmx = [](float a, float b) { return fmaxf(a, b); };
-    const auto fmn = [](float a, float b) { return fminf(a, b); };
     float* sc = p.score + row * p.cols;
-    if (nblk <= p.smem_cols) {
-        for (int i = tid; i < nblk; i += kSelThreads) row_smem[i] = sc[i];
+    const bool in_smem = nblk <= p.smem_cols;
+    float a = INFINITY, b = -INFINITY, big = 0.f;
+    if (in_smem) {
+        for (int i = tid; i < nblk; i += kSelThreads) {
+            const float x = sc[i];
+            row_smem[i] = x;
+            if (i >= f0 && i < f1) {
+                if (x > -INFINITY) a = fminf(a, x);
+                b = fmaxf(b, x);
+            }
+        }
         sc = row_smem;
-    }
-    float big = 0.f;
-    for (int i = tid; i < (nblk + 15) / 16; i += kSelThreads) big = fmaxf(big, p.top[row * (p.cols / 16) + i]);
-    q1 = cta_reduce(q1, fmx, redf);
-    big = cta_reduce(big, fmx, redf);
-    const float eps2 = 2.f * 0x1p-14f * q1 * big;
-
-    float thr = INFINITY;  // blocks above it are in
-    if (k > 0) {
-        float a = INFINITY, b = -INFINITY;
+    } else {
         for (int i = f0 + tid; i < f1; i += kSelThreads) {
             const float x = sc[i];
             if (x > -INFINITY) a = fminf(a, x);
             b = fmaxf(b, x);
         }
-        a = cta_reduce(a, fmn, redf);
-        b = cta_reduce(b, fmx, redf);
+    }
+    for (int i = tid; i < (nblk + 15) / 16; i += kSelThreads) big = fmaxf(big, p.top[row * (p.cols / 16) + i]);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) {
+        a = fminf(a, __shfl_xor_sync(kFull, a, x));
+        b = fmaxf(b, __shfl_xor_sync(kFull, b, x));
+        big = fmaxf(big, __shfl_xor_sync(kFull, big, x));
+    }
+    if (lane == 0) {
+        redf[0][warp] = a;
+        redf[1][warp] = b;
+        redf[2][warp] = big;
+        redf[3][warp] = q1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+        a = fminf(a, redf[0][w]);
+        b = fmaxf(b, redf[1][w]);
+        big = fmaxf(big, redf[2][w]);
+        q1 = fmaxf(q1, redf[3][w]);
+    }
+    const float eps2 = 2.f * 0x1p-14f * q1 * big;
+
+    float thr = INFINITY;  // blocks above it are in
+    if (k > 0) {
         if (!(a <= b)) a = b;  // no finite score at all
-        int above = 0;         // blocks known to score over b
         for (int round = 0; round < 4; ++round) {
             const float scale = kSelBins / (b - a);
             if (!(b > a) || !(scale < INFINITY) || !(scale > 0.f)) break;
-            for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-            __syncthreads();
-            const auto bin_of = [&](float x) {  // monotone in x
-                return min(kSelBins - 1, static_cast<int>((x - a) * scale));
-            };
+            if (round) {
+                for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+                if (tid == 0) sh[4] = 0;
+                __syncthreads();
+            }
+            int over = 0;  // blocks known to score over b
             for (int i = f0 + tid; i < f1; i += kSelThreads) {
                 const float x = sc[i];
-                if (x >= a && x <= b) atomicAdd(&hist[bin_of(x)], 1);
+                if (x > b)
+                    ++over;
+                else if (x >= a)
+                    atomicAdd(&hist[min(kSelBins - 1, static_cast<int>((x - a) * scale))], 1);
+            }
+            if (round) {
+                over = __reduce_add_sync(kFull, over);
+                if (lane == 0 && over) atomicAdd(&sh[4], over);
             }
             __syncthreads();
-            // the bin of the k-th highest: scan from the top, two bins a thread
-            const int top_bin = kSelBins - 1 - 2 * tid;
-            const int c0 = hist[top_bin], c1 = hist[top_bin - 1];
-            const int before = above + cta_scan(c0 + c1, redi);
+            // the bin of the k-th highest: scan from the top, four bins a thread
+            constexpr int PB = kSelBins / kSelThreads;
+            const int top_bin = kSelBins - 1 - PB * tid;
+            int c[PB], sum = 0;
+#pragma unroll
+            for (int i = 0; i < PB; ++i) sum += c[i] = hist[top_bin - i];
+            int before = sh[4] + cta_scan(sum, redi);
             if (tid == 0) sh[0] = -1;
             __syncthreads();
-            if (before < k && before + c0 >= k) {
-                sh[0] = top_bin;
-                sh[1] = before;
-                sh[2] = c0;
-            } else if (before + c0 < k && before + c0 + c1 >= k) {
-                sh[0] = top_bin - 1;
-                sh[1] = before + c0;
-                sh[2] = c1;
+#pragma unroll
+            for (int i = 0; i < PB; ++i) {
+                if (before < k && before + c[i] >= k) {
+                    sh[0] = top_bin - i;
+                    sh[1] = c[i];
+                }
+                before += c[i];
             }
             __syncthreads();
-            const int t = sh[0], cnt = sh[2];
+            const int t = sh[0];
             if (t < 0) {  // the k-th is below every finite score
                 b = a;
                 break;
             }
-            above = sh[1];
-            float na = INFINITY, nb = -INFINITY;
-            for (int i = f0 + tid; i < f1; i += kSelThreads) {
-                const float x = sc[i];
-                if (x >= a && x <= b && bin_of(x) == t) {
-                    na = fminf(na, x);
-                    nb = fmaxf(nb, x);
-                }
-            }
-            a = cta_reduce(na, fmn, redf);
-            b = cta_reduce(nb, fmx, redf);
-            if (cnt <= 16 || b - a <= eps2) break;
+            // the bin's edges, out by 2^-8 of a bin: (x - a) * scale is within 2^-12 of a bin
+            const float lo = a + (t - 0x1p-8f) / scale, hi = a + (t + 1 + 0x1p-8f) / scale;
+            a = fmaxf(a, lo);
+            b = fminf(b, hi);
+            if (sh[1] <= 16 || b - a <= eps2) break;
+            __syncthreads();  // sh and hist are written again
         }
-        // fewer finite scores than k: everything left over is in the band
         float low = a - eps2;
         thr = b + eps2;
         if (!(low > -INFINITY) || !(thr < INFINITY)) {  // no usable bound: all in the band
             low = -INFINITY;
             thr = INFINITY;
         }
-        int sure = 0, band = 0, maybe = 0;
+        // ---- sure of being in, and the band
+        int sure = 0;
         for (int i = f0 + tid; i < f1; i += kSelThreads) {
             const float x = sc[i];
-            sure += x > thr;
-            band += x <= thr && x >= low;
-            maybe += x < low;
+            if (x > thr) {
+                ++sure;
+            } else if (x >= low) {
+                const int at = atomicAdd(&sh[3], 1);
+                if (at < kSelNear) near_id[at] = i;
+            }
         }
-        const auto add = [](int u, int v) { return u + v; };
-        sure = cta_reduce(sure, add, redi);
-        band = cta_reduce(band, add, redi);
-        if (sure + band < k) {  // blocks without a usable score fill up
+        sure = __reduce_add_sync(kFull, sure);
+        if (lane == 0 && sure) atomicAdd(&sh[2], sure);
+        __syncthreads();
+        sure = sh[2];
+        int band = sh[3];
+        const int want = k - sure;
+        bool listed = band <= kSelNear;
+        if (band < want) {  // blocks without a usable score fill up
             low = -INFINITY;
             band = m - sure;
+            listed = false;
         }
-        const int want = k - sure;
-        if (band == want) {
-            thr = low;  // all of the band
-            for (int i = f0 + tid; i < f1; i += kSelThreads)
-                if (sc[i] == low) sc[i] = INFINITY;
-        } else {
-            // ---- 64-bit scores of the band
-            if (tid == 0) sh[3] = 0;
+        __syncthreads();  // sh is written again
+        if (band == want) {  // all of the band
+            for (int i = f0 + tid; i < f1; i += kSelThreads) {
+                const float x = sc[i];
+                if (x <= thr && x >= low) sc[i] = INFINITY;
+            }
+        } else if (listed) {
+            // binary32 first, each within 8 * 2^-24 A: twice that and its double is eps2 / 64
+            for (int i = warp; i < band; i += kSelWarps * kSelAtOnce) {
+                int j[kSelAtOnce];
+                float y[kSelAtOnce];
+#pragma unroll
+                for (int u = 0; u < kSelAtOnce; ++u) j[u] = i + u * kSelWarps < band ? near_id[i + u * kSelWarps] : -1;
+                warp_scores<D, T, float>(p, qs, s, h, j, y);
+#pragma unroll
+                for (int u = 0; u < kSelAtOnce; ++u)
+                    if (lane == 0 && j[u] >= 0) near_f[i + u * kSelWarps] = y[u];
+            }
+            if (tid == 0) sh[3] = sh[2] = 0;
             __syncthreads();
-            const bool few = band <= kSelNear;
-            if (few) {
-                for (int i = f0 + tid; i < f1; i += kSelThreads)
-                    if (sc[i] <= thr && sc[i] >= low) near_id[atomicAdd(&sh[3], 1)] = i;
-                __syncthreads();
-                // binary32 first, each within 8 * 2^-24 A: twice that and its double is eps2 / 64
-                for (int i = warp; i < band; i += kSelThreads / 32) {
-                    const float y = warp_score<D, T, float>(p, s, h, near_id[i]);
-                    if (lane == 0) near_f[i] = y;
+            const float e2 = eps2 * 0x1p-6f;
+            for (int i = tid; i < band; i += kSelThreads) {
+                const float y = near_f[i];
+                int over = 0, near_or_over = 0;
+                for (int j = 0; j < band; ++j) {
+                    over += near_f[j] > y + e2;
+                    near_or_over += !(near_f[j] < y - e2);
                 }
-                if (tid == 0) sh[3] = sh[2] = 0;
-                __syncthreads();
-                const float e2 = eps2 * 0x1p-6f;
-                for (int i = tid; i < band; i += kSelThreads) {
-                    const float y = near_f[i];
-                    int over = 0, near_or_over = 0;
-                    for (int j = 0; j < band; ++j) {
-                        over += near_f[j] > y + e2;
-                        near_or_over += !(near_f[j] < y - e2);
-                    }
-                    const bool in = near_or_over <= want && e2 < INFINITY, off = over >= want && e2 < INFINITY;
-                    if (in) atomicAdd(&sh[2], 1);
-                    if (in || off)
-                        sc[near_id[i]] = in ? INFINITY : -INFINITY;
-                    else
-                        tie[atomicAdd(&sh[3], 1)] = i;
-                }
-                __syncthreads();
-                const int ties = sh[3], left = want - sh[2];
-                // the few that binary32 cannot order: 64 bits
-                for (int i = warp; i < ties; i += kSelThreads / 32) {
-                    const double y = warp_score<D, T, double>(p, s, h, near_id[tie[i]]);
-                    if (lane == 0) near_y[i] = y;
+                const bool in = near_or_over <= want && e2 < INFINITY, off = over >= want && e2 < INFINITY;
+                if (in) atomicAdd(&sh[2], 1);
+                if (in || off)
+                    sc[near_id[i]] = in ? INFINITY : -INFINITY;
+                else
+                    tie[atomicAdd(&sh[3], 1)] = i;
+            }
+            __syncthreads();
+            const int ties = sh[3], left = want - sh[2];
+            if (ties > 0) {  // the few that binary32 cannot order: 64 bits
+                for (int i = warp; i < ties; i += kSelWarps) {
+                    const int j[1] = {near_id[tie[i]]};
+                    double y[1];
+                    warp_scores<D, T, double>(p, qs, s, h, j, y);
+                    if (lane == 0) near_y[i] = y[0];
                 }
                 __syncthreads();
                 for (int i = tid; i < ties; i += kSelThreads) {
@@ -553,67 +594,81 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                     for (int j = 0; j < ties; ++j) rank += near_y[j] > y || (near_y[j] == y && near_id[tie[j]] < at);
                     sc[at] = rank < left ? INFINITY : -INFINITY;
                 }
-            } else {
-                // many near the border (equal scores): radix selection of the want-th
-                // highest 64-bit score, then the lowest numbers among those equal to it
-                double* ex = p.exact + row * p.cols;
-                for (int i = f0 + warp; i < f1; i += kSelThreads / 32) {
-                    const float x = sc[i];
-                    if (!(x <= thr && x >= low)) continue;
-                    const double y = warp_score<D, T, double>(p, s, h, i);
-                    if (lane == 0) ex[i] = y;
-                }
+            }
+        } else {
+            // many near the border (equal scores): radix selection of the want-th
+            // highest 64-bit score, then the lowest numbers among those equal to it
+            double* ex = p.exact + row * p.cols;
+            for (int i = f0 + warp; i < f1; i += kSelWarps) {
+                const float x = sc[i];
+                if (!(x <= thr && x >= low)) continue;
+                const int j[1] = {i};
+                double y[1];
+                warp_scores<D, T, double>(p, qs, s, h, j, y);
+                if (lane == 0) ex[i] = y[0];
+            }
+            __syncthreads();
+            uint64_t prefix = 0, mask = 0;
+            int left = want;
+            for (int shift = 56; shift >= 0; shift -= 8) {
+                hist[tid] = 0;
                 __syncthreads();
-                uint64_t prefix = 0, mask = 0;
-                int left = want;
-                for (int shift = 56; shift >= 0; shift -= 8) {
-                    for (int i = tid; i < 256; i += kSelThreads) hist[i] = 0;
-                    __syncthreads();
-                    for (int i = f0 + tid; i < f1; i += kSelThreads) {
-                        const float x = sc[i];
-                        if (!(x <= thr && x >= low)) continue;
-                        const uint64_t o = order64(ex[i]);
-                        if ((o & mask) == prefix) atomicAdd(&hist[(o >> shift) & 255], 1);
-                    }
-                    __syncthreads();
-                    const int c = tid < 256 ? hist[255 - tid] : 0;
-                    const int before = cta_scan(c, redi);
-                    if (before < left && before + c >= left) {
-                        sh[0] = 255 - tid;
-                        sh[1] = left - before;
-                    }
-                    __syncthreads();
-                    prefix |= static_cast<uint64_t>(sh[0]) << shift;
-                    mask |= 255ull << shift;
-                    left = sh[1];
-                    __syncthreads();
-                }
-                // `left` of the blocks whose score has these bits, lowest numbers first
-                const int per = (m + kSelThreads - 1) / kSelThreads;
-                const int i0 = f0 + tid * per, i1 = min(f1, i0 + per);
-                int same = 0;
-                for (int i = i0; i < i1; ++i) same += sc[i] <= thr && sc[i] >= low && order64(ex[i]) == prefix;
-                int at = cta_scan(same, redi);
-                for (int i = i0; i < i1; ++i) {
+                for (int i = f0 + tid; i < f1; i += kSelThreads) {
                     const float x = sc[i];
                     if (!(x <= thr && x >= low)) continue;
                     const uint64_t o = order64(ex[i]);
-                    const bool in = o > prefix || (o == prefix && at++ < left);
-                    sc[i] = in ? INFINITY : -INFINITY;
+                    if ((o & mask) == prefix) atomicAdd(&hist[(o >> shift) & 255], 1);
                 }
+                __syncthreads();
+                const int c = hist[255 - tid];
+                const int before = cta_scan(c, redi);
+                if (before < left && before + c >= left) {
+                    sh[0] = 255 - tid;
+                    sh[1] = left - before;
+                }
+                __syncthreads();
+                prefix |= static_cast<uint64_t>(sh[0]) << shift;
+                mask |= 255ull << shift;
+                left = sh[1];
+                __syncthreads();
+            }
+            // `left` of the blocks whose score has these bits, lowest numbers first
+            const int per = (m + kSelThreads - 1) / kSelThreads;
+            const int i0 = f0 + tid * per, i1 = min(f1, i0 + per);
+            int same = 0;
+            for (int i = i0; i < i1; ++i) same += sc[i] <= thr && sc[i] >= low && order64(ex[i]) == prefix;
+            int at = cta_scan(same, redi);
+            for (int i = i0; i < i1; ++i) {
+                const float x = sc[i];
+                if (!(x <= thr && x >= low)) continue;
+                const uint64_t o = order64(ex[i]);
+                const bool in = o > prefix || (o == prefix && at++ < left);
+                sc[i] = in ? INFINITY : -INFINITY;
             }
         }
         __syncthreads();
     }
-    // ---- the kept blocks in ascending order
-    const int per = (nblk + kSelThreads - 1) / kSelThreads;
-    const int i0 = tid * per, i1 = min(nblk, i0 + per);
-    const auto kept = [&](int i) { return i < f0 || i >= f1 || (k > 0 && (sc[i] > thr || sc[i] == INFINITY)); };
+    // ---- the kept blocks in ascending order: a warp takes a run of 32-block groups
+    const auto kept = [&](int i) {
+        return i < nblk && (i < f0 || i >= f1 || (k > 0 && (sc[i] > thr || sc[i] == INFINITY)));
+    };
+    const int groups = ((nblk + 31) / 32 + kSelWarps - 1) / kSelWarps;
+    const int g0 = warp * groups;
     int mine = 0;
-    for (int i = i0; i < i1; ++i) mine += kept(i);
-    int at = cta_scan(mine, redi);
-    for (int i = i0; i < i1; ++i)
-        if (kept(i) && at < p.n) out[at++] = i;
+    for (int g = g0; g < g0 + groups && g * 32 < nblk; ++g) mine += __popc(__ballot_sync(kFull, kept(g * 32 + lane)));
+    if (lane == 0) redi[warp] = mine;
+    __syncthreads();
+    int at = 0;
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w)
+        if (w < warp) at += redi[w];
+    for (int g = g0; g < g0 + groups && g * 32 < nblk; ++g) {
+        const bool keep = kept(g * 32 + lane);
+        const uint32_t votes = __ballot_sync(kFull, keep);
+        const int to = at + __popc(votes & ((1u << lane) - 1u));
+        if (keep && to < p.n) out[to] = g * 32 + lane;
+        at += __popc(votes);
+    }
 }
 
 template <int D, typename T>
@@ -626,7 +681,7 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const size_t smem = static_cast<size_t>(p.smem_cols) * 4;
-    if (smem > 32 * 1024) {  // with the static arrays, more than a launch gets unasked
+    if (smem > 24 * 1024) {  // with the static arrays, more than a launch gets unasked
         e = cudaFuncSetAttribute(select_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(smem));
         if (e != cudaSuccess) return e;
@@ -781,10 +836,17 @@ extern "C" pkv_status pkv_select_blocks(const void* q, int32_t q_dtype, int32_t 
     p.n = num_selected;
     p.sink = sink_blocks;
     p.recent = recent_blocks;
-    // eight warps fit an SM: enough units for about two rounds of them, beyond that
-    // a warp takes a run of tiles, which its ring streams
-    const int64_t tiles = static_cast<int64_t>(l.cols / 16) * p.Hkv * p.S;
-    p.tiles = static_cast<int>(std::min<int64_t>(PKV_TILES_CAP, std::max<int64_t>(1, tiles / (num_sms() * 16))));
+    // tiles a warp takes in a run: the number whose whole rounds of resident CTAs
+    // (two an SM, four warps each) cost least, a run's start counted as three tiles
+    const int64_t row_tiles = l.cols / 16, slots = 2 * static_cast<int64_t>(num_sms());
+    int64_t best = INT64_MAX;
+    for (int run = 1; run <= 64; ++run) {
+        const int64_t ctas = cdiv(cdiv(row_tiles, run) * p.Hkv, 4) * p.S, cost = cdiv(ctas, slots) * (run + 3);
+        if (cost < best) {
+            best = cost;
+            p.tiles = run;
+        }
+    }
     constexpr int kSmemCols = 16384;  // 64 KiB; longer rows stay in the workspace
     p.smem_cols = static_cast<int>(std::min<int64_t>(l.cols, kSmemCols));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
