@@ -99,8 +99,13 @@ __device__ __forceinline__ int row_blocks(const SelectParams& p, int s, bool& ba
     return len <= 0 ? 0 : min((len - 1) / kBlockSize + 1, cap);
 }
 
-// Largest |x| of packed 16-bit pairs: magnitudes order like their bits.
-__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t x) { return __vmaxu2(m, x & 0x7fff7fffu); }
+// Largest |x| of packed 16-bit pairs (NaN passed over).
+template <typename T>
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t x) {
+    using P2 = typename std::conditional<std::is_same<T, BF16>::value, __nv_bfloat162, __half2>::type;
+    const P2 r = __hmax2(*reinterpret_cast<const P2*>(&m), __habs2(*reinterpret_cast<const P2*>(&x)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 // Shared memory of the score kernel: a ring of 16-block tiles per warp.  A
 // block's 2 D bound elements lie at a pitch of 64 bytes modulo 128, so that the
@@ -108,14 +113,15 @@ __device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint32_t x) { return __
 template <int D>
 struct ScoreCfg {
     static constexpr int kWarps = 4;
-    static constexpr int kStages = D == 128 ? 3 : 5;
+    static constexpr int kStages = 2;
+    static constexpr int kCtasPerSm = D == 128 ? 3 : 5;
     static constexpr int kRow = 4 * D;  // bytes of a block's bounds for one KV head
     static constexpr int kPitch = kRow + 64;
     static constexpr int kStage = 16 * kPitch;
     static constexpr int kBarOffset = kWarps * kStages * kStage;
     static constexpr int kMaskOffset = kBarOffset + kWarps * kStages * 8;
     static constexpr int kBytes = kMaskOffset + kWarps * kStages * 4 + 128;
-    static_assert(kPitch % 128 == 64 && 2 * (kBytes + 1024) <= 228 * 1024, "two CTAs per SM");
+    static_assert(kPitch % 128 == 64 && kCtasPerSm * (kBytes + 1024) <= 228 * 1024, "residency");
 };
 
 // One warp per (KV head, run of p.tiles 16-block tiles, sequence).  A tile's 16
@@ -236,11 +242,11 @@ __global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) 
                 const uint4 a = lds128(base + 64 * j), b = lds128(base + 8 * C::kPitch + 64 * j);
                 mma16816a<kBF>(sa[0], a.x, b.x, a.y, b.y, qb[2 * j][0], qb[2 * j][1]);
                 mma16816a<kBF>(sa[1], a.z, b.z, a.w, b.w, qb[2 * j + 1][0], qb[2 * j + 1][1]);
-                big0 = abs_max2(abs_max2(abs_max2(abs_max2(big0, a.x), a.y), a.z), a.w);
-                big1 = abs_max2(abs_max2(abs_max2(abs_max2(big1, b.x), b.y), b.z), b.w);
+                big0 = abs_max2<T>(abs_max2<T>(abs_max2<T>(abs_max2<T>(big0, a.x), a.y), a.z), a.w);
+                big1 = abs_max2<T>(abs_max2<T>(abs_max2<T>(abs_max2<T>(big1, b.x), b.y), b.z), b.w);
             }
             const bool ok[2] = {(mask >> g8 & 1u) != 0u, (mask >> (g8 + 8) & 1u) != 0u};
-            const uint32_t big = abs_max2(ok[0] ? big0 : 0u, ok[1] ? big1 : 0u);
+            const uint32_t big = abs_max2<T>(ok[0] ? big0 : 0u, ok[1] ? big1 : 0u);
             float v[2];
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -283,7 +289,6 @@ constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 1024;
 constexpr int kSelNear = 256;  // blocks near the border that are ranked pair by pair
-constexpr int kSelAtOnce = 4;  // of them that a warp scores at once
 
 // Exclusive sum of v over the CTA's threads in order.
 __device__ __forceinline__ int cta_scan(int v, int* red) {
@@ -310,52 +315,89 @@ __device__ __forceinline__ uint64_t order64(double x) {
     return static_cast<uint64_t>(b) ^ (b < 0 ? ~0ull : 1ull << 63);
 }
 
-// The scores of blocks j[0 .. N) by one warp, in binary32 (A = float) or 64 bits.
-// Products of 16-bit values are exact in both; in 64 bits so are, but for
-// extreme ranges, their sums; in binary32 an element's sum takes at most D / 32 -
-// 1 + 5 = 8 additions, each within 2^-24 of the sum of magnitudes.  q: the G query
-// rows in shared memory.  A negative j gives -inf.
-template <int D, typename T, typename A, int N>
-__device__ __forceinline__ void warp_scores(const SelectParams& p, const float* q, int s, int h, const int (&j)[N],
-                                            A (&best)[N]) {
+// This lane's D / 32 channels of a block's bounds for KV head h, as binary32;
+// false for a negative j or a block id outside the pool.
+template <int D, typename T>
+__device__ __forceinline__ bool lane_bounds(const SelectParams& p, int s, int h, int j, float* lo, float* hi) {
     constexpr int V = D / 32;
-    using E = typename T::storage;
+    const int id = j >= 0 ? __ldg(p.block_tables + static_cast<int64_t>(s) * p.MB + j) : -1;
+    const bool ok = id >= 0 && id < p.NB;
+    const unsigned char* b =
+        p.bounds + (static_cast<int64_t>(ok ? id : 0) * p.Hkv + h) * (4 * D) + (threadIdx.x & 31) * (V * 2);
+    uint32_t w[2][V / 2];
+    load_words<V * 2>(b, w[0]);
+    load_words<V * 2>(b + 2 * D, w[1]);
+    Unpack<T, V>::run(w[0], lo);
+    Unpack<T, V>::run(w[1], hi);
+    return ok;
+}
+
+// The binary32 scores of four blocks by one warp; lane l gets that of block j[l / 8].
+// A lane's four (block, channel) strips against the eight query heads are 32 sums,
+// which one reduce-scatter (31 shuffles, not 5 a sum) leaves one a lane.  An
+// element's sum takes at most D / 32 - 1 + 5 = 8 additions of exact products, each
+// within 2^-24 of the sum of magnitudes.  q: the G query rows in shared memory.
+template <int D, typename T>
+__device__ __forceinline__ float four_scores(const SelectParams& p, const float* q, int s, int h, const int (&j)[4]) {
+    constexpr int V = D / 32;
     const int lane = threadIdx.x & 31;
-    E lo[N][V], hi[N][V];
-    bool ok[N];
+    float lo[4][V], hi[4][V], v[32];
+    bool ok = false;
 #pragma unroll
-    for (int n = 0; n < N; ++n) {
-        const int id = j[n] >= 0 ? __ldg(p.block_tables + static_cast<int64_t>(s) * p.MB + j[n]) : -1;
-        ok[n] = id >= 0 && id < p.NB;
-        const E* b = reinterpret_cast<const E*>(p.bounds) + (static_cast<int64_t>(ok[n] ? id : 0) * p.Hkv + h) * 2 * D + lane;
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            lo[n][i] = b[32 * i];
-            hi[n][i] = b[D + 32 * i];
-        }
-        best[n] = static_cast<A>(-INFINITY);
+    for (int n = 0; n < 4; ++n) {
+        const bool in = lane_bounds<D, T>(p, s, h, j[n], lo[n], hi[n]);
+        if ((lane >> 3) == n) ok = in;
     }
+#pragma unroll
+    for (int g = 0; g < 8; ++g) {
+#pragma unroll
+        for (int n = 0; n < 4; ++n) v[8 * n + g] = 0.f;
+        if (g < p.G) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const float x = q[g * D + lane * V + i];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) v[8 * n + g] = fmaf(x, x < 0.f ? lo[n][i] : hi[n][i], v[8 * n + g]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 16; m; m >>= 1) {
+        const bool upper = (lane & m) != 0;
+#pragma unroll
+        for (int k = 0; k < m; ++k) {
+            const float send = upper ? v[k] : v[k + m], keep = upper ? v[k + m] : v[k];
+            v[k] = keep + __shfl_xor_sync(kFull, send, m);
+        }
+    }
+    float best = (lane & 7) < p.G ? v[0] : -INFINITY;
+    if (!(best == best)) best = -INFINITY;  // NaN is dropped
+#pragma unroll
+    for (int m = 1; m < 8; m <<= 1) best = fmaxf(best, __shfl_xor_sync(kFull, best, m));
+    return ok ? best : -INFINITY;
+}
+
+// The score of block j in 64 bits, by one warp: products of 16-bit values are
+// exact, and so, but for extreme ranges, are their sums.
+template <int D, typename T>
+__device__ __forceinline__ double exact_score(const SelectParams& p, const float* q, int s, int h, int j) {
+    constexpr int V = D / 32;
+    const int lane = threadIdx.x & 31;
+    float lo[V], hi[V];
+    const bool ok = lane_bounds<D, T>(p, s, h, j, lo, hi);
+    double best = -HUGE_VAL;
     for (int g = 0; g < p.G; ++g) {
-        A sum[N];
-#pragma unroll
-        for (int n = 0; n < N; ++n) sum[n] = 0;
+        double sum = 0.0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const float x = q[g * D + lane + 32 * i];
-#pragma unroll
-            for (int n = 0; n < N; ++n)
-                sum[n] += static_cast<A>(x) * static_cast<A>(to_float(x < 0.f ? lo[n][i] : hi[n][i]));
+            const float x = q[g * D + lane * V + i];
+            sum += static_cast<double>(x) * static_cast<double>(x < 0.f ? lo[i] : hi[i]);
         }
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-#pragma unroll
-            for (int m = 16; m; m >>= 1) sum[n] += __shfl_xor_sync(kFull, sum[n], m);
-            if (sum[n] > best[n]) best[n] = sum[n];  // NaN is dropped
-        }
+        for (int m = 16; m; m >>= 1) sum += __shfl_xor_sync(kFull, sum, m);
+        if (sum > best) best = sum;  // NaN is dropped
     }
-#pragma unroll
-    for (int n = 0; n < N; ++n)
-        if (!ok[n]) best[n] = static_cast<A>(-INFINITY);
+    return ok ? best : -HUGE_VAL;
 }
 
 // One CTA per (KV head, sequence): the n blocks of the highest scores, in
@@ -375,9 +417,9 @@ __device__ __forceinline__ void warp_scores(const SelectParams& p, const float* 
 // binary32 sums.
 template <int D, typename T>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-    extern __shared__ float row_smem[];
+    extern __shared__ __align__(16) float row_smem[];
     __shared__ int hist[kSelBins];
-    __shared__ float qs[8 * D];
+    __shared__ __align__(16) float qs[8 * D];
     __shared__ float redf[4][kSelWarps];
     __shared__ int redi[kSelWarps];
     __shared__ int near_id[kSelNear];
@@ -420,12 +462,20 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     const bool in_smem = nblk <= p.smem_cols;
     float a = INFINITY, b = -INFINITY, big = 0.f;
     if (in_smem) {
-        for (int i = tid; i < nblk; i += kSelThreads) {
-            const float x = sc[i];
-            row_smem[i] = x;
-            if (i >= f0 && i < f1) {
-                if (x > -INFINITY) a = fminf(a, x);
-                b = fmaxf(b, x);
+        // columns past nblk up to the next tile's end are written too (-inf)
+        const float4* src = reinterpret_cast<const float4*>(sc);
+        float4* dst = reinterpret_cast<float4*>(row_smem);
+        const int quads = (nblk + 3) / 4;
+#pragma unroll 4
+        for (int i = tid; i < quads; i += kSelThreads) {
+            const float4 v = src[i];
+            dst[i] = v;
+            const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = 4 * i + e >= f0 && 4 * i + e < f1;
+                if (in && x[e] > -INFINITY) a = fminf(a, x[e]);
+                if (in) b = fmaxf(b, x[e]);
             }
         }
         sc = row_smem;
@@ -471,6 +521,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
                 __syncthreads();
             }
             int over = 0;  // blocks known to score over b
+#pragma unroll 4
             for (int i = f0 + tid; i < f1; i += kSelThreads) {
                 const float x = sc[i];
                 if (x > b)
@@ -521,6 +572,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         }
         // ---- sure of being in, and the band
         int sure = 0;
+#pragma unroll 4
         for (int i = f0 + tid; i < f1; i += kSelThreads) {
             const float x = sc[i];
             if (x > thr) {
@@ -550,15 +602,12 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             }
         } else if (listed) {
             // binary32 first, each within 8 * 2^-24 A: twice that and its double is eps2 / 64
-            for (int i = warp; i < band; i += kSelWarps * kSelAtOnce) {
-                int j[kSelAtOnce];
-                float y[kSelAtOnce];
+            for (int i = 4 * warp; i < band; i += 4 * kSelWarps) {
+                int j[4];
 #pragma unroll
-                for (int u = 0; u < kSelAtOnce; ++u) j[u] = i + u * kSelWarps < band ? near_id[i + u * kSelWarps] : -1;
-                warp_scores<D, T, float>(p, qs, s, h, j, y);
-#pragma unroll
-                for (int u = 0; u < kSelAtOnce; ++u)
-                    if (lane == 0 && j[u] >= 0) near_f[i + u * kSelWarps] = y[u];
+                for (int u = 0; u < 4; ++u) j[u] = i + u < band ? near_id[i + u] : -1;
+                const float y = four_scores<D, T>(p, qs, s, h, j);
+                if ((lane & 7) == 0 && i + (lane >> 3) < band) near_f[i + (lane >> 3)] = y;
             }
             if (tid == 0) sh[3] = sh[2] = 0;
             __syncthreads();
@@ -581,10 +630,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             const int ties = sh[3], left = want - sh[2];
             if (ties > 0) {  // the few that binary32 cannot order: 64 bits
                 for (int i = warp; i < ties; i += kSelWarps) {
-                    const int j[1] = {near_id[tie[i]]};
-                    double y[1];
-                    warp_scores<D, T, double>(p, qs, s, h, j, y);
-                    if (lane == 0) near_y[i] = y[0];
+                    const double y = exact_score<D, T>(p, qs, s, h, near_id[tie[i]]);
+                    if (lane == 0) near_y[i] = y;
                 }
                 __syncthreads();
                 for (int i = tid; i < ties; i += kSelThreads) {
@@ -602,10 +649,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             for (int i = f0 + warp; i < f1; i += kSelWarps) {
                 const float x = sc[i];
                 if (!(x <= thr && x >= low)) continue;
-                const int j[1] = {i};
-                double y[1];
-                warp_scores<D, T, double>(p, qs, s, h, j, y);
-                if (lane == 0) ex[i] = y[0];
+                const double y = exact_score<D, T>(p, qs, s, h, i);
+                if (lane == 0) ex[i] = y;
             }
             __syncthreads();
             uint64_t prefix = 0, mask = 0;
@@ -655,6 +700,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     const int groups = ((nblk + 31) / 32 + kSelWarps - 1) / kSelWarps;
     const int g0 = warp * groups;
     int mine = 0;
+#pragma unroll 4
     for (int g = g0; g < g0 + groups && g * 32 < nblk; ++g) mine += __popc(__ballot_sync(kFull, kept(g * 32 + lane)));
     if (lane == 0) redi[warp] = mine;
     __syncthreads();
@@ -662,6 +708,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
 #pragma unroll
     for (int w = 0; w < kSelWarps; ++w)
         if (w < warp) at += redi[w];
+#pragma unroll 4
     for (int g = g0; g < g0 + groups && g * 32 < nblk; ++g) {
         const bool keep = kept(g * 32 + lane);
         const uint32_t votes = __ballot_sync(kFull, keep);
@@ -837,8 +884,10 @@ extern "C" pkv_status pkv_select_blocks(const void* q, int32_t q_dtype, int32_t 
     p.sink = sink_blocks;
     p.recent = recent_blocks;
     // tiles a warp takes in a run: the number whose whole rounds of resident CTAs
-    // (two an SM, four warps each) cost least, a run's start counted as three tiles
-    const int64_t row_tiles = l.cols / 16, slots = 2 * static_cast<int64_t>(num_sms());
+    // cost least, a run's start counted as three tiles
+    const int64_t row_tiles = l.cols / 16;
+    const int64_t slots = (d->head_size == 128 ? ScoreCfg<128>::kCtasPerSm : ScoreCfg<64>::kCtasPerSm) *
+                          static_cast<int64_t>(num_sms());
     int64_t best = INT64_MAX;
     for (int run = 1; run <= 64; ++run) {
         const int64_t ctas = cdiv(cdiv(row_tiles, run) * p.Hkv, 4) * p.S, cost = cdiv(ctas, slots) * (run + 3);
