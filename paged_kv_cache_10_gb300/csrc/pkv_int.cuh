@@ -90,6 +90,21 @@ __device__ __forceinline__ void int_load8(const unsigned char* tile, bool value,
     }
 }
 
+// x / (2^BITS - 1), correctly rounded, for x >= 0: with y the correctly rounded
+// reciprocal of the divisor, q = rn(x y) is within an ulp, the remainder r = x -
+// q (2^BITS - 1) is exact in a fused multiply-add, and rn(q + r y) is the rounded
+// quotient (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990).  Outside the range where no step can
+// underflow or overflow, the division itself.
+template <int BITS>
+__device__ __forceinline__ float div_const(float x) {
+    constexpr float d = BITS == 8 ? 255.f : 15.f;
+    constexpr float y = 1.f / d;
+    if (!(x > 0x1p-90f && x < 0x1p120f)) return __fdiv_rn(x, d);
+    const float q = __fmul_rn(x, y);
+    return __fmaf_rn(__fmaf_rn(-q, d, x), y, q);
+}
+
 // Eight 16-bit elements of a row held by the D / 8 consecutive lanes of a group
 // to code bytes: w receives the lane's, in order; (scale, zero) is the row's.
 // Every lane of the warp takes part in the shuffles.  The extrema are found on
@@ -110,10 +125,9 @@ __device__ __forceinline__ float2 int_encode8(uint4 x, uint32_t* w) {
         key = __hmin2(key, *reinterpret_cast<const P2*>(&o));
     }
     const float lo = to_float(key.x), hi = -to_float(key.y);
-    constexpr float top = BITS == 8 ? 255.f : 15.f;
-    float scale = __fdiv_rn(__fsub_rn(hi, lo), top);
+    float scale = div_const<BITS>(__fsub_rn(hi, lo));
     if (!(scale >= 0x1p-126f)) scale = 0.f;
-    const float inv = scale > 0.f ? __fdiv_rn(1.f, scale) : 0.f;
+    const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
     float f[8];
     Unpack<IT, 8>::run(xw, f);
     // rint by adding 2^23 (round to nearest, ties to even, like rint): the code is

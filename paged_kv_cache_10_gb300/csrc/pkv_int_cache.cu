@@ -62,8 +62,9 @@ __global__ void __launch_bounds__(256) append_int_kernel(const uint4* __restrict
         uint32_t w[2];
         const float2 sz = int_encode8<D, BITS, IT>(x, w);
         if (slot >= 0) {
-            unsigned char* tile = pool + (slot / kBlockSize * heads.d + h) * L::kBytes;
-            int_store8<D, BITS>(tile, value, static_cast<int>(slot % kBlockSize), c, w, sz);
+            // tiles of a pool count below 2^32
+            const uint32_t tile = static_cast<uint32_t>(slot >> 4) * heads.d + h;
+            int_store8<D, BITS>(pool + static_cast<uint64_t>(tile) * L::kBytes, value, static_cast<int>(slot) & 15, c, w, sz);
         }
     }
 }
@@ -89,9 +90,9 @@ __global__ void __launch_bounds__(256) read_kernel(const unsigned char* __restri
             if (h == 0 && c == 0 && !value) report(err, PKV_DEVERR_SLOT);
             continue;
         }
-        const unsigned char* tile = pool + (slot / kBlockSize * heads.d + h) * PoolRow<D, KV>::kTile;
+        const uint32_t tile = static_cast<uint32_t>(slot >> 4) * heads.d + h;  // below 2^32
         float f[8];
-        PoolRow<D, KV>::load(tile, value, static_cast<int>(slot % kBlockSize), c, scale, f);
+        PoolRow<D, KV>::load(pool + tile * PoolRow<D, KV>::kTile, value, static_cast<int>(slot) & 15, c, scale, f);
         out[static_cast<int64_t>(row) * LPR + c] = pack8<OT>(f);
     }
 }

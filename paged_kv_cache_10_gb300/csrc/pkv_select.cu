@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) 
 
 // -------------------------------------------------------------- selection
 constexpr int kSelThreads = 256;
+constexpr int kSmemCols = 16384;  // 64 KiB of a row's scores; longer rows stay in the workspace
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 1024;
 constexpr int kSelNear = 256;  // blocks near the border that are ranked pair by pair
@@ -722,17 +723,22 @@ template <int D, typename T>
 cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
     const int64_t units = static_cast<int64_t>((p.cols / 16 + p.tiles - 1) / p.tiles) * p.Hkv;
     constexpr int kScoreSmem = ScoreCfg<D>::kBytes;
-    cudaError_t e = cudaFuncSetAttribute(block_score_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+    static bool configured[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(block_score_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(select_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemCols * 4);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
     block_score_kernel<D, T><<<dim3(static_cast<unsigned>((units + 3) / 4), p.S), 128, kScoreSmem, st>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const size_t smem = static_cast<size_t>(p.smem_cols) * 4;
-    if (smem > 24 * 1024) {  // with the static arrays, more than a launch gets unasked
-        e = cudaFuncSetAttribute(select_kernel<D, T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 static_cast<int>(smem));
-        if (e != cudaSuccess) return e;
-    }
     return launch_maybe_pdl(true, select_kernel<D, T>, dim3(p.Hkv, p.S), dim3(kSelThreads), smem, st, p);
 }
 
@@ -896,7 +902,6 @@ extern "C" pkv_status pkv_select_blocks(const void* q, int32_t q_dtype, int32_t 
             p.tiles = run;
         }
     }
-    constexpr int kSmemCols = 16384;  // 64 KiB; longer rows stay in the workspace
     p.smem_cols = static_cast<int>(std::min<int64_t>(l.cols, kSmemCols));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool bf = q_dtype == PKV_BF16;

@@ -215,12 +215,22 @@ def _desc(d: CacheDesc):
     return r
 
 
-def _on_current_device(*tensors) -> None:
-    """The launch goes to the current device: a tensor of another one is refused."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != cur and t.is_cuda:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{cur}")
+_I32, _I64 = torch.int32, torch.int64
+
+
+def _here(t: torch.Tensor, name: str, dev: int) -> int:
+    """Data pointer of a contiguous tensor on the current device (the launch goes there)."""
+    if t.get_device() != dev:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _stream_on(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
 
 
 def _shape(t: torch.Tensor, want: tuple, name: str) -> None:
@@ -228,10 +238,19 @@ def _shape(t: torch.Tensor, want: tuple, name: str) -> None:
         raise ValueError(f"{name} must have shape {list(want)}, not {list(t.shape)}")
 
 
-def _pool_ptr(t: torch.Tensor, desc: CacheDesc, name: str) -> int:
-    if t.numel() * t.element_size() != _desc(desc)[1]:
+def _pool(t: torch.Tensor, desc: CacheDesc, nbytes: int, name: str, dev: int) -> int:
+    if t.nbytes != nbytes:
         raise ValueError(f"{name} must hold {desc.num_blocks} blocks of {block_bytes(desc)} bytes")
-    return _dev_ptr(t, name)
+    return _here(t, name, dev)
+
+
+def _int_pools(desc: CacheDesc, *pools) -> None:
+    """An int8 / int4 pool's rows carry parameters behind the codes: a tensor without room for them is refused."""
+    if desc.kv_dtype in ("int8", "int4"):
+        nbytes = _desc(desc)[1]
+        for t in pools:
+            if t.nbytes != nbytes:
+                raise ValueError(f"an {desc.kv_dtype} pool must hold {desc.num_blocks} blocks of {block_bytes(desc)} bytes")
 
 
 def block_bytes(desc: CacheDesc) -> int:
@@ -247,6 +266,7 @@ def paged_kv_append(k, v, slot_mapping, k_cache, v_cache, desc: CacheDesc, in_dt
     T = int(slot_mapping.shape[0])
     if slot_mapping.dtype != torch.int64:
         raise TypeError("slot_mapping must be int64")
+    _int_pools(desc, k_cache, v_cache)
     st = lib().pkv_paged_kv_append(_dev_ptr(k, "k"), _dev_ptr(v, "v"), _dtype_code(k, in_dtype), T,
                                    _dev_ptr(slot_mapping, "slot_mapping"), _dev_ptr(k_cache, "k_cache"),
                                    _dev_ptr(v_cache, "v_cache"), _desc(desc)[0], _stream(stream))
@@ -257,18 +277,19 @@ def paged_kv_read(slot_mapping, k_cache, v_cache, desc: CacheDesc, k_out, v_out,
                   stream=None) -> None:
     """Cached rows by slot, as 16-bit values: k_out, v_out [T, Hkv, D]; slot_mapping int64 [T] (device); the
     output rows of negative slots stay as they are."""
-    T = int(slot_mapping.shape[0])
-    if slot_mapping.dtype != torch.int64:
+    T = slot_mapping.shape[0]
+    if slot_mapping.dtype != _I64:
         raise TypeError("slot_mapping must be int64")
-    for o, n in ((k_out, "k_out"), (v_out, "v_out")):
-        _shape(o, (T, desc.num_kv_heads, desc.head_size), n)
+    want = (T, desc.num_kv_heads, desc.head_size)
+    _shape(k_out, want, "k_out")
+    _shape(v_out, want, "v_out")
     if k_out.element_size() != 2 or v_out.dtype != k_out.dtype:
         raise TypeError("k_out and v_out must be of one 16-bit type")
-    _on_current_device(slot_mapping, k_cache, v_cache, k_out, v_out)
-    st = lib().pkv_paged_kv_read(_dev_ptr(slot_mapping, "slot_mapping"), T, _pool_ptr(k_cache, desc, "k_cache"),
-                                 _pool_ptr(v_cache, desc, "v_cache"), _desc(desc)[0],
-                                 _dev_ptr(k_out, "k_out"), _dev_ptr(v_out, "v_out"), _dtype_code(k_out, out_dtype),
-                                 _stream(stream))
+    dev = torch.cuda.current_device()
+    ref, nbytes = _desc(desc)
+    st = lib().pkv_paged_kv_read(_here(slot_mapping, "slot_mapping", dev), T, _pool(k_cache, desc, nbytes, "k_cache", dev),
+                                 _pool(v_cache, desc, nbytes, "v_cache", dev), ref, _here(k_out, "k_out", dev),
+                                 _here(v_out, "v_out", dev), _dtype_code(k_out, out_dtype), _stream_on(stream, dev))
     _check(st, "paged_kv_read")
 
 
@@ -277,6 +298,7 @@ def copy_blocks(k_cache, v_cache, desc: CacheDesc, pairs, num_pairs: int | None 
     n = int(pairs.shape[0]) if num_pairs is None else int(num_pairs)
     if pairs.dtype != torch.int32:
         raise TypeError("pairs must be int32")
+    _int_pools(desc, k_cache, v_cache)
     st = lib().pkv_copy_blocks(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _desc(desc)[0],
                                _dev_ptr(pairs, "pairs") if n > 0 else None, n, _stream(stream))
     _check(st, "copy_blocks")
@@ -302,6 +324,7 @@ def paged_attention_decode(q, k_cache, v_cache, desc: CacheDesc, block_tables, s
     S, Hq = int(q.shape[0]), int(q.shape[1])
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise TypeError("block_tables and seq_lens must be int32")
+    _int_pools(desc, k_cache, v_cache)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_ptr, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
@@ -350,6 +373,7 @@ def paged_attention_decode_noalloc(q, k_cache, v_cache, desc: CacheDesc, block_t
     S, Hq = int(q.shape[0]), int(q.shape[1])
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise TypeError("block_tables and seq_lens must be int32")
+    _int_pools(desc, k_cache, v_cache)
     st = lib().pkv_paged_attention_decode_noalloc(_dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq,
                                                   _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
                                                   _desc(desc)[0], _dev_ptr(block_tables, "block_tables"),
@@ -428,24 +452,36 @@ def paged_key_bounds(k_cache, desc: CacheDesc, block_tables, seq_lens, new_lens,
                      bounds_dtype: str | None = None, stream=None) -> None:
     """Channelwise minimum and maximum of the keys of every block that holds one of a sequence's last
     new_lens[s] tokens (int32 [S], device; None: all its tokens): bounds [NB, Hkv, 2, D], row 0 the minimum."""
-    S = int(seq_lens.shape[0])
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+    S = seq_lens.shape[0]
+    if block_tables.dtype != _I32 or seq_lens.dtype != _I32:
         raise TypeError("block_tables and seq_lens must be int32")
-    if new_lens is not None and (new_lens.dtype != torch.int32 or int(new_lens.shape[0]) != S):
+    if new_lens is not None and (new_lens.dtype != _I32 or new_lens.shape[0] != S):
         raise ValueError("new_lens must be int32 with one entry per sequence")
-    if int(block_tables.shape[0]) != S:
+    rows, MB = block_tables.shape
+    if rows != S:
         raise ValueError("block_tables must have one row per sequence")
     _shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_size), "bounds")
     if bounds.element_size() != 2:
         raise TypeError("bounds must be of a 16-bit type")
-    _on_current_device(k_cache, block_tables, seq_lens, new_lens, bounds)
-    st = lib().pkv_paged_key_bounds(_pool_ptr(k_cache, desc, "k_cache"), _desc(desc)[0],
-                                    _dev_ptr(block_tables, "block_tables"), int(block_tables.shape[1]),
-                                    _dev_ptr(seq_lens, "seq_lens"),
-                                    _dev_ptr(new_lens, "new_lens") if new_lens is not None else None,
-                                    int(max_new_len), S, _dev_ptr(bounds, "bounds"),
-                                    _dtype_code(bounds, bounds_dtype), _stream(stream))
+    dev = torch.cuda.current_device()
+    ref, nbytes = _desc(desc)
+    st = lib().pkv_paged_key_bounds(_pool(k_cache, desc, nbytes, "k_cache", dev), ref,
+                                    _here(block_tables, "block_tables", dev), MB, _here(seq_lens, "seq_lens", dev),
+                                    _here(new_lens, "new_lens", dev) if new_lens is not None else None,
+                                    max_new_len, S, _here(bounds, "bounds", dev), _dtype_code(bounds, bounds_dtype),
+                                    _stream_on(stream, dev))
     _check(st, "paged_key_bounds")
+
+
+def _lists(selected, block_tables, seq_lens, S: int, D: int, desc: CacheDesc) -> int:
+    """Checks the shapes that selection and sparse decode share; the entries of a list."""
+    if D != desc.head_size:
+        raise ValueError("q must have the cache's head_size")
+    if selected.dim() != 3 or selected.shape[:2] != (S, desc.num_kv_heads):
+        raise ValueError("selected must have shape [num_seqs, num_kv_heads, n]")
+    if block_tables.shape[0] != S or seq_lens.shape[0] != S:
+        raise ValueError("block_tables and seq_lens must have one row per sequence")
+    return selected.shape[2]
 
 
 def select_blocks_workspace_bytes(num_seqs: int, num_kv_heads: int, max_seq_len: int) -> int:
@@ -456,24 +492,19 @@ def select_blocks(q, bounds, desc: CacheDesc, block_tables, seq_lens, max_seq_le
                   sink_blocks: int = 1, recent_blocks: int = 1, q_dtype: str | None = None, stream=None) -> None:
     """The blocks each (sequence, KV head) attends to: q [S, Hq, D], bounds [NB, Hkv, 2, D] of q's type,
     selected int32 [S, Hkv, n] (logical block numbers, ascending, then -1)."""
-    S, Hq = int(q.shape[0]), int(q.shape[1])
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or selected.dtype != torch.int32:
+    S, Hq, D = q.shape
+    if block_tables.dtype != _I32 or seq_lens.dtype != _I32 or selected.dtype != _I32:
         raise TypeError("block_tables, seq_lens and selected must be int32")
     if bounds.dtype != q.dtype:
         raise TypeError("bounds must have q's type")
-    _shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_size), "bounds")
-    _shape(q, (S, Hq, desc.head_size), "q")
-    if selected.dim() != 3 or tuple(selected.shape[:2]) != (S, desc.num_kv_heads):
-        raise ValueError("selected must have shape [num_seqs, num_kv_heads, n]")
-    if int(block_tables.shape[0]) != S or int(seq_lens.shape[0]) != S:
-        raise ValueError("block_tables and seq_lens must have one row per sequence")
-    _on_current_device(q, bounds, block_tables, seq_lens, selected, workspace)
-    st = lib().pkv_select_blocks(_dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq, _dev_ptr(bounds, "bounds"),
-                                 _desc(desc)[0], _dev_ptr(block_tables, "block_tables"),
-                                 int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"), int(max_seq_len),
-                                 int(selected.shape[2]), int(sink_blocks), int(recent_blocks),
-                                 _dev_ptr(selected, "selected"), _dev_ptr(workspace, "workspace"),
-                                 workspace.numel() * workspace.element_size(), _stream(stream))
+    n = _lists(selected, block_tables, seq_lens, S, D, desc)
+    _shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, D), "bounds")
+    dev = torch.cuda.current_device()
+    st = lib().pkv_select_blocks(_here(q, "q", dev), _dtype_code(q, q_dtype), S, Hq, _here(bounds, "bounds", dev),
+                                 _desc(desc)[0], _here(block_tables, "block_tables", dev), block_tables.shape[1],
+                                 _here(seq_lens, "seq_lens", dev), max_seq_len, n, sink_blocks, recent_blocks,
+                                 _here(selected, "selected", dev), _here(workspace, "workspace", dev),
+                                 workspace.nbytes, _stream_on(stream, dev))
     _check(st, "select_blocks")
 
 
@@ -488,27 +519,20 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, desc: CacheDesc, block_ta
                                   q_dtype: str | None = None, stream=None) -> None:
     """Decode attention over the blocks that selected (int32 [S, Hkv, n], as select_blocks writes it) names:
     q, out [S, Hq, D]."""
-    S, Hq = int(q.shape[0]), int(q.shape[1])
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32 or selected.dtype != torch.int32:
+    S, Hq, D = q.shape
+    if block_tables.dtype != _I32 or seq_lens.dtype != _I32 or selected.dtype != _I32:
         raise TypeError("block_tables, seq_lens and selected must be int32")
-    _shape(q, (S, Hq, desc.head_size), "q")
-    _shape(out, (S, Hq, desc.head_size), "out")
-    if out.dtype != q.dtype:
-        raise TypeError("out must have q's type")
-    if selected.dim() != 3 or tuple(selected.shape[:2]) != (S, desc.num_kv_heads):
-        raise ValueError("selected must have shape [num_seqs, num_kv_heads, n]")
-    if int(block_tables.shape[0]) != S or int(seq_lens.shape[0]) != S:
-        raise ValueError("block_tables and seq_lens must have one row per sequence")
-    _on_current_device(q, k_cache, v_cache, block_tables, seq_lens, selected, out, workspace)
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        ws_ptr, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    if out.dtype != q.dtype or out.shape != q.shape:
+        raise ValueError("out must have q's shape and type")
+    n = _lists(selected, block_tables, seq_lens, S, D, desc)
+    dev = torch.cuda.current_device()
+    ref, nbytes = _desc(desc)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (_here(workspace, "workspace", dev), workspace.nbytes)
     st = lib().pkv_paged_attention_decode_sparse(
-        _dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq, _pool_ptr(k_cache, desc, "k_cache"),
-        _pool_ptr(v_cache, desc, "v_cache"), _desc(desc)[0], _dev_ptr(block_tables, "block_tables"),
-        int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(selected, "selected"),
-        int(selected.shape[2]), float(scale), _dev_ptr(out, "out"), ws_ptr, ws_bytes, int(partition_blocks),
-        _stream(stream))
+        _here(q, "q", dev), _dtype_code(q, q_dtype), S, Hq, _pool(k_cache, desc, nbytes, "k_cache", dev),
+        _pool(v_cache, desc, nbytes, "v_cache", dev), ref, _here(block_tables, "block_tables", dev),
+        block_tables.shape[1], _here(seq_lens, "seq_lens", dev), _here(selected, "selected", dev), n, scale,
+        _here(out, "out", dev), ws_ptr, ws_bytes, partition_blocks, _stream_on(stream, dev))
     _check(st, "paged_attention_decode_sparse")
 
 
@@ -559,6 +583,7 @@ def paged_attention_prefill(q, k_cache, v_cache, desc: CacheDesc, query_start, m
     S = int(seq_lens.shape[0])
     if int(query_start.shape[0]) != S + 1:
         raise ValueError("query_start must have num_seqs + 1 entries")
+    _int_pools(desc, k_cache, v_cache)
     nw = 0 if work_units is None else int(work_units.numel())
     wp = _dev_ptr(work_units, "work_units") if nw else None
     ws_ptr, ws_bytes = None, 0
@@ -629,6 +654,7 @@ def swap_blocks(k_cache, v_cache, desc: CacheDesc, k_host, v_host, pairs, direct
     for t, n in ((k_host, "k_host"), (v_host, "v_host")):
         if t.is_cuda or not t.is_pinned() or not t.is_contiguous():
             raise ValueError(f"{n} must be a contiguous pinned CPU tensor")
+    _int_pools(desc, k_cache, v_cache)
     n = int(pairs.shape[0])
     st = lib().pkv_swap_blocks(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _desc(desc)[0],
                                k_host.data_ptr(), v_host.data_ptr(), int(k_host.shape[0]),
