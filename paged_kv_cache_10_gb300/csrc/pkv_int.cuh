@@ -55,11 +55,15 @@ __device__ __forceinline__ void int_value4(uint32_t w, float2 sz, float* f, int 
         f[i * step] = fmaf(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7440 | i)) - 8388608.f, sz.x, sz.y);
 }
 
-// Eight elements 8 * c .. 8 * c + 7 of token t of a tile in global memory.
+// Eight elements 8 * c .. 8 * c + 7 of token t of a tile in global memory, with the
+// row's (scale, zero) sz.
 template <int D, int BITS>
-__device__ __forceinline__ void int_load8(const unsigned char* tile, bool value, int t, int c, float* f) {
+__device__ __forceinline__ float2 int_params(const unsigned char* tile, int t) {
+    return *reinterpret_cast<const float2*>(tile + IntTile<D, BITS>::param(t));
+}
+template <int D, int BITS>
+__device__ __forceinline__ void int_load8(const unsigned char* tile, bool value, int t, int c, float2 sz, float* f) {
     using L = IntTile<D, BITS>;
-    const float2 sz = *reinterpret_cast<const float2*>(tile + L::param(t));
     uint32_t w[BITS / 4];  // the 8 elements' code bytes, in order
     if (!value) {
         const unsigned char* p = tile + L::key(t, c * BITS);
@@ -80,10 +84,8 @@ __device__ __forceinline__ void int_load8(const unsigned char* tile, bool value,
         }
     }
     if constexpr (BITS == 4) {
-        const uint32_t x = w[0];
-        uint32_t lo = x & 0x0f0f0f0fu, hi = (x >> 4) & 0x0f0f0f0fu;
-        int_value4(lo, sz, f, 2);
-        int_value4(hi, sz, f + 1, 2);
+        int_value4(w[0] & 0x0f0f0f0fu, sz, f, 2);
+        int_value4((w[0] >> 4) & 0x0f0f0f0fu, sz, f + 1, 2);
     } else {
         int_value4(w[0], sz, f, 1);
         int_value4(w[1], sz, f + 4, 1);
@@ -105,22 +107,27 @@ __device__ __forceinline__ float div_const(float x) {
     return __fmaf_rn(__fmaf_rn(-q, d, x), y, q);
 }
 
-// Eight 16-bit elements of a row held by the D / 8 consecutive lanes of a group
-// to code bytes: w receives the lane's, in order; (scale, zero) is the row's.
-// Every lane of the warp takes part in the shuffles.  The extrema are found on
-// 16-bit pairs, (min, -max) in one register from the first shuffle on.
+// A row held by D / 16 consecutive lanes, two 16-byte vectors of eight 16-bit
+// elements each, to code bytes: w[i] receives those of vector i, in order; (scale,
+// zero) is the row's.  Every lane of the warp takes part in the shuffles.  The
+// extrema are found on 16-bit pairs, (min, -max) in one register from the first
+// shuffle on.
 template <int D, int BITS, typename IT>
-__device__ __forceinline__ float2 int_encode8(uint4 x, uint32_t* w) {
+__device__ __forceinline__ float2 int_encode16(const uint4 (&x)[2], uint32_t (&w)[2][2]) {
     using P2 = typename std::conditional<std::is_same<IT, BF16>::value, __nv_bfloat162, __half2>::type;
-    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-    const P2* v = reinterpret_cast<const P2*>(xw);
-    const P2 mn = __hmin2(__hmin2(v[0], v[1]), __hmin2(v[2], v[3]));
-    const P2 mx = __hmax2(__hmax2(v[0], v[1]), __hmax2(v[2], v[3]));
+    const uint32_t xw[2][4] = {{x[0].x, x[0].y, x[0].z, x[0].w}, {x[1].x, x[1].y, x[1].z, x[1].w}};
+    const P2* v = reinterpret_cast<const P2*>(&xw[0][0]);
+    P2 mn = v[0], mx = v[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        mn = __hmin2(mn, v[i]);
+        mx = __hmax2(mx, v[i]);
+    }
     P2 key;
     key.x = __hmin(mn.x, mn.y);
     key.y = __hneg(__hmax(mx.x, mx.y));
 #pragma unroll
-    for (int m = 1; m < D / 8; m <<= 1) {
+    for (int m = 1; m < D / 16; m <<= 1) {
         const uint32_t o = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&key), m);
         key = __hmin2(key, *reinterpret_cast<const P2*>(&o));
     }
@@ -128,31 +135,33 @@ __device__ __forceinline__ float2 int_encode8(uint4 x, uint32_t* w) {
     float scale = div_const<BITS>(__fsub_rn(hi, lo));
     if (!(scale >= 0x1p-126f)) scale = 0.f;
     const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
-    float f[8];
-    Unpack<IT, 8>::run(xw, f);
     // rint by adding 2^23 (round to nearest, ties to even, like rint): the code is
     // the sum's low bits.  (x - lo) * inv <= top (1 + 2^-22), so no code passes top.
-    uint32_t c[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-        c[e] = __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(f[e], lo), inv), 8388608.f));
-    if constexpr (BITS == 8) {
+    for (int r = 0; r < 2; ++r) {
+        float f[8];
+        Unpack<IT, 8>::run(xw[r], f);
+        uint32_t c[8];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            w[i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040), __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040),
-                               0x5410);
-    } else {
+        for (int e = 0; e < 8; ++e)
+            c[e] = __float_as_uint(__fadd_rn(__fmul_rn(__fsub_rn(f[e], lo), inv), 8388608.f));
+        if constexpr (BITS == 8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) c[i] = c[2 * i] + (c[2 * i + 1] << 4);  // low byte: both codes
-        w[0] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+            for (int i = 0; i < 2; ++i)
+                w[r][i] = __byte_perm(__byte_perm(c[4 * i], c[4 * i + 1], 0x0040),
+                                      __byte_perm(c[4 * i + 2], c[4 * i + 3], 0x0040), 0x5410);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) c[i] = c[2 * i] + (c[2 * i + 1] << 4);  // low byte: both codes
+            w[r][0] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+        }
     }
     return make_float2(scale, lo);
 }
 
-// Stores the lane's code bytes of int_encode8 (elements 8c .. 8c + 7) and, from
-// the group's first lane, the row's parameters.
+// Stores the code bytes of elements 8c .. 8c + 7.
 template <int D, int BITS>
-__device__ __forceinline__ void int_store8(unsigned char* tile, bool value, int t, int c, const uint32_t* w, float2 sz) {
+__device__ __forceinline__ void int_store8(unsigned char* tile, bool value, int t, int c, const uint32_t* w) {
     using L = IntTile<D, BITS>;
     if (!value) {
         unsigned char* p = tile + L::key(t, c * BITS);
@@ -168,7 +177,6 @@ __device__ __forceinline__ void int_store8(unsigned char* tile, bool value, int 
             *reinterpret_cast<uint16_t*>(p + 8 * i + 4) = static_cast<uint16_t>(w[i] >> 16);
         }
     }
-    if (c == 0) *reinterpret_cast<float2*>(tile + L::param(t)) = sz;
 }
 
 // Calls fn(IntTile<D, BITS>) for an integer pool type and head size.

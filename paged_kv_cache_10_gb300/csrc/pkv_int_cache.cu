@@ -3,9 +3,10 @@
 // pool type), and the 16-bit copy of integer-coded blocks that prefill reads.
 //
 // All three are bound by HBM: they move 16-byte vectors of 16-bit values on
-// one side and a lane's 4 to 8 code bytes on the other.  D / 8 consecutive
-// lanes hold a row, eight elements each, so a row's minimum and maximum are
-// 3 or 4 shuffle steps and no shared memory is used.
+// one side and a lane's 4 to 8 code bytes on the other.  D / 16 consecutive
+// lanes hold a row, two vectors of eight elements each (vectors c and c + D / 16, so
+// that a row's loads and stores stay contiguous over its lanes), so a row's
+// minimum and maximum are 2 or 3 shuffle steps and no shared memory is used.
 #include <cstdint>
 
 #include "pkv_append.cuh"
@@ -28,7 +29,7 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, RowDiv v) {
     return static_cast<uint32_t>((static_cast<uint64_t>(n) * v.mul) >> v.shift);
 }
 
-// Append into an integer-coded pool: one group of D / 8 lanes per row (t, h),
+// Append into an integer-coded pool: one group of D / 16 lanes per row (t, h),
 // blockIdx.y = 0 keys, 1 values.  Lanes of a warp whose row is padding or out
 // of range still take part in the group's shuffles.
 template <int D, int BITS, typename IT>
@@ -37,7 +38,7 @@ __global__ void __launch_bounds__(256) append_int_kernel(const uint4* __restrict
                                                          unsigned char* vc, uint32_t rows, RowDiv heads,
                                                          int64_t num_slots, unsigned int* err) {
     using L = IntTile<D, BITS>;
-    constexpr int LPR = D / 8, RPC = 256 / LPR;  // lanes of a row, rows of a CTA
+    constexpr int LPR = D / 16, RPC = 256 / LPR;  // lanes of a row, rows of a CTA
     const bool value = blockIdx.y != 0;
     const uint4* src = value ? v : k;
     unsigned char* pool = value ? vc : kc;
@@ -47,36 +48,42 @@ __global__ void __launch_bounds__(256) append_int_kernel(const uint4* __restrict
     for (uint32_t base = blockIdx.x * RPC; base < rows; base += gridDim.x * RPC) {
         const uint32_t row = base + threadIdx.x / LPR;
         int64_t slot = -1;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        uint4 x[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
         uint32_t h = 0;
         if (row < rows) {
             const uint32_t t = quotient(row, heads);
             h = row - t * heads.d;
-            x = __ldg(src + static_cast<int64_t>(row) * LPR + c);
+            const uint4* p = src + static_cast<int64_t>(row) * (2 * LPR) + c;
+            x[0] = __ldg(p);
+            x[1] = __ldg(p + LPR);
             slot = __ldg(slots + t);
             if (slot >= num_slots) {
                 if (h == 0 && c == 0 && !value) report(err, PKV_DEVERR_SLOT);
                 slot = -1;
             }
         }
-        uint32_t w[2];
-        const float2 sz = int_encode8<D, BITS, IT>(x, w);
+        uint32_t w[2][2];
+        const float2 sz = int_encode16<D, BITS, IT>(x, w);
         if (slot >= 0) {
             // tiles of a pool count below 2^32
-            const uint32_t tile = static_cast<uint32_t>(slot >> 4) * heads.d + h;
-            int_store8<D, BITS>(pool + static_cast<uint64_t>(tile) * L::kBytes, value, static_cast<int>(slot) & 15, c, w, sz);
+            unsigned char* tile =
+                pool + static_cast<uint64_t>(static_cast<uint32_t>(slot >> 4) * heads.d + h) * L::kBytes;
+            const int t = static_cast<int>(slot) & 15;
+            int_store8<D, BITS>(tile, value, t, c, w[0]);
+            int_store8<D, BITS>(tile, value, t, c + LPR, w[1]);
+            if (c == 0) *reinterpret_cast<float2*>(tile + L::param(t)) = sz;
         }
     }
 }
 
-// Read by slot: D / 8 lanes per row (t, h), blockIdx.y = 0 keys, 1 values.
+// Read by slot: D / 16 lanes per row (t, h), blockIdx.y = 0 keys, 1 values.
 template <int D, int KV, typename OT>
 __global__ void __launch_bounds__(256) read_kernel(const unsigned char* __restrict__ kc,
                                                    const unsigned char* __restrict__ vc,
                                                    const int64_t* __restrict__ slots, uint4* k_out, uint4* v_out,
                                                    uint32_t rows, RowDiv heads, int64_t num_slots, float k_scale,
                                                    float v_scale, unsigned int* err) {
-    constexpr int LPR = D / 8, RPC = 256 / LPR;
+    constexpr int LPR = D / 16, RPC = 256 / LPR;
     const bool value = blockIdx.y != 0;
     const unsigned char* pool = value ? vc : kc;
     uint4* out = value ? v_out : k_out;
@@ -91,9 +98,14 @@ __global__ void __launch_bounds__(256) read_kernel(const unsigned char* __restri
             continue;
         }
         const uint32_t tile = static_cast<uint32_t>(slot >> 4) * heads.d + h;  // below 2^32
-        float f[8];
-        PoolRow<D, KV>::load(pool + tile * PoolRow<D, KV>::kTile, value, static_cast<int>(slot) & 15, c, scale, f);
-        out[static_cast<int64_t>(row) * LPR + c] = pack8<OT>(f);
+        const unsigned char* p = pool + tile * PoolRow<D, KV>::kTile;
+        float f[2][8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            PoolRow<D, KV>::load(p, value, static_cast<int>(slot) & 15, c + i * LPR, scale, f[i]);
+        uint4* o = out + static_cast<int64_t>(row) * (2 * LPR) + c;
+        o[0] = pack8<OT>(f[0]);
+        o[LPR] = pack8<OT>(f[1]);
     }
 }
 
@@ -129,7 +141,10 @@ __global__ void __launch_bounds__(256) stage_int_kernel(const unsigned char* __r
     for (int i = threadIdx.x; i < total; i += 256) {
         const int h = i / per_head, t = i % per_head / (D / 8), c = i % (D / 8);
         float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (!bad && t < valid) int_load8<D, BITS>(src + static_cast<int64_t>(h) * L::kBytes, value, t, c, f);
+        if (!bad && t < valid) {
+            const unsigned char* tile = src + static_cast<int64_t>(h) * L::kBytes;
+            int_load8<D, BITS>(tile, value, t, c, int_params<D, BITS>(tile, t), f);
+        }
         dst[i] = pack8<OT>(f);
     }
 }
@@ -137,7 +152,7 @@ __global__ void __launch_bounds__(256) stage_int_kernel(const unsigned char* __r
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 unsigned row_grid(int64_t rows, int rows_per_cta) {
-    const int64_t need = (rows + rows_per_cta - 1) / rows_per_cta, cap = static_cast<int64_t>(num_sms()) * 16;
+    const int64_t need = (rows + rows_per_cta - 1) / rows_per_cta, cap = static_cast<int64_t>(num_sms()) * 4;
     return static_cast<unsigned>(need < cap ? need : cap);
 }
 
@@ -153,7 +168,7 @@ cudaError_t launch_read(int kv, const void* kc, const void* vc, const int64_t* s
     case PKV_INT8: kern = read_kernel<D, PKV_INT8, OT>; break;
     default: kern = read_kernel<D, PKV_INT4, OT>; break;
     }
-    kern<<<dim3(row_grid(rows, 256 * 8 / D), 2), 256, 0, st>>>(
+    kern<<<dim3(row_grid(rows, 256 * 16 / D), 2), 256, 0, st>>>(
         static_cast<const unsigned char*>(kc), static_cast<const unsigned char*>(vc), slots, static_cast<uint4*>(ko),
         static_cast<uint4*>(vo), static_cast<uint32_t>(rows), row_div(d->num_kv_heads), static_cast<int64_t>(d->num_blocks) * kBlockSize, d->k_scale,
         d->v_scale, err);
@@ -170,7 +185,7 @@ cudaError_t launch_append_int(const void* k, const void* v, int in_dtype, int64_
         constexpr int D = L::kD, BITS = L::kBits;
         const int64_t rows = num_tokens * d->num_kv_heads;
         auto kern = in_dtype == PKV_BF16 ? append_int_kernel<D, BITS, BF16> : append_int_kernel<D, BITS, F16>;
-        kern<<<dim3(row_grid(rows, 256 * 8 / D), 2), 256, 0, st>>>(
+        kern<<<dim3(row_grid(rows, 256 * 16 / D), 2), 256, 0, st>>>(
             static_cast<const uint4*>(k), static_cast<const uint4*>(v), slots, static_cast<unsigned char*>(k_cache),
             static_cast<unsigned char*>(v_cache), static_cast<uint32_t>(rows), row_div(d->num_kv_heads),
             static_cast<int64_t>(d->num_blocks) * kBlockSize, err);

@@ -18,9 +18,9 @@ struct PoolRow {
     __device__ __forceinline__ static void load(const unsigned char* tile, bool value, int t, int c, float scale,
                                                 float* f) {
         if constexpr (KV == PKV_INT8) {
-            int_load8<D, 8>(tile, value, t, c, f);
+            int_load8<D, 8>(tile, value, t, c, int_params<D, 8>(tile, t), f);
         } else if constexpr (KV == PKV_INT4) {
-            int_load8<D, 4>(tile, value, t, c, f);
+            int_load8<D, 4>(tile, value, t, c, int_params<D, 4>(tile, t), f);
         } else if constexpr (KV == PKV_FP8_E4M3) {
             const uint2 x = *reinterpret_cast<const uint2*>(tile + t * D + 8 * c);
             const uint32_t w[2] = {x.x, x.y};
