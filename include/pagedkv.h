@@ -601,7 +601,8 @@ pkv_status pkv_prefill_plan(const int32_t* query_start, const int32_t* seq_lens,
  * these sizes on the current device, or a negative pkv_status on error.
  * planned != 0: the size for a launch with a work list (no 2048-token cap,
  * see pkv_paged_attention_decode_append); 0: grid order (every other decode
- * entry point).
+ * entry point).  Over integer-coded pools the decode's own kernel may take
+ * larger partitions than this.
  */
 int32_t pkv_decode_auto_partition(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
                                   int32_t head_size, int32_t max_seq_len, int32_t planned);

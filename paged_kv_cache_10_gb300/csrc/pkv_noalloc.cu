@@ -60,6 +60,8 @@ extern "C" pkv_status pkv_paged_attention_decode_noalloc(const void* q, int32_t 
     if (P == 0) {
         P = pkv_decode_auto_partition(num_seqs, num_q_heads, desc->num_kv_heads, desc->head_size, max_seq_len, 0);
         if (P < 0) return static_cast<pkv_status>(-P);
+        if (is_int_pool(desc->kv_dtype))
+            P = auto_partition_int(num_seqs, desc->num_kv_heads, max_seq_len, desc->kv_dtype, desc->head_size);
     }
     const size_t need = pkv_decode_workspace_bytes(num_seqs, num_q_heads, desc->head_size, max_seq_len, P);
     if (need > kNoAllocScratchBytes) return PKV_ERR_WORKSPACE;  // beyond the built-in maximum

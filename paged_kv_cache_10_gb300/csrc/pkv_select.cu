@@ -942,9 +942,12 @@ extern "C" pkv_status pkv_paged_attention_decode_sparse(const void* q, int32_t q
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4))
         return PKV_ERR_INVALID;
     const int G = num_q_heads / d->num_kv_heads;
-    const int per = partition_blocks > 0
-                        ? partition_blocks
-                        : auto_partition(num_seqs, d->num_kv_heads, num_selected * kBlockSize, false) / kBlockSize;
+    const int list_tokens = num_selected * kBlockSize;
+    const int per = partition_blocks > 0 ? partition_blocks
+                    : (is_int_pool(d->kv_dtype)
+                           ? auto_partition_int(num_seqs, d->num_kv_heads, list_tokens, d->kv_dtype, d->head_size)
+                           : auto_partition(num_seqs, d->num_kv_heads, list_tokens, false)) /
+                          kBlockSize;
     const int64_t NP = cdiv(num_selected, per);
     const size_t need = NP > 1 ? partials_bytes(num_seqs, num_q_heads, d->head_size, NP) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return PKV_ERR_WORKSPACE;
