@@ -144,6 +144,9 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // sparse: a programmatic dependent of the kernel before it on the stream, which it
+    // waits for before it lets its own dependent (the merge) start
+    if constexpr (SPARSE) wait_primary_grid();
     allow_dependent_launch();  // the merge may stage its CTAs behind this grid's last wave
     const int hf = lane >> 4, li = lane & 15;
     int part, h, s;
@@ -464,7 +467,7 @@ cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t st) {
     }
     const dim3 grid = p.work ? dim3(static_cast<unsigned>(static_cast<int64_t>(p.num_work) * p.Hkv))
                              : dim3(p.NP - p.part_base, p.Hkv, p.S + (p.join_primary ? 1 : 0));  // this launch's partitions
-    return launch_maybe_pdl(p.join_primary != 0 && !p.work, kern, grid, dim3(NW * 32), SMEM, st, p);
+    return launch_maybe_pdl(SPARSE || (p.join_primary != 0 && !p.work), kern, grid, dim3(NW * 32), SMEM, st, p);
 }
 
 template <typename KT, typename QT, bool SPARSE = false>

@@ -116,9 +116,19 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     unsigned char* smem = smem_raw + ((128 - (smem_addr(smem_raw) & 127)) & 127);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g8 = lane >> 2, qd = lane & 3;
-    allow_dependent_launch();
     const int part = blockIdx.x, h = blockIdx.y, s = blockIdx.z;
 
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset) + warp * NST;
+    if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < NST; ++i) mbar_init(&bars[i], 1);
+        mbar_init_fence();
+    }
+    // A programmatic dependent of the kernel before it on the stream: what it reads
+    // may come from there.  Its own dependent, the merge, reads the lengths before it
+    // waits, so it may start only now.
+    wait_primary_grid();
+    allow_dependent_launch();
     // the first window's table (or list) entries, loaded beside the length
     const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.MB;
     const int j0 = part * (p.P / kBlockSize);  // first block (or list entry) of this partition
@@ -152,16 +162,10 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     const int ns_w = warp < nstep ? (nstep - warp + NW - 1) / NW : 0;
 
     unsigned char* ring = smem + warp * NST * STAGE;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset) + warp * NST;
     volatile int* info = reinterpret_cast<int*>(smem + C::kInfoOffset) + warp * NST * 2;
     const unsigned char* kpool = static_cast<const unsigned char*>(p.k_cache);
     const unsigned char* vpool = static_cast<const unsigned char*>(p.v_cache);
     const uint64_t pol = policy_evict_first();
-    if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < NST; ++i) mbar_init(&bars[i], 1);
-        mbar_init_fence();
-    }
     __syncwarp();
 
     // Lane 2k + u of (tbl, val) holds the physical block and the valid tokens of
@@ -561,8 +565,8 @@ cudaError_t launch_decode_int_t(const DecodeParams& p, int G, int q_dtype, cudaS
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    kern<<<dim3(p.NP, p.Hkv, p.S), IntCfg<D, BITS, FOLD>::kWarps * 32, SMEM, st>>>(p, G, q_dtype == PKV_BF16 ? 1 : 0);
-    return cudaGetLastError();
+    return launch_maybe_pdl(true, kern, dim3(p.NP, p.Hkv, p.S), dim3(IntCfg<D, BITS, FOLD>::kWarps * 32), SMEM, st, p, G,
+                            q_dtype == PKV_BF16 ? 1 : 0);
 }
 
 template <int BITS>

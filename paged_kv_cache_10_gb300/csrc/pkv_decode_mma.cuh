@@ -386,6 +386,9 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // sparse: a programmatic dependent of the kernel before it on the stream, which it
+    // waits for before it lets its own dependent (the merge) start
+    if constexpr (SPARSE) wait_primary_grid();
     allow_dependent_launch();  // the merge may stage its CTAs behind this grid's last wave
     const int g8 = lane >> 2, qd = lane & 3;  // fragment row group / quad member
     int part, h, s;
@@ -674,7 +677,7 @@ cudaError_t launch_decode_mma_t(const DecodeParams& p, const CUtensorMap& tk, co
     }
     const dim3 grid = p.work ? dim3(static_cast<unsigned>(static_cast<int64_t>(p.num_work) * p.Hkv))
                              : dim3(p.NP - p.part_base, p.Hkv, p.S + (p.join_primary ? 1 : 0));  // this launch's partitions
-    return launch_maybe_pdl(p.join_primary != 0 && !p.work, kern, grid, dim3(NW * 32), SMEM, st, p, tk, tv);
+    return launch_maybe_pdl(SPARSE || (p.join_primary != 0 && !p.work), kern, grid, dim3(NW * 32), SMEM, st, p, tk, tv);
 }
 
 template <typename KT, typename QT, bool SPARSE = false>

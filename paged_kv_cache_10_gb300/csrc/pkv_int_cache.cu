@@ -39,6 +39,7 @@ __global__ void __launch_bounds__(256) append_int_kernel(const uint4* __restrict
                                                          int64_t num_slots, unsigned int* err) {
     using L = IntTile<D, BITS>;
     constexpr int LPR = D / 16, RPC = 256 / LPR;  // lanes of a row, rows of a CTA
+    wait_primary_grid();  // a programmatic dependent of the kernel before it on the stream
     const bool value = blockIdx.y != 0;
     const uint4* src = value ? v : k;
     unsigned char* pool = value ? vc : kc;
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(256) read_kernel(const unsigned char* __restri
                                                    uint32_t rows, RowDiv heads, int64_t num_slots, float k_scale,
                                                    float v_scale, unsigned int* err) {
     constexpr int LPR = D / 16, RPC = 256 / LPR;
+    wait_primary_grid();
     const bool value = blockIdx.y != 0;
     const unsigned char* pool = value ? vc : kc;
     uint4* out = value ? v_out : k_out;
@@ -168,11 +170,11 @@ cudaError_t launch_read(int kv, const void* kc, const void* vc, const int64_t* s
     case PKV_INT8: kern = read_kernel<D, PKV_INT8, OT>; break;
     default: kern = read_kernel<D, PKV_INT4, OT>; break;
     }
-    kern<<<dim3(row_grid(rows, 256 * 16 / D), 2), 256, 0, st>>>(
-        static_cast<const unsigned char*>(kc), static_cast<const unsigned char*>(vc), slots, static_cast<uint4*>(ko),
-        static_cast<uint4*>(vo), static_cast<uint32_t>(rows), row_div(d->num_kv_heads), static_cast<int64_t>(d->num_blocks) * kBlockSize, d->k_scale,
-        d->v_scale, err);
-    return cudaGetLastError();
+    return launch_maybe_pdl(true, kern, dim3(row_grid(rows, 256 * 16 / D), 2), dim3(256), 0, st,
+                            static_cast<const unsigned char*>(kc), static_cast<const unsigned char*>(vc), slots,
+                            static_cast<uint4*>(ko), static_cast<uint4*>(vo), static_cast<uint32_t>(rows),
+                            row_div(d->num_kv_heads), static_cast<int64_t>(d->num_blocks) * kBlockSize, d->k_scale,
+                            d->v_scale, err);
 }
 
 }  // namespace
@@ -185,11 +187,11 @@ cudaError_t launch_append_int(const void* k, const void* v, int in_dtype, int64_
         constexpr int D = L::kD, BITS = L::kBits;
         const int64_t rows = num_tokens * d->num_kv_heads;
         auto kern = in_dtype == PKV_BF16 ? append_int_kernel<D, BITS, BF16> : append_int_kernel<D, BITS, F16>;
-        kern<<<dim3(row_grid(rows, 256 * 16 / D), 2), 256, 0, st>>>(
-            static_cast<const uint4*>(k), static_cast<const uint4*>(v), slots, static_cast<unsigned char*>(k_cache),
-            static_cast<unsigned char*>(v_cache), static_cast<uint32_t>(rows), row_div(d->num_kv_heads),
-            static_cast<int64_t>(d->num_blocks) * kBlockSize, err);
-        return cudaGetLastError();
+        return launch_maybe_pdl(true, kern, dim3(row_grid(rows, 256 * 16 / D), 2), dim3(256), 0, st,
+                                static_cast<const uint4*>(k), static_cast<const uint4*>(v), slots,
+                                static_cast<unsigned char*>(k_cache), static_cast<unsigned char*>(v_cache),
+                                static_cast<uint32_t>(rows), row_div(d->num_kv_heads),
+                                static_cast<int64_t>(d->num_blocks) * kBlockSize, err);
     });
 }
 

@@ -31,6 +31,7 @@ __global__ void __launch_bounds__(128) key_bounds_kernel(const unsigned char* __
                                                          const int32_t* __restrict__ new_lens, int max_new, int NB,
                                                          int Hkv, float k_scale, unsigned char* __restrict__ bounds,
                                                          unsigned int* err) {
+    wait_primary_grid();  // a programmatic dependent of the kernel before it on the stream
     const int s = blockIdx.y;
     const int len = __ldg(seq_lens + s);
     const int fresh = new_lens ? __ldg(new_lens + s) : len;
@@ -137,17 +138,10 @@ __global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) 
     constexpr int NST = C::kStages;
     extern __shared__ unsigned char smem_raw[];
     unsigned char* smem = smem_raw + ((128 - (smem_addr(smem_raw) & 127)) & 127);
-    allow_dependent_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g8 = lane >> 2, qd = lane & 3;
     const int64_t unit = blockIdx.x * 4ll + warp;
     const int h = static_cast<int>(unit % p.Hkv), s = blockIdx.y;
     const int first = static_cast<int>(unit / p.Hkv) * p.tiles;
-    bool bad;
-    const int nblk = row_blocks(p, s, bad);
-    if (bad && unit == 0 && lane == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
-    if (first * 16 >= nblk || nblk <= p.n) return;  // a row that keeps every block needs no scores
-    const int tiles = min(p.tiles, (nblk + 15) / 16 - first);
-
     unsigned char* ring = smem + warp * NST * C::kStage;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kBarOffset) + warp * NST;
     volatile uint32_t* masks = reinterpret_cast<uint32_t*>(smem + C::kMaskOffset) + warp * NST;
@@ -156,6 +150,17 @@ __global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) 
         for (int i = 0; i < NST; ++i) mbar_init(&bars[i], 1);
         mbar_init_fence();
     }
+    // A programmatic dependent of the kernel before it on the stream.  Its own, the
+    // selection, reads q and the lengths and writes short rows before it waits, so
+    // it may start only now.
+    wait_primary_grid();
+    allow_dependent_launch();
+    bool bad;
+    const int nblk = row_blocks(p, s, bad);
+    if (bad && unit == 0 && lane == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+    if (first * 16 >= nblk || nblk <= p.n) return;  // a row that keeps every block needs no scores
+    const int tiles = min(p.tiles, (nblk + 15) / 16 - first);
+
     __syncwarp();
     const uint64_t pol = policy_evict_first();
     const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.MB;
@@ -735,8 +740,8 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t st) {
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
-    block_score_kernel<D, T><<<dim3(static_cast<unsigned>((units + 3) / 4), p.S), 128, kScoreSmem, st>>>(p);
-    e = cudaGetLastError();
+    e = launch_maybe_pdl(true, block_score_kernel<D, T>, dim3(static_cast<unsigned>((units + 3) / 4), p.S), dim3(128),
+                         kScoreSmem, st, p);
     if (e != cudaSuccess) return e;
     const size_t smem = static_cast<size_t>(p.smem_cols) * 4;
     return launch_maybe_pdl(true, select_kernel<D, T>, dim3(p.Hkv, p.S), dim3(kSelThreads), smem, st, p);
@@ -755,9 +760,8 @@ cudaError_t launch_bounds_of(int kv, dim3 grid, cudaStream_t st, const unsigned 
     case PKV_INT8: kern = key_bounds_kernel<D, PKV_INT8, OT>; break;
     default: kern = key_bounds_kernel<D, PKV_INT4, OT>; break;
     }
-    kern<<<grid, 128, 0, st>>>(kc, tables, MB, lens, fresh, max_new, d->num_blocks, d->num_kv_heads, d->k_scale, bounds,
-                               err);
-    return cudaGetLastError();
+    return launch_maybe_pdl(true, kern, grid, dim3(128), 0, st, kc, tables, MB, lens, fresh, max_new, d->num_blocks,
+                            d->num_kv_heads, d->k_scale, bounds, err);
 }
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
