@@ -377,3 +377,182 @@ def test_decode_loop(pk, kv, dtype):
         # scaled codes: ref is on values rounded once more to 16 bits, half a step of the largest value and key
         extra = 0 if kv in qu.TORCH else eps * float(np.abs(pools.vh).max()) * (1 + float(np.abs(ref).max()))
         assert max_error(out.double().cpu().numpy(), ref, dtype, TOL[dtype], 4.0) <= TOL[dtype] + extra
+
+
+@pytest.mark.parametrize("kv,dtype", [("bf16", "bf16"), ("int8", "bf16"), ("int4", "f16")])
+def test_calls_back_to_back_see_their_inputs(pk, kv, dtype):
+    """Each call may start while the kernel before it ends: inputs that a kernel writes just before, outputs
+    that the call before still reads.  40 steps with changing inputs in the same buffers, nothing waited for
+    in between, against the same steps with a wait after every call."""
+    rng = np.random.default_rng(41)
+    D, Hkv, G, n, S = 128, 2, 4, 9, 5
+    lens = [700, 33, 1, 160, 400]
+    NB, tables = qu.make_tables(rng, lens)
+    pools = qu.Pools(rng, NB, Hkv, D, kv)
+    kd, vd = pools.dev()
+    dt = qu.TORCH[dtype]
+    bounds = torch.zeros(NB, Hkv, 2, D, dtype=dt, device="cuda")
+    t = dev32(tables)
+    steps = 40
+    qs = torch.randn(steps, S, Hkv * G, D, device="cuda").to(dt)
+    kn, vn = (torch.randn(steps, S, Hkv, D, device="cuda").to(dt) for _ in range(2))
+    ls = torch.stack([dev32([max(1, L - i % 7) for L in lens]) for i in range(steps)])
+    slots = torch.stack([torch.tensor([int(tables[s][(int(ls[i][s]) - 1) // 16]) * 16 + (int(ls[i][s]) - 1) % 16
+                                       for s in range(S)], device="cuda") for i in range(steps)])
+    q, l, sl, one = qs[0].clone(), ls[0].clone(), slots[0].clone(), torch.ones(S, dtype=torch.int32, device="cuda")
+    k1, v1 = kn[0].clone(), vn[0].clone()
+    sel = torch.zeros(S, Hkv, n, dtype=torch.int32, device="cuda")
+    out, dense = torch.zeros_like(q), torch.zeros_like(q)
+    ko, vo = torch.zeros_like(k1), torch.zeros_like(v1)
+    ws1 = torch.zeros(pk.select_blocks_workspace_bytes(S, Hkv, 700), dtype=torch.uint8, device="cuda")
+    ws2 = torch.zeros(pk.decode_sparse_workspace_bytes(S, Hkv * G, D, n, 2), dtype=torch.uint8, device="cuda")
+    ws3 = torch.zeros(pk.decode_workspace_bytes(S, Hkv * G, D, 700, 64), dtype=torch.uint8, device="cuda")
+
+    def run(wait):
+        kc, vc = kd.clone(), vd.clone()
+        bounds.zero_()
+        pk.paged_key_bounds(kc, pools.desc, t, ls[0], None, 700, bounds)
+        kept = []
+        sync = torch.cuda.synchronize if wait else (lambda: None)
+        for i in range(steps):
+            for dst, src in ((q, qs[i]), (l, ls[i]), (sl, slots[i]), (k1, kn[i]), (v1, vn[i])):
+                dst.copy_(src)
+                sync()
+            pk.paged_kv_append(k1, v1, sl, kc, vc, pools.desc)
+            sync()
+            pk.paged_kv_read(sl, kc, vc, pools.desc, ko, vo)
+            sync()
+            pk.paged_key_bounds(kc, pools.desc, t, l, one, 1, bounds)
+            sync()
+            pk.select_blocks(q, bounds, pools.desc, t, l, 700, sel, ws1)
+            sync()
+            pk.paged_attention_decode_sparse(q, kc, vc, pools.desc, t, l, sel, 0.1, out, workspace=ws2, partition_blocks=2)
+            sync()
+            pk.paged_attention_decode(q, kc, vc, pools.desc, t, l, 700, 0.1, dense, workspace=ws3, partition_tokens=64)
+            sync()
+            kept.append([x.clone() for x in (sel, out, dense, ko, vo)])
+        torch.cuda.synchronize()
+        return kept
+
+    want = run(True)
+    for _ in range(3):
+        for i, (a, b) in enumerate(zip(want, run(False))):
+            for x, y in zip(a, b):
+                assert torch.equal(x, y), i
+    assert pk.get_device_error() == 0
+
+
+def test_two_streams_at_once(pk):
+    """The same calls on two streams, each with its own outputs and workspaces."""
+    rng = np.random.default_rng(43)
+    lens = [3000, 900, 2000, 17]
+    NB, tables = qu.make_tables(rng, lens)
+    pools = qu.Pools(rng, NB, 2, 128, "int4")
+    kd, vd = pools.dev()
+    t, l = dev32(tables), dev32(lens)
+    q = qu.queries(rng, 4, 16, 128, "bf16").cuda()
+    bounds = torch.zeros(NB, 2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    pk.paged_key_bounds(kd, pools.desc, t, l, None, 3000, bounds)
+    torch.cuda.synchronize()
+
+    class One:
+        def __init__(self):
+            self.stream = torch.cuda.Stream()
+            self.sel = torch.zeros(4, 2, 40, dtype=torch.int32, device="cuda")
+            self.out, self.dense = torch.zeros_like(q), torch.zeros_like(q)
+            self.ws = [torch.zeros(b, dtype=torch.uint8, device="cuda") for b in
+                       (pk.select_blocks_workspace_bytes(4, 2, 3000), pk.decode_sparse_workspace_bytes(4, 16, 128, 40, 4),
+                        pk.decode_workspace_bytes(4, 16, 128, 3000, 256))]
+
+        def go(self):
+            pk.select_blocks(q, bounds, pools.desc, t, l, 3000, self.sel, self.ws[0], stream=self.stream)
+            pk.paged_attention_decode_sparse(q, kd, vd, pools.desc, t, l, self.sel, 0.1, self.out, workspace=self.ws[1],
+                                             partition_blocks=4, stream=self.stream)
+            pk.paged_attention_decode(q, kd, vd, pools.desc, t, l, 3000, 0.1, self.dense, workspace=self.ws[2],
+                                      partition_tokens=256, stream=self.stream)
+
+    a, b = One(), One()
+    torch.cuda.synchronize()
+    a.go()
+    torch.cuda.synchronize()
+    want = [x.clone() for x in (a.sel, a.out, a.dense)]
+    for _ in range(20):
+        a.go()
+        b.go()
+    torch.cuda.synchronize()
+    for o in (a, b):
+        for x, y in zip(want, (o.sel, o.out, o.dense)):
+            assert torch.equal(x, y)
+    assert pk.get_device_error() == 0
+
+
+def test_blocks_past_four_gigabytes(pk):
+    """Tables that name the last blocks of pools and bounds larger than 2^32 bytes."""
+    rng = np.random.default_rng(47)
+    D, Hkv, dtype = 128, 8, "bf16"
+    NB = (1 << 32) // (Hkv * 4 * D) + 4000  # bounds alone pass 4 GiB
+    lens = [300, 50]
+    n_blocks, small = qu.make_tables(rng, lens, spare=0)
+    pools = qu.Pools(rng, n_blocks, Hkv, D, "int4")
+    desc = pk.CacheDesc(num_blocks=NB, num_kv_heads=Hkv, head_size=D, kv_dtype="int4")
+    tables = np.where(small >= 0, small + NB - n_blocks, -1).astype(np.int32)
+    big = [torch.empty(NB, *a.shape[1:], dtype=torch.uint8, device="cuda") for a in (pools.k_host, pools.v_host)]
+    for x, a in zip(big, (pools.k_host, pools.v_host)):
+        x[NB - n_blocks:] = torch.from_numpy(a).cuda()
+    t, l = dev32(tables), dev32(lens)
+    bounds = torch.empty(NB, Hkv, 2, D, dtype=torch.bfloat16, device="cuda")
+    pk.paged_key_bounds(big[0], desc, t, l, None, 300, bounds)
+    want = qu.ref_bounds(pools, small, lens, lens, np.zeros((n_blocks, Hkv, 2, D), np.float32), dtype)
+    got = bounds[NB - n_blocks:].float().cpu().numpy()
+    used = np.unique(small[small >= 0])
+    assert np.array_equal(got[used], want[used])
+    q = qu.queries(rng, 2, 16, D, dtype)
+    sel = torch.zeros(2, Hkv, 5, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(pk.select_blocks_workspace_bytes(2, Hkv, 300), dtype=torch.uint8, device="cuda")
+    pk.select_blocks(q.cuda(), bounds, desc, t, l, 300, sel, ws)
+    assert np.array_equal(sel.cpu().numpy(), qu.ref_select(q, want.astype(np.float64), small, lens, 5, 1, 1, Hkv))
+    out = torch.zeros_like(q).cuda()
+    pk.paged_attention_decode(q.cuda(), big[0], big[1], desc, t, l, 300, 0.1, out,
+                              workspace=torch.zeros(max(16, pk.decode_workspace_bytes(2, 16, D, 300, 0)), dtype=torch.uint8,
+                                                    device="cuda"))
+    ref = qu.ref_dense(q, pools, small, lens, 0.1)
+    assert max_error(out.double().cpu().numpy(), ref, dtype, TOL[dtype], float(np.abs(pools.vh).max())) <= TOL[dtype]
+    x = torch.randn(1, Hkv, D, device="cuda").bfloat16()
+    slot = torch.tensor([int(tables[0][3]) * 16 + 5], device="cuda")
+    ko, vo = torch.zeros_like(x), torch.zeros_like(x)
+    pk.paged_kv_append(x, x, slot, big[0], big[1], desc)
+    pk.paged_kv_read(slot, big[0], big[1], desc, ko, vo)
+    held = qu.round_to(qu.held(x.float().cpu().numpy(), 4), "bf16")
+    # the read forms the value in one binary32 operation: half a step of 16 bits at a tie at most
+    assert np.max(np.abs(ko.float().cpu().numpy() - held)) <= 2.0 ** -8 * np.abs(held).max()
+    assert torch.equal(ko, vo) and pk.get_device_error() == 0
+
+
+def test_binding_refusals_on_device_tensors(pk):
+    desc = pk.CacheDesc(num_blocks=4, num_kv_heads=2, head_size=64, kv_dtype="int8")
+    pool = torch.zeros(4, 2, 16 * 72, dtype=torch.uint8, device="cuda")
+    slots = torch.zeros(3, dtype=torch.int64, device="cuda")
+    o = torch.zeros(3, 2, 64, device="cuda").half()
+    read = lambda kc=pool, k=o, v=o, s=slots, **kw: pk.paged_kv_read(s, kc, pool, desc, k, v, **kw)
+    read()
+    for bad, err in ((dict(kc=pool[..., :16 * 64].contiguous()), ValueError),      # no room for the parameters
+                     (dict(k=o.transpose(0, 1).contiguous().transpose(0, 1)), ValueError),  # not contiguous
+                     (dict(k=o.cpu()), TypeError), (dict(k=o.float(), v=o.float()), TypeError),
+                     (dict(v=o.bfloat16()), TypeError), (dict(k=o[:2]), ValueError), (dict(s=slots.int()), TypeError),
+                     (dict(out_dtype="f8"), KeyError)):
+        with pytest.raises(err):
+            read(**bad)
+    x = o.clone()
+    with pytest.raises(ValueError):
+        pk.paged_kv_append(x, x, slots, pool[..., :16 * 64].contiguous(), pool, desc)
+    with pytest.raises(pk.PagedKVError):
+        pk.paged_attention_decode(torch.zeros(1, 6, 64, device="cuda").half(), pool, pool, desc,
+                                  torch.zeros(1, 4, dtype=torch.int32, device="cuda"),
+                                  torch.zeros(1, dtype=torch.int32, device="cuda"), 4, 0.1,
+                                  torch.zeros(1, 6, 64, device="cuda").half())  # three heads a KV head
+    # a stream object, and its handle
+    st = torch.cuda.Stream()
+    read(stream=st)
+    read(stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    assert pk.get_device_error() == 0
