@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     float* sc = p.score + row * p.cols;
     const bool in_smem = nblk <= p.smem_cols;
     float a = INFINITY, b = -INFINITY, big = 0.f;
+    for (int i = tid; i < (nblk + 15) / 16; i += kSelThreads) big = fmaxf(big, __ldcg(p.top + row * (p.cols / 16) + i));
     if (in_smem) {
         // columns past nblk up to the next tile's end are written too (-inf)
         const float4* src = reinterpret_cast<const float4*>(sc);
@@ -474,7 +475,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         const int quads = (nblk + 3) / 4;
 #pragma unroll 4
         for (int i = tid; i < quads; i += kSelThreads) {
-            const float4 v = src[i];
+            const float4 v = __ldcg(src + i);
             dst[i] = v;
             const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -492,7 +493,6 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
             b = fmaxf(b, x);
         }
     }
-    for (int i = tid; i < (nblk + 15) / 16; i += kSelThreads) big = fmaxf(big, p.top[row * (p.cols / 16) + i]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) {
         a = fminf(a, __shfl_xor_sync(kFull, a, x));
