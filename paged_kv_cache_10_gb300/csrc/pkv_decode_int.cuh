@@ -49,9 +49,9 @@ struct IntCfg {
     static constexpr int kBarOffset = kRing;
     static constexpr int kInfoOffset = kBarOffset + kWarps * kStages * 8;  // valid tokens of a stage's two blocks
     static constexpr int kMergeOffset = kInfoOffset + (kWarps * kStages * 2 + 15) / 16 * 16;
-    static constexpr int kQOffset = (kMergeOffset + (kWarps * 16 + 16) * 4 + 15) / 16 * 16;  // Q^T fragments, 8 bytes a lane and k-step
+    static constexpr int kQOffset = (kMergeOffset + kWarps * 24 * 4 + 15) / 16 * 16;  // Q^T fragments, 8 bytes a lane and k-step
     static constexpr int kBytes = kQOffset + (D / 16) * 32 * 8 + 128;  // + alignment slack
-    static constexpr int kState = (24 + 4 * (D / 16) * 33) * 4;  // a warp's state for the cross-warp merge
+    static constexpr int kState = 8 * (D + 4) * 4;  // a warp's accumulators for the cross-warp merge
     static_assert(kState <= kStages * kStage, "the merge state reuses the warp's ring");
     static_assert(kCtasPerSm * (kBytes + 1024) <= 228 * 1024 || BITS == 8, "residency");
 };
@@ -472,8 +472,9 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
         }
     }
 
-    // ---- warp state: [8] m, [8] l, [8] z, then the accumulators in value units,
-    // fragment order, 33-word pitch
+    // ---- the warps' states meet: maxima first, then each warp writes its sums and
+    // accumulators relative to the CTA's maximum, in value units, as rows [column][D]
+    // of its ring, so that the last pass only adds them up
 #pragma unroll
     for (int mask = 4; mask < 32; mask <<= 1) {
         lA += __shfl_xor_sync(kFull, lA, mask);
@@ -481,82 +482,72 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
         zA += __shfl_xor_sync(kFull, zA, mask);
         zB += __shfl_xor_sync(kFull, zB, mask);
     }
-    float* ws = reinterpret_cast<float*>(ring);
-    __syncwarp();
+    float2* wm = reinterpret_cast<float2*>(msc);  // [NW][4] maxima of columns 2 qd, 2 qd + 1
+    float2* wl = wm + NW * 4;
+    float2* wz = wl + NW * 4;
+    if (aborted) mA = mB = -INFINITY;
+    if (g8 == 0) wm[warp * 4 + qd] = make_float2(mA, mB);
+    __syncthreads();
+    float MA = -INFINITY, MB = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+        const float2 m = wm[w * 4 + qd];
+        MA = fmaxf(MA, m.x);
+        MB = fmaxf(MB, m.y);
+    }
+    const float scA = mA != -INFINITY ? ex2(mA - MA) : 0.f, scB = mB != -INFINITY ? ex2(mB - MB) : 0.f;
     if (g8 == 0) {
-        ws[2 * qd] = aborted ? -INFINITY : mA;
-        ws[2 * qd + 1] = aborted ? -INFINITY : mB;
-        ws[8 + 2 * qd] = aborted ? 0.f : lA;
-        ws[8 + 2 * qd + 1] = aborted ? 0.f : lB;
-        ws[16 + 2 * qd] = aborted ? 0.f : zA;
-        ws[16 + 2 * qd + 1] = aborted ? 0.f : zB;
+        wl[warp * 4 + qd] = make_float2(scA * lA, scB * lB);
+        wz[warp * 4 + qd] = make_float2(scA * zA, scB * zB);
     }
-    const float os = __uint_as_float(vref) * 0x1p24f;
+    constexpr int PW = D + 4;
+    {
+        const float os = __uint_as_float(vref) * 0x1p24f, oA = os * scA, oB = os * scB;
+        constexpr float odd = BITS == 4 ? 0.0625f : 1.f;  // odd rows of 4-bit words come times 16
+        float* ws = reinterpret_cast<float*>(ring) + 2 * qd * PW;
 #pragma unroll
-    for (int i = 0; i < KS; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-            ws[24 + (4 * i + c) * 33 + lane] =
-                aborted ? 0.f : o[i][c] * (c >= 2 && BITS == 4 ? os * 0.0625f : os);
-    __syncthreads();
-
-    // ---- cross-warp log-sum-exp weights, once per (warp, head)
-    // msc: [NW][8]
-    float* minv = msc + NW * 8;
-    if (threadIdx.x < G) {
-        const int g = threadIdx.x;
-        float M = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) M = fmaxf(M, reinterpret_cast<float*>(smem + w * NST * STAGE)[g]);
-        float den = 0.f;
-#pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            const float* wsw = reinterpret_cast<float*>(smem + w * NST * STAGE);
-            const float sc = (M != -INFINITY && wsw[g] != -INFINITY) ? exp2f(wsw[g] - M) : 0.f;
-            msc[w * 8 + g] = sc;
-            den = fmaf(sc, wsw[8 + g], den);
-        }
-        minv[g] = den > 0.f ? 1.f / den : (den == den ? 0.f : den);
-        const int64_t row = static_cast<int64_t>(s) * p.Hq + h * G + g;
-        if (p.NP > 1) {
-            p.part_m[row * p.NP + part] = M;
-            p.part_l[row * p.NP + part] = den;
+        for (int i = 0; i < KS; i += 2) {  // m-tiles i, i + 1 hold four consecutive dimensions from d
+            const int d = D == 128 && BITS == 8 ? 8 * g8 + 64 * (i >> 2) + 2 * (i & 3) : 2 * KS * g8 + 2 * i;
+            *reinterpret_cast<float4*>(ws + d) =
+                make_float4(o[i][0] * oA, o[i][2] * (oA * odd), o[i + 1][0] * oA, o[i + 1][2] * (oA * odd));
+            *reinterpret_cast<float4*>(ws + PW + d) =
+                make_float4(o[i][1] * oB, o[i][3] * (oB * odd), o[i + 1][1] * oB, o[i + 1][3] * (oB * odd));
         }
     }
     __syncthreads();
 
-    // ---- output: element pairs (head g, dimensions d, d + 1) over the threads
+    // ---- output: four dimensions of a head a thread
     const bool direct = SPARSE ? p.NP == 1 : len <= p.P;
-    for (int i2 = threadIdx.x; i2 < G * (D / 2); i2 += NW * 32) {
-        const int g = i2 / (D / 2), d = 2 * (i2 % (D / 2));
-        // inverse of the fragment layout: m-tile i of lane group gl holds (d, d + 1) in its two row halves
-        int i, gl;
-        if constexpr (D == 128 && BITS == 8) {
-            i = 4 * (d >> 6) + ((d >> 1) & 3);
-            gl = (d >> 3) & 7;
-        } else {
-            i = (d >> 1) % KS;
-            gl = d / (2 * KS);
-        }
-        const int frag = 24 + (4 * i + (g & 1)) * 33 + 4 * gl + (g >> 1);
-        float r0 = 0.f, r1 = 0.f;
+    for (int i4 = threadIdx.x; i4 < G * (D / 4); i4 += NW * 32) {
+        const int g = i4 / (D / 4), d = 4 * (i4 % (D / 4));
+        float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
+        float den = 0.f, z = 0.f, M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
-            const float* wsw = reinterpret_cast<float*>(smem + w * NST * STAGE);
-            const float sc = msc[w * 8 + g];
-            if (sc != 0.f) {
-                // FOLD: the tails' sums are those of column g + 4, two lanes on
-                r0 = fmaf(sc, wsw[frag] + (FOLD ? wsw[frag + 2] : 0.f) + wsw[16 + g], r0);
-                r1 = fmaf(sc, wsw[frag + 66] + (FOLD ? wsw[frag + 68] : 0.f) + wsw[16 + g], r1);
+            const float* x = reinterpret_cast<const float*>(smem + w * NST * STAGE) + g * PW + d;
+            const float4 u = *reinterpret_cast<const float4*>(x);
+            r.x += u.x; r.y += u.y; r.z += u.z; r.w += u.w;
+            if constexpr (FOLD) {  // the tails' columns
+                const float4 v = *reinterpret_cast<const float4*>(x + 4 * PW);
+                r.x += v.x; r.y += v.y; r.z += v.z; r.w += v.w;
             }
+            M = fmaxf(M, msc[w * 8 + g]);
+            den += msc[(NW + w) * 8 + g];
+            z += msc[(2 * NW + w) * 8 + g];
         }
-        r0 *= minv[g];
-        r1 *= minv[g];
+        const float inv = den > 0.f ? 1.f / den : (den == den ? 0.f : den);
+        r = make_float4((r.x + z) * inv, (r.y + z) * inv, (r.z + z) * inv, (r.w + z) * inv);
         const int64_t row = static_cast<int64_t>(s) * p.Hq + h * G + g;
         if (direct) {
-            reinterpret_cast<uint32_t*>(p.out)[(row * D + d) / 2] = q_bf16 ? pack2<true>(r0, r1) : pack2<false>(r0, r1);
+            reinterpret_cast<uint2*>(p.out)[(row * D + d) / 4] =
+                q_bf16 ? make_uint2(pack2<true>(r.x, r.y), pack2<true>(r.z, r.w))
+                       : make_uint2(pack2<false>(r.x, r.y), pack2<false>(r.z, r.w));
         } else {
-            *reinterpret_cast<float2*>(p.part_o + (row * p.NP + part) * D + d) = make_float2(r0, r1);
+            *reinterpret_cast<float4*>(p.part_o + (row * p.NP + part) * D + d) = r;
+            if (d == 0) {
+                p.part_m[row * p.NP + part] = M;
+                p.part_l[row * p.NP + part] = den;
+            }
         }
     }
 }
