@@ -23,13 +23,30 @@
 // pair, `word & 0x000f000f` two 4-bit codes, `word & 0x00f000f0` two more, times
 // 16.  2^24 joins the score scale and the output scale, the 16 the query (keys)
 // or the odd rows of the output (values).  One logic operation gives two
-// elements; 4 bits need a shift per eight.  The tile's byte order (pkv_int.cuh)
+// elements; 4 bits need a byte shuffle per eight.  The tile's byte order (pkv_int.cuh)
 // makes the pairs lie along the contraction axis in both products.
 //
 // The query is scaled by a power of two per head so that its largest element
 // is in [2^9, 2^10): every bf16 element above 2^-23 of it keeps all its bits as
-// f16.  p_t s'_t enters as an f16 head plus tail (two MMAs), 22 significant
-// bits, against a power of two that follows the largest s' the warp has seen.
+// f16.  p_t s'_t enters as an f16 head plus tail, 22 significant bits, against a
+// power of two that follows the largest s' the warp has seen: two MMAs, or one for
+// groups of up to four heads, whose tails ride in the spare columns 4 .. 7 (64 x
+// U[512, 4096] 32/32 heads, int4: 135.7 -> 128.5 us).
+//
+// A warp's step is two blocks: one barrier wait, one vote and one load of Q's
+// fragments for 32 tokens, and two independent chains of MMAs.  A ring of two steps
+// a warp and 16 warps an SM (12 for 8 bits at D = 128, by shared memory) keep 140 to
+// 210 KB of copies in flight; a third step, a fifth CTA (96 registers, which
+// spill) and CTAs of 2, 3 or 8 warps measured slower.
+//
+// Measured on one GB300 (calls replayed in a graph, share of the measured HBM copy
+// bandwidth on the bytes the call cannot do without): int8 256 x U[128, 2048],
+// 32/8 heads 96.5 us (0.98); int8 64 x U[512, 4096], 32/32 heads 187 us (1.04);
+// int4 8 x 32768, 64/8 heads 57.2 us (0.78); int4 256 x U[128, 2048], 32/8 heads
+// 66.7 us (0.76).  8 bits are bound by HBM.  4 bits halve the bytes but not the
+// instructions: 237 a block and warp plus 900 a warp for its start and end (600
+// since), issued in 54 % of the cycles; with its copies left out an earlier
+// version took 55 of its 63 us.
 #pragma once
 
 #include "pkv_decode_mma.cuh"

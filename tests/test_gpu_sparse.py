@@ -556,3 +556,33 @@ def test_binding_refusals_on_device_tensors(pk):
     read(stream=st.cuda_stream)
     torch.cuda.synchronize()
     assert pk.get_device_error() == 0
+
+
+def test_readme_example_of_an_int4_cache_and_sparse_decode():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    code = [c for c in re.findall(r"```python\n(.*?)```", text, re.S) if "int4" in c]
+    assert len(code) == 1
+    e = {}
+    exec(compile(code[0], "README.md example", "exec"), e)
+    k, q = e["k"].float().cpu().numpy(), e["q"].double().cpu().numpy()
+    kh, vh = qu.held(k, 4), qu.held(e["v"].float().cpu().numpy(), 4)
+    start = [0, int(e["lens"][0])]
+    sel = e["selected"].cpu().numpy()
+    got = e["out"].double().cpu().numpy()
+    G = e["Hq"] // e["Hkv"]
+    ref = np.zeros_like(got)
+    for s in range(e["S"]):
+        L = int(e["lens"][s])
+        nb = (L + 15) // 16
+        for h in range(e["Hkv"]):
+            js = sel[s, h][sel[s, h] >= 0]
+            assert len(js) == min(nb, e["n"]) and np.all(np.diff(js) > 0) and {0, nb - 2, nb - 1} <= set(js.tolist())
+            pos = (js[:, None] * 16 + np.arange(16)).reshape(-1)
+            pos = start[s] + pos[pos < L]
+            ref[s, h * G:(h + 1) * G] = qu.attend(q[s, h * G:(h + 1) * G], kh[None, pos, h], vh[None, pos, h], [0], [len(pos)],
+                                                  e["D"] ** -0.5)
+    assert max_error(got, ref, "bf16", TOL["bf16"], float(np.abs(vh).max())) <= TOL["bf16"]
+    # the read-back: one binary32 operation, one rounding to bf16
+    assert np.all(np.abs(e["k16"].double().cpu().numpy() - kh) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(kh) + 2.0 ** -24)
