@@ -127,9 +127,9 @@ typedef struct {
  *   Token t is written to block slot / b at offset slot % b of every KV
  *   head.  For an fp8 cache each element is stored as the E4M3 code nearest
  *   (ties to even, saturating at +-448) to binary32(x) / k_scale (v_scale).
- *   For an integer-coded pool in_dtype is PKV_BF16 or PKV_F16 and each row is
- *   encoded as described above; two blocks' tokens may be appended in any
- *   order and by concurrent calls.
+ *   For an integer-coded pool in_dtype is PKV_BF16 or PKV_F16, each row is
+ *   encoded as described above, and num_tokens * num_kv_heads stays below 2^31
+ *   (else PKV_ERR_UNSUPPORTED, as in pkv_paged_kv_read).
  *   Two tokens with the same slot race (which one lands is unspecified; in an
  *   integer-coded pool the codes of one may meet the scale of the other).
  * k_cache, v_cache: device pools in the layout above, written in place.
@@ -485,7 +485,7 @@ size_t pkv_decode_sparse_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, 
  * entry at or past the sequence's last block + 1 sets PKV_DEVERR_BLOCK_ID and
  * is skipped; a block listed twice is attended to twice.  A row whose list
  * names no token gives zeros.  Pools of every type; q, out, tables and errors as for
- * pkv_paged_attention_decode.
+ * pkv_paged_attention_decode (pkv_set_decode_path does not apply).
  * partition_blocks: list entries per split-K partition, or 0 to let the
  *   library choose.  workspace: pkv_decode_sparse_workspace_bytes(...) bytes
  *   (may be NULL when that is 0).

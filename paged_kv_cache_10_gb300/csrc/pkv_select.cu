@@ -421,7 +421,8 @@ __device__ __forceinline__ double exact_score(const SelectParams& p, const float
 // addend, with an error of at most 17 * 2^-23 of it, and a score is D / 8 MMAs
 // in two chains of at most 8, so with A = max_g |q_g|_1 * max |bound| it is within
 // 8 * 17 * 2^-23 A + 2^-23 A < 2^-15 A of the true score.  eps = 2^-14 A covers it
-// twice.  A histogram over the scores' range finds the bin that holds the k-th
+// twice; 2^-117 more covers products and sums below 2^-126, each of which may be
+// flushed (2 D of them, twice).  A histogram over the scores' range finds the bin that holds the k-th
 // highest, zooming in while the bin is wide and full; with [tl, th] around the
 // scores in it, a block above th + 2 eps is in and one below tl - 2 eps is out,
 // and the few between them are scored again, in binary32 with a far smaller
@@ -525,7 +526,7 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         big = fmaxf(big, redf[2][w]);
         q1 = fmaxf(q1, redf[3][w]);
     }
-    const float eps2 = 2.f * 0x1p-14f * q1 * big;
+    const float eps2 = 2.f * (0x1p-14f * q1 * big + 0x1p-117f);
 
     float thr = INFINITY;  // blocks above it are in
     if (k > 0) {

@@ -131,7 +131,8 @@ def test_selection_with_other_pool_types(pk):
             assert np.array_equal(got, qu.ref_select(q, bounds.double().numpy(), tables, lens, 9, 1, 1, 2))
 
 
-@pytest.mark.parametrize("case", ["equal", "zero_q", "pairs", "outlier", "near", "huge", "tiny", "neg_inf", "inf", "nan"])
+@pytest.mark.parametrize("case", ["equal", "zero_q", "pairs", "outlier", "near", "huge", "tiny", "denormal", "neg_inf", "inf", "nan",
+                                  "q_nan", "q_inf"])
 def test_selection_ties_and_extreme_scores(pk, case):
     """Equal scores go to the lowest numbers, in bands of two blocks and of all; scores next to the
     border, far outliers, overflow, infinities and NaN leave the answer defined."""
@@ -160,6 +161,15 @@ def test_selection_ties_and_extreme_scores(pk, case):
     elif case == "tiny":
         bounds *= 1e-30
         q *= 1e-8
+    elif case == "denormal":  # products below the smallest normal binary32
+        bounds *= 1e-36
+        q *= 1e-3
+    elif case == "q_nan":
+        q[0, 3, 5] = float("nan")
+        q[1] = float("nan")
+    elif case == "q_inf":
+        q[0, 3, 5] = float("inf")
+        q[1, :, 0] = float("-inf")
     elif case == "neg_inf":
         bounds[::7] = float("-inf")
     elif case == "inf":
