@@ -596,3 +596,52 @@ def test_readme_example_of_an_int4_cache_and_sparse_decode():
     assert max_error(got, ref, "bf16", TOL["bf16"], float(np.abs(vh).max())) <= TOL["bf16"]
     # the read-back: one binary32 operation, one rounding to bf16
     assert np.all(np.abs(e["k16"].double().cpu().numpy() - kh) <= (2.0 ** -8 + 2.0 ** -23) * np.abs(kh) + 2.0 ** -24)
+
+
+def test_capture_after_copies_and_across_streams(pk):
+    """In one captured graph: calls right after a host-to-device copy, a memset and a device copy, and calls
+    on a second stream forked off and joined again."""
+    rng = np.random.default_rng(53)
+    lens = [900, 40]
+    NB, tables = qu.make_tables(rng, lens)
+    pools = qu.Pools(rng, NB, 2, 128, "int8")
+    kd, vd = pools.dev()
+    t, l = dev32(tables), dev32(lens)
+    host = qu.queries(rng, 2, 8, 128, "bf16").pin_memory()
+    q, out, dense = (torch.zeros(2, 8, 128, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    bounds = torch.zeros(NB, 2, 2, 128, dtype=torch.bfloat16, device="cuda")
+    sel = torch.zeros(2, 2, 12, dtype=torch.int32, device="cuda")
+    ws = [torch.zeros(n, dtype=torch.uint8, device="cuda") for n in
+          (pk.select_blocks_workspace_bytes(2, 2, 900), pk.decode_sparse_workspace_bytes(2, 8, 128, 12, 2),
+           pk.decode_workspace_bytes(2, 8, 128, 900, 256))]
+    side = torch.cuda.Stream()
+
+    def step():
+        bounds.zero_()
+        pk.paged_key_bounds(kd, pools.desc, t, l, None, 900, bounds)
+        q.copy_(host, non_blocking=True)
+        pk.select_blocks(q, bounds, pools.desc, t, l, 900, sel, ws[0])
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            pk.paged_attention_decode(q, kd, vd, pools.desc, t, l, 900, 0.1, dense, workspace=ws[2], partition_tokens=256)
+        out.zero_()
+        pk.paged_attention_decode_sparse(q, kd, vd, pools.desc, t, l, sel, 0.1, out, workspace=ws[1], partition_blocks=2)
+        torch.cuda.current_stream().wait_stream(side)
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step()
+    for seed in range(3):
+        host.copy_(qu.queries(np.random.default_rng(seed), 2, 8, 128, "bf16"))
+        g.replay()
+        torch.cuda.synchronize()
+        want = qu.ref_select(host, bounds.double().cpu().numpy(), tables, lens, 12, 1, 1, 2)
+        assert np.array_equal(sel.cpu().numpy(), want)
+        vmax = float(np.abs(pools.vh).max())
+        ref = qu.ref_sparse(host, pools, tables, lens, want, 0.1)
+        assert max_error(out.double().cpu().numpy(), ref, "bf16", TOL["bf16"], vmax) <= TOL["bf16"]
+        ref = qu.ref_dense(host, pools, tables, lens, 0.1)
+        assert max_error(dense.double().cpu().numpy(), ref, "bf16", TOL["bf16"], vmax) <= TOL["bf16"]
+    assert pk.get_device_error() == 0
