@@ -487,8 +487,10 @@ size_t pkv_decode_sparse_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, 
  * names no token gives zeros.  Pools of every type; q, out, tables and errors as for
  * pkv_paged_attention_decode (pkv_set_decode_path does not apply).
  * partition_blocks: list entries per split-K partition, or 0 to let the
- *   library choose.  workspace: pkv_decode_sparse_workspace_bytes(...) bytes
- *   (may be NULL when that is 0).
+ *   library choose, which it does among partitions of 16 entries and more, and
+ *   of 8 for short launches whose workspace holds those.  workspace:
+ *   pkv_decode_sparse_workspace_bytes(...) bytes (may be NULL when that is 0);
+ *   with partition_blocks = 0, what it gives for 16 is enough.
  */
 pkv_status pkv_paged_attention_decode_sparse(const void* q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
                                              const void* k_cache, const void* v_cache, const pkv_cache_desc* desc,

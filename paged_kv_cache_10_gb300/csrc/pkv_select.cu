@@ -930,10 +930,38 @@ extern "C" pkv_status pkv_select_blocks(const void* q, int32_t q_dtype, int32_t 
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+// List entries per partition of the automatic choice: the dense decode's rule for
+// a sequence of the list's length, whose least is 16 blocks, but 8 where 8 still
+// leave the launch within one CTA an SM: then a CTA's chain of loads is what the
+// call waits for, and halving it gains more than the merge's doubled rows cost.
+// 1 sequence x 8 KV heads x 128 blocks, bf16: 6.4 us against 7.4 (128 and 64
+// CTAs), int8 4.9 against 5.6; 1 x 1 x 400: 5.7 against 6.9; with more CTAs, 2 x
+// 8 x 128, int8: 6.1 against 5.7.  Four blocks: 6.7, 5.4, 6.0.  A workspace that
+// holds partitions of 16 blocks only is taken too, with those.
+constexpr int kSmallPartition = 8, kSmallLaunch = 152;
+
+static bool small_lists(int64_t S, int64_t Hkv, int n) {
+    return n > kAutoMinPartition / kBlockSize && S * Hkv <= kSmallLaunch &&
+           S * Hkv * cdiv(n, kSmallPartition) <= kSmallLaunch;
+}
+
+static int auto_list_partition(int S, int Hq, const pkv_cache_desc* d, int n, size_t workspace_bytes) {
+    if (small_lists(S, d->num_kv_heads, n) &&
+        workspace_bytes >= partials_bytes(S, Hq, d->head_size, cdiv(n, kSmallPartition)))
+        return kSmallPartition;
+    const int tokens = n * kBlockSize;
+    return (is_int_pool(d->kv_dtype) ? auto_partition_int(S, d->num_kv_heads, tokens, d->kv_dtype, d->head_size)
+                                     : auto_partition(S, d->num_kv_heads, tokens, false)) /
+           kBlockSize;
+}
+
 extern "C" size_t pkv_decode_sparse_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t head_size,
                                                     int32_t num_selected, int32_t partition_blocks) {
     if (num_seqs < 0 || num_q_heads <= 0 || head_size <= 0 || num_selected <= 0 || partition_blocks < 0) return 0;
-    const int64_t NP = cdiv(num_selected, partition_blocks > 0 ? partition_blocks : kAutoMinPartition / kBlockSize);
+    // one KV head gives the automatic choice its smallest partitions
+    const int per = partition_blocks > 0 ? partition_blocks : small_lists(num_seqs, 1, num_selected) ? kSmallPartition
+                                                            : kAutoMinPartition / kBlockSize;
+    const int64_t NP = cdiv(num_selected, per);
     return NP <= 1 ? 0 : partials_bytes(num_seqs, num_q_heads, head_size, NP);
 }
 
@@ -959,12 +987,9 @@ extern "C" pkv_status pkv_paged_attention_decode_sparse(const void* q, int32_t q
         !aligned(block_tables, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4))
         return PKV_ERR_INVALID;
     const int G = num_q_heads / d->num_kv_heads;
-    const int list_tokens = num_selected * kBlockSize;
-    const int per = partition_blocks > 0 ? partition_blocks
-                    : (is_int_pool(d->kv_dtype)
-                           ? auto_partition_int(num_seqs, d->num_kv_heads, list_tokens, d->kv_dtype, d->head_size)
-                           : auto_partition(num_seqs, d->num_kv_heads, list_tokens, false)) /
-                          kBlockSize;
+    const int per = partition_blocks > 0
+                        ? partition_blocks
+                        : auto_list_partition(num_seqs, num_q_heads, d, num_selected, workspace_bytes);
     const int64_t NP = cdiv(num_selected, per);
     const size_t need = NP > 1 ? partials_bytes(num_seqs, num_q_heads, d->head_size, NP) : 0;
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 16))) return PKV_ERR_WORKSPACE;

@@ -242,7 +242,7 @@ def run_sparse(pk, pools, q, tables, lens, sel, scale, part):
 @pytest.mark.parametrize("kv,dtype", ALL_KV)
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("G", [1, 2, 4, 8])
-@pytest.mark.parametrize("n,part", [(1, 0), (13, 0), (13, 1), (40, 3), (40, 16)])
+@pytest.mark.parametrize("n,part", [(1, 0), (13, 0), (13, 1), (40, 0), (40, 3), (40, 16)])
 def test_sparse_decode_matches_64_bits(pk, kv, dtype, D, G, n, part):
     rng = np.random.default_rng(n + part + D + G)
     lens = [0, 1, 16, 17, 100, 333, 1000]
@@ -257,6 +257,33 @@ def test_sparse_decode_matches_64_bits(pk, kv, dtype, D, G, n, part):
     got = out.double().cpu().numpy()
     assert np.all(np.isfinite(got)) and np.all(got[0] == 0)
     assert max_error(got, ref, dtype, TOL[dtype], float(np.abs(pools.vh).max())) <= TOL[dtype]
+
+
+@pytest.mark.parametrize("kv,dtype", ALL_KV)
+def test_automatic_partitions_fit_the_workspace(pk, kv, dtype):
+    """A short launch splits its lists as finely as its workspace holds, and writes nothing behind it."""
+    rng = np.random.default_rng(8)
+    lens, Hkv, G, D, n = [900, 411], 2, 4, 128, 40
+    NB, tables = qu.make_tables(rng, lens)
+    pools = qu.Pools(rng, NB, Hkv, D, kv)
+    q = qu.queries(rng, len(lens), Hkv * G, D, dtype)
+    sel = random_lists(rng, lens, Hkv, n)
+    kd, vd = pools.dev()
+    sizes = [pk.decode_sparse_workspace_bytes(2, Hkv * G, D, n, part) for part in (8, 16)]
+    assert sizes[0] == pk.decode_sparse_workspace_bytes(2, Hkv * G, D, n, 0) > sizes[1]
+
+    def call(part, nbytes):
+        out = torch.full((2, Hkv * G, D), 7.0, device="cuda").to(q.dtype)
+        ws = torch.full((nbytes + 256,), 255, dtype=torch.uint8, device="cuda")
+        pk.paged_attention_decode_sparse(q.cuda(), kd, vd, pools.desc, dev32(tables), dev32(lens), dev32(sel), D ** -0.5,
+                                         out, workspace=ws[:nbytes], partition_blocks=part)
+        assert bool((ws[nbytes:] == 255).all())
+        return out
+
+    assert torch.equal(call(0, sizes[0]), call(8, sizes[0]))
+    for nbytes in (sizes[1], sizes[0] - 16):
+        assert torch.equal(call(0, nbytes), call(16, sizes[1]))
+    assert pk.get_device_error() == 0
 
 
 @pytest.mark.parametrize("kv,dtype", ALL_KV[:1] + ALL_KV[2:4])

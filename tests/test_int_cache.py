@@ -156,7 +156,12 @@ def test_sparse_refusals(pk):
     assert call(n=2 ** 28) == call(part=2 ** 28) == pk.ERR_INVALID
     need = pk.decode_sparse_workspace_bytes(2, 8, 128, 4, 1)
     assert need > 0 and pk.decode_sparse_workspace_bytes(2, 8, 128, 16, 0) == 0
-    assert pk.decode_sparse_workspace_bytes(2, 8, 128, 17, 0) == pk.decode_sparse_workspace_bytes(2, 8, 128, 17, 16) > 0
+    assert pk.decode_sparse_workspace_bytes(2, 8, 128, 17, 0) == pk.decode_sparse_workspace_bytes(2, 8, 128, 17, 8) > 0
+    # 50 sequences x 4 partitions of eight blocks are more than one CTA an SM: sixteen
+    assert pk.decode_sparse_workspace_bytes(50, 8, 128, 32, 0) == pk.decode_sparse_workspace_bytes(50, 8, 128, 32, 16)
+    assert pk.decode_sparse_workspace_bytes(38, 8, 128, 32, 0) == pk.decode_sparse_workspace_bytes(38, 8, 128, 32, 8)
+    small = pk.decode_sparse_workspace_bytes(2, 8, 128, 17, 16)
+    assert call(n=17) == call(n=17, ws=FAKE, nb=small - 1) == call(n=17, ws=FAKE + 4, nb=small) == pk.ERR_WORKSPACE
     assert call(part=1) == call(part=1, ws=FAKE, nb=need - 1) == call(part=1, ws=FAKE + 4, nb=need) == pk.ERR_WORKSPACE
     for kv in ("int8", "int4"):
         assert call(desc_of(pk, kv), dt=2) == pk.ERR_INVALID
