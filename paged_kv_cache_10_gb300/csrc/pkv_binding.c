@@ -189,9 +189,28 @@ static int pool_size(PyObject* t, const pkv_cache_desc* c, const char* name) {
     return 0;
 }
 
+static int is_int(const pkv_cache_desc* c) { return c->kv_dtype == PKV_INT8 || c->kv_dtype == PKV_INT4; }
+
 static int int_pools(const pkv_cache_desc* c, PyObject* k, PyObject* v) {
-    if (c->kv_dtype != PKV_INT8 && c->kv_dtype != PKV_INT4) return 0;
+    if (!is_int(c)) return 0;
     return pool_size(k, c, "k_cache") || pool_size(v, c, "v_cache") ? -1 : 0;
+}
+
+/* Two operands of a call on an integer-coded pool: one type, and rows for each token or query head. */
+static int int_rows(const pkv_cache_desc* c, PyObject* x, PyObject* y, int32_t n, int32_t heads, const char* what) {
+    if (!is_int(c)) return 0;
+    size_t nx, ny;
+    PyObject* d = PyObject_GetAttr(x, s_dtype);
+    if (!d) return -1;
+    const int alike = is_type(y, d);
+    Py_DECREF(d);
+    if (alike < 0 || bytes_of(x, &nx) || bytes_of(y, &ny)) return -1;
+    const size_t want = heads < 0 || c->head_size < 0 ? 0 : (size_t)n * heads * c->head_size * 2;
+    if (!alike || nx < want || ny < want) {
+        PyErr_Format(PyExc_ValueError, "%s must be of one 16-bit type and hold %zu bytes each", what, want);
+        return -1;
+    }
+    return 0;
 }
 
 static int current_device(long* dev) {
@@ -200,6 +219,14 @@ static int current_device(long* dev) {
     *dev = PyLong_AsLong(r);
     Py_DECREF(r);
     return *dev == -1 && PyErr_Occurred() ? -1 : 0;
+}
+
+/* The device that a call on an integer-coded pool expects its tensors on, that of x and current; -1 (any) otherwise. */
+static int int_device(const pkv_cache_desc* c, PyObject* x, const char* name, long* dev) {
+    void* p;
+    *dev = -1;
+    if (!is_int(c)) return 0;
+    return ptr_of(x, name, -1, &p) || current_device(dev) ? -1 : 0;
 }
 
 /* The stream's handle: the current one of the current device for None. */
@@ -254,6 +281,7 @@ static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     pkv_cache_desc c;
     int32_t type, T[1];
     void *k, *v, *slots, *kc, *vc, *st;
+    long dev;
     if (!nargs_ok(n, 8)) return NULL;
     const int i64 = is_type(a[2], t_i64);
     if (i64 < 0) return NULL;
@@ -262,9 +290,10 @@ static PyObject* py_append(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         return NULL;
     }
     if (get_desc(a[5], &c) || int_pools(&c, a[3], a[4]) || sizes(a[2], "slot_mapping", 1, 1, T) ||
-        ptr_of(a[0], "k", -1, &k) || ptr_of(a[1], "v", -1, &v) || element_type(a[0], a[6], &type) ||
-        ptr_of(a[2], "slot_mapping", -1, &slots) || ptr_of(a[3], "k_cache", -1, &kc) ||
-        ptr_of(a[4], "v_cache", -1, &vc) || stream_of(a[7], &st))
+        int_rows(&c, a[0], a[1], T[0], c.num_kv_heads, "k and v") || int_device(&c, a[0], "k", &dev) ||
+        ptr_of(a[0], "k", dev, &k) || ptr_of(a[1], "v", dev, &v) || element_type(a[0], a[6], &type) ||
+        ptr_of(a[2], "slot_mapping", dev, &slots) || ptr_of(a[3], "k_cache", dev, &kc) ||
+        ptr_of(a[4], "v_cache", dev, &vc) || stream_of(a[7], &st))
         return NULL;
     DONE(fn.append(k, v, type, T[0], (const int64_t*)slots, kc, vc, &c, st));
 }
@@ -317,9 +346,10 @@ static PyObject* py_read(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 static PyObject* py_decode(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     (void)self;
     pkv_cache_desc c;
-    int32_t type, qs[2], ts[2], max_len, part;
+    int32_t type, qs[2], ts[2], S[1], max_len, part;
     void *q, *kc, *vc, *tables, *lens, *out, *ws, *st;
     size_t wn;
+    long dev;
     if (!nargs_ok(n, 13)) return NULL;
     if (want_i32(a[4], "block_tables and seq_lens") || want_i32(a[5], "block_tables and seq_lens") ||
         get_desc(a[3], &c) || int_pools(&c, a[1], a[2]) || sizes(a[0], "q", 2, 1, qs) || sizes(a[4], "block_tables", 2, 1, ts) ||
@@ -327,9 +357,17 @@ static PyObject* py_decode(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         return NULL;
     const double scale = PyFloat_AsDouble(a[7]);
     if (scale == -1.0 && PyErr_Occurred()) return NULL;
-    if (ptr_of(a[0], "q", -1, &q) || element_type(a[0], a[11], &type) || ptr_of(a[1], "k_cache", -1, &kc) ||
-        ptr_of(a[2], "v_cache", -1, &vc) || ptr_of(a[4], "block_tables", -1, &tables) ||
-        ptr_of(a[5], "seq_lens", -1, &lens) || ptr_of(a[8], "out", -1, &out) || workspace_of(a[9], -1, &ws, &wn) ||
+    if (is_int(&c)) {
+        if (int_rows(&c, a[0], a[8], qs[0], qs[1], "q and out") || sizes(a[5], "seq_lens", 1, 1, S)) return NULL;
+        if (ts[0] < qs[0] || S[0] < qs[0]) {
+            PyErr_SetString(PyExc_ValueError, "block_tables and seq_lens must have a row for each sequence");
+            return NULL;
+        }
+    }
+    if (int_device(&c, a[0], "q", &dev) || ptr_of(a[0], "q", dev, &q) || element_type(a[0], a[11], &type) ||
+        ptr_of(a[1], "k_cache", dev, &kc) || ptr_of(a[2], "v_cache", dev, &vc) ||
+        ptr_of(a[4], "block_tables", dev, &tables) || ptr_of(a[5], "seq_lens", dev, &lens) ||
+        ptr_of(a[8], "out", dev, &out) || workspace_of(a[9], dev, &ws, &wn) ||
         stream_of(a[12], &st))
         return NULL;
     DONE(fn.decode(q, type, qs[0], qs[1], kc, vc, &c, (const int32_t*)tables, ts[1], (const int32_t*)lens, max_len,

@@ -188,3 +188,31 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(pk):
                                          torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32),
                                          torch.zeros(2, 3, 3, dtype=torch.int32), 0.1,
                                          torch.zeros(2, 4, 64, dtype=torch.bfloat16))
+
+
+@pytest.mark.parametrize("kv", ["int8", "int4"])
+def test_binding_refuses_short_operands_of_coded_pools(pk, kv):
+    """Rows that the tensors do not hold are refused before anything is launched; sound ones get as far as the
+    check for CUDA tensors."""
+    import torch
+    d = pk.CacheDesc(num_blocks=4, num_kv_heads=2, head_size=64, kv_dtype=kv)
+    pool = torch.zeros(4 * pk.block_bytes(d), dtype=torch.uint8)
+    rows = lambda n, h=2, dt=torch.bfloat16: torch.zeros(n, h, 64, dtype=dt)
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)
+
+    def append(k=rows(3), v=rows(3)):
+        pk.paged_kv_append(k, v, torch.zeros(3, dtype=torch.int64), pool, pool, d)
+
+    def decode(q=rows(3, 4), out=rows(3, 4), tables=i32(3, 4), lens=i32(3)):
+        pk.paged_attention_decode(q, pool, pool, d, tables, lens, 64, 0.1, out)
+
+    for call, bad in ((append, dict(k=rows(2))), (append, dict(v=rows(3, 1))), (append, dict(v=rows(3, dt=torch.float16))),
+                      (decode, dict(out=rows(3, 2))), (decode, dict(out=rows(3, 4, torch.float16))),
+                      (decode, dict(tables=i32(2, 4))), (decode, dict(lens=i32(2)))):
+        with pytest.raises(ValueError):
+            call(**bad)
+    for call in (append, decode):
+        with pytest.raises(TypeError, match="CUDA tensor"):
+            call()
+    with pytest.raises(TypeError, match="CUDA tensor"):  # longer ones hold the rows
+        append(k=rows(5))
