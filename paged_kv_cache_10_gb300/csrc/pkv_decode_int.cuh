@@ -27,11 +27,14 @@
 // makes the pairs lie along the contraction axis in both products.
 //
 // The query is scaled by a power of two per head so that its largest element
-// is in [2^9, 2^10): every bf16 element above 2^-23 of it keeps all its bits as
-// f16.  p_t s'_t enters as an f16 head plus tail, 22 significant bits, against a
-// power of two that follows the largest s' the warp has seen: two MMAs, or one for
-// groups of up to four heads, whose tails ride in the spare columns 4 .. 7 (64 x
-// U[512, 4096] 32/32 heads, int4: 135.7 -> 128.5 us).
+// is in [2^9, 2^10), and enters as f16: an element loses bits only below 2^-19 of
+// that (2^-22 from bf16), where a step is 2^-30 of the largest.  p_t s'_t enters
+// as an f16 head plus tail, scaled by a power of two c per head that follows the
+// largest p_t s'_t of the head's rows so far (kept between 2^6 and 2^15, so that
+// the pair's steps, 22 significant bits or 2^-25, are at most 2^-31 of it): a row
+// of a wide range that the query does not attend to takes no bits of the others.
+// Two MMAs, or one for groups of up to four heads, whose tails ride in the spare
+// columns 4 .. 7 (64 x U[512, 4096] 32/32 heads, int4: 135.7 -> 128.5 us).
 //
 // A warp's step is two blocks: one barrier wait, one vote and one load of Q's
 // fragments for 32 tokens, and two independent chains of MMAs.  A ring of two steps
@@ -60,7 +63,7 @@ struct IntCfg {
     using L = IntTile<D, BITS>;
     static constexpr int kWarps = 4;
     static constexpr int kStages = 2;
-    static constexpr int kCtasPerSm = 4;
+    static constexpr int kCtasPerSm = BITS == 8 && D == 128 ? 3 : 4;  // as many as shared memory holds
     static constexpr int kStage = 4 * L::kBytes;  // two blocks: K, V, K, V
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kBarOffset = kRing;
@@ -70,7 +73,7 @@ struct IntCfg {
     static constexpr int kBytes = kQOffset + (D / 16) * 32 * 8 + 128;  // + alignment slack
     static constexpr int kState = 8 * (D + 4) * 4;  // a warp's accumulators for the cross-warp merge
     static_assert(kState <= kStages * kStage, "the merge state reuses the warp's ring");
-    static_assert(kCtasPerSm * (kBytes + 1024) <= 228 * 1024 || BITS == 8, "residency");
+    static_assert(kCtasPerSm * (kBytes + 1024) <= 228 * 1024, "residency");
 };
 
 __device__ __forceinline__ uint2 lds64(uint32_t addr) {
@@ -115,6 +118,29 @@ __device__ __forceinline__ void code_pairs(uint32_t w, int j, uint32_t& lo, uint
         const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&hi));
         lo = *reinterpret_cast<const uint32_t*>(&d);
     }
+}
+
+constexpr float kNoScore = -3e38f;  // softmax reference before the first score
+
+// 2^e / c for a power of two c, the quotient within binary32's normal range.
+__device__ __forceinline__ float pow2_over(int e, float c) {
+    return __uint_as_float((static_cast<uint32_t>(254 + e) << 23) - __float_as_uint(c));
+}
+
+// Moves a head's scale c of its weights p s' and lim = 2^15 / c, the largest p s' that
+// it takes, the softmax maximum having moved by the factor a (1: it stays); y is the
+// largest p s' of the step against the new maximum.  The larger of y and of what was
+// seen before, taken as 2^6 / c, comes to lie in [2^6, 2^7) / c; c stays within
+// 2^+-118, lim below 2^128.  Returns the accumulators' factor.
+__device__ __forceinline__ float move_weights(float& c, float& lim, float a, float y) {
+    if (a == 1.f && y <= lim) return 1.f;
+    const int was = static_cast<int>(__float_as_uint(c) >> 23);
+    const float top = fmaxf(y, a * pow2_over(6, c));
+    const int now = min(max(127 + 6 + 127 - static_cast<int>(__float_as_uint(top) >> 23), 127 - 118), 127 + 118);
+    c = __int_as_float(now << 23);
+    lim = __int_as_float(min(127 + 15 + 127 - now, 254) << 23);
+    const int d = now - was, half = d >> 1;  // 2^d in two steps: d is within +-236
+    return a * __int_as_float((127 + half) << 23) * __int_as_float((127 + d - half) << 23);
 }
 
 template <int D, int BITS, bool FOLD, bool SPARSE>
@@ -301,10 +327,8 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     float o[KS][4];
 #pragma unroll
     for (int i = 0; i < KS; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float tA = -INFINITY, tB = -INFINITY;  // scores past these move the maxima
-    float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f, zA = 0.f, zB = 0.f;
-    uint32_t vref = 0u;  // bits of the power of two that the value scales are taken against
-    float vinv = 0.f;
+    float mA = kNoScore, mB = kNoScore, lA = 0.f, lB = 0.f, zA = 0.f, zB = 0.f;
+    float cA = 0x1p118f, cB = 0x1p118f, limA = 0x1p-103f, limB = 0x1p-103f;  // scales of the weights p s'
 
     // the lane's fragment offsets in a tile
     const uint32_t koff = g8 * L::KW + qd * (L::KW / 4);
@@ -387,41 +411,44 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
                     }
                 }
                 // Lazy references, checked lane by lane: the probabilities' maximum moves when a
-                // score passes it by 2^kRebaseLog2, the value scales' (a power of two, only up)
-                // when a scale reaches it.  Steps without a move, nearly all, reduce nothing
-                // over the warp but this vote.
+                // score passes it by 2^kRebaseLog2, the weights' scale when a weight may pass its
+                // limit (bounded by the lane's largest probability times its largest value scale).
+                // Steps without a move, nearly all, reduce nothing over the warp but this vote.
                 const float vm = fmaxf(fmaxf(vs[0][0], vs[0][1]), fmaxf(vs[1][0], vs[1][1]));
-                if (__builtin_expect(__any_sync(kFull, bA > tA || bB > tB || __float_as_uint(vm) >= vref), 0)) {
+                const float xA = bA - mA, xB = bB - mB;
+                if (__builtin_expect(__any_sync(kFull, xA > kRebaseLog2 || xB > kRebaseLog2 ||
+                                                           ex2(xA) * vm > limA || ex2(xB) * vm > limB), 0)) {
 #pragma unroll
                     for (int mask = 4; mask < 32; mask <<= 1) {
                         bA = fmaxf(bA, __shfl_xor_sync(kFull, bA, mask));
                         bB = fmaxf(bB, __shfl_xor_sync(kFull, bB, mask));
                     }
                     float alA = 1.f, alB = 1.f;
-                    if (bA > tA) {
-                        alA = ex2(mA - bA);  // 0 on the first block (mA = -inf)
+                    if (bA - mA > kRebaseLog2) {
+                        alA = ex2(mA - bA);  // 0 on the first block
                         mA = bA;
-                        tA = bA + kRebaseLog2;
                     }
-                    if (bB > tB) {
+                    if (bB - mB > kRebaseLog2) {
                         alB = ex2(mB - bB);
                         mB = bB;
-                        tB = bB + kRebaseLog2;
                     }
                     lA *= alA;
                     lB *= alB;
                     zA *= alA;
                     zB *= alB;
-                    const uint32_t vmax = __reduce_max_sync(kFull, __float_as_uint(vm));
-                    if (vmax >= vref) {
-                        const uint32_t next = (min(vmax >> 23, 251u) + 1u) << 23;
-                        const float inv = __uint_as_float((254u << 23) - next);
-                        const float f = __uint_as_float(vref) * inv;  // 0 on the first block
-                        vref = next;
-                        vinv = inv;
-                        alA *= f;
-                        alB *= f;
+                    float yA = 0.f, yB = 0.f;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        yA = fmaxf(yA, fmaxf(ex2(sv[b][0] - mA) * vs[b][0], ex2(sv[b][2] - mA) * vs[b][1]));
+                        yB = fmaxf(yB, fmaxf(ex2(sv[b][1] - mB) * vs[b][0], ex2(sv[b][3] - mB) * vs[b][1]));
                     }
+#pragma unroll
+                    for (int mask = 4; mask < 32; mask <<= 1) {
+                        yA = fmaxf(yA, __shfl_xor_sync(kFull, yA, mask));
+                        yB = fmaxf(yB, __shfl_xor_sync(kFull, yB, mask));
+                    }
+                    alA = move_weights(cA, limA, alA, yA);
+                    alB = move_weights(cB, limB, alB, yB);
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
                         o[i][0] *= alA;
@@ -439,10 +466,10 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
                     lB += p1 + p3;
                     zA = fmaf(p0, vz[b][0], fmaf(p2, vz[b][1], zA));
                     zB = fmaf(p1, vz[b][0], fmaf(p3, vz[b][1], zB));
-                    const float u0 = vs[b][0] * vinv, u1 = vs[b][1] * vinv;
+                    // (p c) s', in this order: a wide row that is not attended to gives 0, not 0 * inf
                     uint32_t h01, t01, h23, t23;
-                    pack2_split<false>(p0 * u0, p1 * u0, h01, t01);
-                    pack2_split<false>(p2 * u1, p3 * u1, h23, t23);
+                    pack2_split<false>(p0 * cA * vs[b][0], p1 * cB * vs[b][0], h01, t01);
+                    pack2_split<false>(p2 * cA * vs[b][1], p3 * cB * vs[b][1], h23, t23);
                     uint32_t pb0, pb1, pt0 = 0u, pt1 = 0u;  // tokens 0 .. 7, tokens 8 .. 15
                     if constexpr (FOLD) {
                         // columns 4 .. 7 (lanes qd >= 2) hold the same probabilities: they
@@ -502,33 +529,35 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     float2* wm = reinterpret_cast<float2*>(msc);  // [NW][4] maxima of columns 2 qd, 2 qd + 1
     float2* wl = wm + NW * 4;
     float2* wz = wl + NW * 4;
-    if (aborted) mA = mB = -INFINITY;
+    if (aborted) mA = mB = kNoScore;
     if (g8 == 0) wm[warp * 4 + qd] = make_float2(mA, mB);
     __syncthreads();
-    float MA = -INFINITY, MB = -INFINITY;
+    float MA = kNoScore, MB = kNoScore;
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
         const float2 m = wm[w * 4 + qd];
         MA = fmaxf(MA, m.x);
         MB = fmaxf(MB, m.y);
     }
-    const float scA = mA != -INFINITY ? ex2(mA - MA) : 0.f, scB = mB != -INFINITY ? ex2(mB - MB) : 0.f;
+    const float scA = aborted ? 0.f : ex2(mA - MA), scB = aborted ? 0.f : ex2(mB - MB);
     if (g8 == 0) {
         wl[warp * 4 + qd] = make_float2(scA * lA, scB * lB);
         wz[warp * 4 + qd] = make_float2(scA * zA, scB * zB);
     }
     constexpr int PW = D + 4;
     {
-        const float os = __uint_as_float(vref) * 0x1p24f, oA = os * scA, oB = os * scB;
+        // 2^24 sc / c in two factors, neither of which overflows
+        const float kA = scA * 0x1p16f, kB = scB * 0x1p16f;
+        const float oA = pow2_over(8, cA), oB = pow2_over(8, cB);
         constexpr float odd = BITS == 4 ? 0.0625f : 1.f;  // odd rows of 4-bit words come times 16
         float* ws = reinterpret_cast<float*>(ring) + 2 * qd * PW;
 #pragma unroll
         for (int i = 0; i < KS; i += 2) {  // m-tiles i, i + 1 hold four consecutive dimensions from d
             const int d = D == 128 && BITS == 8 ? 8 * g8 + 64 * (i >> 2) + 2 * (i & 3) : 2 * KS * g8 + 2 * i;
             *reinterpret_cast<float4*>(ws + d) =
-                make_float4(o[i][0] * oA, o[i][2] * (oA * odd), o[i + 1][0] * oA, o[i + 1][2] * (oA * odd));
+                make_float4(o[i][0] * kA * oA, o[i][2] * (kA * odd) * oA, o[i + 1][0] * kA * oA, o[i + 1][2] * (kA * odd) * oA);
             *reinterpret_cast<float4*>(ws + PW + d) =
-                make_float4(o[i][1] * oB, o[i][3] * (oB * odd), o[i + 1][1] * oB, o[i + 1][3] * (oB * odd));
+                make_float4(o[i][1] * kB * oB, o[i][3] * (kB * odd) * oB, o[i + 1][1] * kB * oB, o[i + 1][3] * (kB * odd) * oB);
         }
     }
     __syncthreads();
@@ -538,7 +567,7 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     for (int i4 = threadIdx.x; i4 < G * (D / 4); i4 += NW * 32) {
         const int g = i4 / (D / 4), d = 4 * (i4 % (D / 4));
         float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-        float den = 0.f, z = 0.f, M = -INFINITY;
+        float den = 0.f, z = 0.f, M = kNoScore;
 #pragma unroll
         for (int w = 0; w < NW; ++w) {
             const float* x = reinterpret_cast<const float*>(smem + w * NST * STAGE) + g * PW + d;
