@@ -184,8 +184,9 @@ pkv_status pkv_copy_blocks(void* k_cache, void* v_cache, const pkv_cache_desc* d
  * blocks are moved to CPU memory and brought back later instead of being
  * recomputed).
  *
- * k_host, v_host: host pools in the pool layout ([num_host_blocks][Hkv][16]
- *   [D] each), pinned and mapped into the device address space (e.g.
+ * k_host, v_host: host pools in the pool layout, num_host_blocks blocks of
+ *   pkv_cache_block_bytes each ([Hkv][16][D] elements, or [Hkv] tiles of an
+ *   integer-coded pool), pinned and mapped into the device address space (e.g.
  *   cudaHostAlloc with cudaHostAllocMapped, or registered with
  *   cudaHostRegisterMapped); otherwise PKV_ERR_INVALID.  The copy runs as
  *   one kernel that reads or writes host memory directly.

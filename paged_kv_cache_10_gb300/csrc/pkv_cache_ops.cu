@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(256) copy_blocks_kernel(unsigned char* kc, uns
 
 // Swap: grid (num_pairs, kCopySplit, 2 pools); moves 1/kCopySplit of one
 // block of one pool between the device pool and the host pool (pinned,
-// device-mapped memory, same [blocks][Hkv][16][D] layout) with 16-byte
+// device-mapped memory, same layout: NH blocks of block_bytes) with 16-byte
 // vectors.  direction 0: device -> host, 1: host -> device.
 __global__ void __launch_bounds__(256) swap_blocks_kernel(unsigned char* kc, unsigned char* vc, unsigned char* kh,
                                                           unsigned char* vh, const int32_t* __restrict__ pairs,

@@ -574,8 +574,13 @@ SWAP_OUT, SWAP_IN = 0, 1
 
 
 def swap_blocks(k_cache, v_cache, desc: CacheDesc, k_host, v_host, pairs, direction: int, stream=None) -> None:
-    """k_host, v_host: pinned CPU tensors [NH, Hkv, 16, D] (torch pin_memory
-    memory is mapped); pairs: int32 device [n, 2] of (device block, host block)."""
+    """k_host, v_host: pinned CPU tensors (torch pin_memory memory is mapped) of
+    NH blocks of block_bytes(desc) bytes, [NH, Hkv, 16, D] or for int8 / int4 pools
+    uint8 [NH, Hkv, tile bytes]; pairs: int32 device [n, 2] of (device block, host block)."""
+    need = int(k_host.shape[0]) * block_bytes(desc)
+    for t, n in ((k_host, "k_host"), (v_host, "v_host")):
+        if t.nbytes < need or (desc.kv_dtype in ("int8", "int4") and t.nbytes != need):
+            raise ValueError(f"{n} must hold {k_host.shape[0]} blocks of {block_bytes(desc)} bytes")
     for t, n in ((k_host, "k_host"), (v_host, "v_host")):
         if t.is_cuda or not t.is_pinned() or not t.is_contiguous():
             raise ValueError(f"{n} must be a contiguous pinned CPU tensor")
