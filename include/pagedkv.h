@@ -53,8 +53,9 @@
  * and zero of its own: lo = min x, hi = max x, scale = (hi - lo) / (2^b - 1) (0
  * where that is below 2^-126), zero = lo, code = min(rint((x - lo) * (1 /
  * scale)), 2^b - 1), each step one IEEE binary32 operation; the value held is
- * zero + scale * code.  hi - lo must be finite.  The tile of one block and KV
- * head is, instead of 16 * D elements, 16 * RB code bytes (RB = D * b / 8) and
+ * zero + scale * code.  A row with a NaN, or whose hi - lo is not finite, is held
+ * as codes 0 with scale and zero NaN: all its values read back as NaN.  The tile
+ * of one block and KV head is, instead of 16 * D elements, 16 * RB code bytes (RB = D * b / 8) and
  * then 16 pairs (scale, zero): 16 * (RB + 8) bytes, so a pool is
  * [num_blocks][num_kv_heads][16 * (RB + 8)] bytes (pkv_cache_block_bytes).  Byte
  * k of token t's row holds element k, or for 4 bits elements 2k (low half) and

@@ -7,7 +7,9 @@
 //   lo = min x, hi = max x, scale = (hi - lo) / (2^b - 1), zero = lo,
 //   code = min(rint((x - lo) * (1 / scale)), 2^b - 1),  value = zero + scale * code
 // each step one IEEE binary32 operation, so that the codes are the same on
-// every machine.  A scale below 2^-126 (a constant row) is stored as 0.
+// every machine.  A scale below 2^-126 (a constant row) is stored as 0.  A row with
+// a NaN, or whose hi - lo is not finite, is held as codes 0 with scale and zero NaN,
+// so that it reads back as NaN instead of as numbers that it did not hold.
 //
 // A tile (16 tokens of one block and KV head, in one pool) is 16 * RB code
 // bytes (RB = D * b / 8) followed by 16 pairs (scale, zero), one contiguous
@@ -120,19 +122,20 @@ __device__ __forceinline__ float2 int_encode16(const uint4 (&x)[2], uint32_t (&w
     P2 mn = v[0], mx = v[0];
 #pragma unroll
     for (int i = 1; i < 8; ++i) {
-        mn = __hmin2(mn, v[i]);
-        mx = __hmax2(mx, v[i]);
+        mn = __hmin2_nan(mn, v[i]);
+        mx = __hmax2_nan(mx, v[i]);
     }
     P2 key;
-    key.x = __hmin(mn.x, mn.y);
-    key.y = __hneg(__hmax(mx.x, mx.y));
+    key.x = __hmin_nan(mn.x, mn.y);
+    key.y = __hneg(__hmax_nan(mx.x, mx.y));
 #pragma unroll
     for (int m = 1; m < D / 16; m <<= 1) {
         const uint32_t o = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<const uint32_t*>(&key), m);
-        key = __hmin2(key, *reinterpret_cast<const P2*>(&o));
+        key = __hmin2_nan(key, *reinterpret_cast<const P2*>(&o));
     }
-    const float lo = to_float(key.x), hi = -to_float(key.y);
-    float scale = div_const<BITS>(__fsub_rn(hi, lo));
+    const float lo = to_float(key.x), hi = -to_float(key.y), range = __fsub_rn(hi, lo);
+    const bool finite = range < INFINITY;  // false for NaN
+    float scale = div_const<BITS>(range);
     if (!(scale >= 0x1p-126f)) scale = 0.f;
     const float inv = scale > 0.f ? __frcp_rn(scale) : 0.f;
     // rint by adding 2^23 (round to nearest, ties to even, like rint): the code is
@@ -155,8 +158,9 @@ __device__ __forceinline__ float2 int_encode16(const uint4 (&x)[2], uint32_t (&w
             for (int i = 0; i < 4; ++i) c[i] = c[2 * i] + (c[2 * i + 1] << 4);  // low byte: both codes
             w[r][0] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
         }
+        if (!finite) w[r][0] = w[r][1] = 0u;
     }
-    return make_float2(scale, lo);
+    return finite ? make_float2(scale, lo) : make_float2(__int_as_float(0x7fffffff), __int_as_float(0x7fffffff));
 }
 
 // Stores the code bytes of elements 8c .. 8c + 7.

@@ -39,9 +39,10 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, RowDiv v) {
 
 // Append into an integer-coded pool: one group of D / 16 lanes per row (t, h),
 // blockIdx.y = 0 keys, 1 values.  Lanes of a warp whose row is padding or out
-// of range still take part in the group's shuffles.
+// of range still take part in the group's shuffles.  Eight CTAs an SM, four a pool,
+// leave a thread 32 registers.
 template <int D, int BITS, typename IT>
-__global__ void __launch_bounds__(256) append_int_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
+__global__ void __launch_bounds__(256, 8) append_int_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
                                                          const int64_t* __restrict__ slots, unsigned char* kc,
                                                          unsigned char* vc, uint32_t rows, RowDiv heads,
                                                          int64_t num_slots, unsigned int* err) {
