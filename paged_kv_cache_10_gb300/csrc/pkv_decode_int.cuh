@@ -591,8 +591,11 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
         } else {
             *reinterpret_cast<float4*>(p.part_o + (row * p.NP + part) * D + d) = r;
             if (d == 0) {
-                p.part_m[row * p.NP + part] = M;
-                p.part_l[row * p.NP + part] = den;
+                // NaN (of a score or a value) outweighs every other partition in the merge, which
+                // leaves out partitions without a positive sum: the row is NaN however it is split
+                const bool nan = !(den == den) || !(z == z);
+                p.part_m[row * p.NP + part] = nan ? 3.4e38f : M;
+                p.part_l[row * p.NP + part] = nan ? 1.f : den;
             }
         }
     }
