@@ -452,8 +452,10 @@ size_t pkv_select_blocks_workspace_bytes(int32_t num_seqs, int32_t num_kv_heads,
 /*
  * Block selection.  The score of block j of sequence s for KV head h is
  *     max over the query heads g of h of  sum_d max(q_gd lo_d, q_gd hi_d)
- * with (lo, hi) the block's bounds, taken exactly (as real numbers; a NaN score
- * counts as the lowest).  Row (s, h) of selected, device int32 [num_seqs]
+ * with (lo, hi) the block's bounds, ordered as real numbers (by binary64 sums of
+ * exact products where binary32 cannot tell, so to 2^-46 of sum_d |q_gd| max(|lo_d|,
+ * |hi_d|); a NaN score counts as the lowest, and so does that of a block whose
+ * keys are NaN in some channel throughout, whose bounds there are (inf, -inf)).  Row (s, h) of selected, device int32 [num_seqs]
  * [num_kv_heads][num_selected], receives logical block numbers in ascending
  * order: the first sink_blocks and the last recent_blocks blocks of the
  * sequence and those of the highest scores among the others, ties to the

@@ -428,7 +428,8 @@ __device__ __forceinline__ double exact_score(const SelectParams& p, const float
 // and the few between them are scored again, in binary32 with a far smaller
 // bound and, where that leaves an order open, in 64 bits, and ranked by (score,
 // number).  So the answer is that of exact arithmetic whatever the order of the
-// binary32 sums.
+// binary32 sums.  Where A is not below 2^126 they may have overflowed on the way
+// to a finite score, and every block is scored in 64 bits.
 //
 // Bound by latency, a dozen barriers and three chains of loads: 5 us after the
 // scores for 8 rows of 512 blocks, 13 us for 256 rows of 2000.  64-bit scores for
@@ -526,7 +527,8 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
         big = fmaxf(big, redf[2][w]);
         q1 = fmaxf(q1, redf[3][w]);
     }
-    const float eps2 = 2.f * (0x1p-14f * q1 * big + 0x1p-117f);
+    const float A = q1 * big;  // from 2^126 on sums may have overflowed: every block in the band
+    const float eps2 = A < 0x1p126f ? 2.f * (0x1p-14f * A + 0x1p-117f) : INFINITY;
 
     float thr = INFINITY;  // blocks above it are in
     if (k > 0) {
