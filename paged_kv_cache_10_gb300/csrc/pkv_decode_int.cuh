@@ -179,10 +179,10 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     const int list_len = (SPARSE ? p.nsel : p.MB) - j0;
     const auto entry = [&](int k) {  // lane 2i + u: block u of this warp's step k + i
         const int j = 2 * (warp + (k + (lane >> 1)) * NW) + (lane & 1);
-        return j < list_len ? __ldg(list + j) : -1;
+        return j < list_len ? load_live(list + j) : -1;
     };
     int next = entry(0);
-    int len = __ldg(p.seq_lens + s);
+    int len = load_live(p.seq_lens + s);
     const int cap = p.MB * kBlockSize;
     bool bad = len < 0 || len > cap;
     len = len < 0 ? 0 : (len > cap ? cap : len);

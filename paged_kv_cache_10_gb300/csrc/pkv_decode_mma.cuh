@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     // Sequence length, clamped to the block table's reach and to the
     // partitions this launch covers; the sequence's own range starts after
     // its shared prefix (cascade decode) or at 0.
-    int L = __ldg(p.seq_lens + s);
+    int L = load_live(p.seq_lens + s);
     const int Lcap = p.MB * kBlockSize;
     bool bad = L < 0 || L > Lcap;
     L = L < 0 ? 0 : (L > Lcap ? Lcap : L);
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     auto issue_next = [&](const int stage) {  // warp-uniform call; stage = k_issue % NST
         if ((k_issue & 31) == 0) {
             const int k = k_issue + lane;
-            tbl = k < nb_w ? __ldg(bt + static_cast<int64_t>(k) * NW) : -1;
+            tbl = k < nb_w ? load_live(bt + static_cast<int64_t>(k) * NW) : -1;
             if constexpr (SPARSE) tbl = sparse_block(p, s, tbl, L, val);
         }
         const int phys = __shfl_sync(kFull, tbl, k_issue & 31);

@@ -182,6 +182,15 @@ __device__ __forceinline__ __nv_bfloat16 from_float<BF16>(float x) { return __fl
 // visible; returns at once for a launch without that dependency.
 __device__ __forceinline__ void wait_primary_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Load of what a kernel before this one on the stream may have written while this
+// one, a programmatic dependent, was resident already: an ordinary coherent load,
+// which the wait above orders.  __ldg and const __restrict__ pointers are for data
+// that nobody writes as long as the kernel lives.
+template <typename T>
+__device__ __forceinline__ T load_live(const T* p) {
+    return *p;
+}
+
 // Lets the launch that programmatically depends on this grid start its
 // CTAs once every CTA of this grid has made this call (or exited).
 __device__ __forceinline__ void allow_dependent_launch() {

@@ -42,8 +42,8 @@ __device__ __forceinline__ uint32_t quotient(uint32_t n, RowDiv v) {
 // of range still take part in the group's shuffles.  Eight CTAs an SM, four a pool,
 // leave a thread 32 registers.
 template <int D, int BITS, typename IT>
-__global__ void __launch_bounds__(256, 8) append_int_kernel(const uint4* __restrict__ k, const uint4* __restrict__ v,
-                                                         const int64_t* __restrict__ slots, unsigned char* kc,
+__global__ void __launch_bounds__(256, 8) append_int_kernel(const uint4* k, const uint4* v,
+                                                         const int64_t* slots, unsigned char* kc,
                                                          unsigned char* vc, uint32_t rows, RowDiv heads,
                                                          int64_t num_slots, unsigned int* err) {
     using L = IntTile<D, BITS>;
@@ -64,9 +64,9 @@ __global__ void __launch_bounds__(256, 8) append_int_kernel(const uint4* __restr
             const uint32_t t = quotient(row, heads);
             h = row - t * heads.d;
             const uint4* p = src + static_cast<int64_t>(row) * (2 * LPR) + c;
-            x[0] = __ldg(p);
-            x[1] = __ldg(p + LPR);
-            slot = __ldg(slots + t);
+            x[0] = load_live(p);
+            x[1] = load_live(p + LPR);
+            slot = load_live(slots + t);
             if (slot >= num_slots) {
                 if (h == 0 && c == 0 && !value) report(err, PKV_DEVERR_SLOT);
                 slot = -1;
@@ -88,9 +88,9 @@ __global__ void __launch_bounds__(256, 8) append_int_kernel(const uint4* __restr
 
 // Read by slot: D / 16 lanes per row (t, h), blockIdx.y = 0 keys, 1 values.
 template <int D, int KV, typename OT>
-__global__ void __launch_bounds__(256) read_kernel(const unsigned char* __restrict__ kc,
-                                                   const unsigned char* __restrict__ vc,
-                                                   const int64_t* __restrict__ slots, uint4* k_out, uint4* v_out,
+__global__ void __launch_bounds__(256) read_kernel(const unsigned char* kc,
+                                                   const unsigned char* vc,
+                                                   const int64_t* slots, uint4* k_out, uint4* v_out,
                                                    uint32_t rows, RowDiv heads, int64_t num_slots, float k_scale,
                                                    float v_scale, unsigned int* err) {
     constexpr int LPR = D / 16, RPC = 256 / LPR;
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(256) read_kernel(const unsigned char* __restri
     const int c = threadIdx.x % LPR;
     for (uint32_t row = blockIdx.x * RPC + threadIdx.x / LPR; row < rows; row += gridDim.x * RPC) {
         const uint32_t t = quotient(row, heads), h = row - t * heads.d;
-        const int64_t slot = __ldg(slots + t);
+        const int64_t slot = load_live(slots + t);
         if (slot < 0) continue;
         if (slot >= num_slots) {
             if (h == 0 && c == 0 && !value) report(err, PKV_DEVERR_SLOT);

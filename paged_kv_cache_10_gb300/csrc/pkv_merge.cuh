@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(256) merge_kernel(const DecodeParams p) {
             float m_u = -INFINITY, l_u = 0.f;
             if (lane < cnt) {
                 const int j = wr + (c0 + lane) * WPR;
-                l_u = __ldg(pl + j);
-                m_u = __ldg(pm + j);
+                l_u = load_live(pl + j);
+                m_u = load_live(pm + j);
             }
             float o[kMergeChunk][VD];
 #pragma unroll
@@ -90,10 +90,10 @@ __global__ void __launch_bounds__(256) merge_kernel(const DecodeParams p) {
                 if (u < cnt) {
                     const float* src = po + static_cast<int64_t>(wr + (c0 + u) * WPR) * D;
                     if constexpr (VD == 4) {
-                        const float4 x = __ldg(reinterpret_cast<const float4*>(src));
+                        const float4 x = load_live(reinterpret_cast<const float4*>(src));
                         o[u][0] = x.x; o[u][1] = x.y; o[u][2] = x.z; o[u][3] = x.w;
                     } else {
-                        const float2 x = __ldg(reinterpret_cast<const float2*>(src));
+                        const float2 x = load_live(reinterpret_cast<const float2*>(src));
                         o[u][0] = x.x; o[u][1] = x.y;
                     }
                 } else {

@@ -226,7 +226,7 @@ struct Unit {
 __device__ bool prefill_unit(const PrefillParams& p, int64_t lin, int RQ, bool rep, Unit& u) {
     int s, qt;
     if (p.work) {
-        const int w = __ldg(p.work + lin / p.Hkv);
+        const int w = load_live(p.work + lin / p.Hkv);
         u.h = static_cast<int>(lin % p.Hkv);
         if (w < 0 || w >= p.S * p.num_qtiles) {
             if (rep) report(p.err, PKV_DEVERR_SEQ_LEN);
@@ -239,10 +239,10 @@ __device__ bool prefill_unit(const PrefillParams& p, int64_t lin, int RQ, bool r
         u.h = static_cast<int>((lin / p.num_qtiles) % p.Hkv);
         s = static_cast<int>(lin / (static_cast<int64_t>(p.num_qtiles) * p.Hkv));
     }
-    u.q0 = __ldg(p.query_start + s);
-    const int q1 = __ldg(p.query_start + s + 1);
+    u.q0 = load_live(p.query_start + s);
+    const int q1 = load_live(p.query_start + s + 1);
     u.n = q1 - u.q0;
-    const int L = __ldg(p.seq_lens + s);
+    const int L = load_live(p.seq_lens + s);
     if (u.q0 < 0 || u.n < 0 || q1 > p.T || L < u.n || L > p.MB * kBlockSize) {
         if (rep) report(p.err, PKV_DEVERR_SEQ_LEN);
         return false;
@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kMaxPerLane; ++i) {
                     const int mi = lane + 32 * i;
                     bs[i] = seq0;
-                    if (mi < ntiles * RQ && mrow0 + mi < members) bs[i] = __ldg(p.group_members + m0 + mrow0 + mi);
+                    if (mi < ntiles * RQ && mrow0 + mi < members) bs[i] = load_live(p.group_members + m0 + mrow0 + mi);
                 }
                 if (lane == 0) mbar_arrive_expect_tx(q_full, ntiles * kOpBytes);
                 __syncwarp();
@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // use: lane l holds the id of block 32 * batch + l
             auto load_ids = [&](int batch) {
                 const int idx = batch * 32 + lane;
-                return idx < nblk ? __ldg(u.bt + idx) : 0;
+                return idx < nblk ? load_live(u.bt + idx) : 0;
             };
             int ids_cur = load_ids(0);
             int ids_nxt = load_ids(1);
@@ -806,7 +806,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // prefix pass: this row's batch row, read now so the epilogue
             // does not wait for it
             const int member_row =
-                kPrefix && row_valid ? __ldg(p.group_members + m0 + mrow0 + X * RQ + rq) : -1;
+                kPrefix && row_valid ? load_live(p.group_members + m0 + mrow0 + X * RQ + rq) : -1;
             float m_ref = -INFINITY, l = 0.f;
             for (int j = 0; j < ntx; ++j) {
                 ok = warp_all(tc::wait_spin(s_full + X, (tp + j) & 1));

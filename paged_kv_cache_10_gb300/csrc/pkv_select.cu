@@ -27,16 +27,16 @@ namespace {
 // keys -> bounds: 2.6 us for the 256 blocks of a decode step (5.6 MB), 4.1 us for
 // 8 x 1024 new tokens (19 MB, 4.6 TB/s).
 template <int D, int KV, typename OT>
-__global__ void __launch_bounds__(128) key_bounds_kernel(const unsigned char* __restrict__ kc,
-                                                         const int32_t* __restrict__ block_tables, int MB,
-                                                         const int32_t* __restrict__ seq_lens,
-                                                         const int32_t* __restrict__ new_lens, int max_new, int NB,
-                                                         int Hkv, float k_scale, unsigned char* __restrict__ bounds,
+__global__ void __launch_bounds__(128) key_bounds_kernel(const unsigned char* kc,
+                                                         const int32_t* block_tables, int MB,
+                                                         const int32_t* seq_lens,
+                                                         const int32_t* new_lens, int max_new, int NB,
+                                                         int Hkv, float k_scale, unsigned char* bounds,
                                                          unsigned int* err) {
     wait_primary_grid();  // a programmatic dependent of the kernel before it on the stream
     const int s = blockIdx.y;
-    const int len = __ldg(seq_lens + s);
-    const int fresh = new_lens ? __ldg(new_lens + s) : len;
+    const int len = load_live(seq_lens + s);
+    const int fresh = new_lens ? load_live(new_lens + s) : len;
     if (len < 0 || len > MB * kBlockSize || fresh < 0 || fresh > len || fresh > max_new) {
         if (threadIdx.x == 0 && blockIdx.x == 0) report(err, PKV_DEVERR_SEQ_LEN);
         return;
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(128) key_bounds_kernel(const unsigned char* __
     if (fresh == 0) return;
     const int j = (len - fresh) / kBlockSize + blockIdx.x;
     if (j > (len - 1) / kBlockSize) return;
-    const int id = __ldg(block_tables + static_cast<int64_t>(s) * MB + j);
+    const int id = load_live(block_tables + static_cast<int64_t>(s) * MB + j);
     if (id < 0 || id >= NB) {
         if (threadIdx.x == 0) report(err, PKV_DEVERR_BLOCK_ID);
         return;
@@ -96,7 +96,7 @@ struct SelectParams {
 
 // The row's blocks, clamped to what the launch covers.
 __device__ __forceinline__ int row_blocks(const SelectParams& p, int s, bool& bad) {
-    int len = __ldg(p.seq_lens + s);
+    int len = load_live(p.seq_lens + s);
     const int cap = min(p.MB, p.cols);
     bad = len < 0 || (len > 0 && (len - 1) / kBlockSize >= cap);
     return len <= 0 ? 0 : min((len - 1) / kBlockSize + 1, cap);
@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) 
     // none); a pair is loaded two pairs ahead of its use.
     const auto ids_of = [&](int k) {
         const int j = (first + 2 * k) * 16 + lane;
-        return 2 * k + (lane >> 4) < tiles && j < nblk ? __ldg(table + j) : -1;
+        return 2 * k + (lane >> 4) < tiles && j < nblk ? load_live(table + j) : -1;
     };
     int ids[2] = {ids_of(0), ids_of(1)};
     const auto issue = [&](int t, int stage) {  // warp-uniform; tiles in order
@@ -217,7 +217,7 @@ __global__ void __launch_bounds__(128) block_score_kernel(const SelectParams p) 
         for (int j = 0; j < CH; ++j) {
             const int c = 4 * j + qd;  // chunk of the 2 D row: the first D / 8 are lo's
             const bool low = c < D / 8;
-            const uint4 x = live ? __ldg(row + (low ? c : c - D / 8)) : make_uint4(0u, 0u, 0u, 0u);
+            const uint4 x = live ? load_live(row + (low ? c : c - D / 8)) : make_uint4(0u, 0u, 0u, 0u);
             const uint32_t w[4] = {x.x, x.y, x.z, x.w};
             uint32_t y[4];
 #pragma unroll
@@ -333,7 +333,7 @@ __device__ __forceinline__ uint64_t order64(double x) {
 template <int D, typename T>
 __device__ __forceinline__ bool lane_bounds(const SelectParams& p, int s, int h, int j, float* lo, float* hi) {
     constexpr int V = D / 32;
-    const int id = j >= 0 ? __ldg(p.block_tables + static_cast<int64_t>(s) * p.MB + j) : -1;
+    const int id = j >= 0 ? load_live(p.block_tables + static_cast<int64_t>(s) * p.MB + j) : -1;
     const bool ok = id >= 0 && id < p.NB;
     const unsigned char* b =
         p.bounds + (static_cast<int64_t>(ok ? id : 0) * p.Hkv + h) * (4 * D) + (threadIdx.x & 31) * (V * 2);
