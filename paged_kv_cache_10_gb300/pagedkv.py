@@ -21,6 +21,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpagedkv.so")
+BINDING_PATH = os.path.join(_HERE, "_pkv_binding.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_OOM, ERR_CUDA, ERR_WORKSPACE, ERR_NOT_FOUND = range(7)
 F16, BF16, FP8_E4M3, INT8, INT4 = 0, 1, 2, 3, 4
@@ -158,32 +159,29 @@ def lib():
         fn.restype = res
         fn.argtypes = args
     _lib = L
-    _bind(L)
     return L
 
 
 _native = None
 
 
-def _bind(L) -> None:
-    """Loads the marshalling module and gives it the library's addresses."""
+def _calls():
+    """The marshalling module of the per-step calls, loaded and given the library's addresses at the first of
+    them (raises if it has not been built or does not load; it is kept only once it is complete)."""
     global _native
-    path = os.path.join(_HERE, "_pkv_binding.so")
-    if not os.path.exists(path):
-        raise RuntimeError(f"{path} is missing: build it with paged_kv_cache_10_gb300.build.build()")
-    spec = importlib.util.spec_from_file_location("_pkv_binding", path)
+    if _native is not None:
+        return _native
+    L = lib()
+    if not os.path.exists(BINDING_PATH):
+        raise RuntimeError(f"{BINDING_PATH} is missing: build it with paged_kv_cache_10_gb300.build.build()")
+    spec = importlib.util.spec_from_file_location("_pkv_binding", BINDING_PATH)
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     names = ("pkv_paged_kv_append", "pkv_paged_kv_read", "pkv_paged_attention_decode", "pkv_paged_key_bounds",
              "pkv_select_blocks", "pkv_paged_attention_decode_sparse", "pkv_cache_block_bytes")
     m.bind(torch, {n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _stream)
     _native = m
-
-
-def _calls():
-    if _native is None:
-        lib()
-    return _native
+    return m
 
 
 def status_string(status: int) -> str:
