@@ -17,7 +17,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpagedkv.so")
-BINDING = os.path.join(HERE, "_pkv_binding.so")  # CPython module: marshalling of the per-step calls
+# CPython module (marshalling of the per-step calls): it uses the interpreter's full API, so its name carries
+# that interpreter's ABI tag, and each interpreter builds and loads its own
+BINDING = os.path.join(HERE, "_pkv_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
+BINDING_SOURCE = "pkv_binding.c"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2", "--expt-relaxed-constexpr"]
@@ -33,18 +36,27 @@ def sources():
     return sorted(f for f in os.listdir(CSRC) if f.endswith((".cu", ".cpp")))
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _stale(target: str, files) -> bool:
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    deps = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    deps.append(os.path.join(HERE, "..", "include", "pagedkv.h"))
-    deps.append(os.path.abspath(__file__))
-    return any(os.path.getmtime(d) > t for d in deps)
+    deps = [os.path.join(CSRC, f) for f in files]
+    deps += [os.path.join(HERE, "..", "include", "pagedkv.h"), os.path.abspath(__file__)]
+    return any(os.path.getmtime(d) > os.path.getmtime(target) for d in deps)
+
+
+def _compile_binding() -> None:
+    cmd = ["gcc", "-O2", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_path("include"),
+           os.path.join(CSRC, BINDING_SOURCE), "-o", BINDING + ".tmp"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(BINDING + ".tmp", BINDING)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
+    if force or _stale(BINDING, [BINDING_SOURCE]):
+        _compile_binding()
+    if not force and not _stale(LIB, [f for f in os.listdir(CSRC) if f != BINDING_SOURCE]):
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
@@ -63,16 +75,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
         return obj, r.stderr
 
-    def compile_binding():
-        cmd = ["gcc", "-O2", "-fPIC", "-shared", "-Wall", "-I", sysconfig.get_path("include"),
-               os.path.join(CSRC, "pkv_binding.c"), "-o", BINDING + ".tmp"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
-        os.replace(BINDING + ".tmp", BINDING)
-
     srcs = sources()
-    compile_binding()
     with ThreadPoolExecutor(max(1, min(len(srcs), os.cpu_count() or 4))) as ex:
         results = list(ex.map(compile_one, srcs))
     if verbose:

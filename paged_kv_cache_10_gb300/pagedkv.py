@@ -14,6 +14,7 @@ from __future__ import annotations
 import ctypes
 import importlib.util
 import os
+import sysconfig
 from dataclasses import dataclass
 
 import numpy as np
@@ -21,7 +22,7 @@ import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpagedkv.so")
-BINDING_PATH = os.path.join(_HERE, "_pkv_binding.so")
+BINDING_PATH = os.path.join(_HERE, "_pkv_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_OOM, ERR_CUDA, ERR_WORKSPACE, ERR_NOT_FOUND = range(7)
 F16, BF16, FP8_E4M3, INT8, INT4 = 0, 1, 2, 3, 4

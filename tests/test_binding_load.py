@@ -59,3 +59,19 @@ def test_threads_that_come_first_at_once(pk):
     for t in threads:
         t.join()
     assert len(errors) == 8 and all(isinstance(e, TypeError) and "CUDA tensor" in str(e) for e in errors)
+
+
+def test_the_module_is_the_running_interpreters(pk, monkeypatch):
+    """Its name carries the interpreter's ABI tag, and a build for another interpreter neither takes this one's
+    module for its own nor compiles the library again."""
+    import importlib.machinery
+    import os
+    from paged_kv_cache_10_gb300 import build
+    assert pk.BINDING_PATH == build.BINDING and os.path.exists(build.BINDING)
+    assert pk.BINDING_PATH.endswith("_pkv_binding" + importlib.machinery.EXTENSION_SUFFIXES[0])
+    assert importlib.machinery.EXTENSION_SUFFIXES[0] != ".so"
+    made = []
+    monkeypatch.setattr(build, "BINDING", build.BINDING.replace("_pkv_binding.", "_pkv_binding.other-"))
+    monkeypatch.setattr(build, "_compile_binding", lambda: made.append(1))
+    monkeypatch.setattr(build, "ThreadPoolExecutor", None)  # compiling the library would need it
+    assert build.build() == build.LIB and made == [1]
