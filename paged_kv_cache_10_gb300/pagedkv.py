@@ -251,6 +251,21 @@ def _int_pools(desc: CacheDesc, *pools) -> None:
                 raise ValueError(f"an {desc.kv_dtype} pool must hold {desc.num_blocks} blocks of {block_bytes(desc)} bytes")
 
 
+def _int_operands(desc: CacheDesc, q, out, num_seqs: int, block_tables, seq_lens, **others) -> None:
+    """What an attention call over an int8 / int4 pool is given besides the pools: q and out of one 16-bit type that
+    hold a row for each token and query head, tables and lengths for each sequence, all on the current device."""
+    if desc.kv_dtype not in ("int8", "int4"):
+        return
+    want = int(q.shape[0]) * int(q.shape[1]) * desc.head_size * 2
+    if q.dtype != out.dtype or q.nbytes < want or out.nbytes < want:
+        raise ValueError(f"q and out must be of one 16-bit type and hold {want} bytes each")
+    if block_tables.dim() != 2 or block_tables.shape[0] < num_seqs or seq_lens.numel() < num_seqs:
+        raise ValueError("block_tables and seq_lens must have a row for each sequence")
+    for n, t in dict(q=q, out=out, block_tables=block_tables, seq_lens=seq_lens, **others).items():
+        if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
+            raise ValueError(f"{n} is on cuda:{t.get_device()}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 def block_bytes(desc: CacheDesc) -> int:
     """Bytes of one block (every KV head) of one pool, 0 for a description that is not supported.  An
     int8 / int4 pool is a uint8 tensor [num_blocks, num_kv_heads, tile bytes]."""
@@ -346,6 +361,7 @@ def paged_attention_decode_noalloc(q, k_cache, v_cache, desc: CacheDesc, block_t
     if block_tables.dtype != torch.int32 or seq_lens.dtype != torch.int32:
         raise TypeError("block_tables and seq_lens must be int32")
     _int_pools(desc, k_cache, v_cache)
+    _int_operands(desc, q, out, S, block_tables, seq_lens, k_cache=k_cache, v_cache=v_cache)
     st = lib().pkv_paged_attention_decode_noalloc(_dev_ptr(q, "q"), _dtype_code(q, q_dtype), S, Hq,
                                                   _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"),
                                                   _desc(desc)[0], _dev_ptr(block_tables, "block_tables"),
@@ -502,12 +518,18 @@ def paged_attention_prefill(q, k_cache, v_cache, desc: CacheDesc, query_start, m
     """Causal paged prefill: q, out [T, Hq, D]; query_start int32 [S + 1],
     block_tables int32 [S, MB], seq_lens int32 [S] (device tensors);
     work_units: optional device int32 CTA order from prefill_plan;
-    workspace: device buffer of prefill_workspace_bytes(...) bytes (fp8 pools)."""
+    workspace: device buffer of prefill_workspace_bytes(...) bytes (fp8, int8 and
+    int4 pools, which are copied to 16 bits first)."""
     T, Hq = int(q.shape[0]), int(q.shape[1])
     S = int(seq_lens.shape[0])
     if int(query_start.shape[0]) != S + 1:
         raise ValueError("query_start must have num_seqs + 1 entries")
     _int_pools(desc, k_cache, v_cache)
+    if desc.kv_dtype in ("int8", "int4") and any(t is not None and t.dtype != torch.int32 for t in
+                                                 (query_start, block_tables, seq_lens, work_units)):
+        raise TypeError("query_start, block_tables, seq_lens and work_units must be int32")
+    _int_operands(desc, q, out, S, block_tables, seq_lens, k_cache=k_cache, v_cache=v_cache, query_start=query_start,
+                  work_units=work_units, workspace=workspace)
     nw = 0 if work_units is None else int(work_units.numel())
     wp = _dev_ptr(work_units, "work_units") if nw else None
     ws_ptr, ws_bytes = None, 0

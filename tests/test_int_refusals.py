@@ -30,3 +30,62 @@ def test_swap_refuses_host_pools_that_do_not_hold_the_blocks(pk, kv):
             swap(*(torch.zeros(3, 2, 16, 64, dtype=torch.uint8) for _ in range(2)))
     with pytest.raises(ValueError, match="pinned"):  # the right size gets as far as the next check
         swap(host(), host())
+
+
+@pytest.mark.parametrize("kv", ["int8", "int4"])
+def test_noalloc_decode_and_prefill_refuse_what_decode_refuses(pk, kv):
+    """Short, mixed and foreign operands of the calls over coded pools that are marshalled in Python; sound ones get
+    as far as the check for CUDA tensors."""
+    d = pk.CacheDesc(num_blocks=4, num_kv_heads=2, head_size=64, kv_dtype=kv)
+    pool = torch.zeros(4 * pk.block_bytes(d), dtype=torch.uint8)
+    rows = lambda n, h=4, dt=torch.bfloat16: torch.zeros(n, h, 64, dtype=dt)
+
+    def noalloc(q=rows(3), out=rows(3), tables=i32(3, 4), lens=i32(3), k=pool):
+        pk.paged_attention_decode_noalloc(q, k, pool, d, tables, lens, 64, 0.1, out)
+
+    def prefill(q=rows(9), out=rows(9), start=i32(4), tables=i32(3, 4), lens=i32(3), k=pool, work=None):
+        pk.paged_attention_prefill(q, k, pool, d, start, 3, tables, lens, 0.1, out, work_units=work)
+
+    for call, n in ((noalloc, 3), (prefill, 9)):
+        for bad in (dict(out=rows(n - 1)), dict(out=rows(n, 2)), dict(out=rows(n, dt=torch.float16)), dict(tables=i32(2, 4)),
+                    dict(tables=i32(12)), dict(k=pool[:-16]), dict(q=torch.zeros(n, 4, 64, dtype=torch.uint8),
+                                                                    out=torch.zeros(n, 4, 64, dtype=torch.uint8))):
+            with pytest.raises(ValueError):
+                call(**bad)
+        with pytest.raises(TypeError, match="must be int32"):
+            call(tables=torch.zeros(3, 4, dtype=torch.int64))
+        with pytest.raises(TypeError, match="CUDA tensor"):
+            call()
+    with pytest.raises(ValueError):
+        noalloc(lens=i32(2))
+    with pytest.raises(ValueError):
+        prefill(start=i32(3))
+    for bad in (dict(start=torch.zeros(4, dtype=torch.int64)), dict(work=torch.zeros(3, dtype=torch.int64))):
+        with pytest.raises(TypeError, match="must be int32"):
+            prefill(**bad)
+
+
+def test_operands_on_another_device_are_refused(pk, monkeypatch):
+    """With stand-ins for tensors of a second device: nothing here needs one."""
+    class On:
+        is_cuda, dtype, nbytes, shape = True, torch.bfloat16, 3 * 4 * 64 * 2, (3, 4, 64)
+
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+        def dim(self):
+            return 2
+
+        def numel(self):
+            return 3
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    d = pk.CacheDesc(num_blocks=4, num_kv_heads=2, head_size=64, kv_dtype="int8")
+    sound = dict(q=On(0), out=On(0), num_seqs=3, block_tables=On(0), seq_lens=On(0), k_cache=On(0), workspace=None)
+    pk._int_operands(d, **sound)
+    for n in ("q", "out", "block_tables", "seq_lens", "k_cache", "workspace"):
+        with pytest.raises(ValueError, match=f"{n} is on cuda:1"):
+            pk._int_operands(d, **{**sound, n: On(1)})
