@@ -176,6 +176,15 @@ static int bytes_of(PyObject* t, size_t* out) {
     return *out == (size_t)-1 && PyErr_Occurred() ? -1 : 0;
 }
 
+/* A tensor whose type may be declared by name has n elements of 16 bits. */
+static int bytes16(PyObject* t, size_t n, const char* name) {
+    size_t got;
+    if (bytes_of(t, &got)) return -1;
+    if (got == 2 * n) return 0;
+    PyErr_Format(PyExc_TypeError, "%s must be of a 16-bit type", name);
+    return -1;
+}
+
 /* A pool tensor has the size its description gives (a description that is not
  * supported is left to the call's own checks). */
 static int pool_size(PyObject* t, const pkv_cache_desc* c, const char* name) {
@@ -380,7 +389,6 @@ static PyObject* py_bounds(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     pkv_cache_desc c;
     int32_t type, ts[2], S[1], N[1], bs[4], max_new;
     void *kc, *tables, *lens, *fresh = NULL, *bounds, *st;
-    size_t nb;
     long dev;
     if (!nargs_ok(n, 9)) return NULL;
     if (want_i32(a[2], "block_tables and seq_lens") || want_i32(a[3], "block_tables and seq_lens") ||
@@ -399,11 +407,7 @@ static PyObject* py_bounds(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     const int32_t want[4] = {c.num_blocks, c.num_kv_heads, 2, c.head_size};
     for (int i = 0; i < 4; ++i)
         if (same(bs[i], want[i], "bounds must have shape [num_blocks, num_kv_heads, 2, head_size]")) return NULL;
-    if (element_type(a[6], a[7], &type) || bytes_of(a[6], &nb)) return NULL;
-    if (nb != (size_t)bs[0] * bs[1] * 2 * bs[3] * 2) {
-        PyErr_SetString(PyExc_TypeError, "bounds must be of a 16-bit type");
-        return NULL;
-    }
+    if (element_type(a[6], a[7], &type) || bytes16(a[6], (size_t)bs[0] * bs[1] * 2 * bs[3], "bounds")) return NULL;
     if (ptr_of(a[3], "seq_lens", -1, &lens) || current_device(&dev) || ptr_of(a[3], "seq_lens", dev, &lens) ||
         pool_size(a[0], &c, "k_cache") || ptr_of(a[0], "k_cache", dev, &kc) ||
         ptr_of(a[2], "block_tables", dev, &tables) || (a[4] != Py_None && ptr_of(a[4], "new_lens", dev, &fresh)) ||
@@ -426,7 +430,7 @@ static int lists_ok(PyObject* q, PyObject* tables, PyObject* lens, PyObject* sel
         same(ts[0], qs[0], "block_tables and seq_lens must have one row per sequence") ||
         same(S[0], qs[0], "block_tables and seq_lens must have one row per sequence"))
         return -1;
-    return 0;
+    return bytes16(q, (size_t)qs[0] * qs[1] * qs[2], "q");
 }
 
 /* select(q, bounds, desc, block_tables, seq_lens, max_seq_len, selected, workspace, sink_blocks, recent_blocks, q_dtype,
@@ -452,6 +456,7 @@ static PyObject* py_select(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     const int32_t want[4] = {c.num_blocks, c.num_kv_heads, 2, c.head_size};
     for (int i = 0; i < 4; ++i)
         if (same(bs[i], want[i], "bounds must have shape [num_blocks, num_kv_heads, 2, head_size]")) return NULL;
+    if (bytes16(a[1], (size_t)bs[0] * bs[1] * 2 * bs[3], "bounds")) return NULL;
     if (as_i32(a[5], &max_len) || as_i32(a[8], &sink) || as_i32(a[9], &recent) || element_type(a[0], a[10], &type) ||
         ptr_of(a[0], "q", -1, &q) || current_device(&dev) || ptr_of(a[0], "q", dev, &q) ||
         ptr_of(a[1], "bounds", dev, &bounds) || ptr_of(a[3], "block_tables", dev, &tables) ||

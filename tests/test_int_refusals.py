@@ -89,3 +89,19 @@ def test_operands_on_another_device_are_refused(pk, monkeypatch):
     for n in ("q", "out", "block_tables", "seq_lens", "k_cache", "workspace"):
         with pytest.raises(ValueError, match=f"{n} is on cuda:1"):
             pk._int_operands(d, **{**sound, n: On(1)})
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int4"])
+def test_selection_and_sparse_decode_refuse_elements_that_are_not_16_bits(pk, kv):
+    """A type declared by name does not make a tensor of bytes hold as many elements as its shape says."""
+    d = pk.CacheDesc(num_blocks=4, num_kv_heads=2, head_size=64, kv_dtype=kv)
+    tables, lens, sel = i32(3, 4), i32(3), i32(3, 2, 2)
+    pool = torch.zeros(4 * pk.block_bytes(d), dtype=torch.uint8)
+    for dt, err in ((torch.uint8, "16-bit"), (torch.float32, "16-bit"), (torch.int16, "CUDA tensor")):
+        q, bounds = torch.zeros(3, 4, 64, dtype=dt), torch.zeros(4, 2, 2, 64, dtype=dt)
+        with pytest.raises(TypeError, match=err):
+            pk.select_blocks(q, bounds, d, tables, lens, 64, sel, None, q_dtype="bf16")
+        with pytest.raises(TypeError, match=err):
+            pk.paged_attention_decode_sparse(q, pool, pool, d, tables, lens, sel, 0.1, q, q_dtype="bf16")
+        with pytest.raises(TypeError, match=err):
+            pk.paged_key_bounds(pool, d, tables, lens, None, 64, bounds, bounds_dtype="bf16")
