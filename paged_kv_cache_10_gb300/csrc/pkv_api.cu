@@ -326,7 +326,8 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
                   : int_pool ? auto_partition_int(num_seqs, d->num_kv_heads, max_seq_len, d->kv_dtype, d->head_size)
                              : auto_partition(num_seqs, d->num_kv_heads, max_seq_len, work != nullptr);
     const int64_t NP = max_seq_len > 0 ? ceil_div(max_seq_len, P) : 1;
-    if (NP > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+    // positions, and the end of a row's last partition, are 32-bit in the kernels
+    if (NP * P > 0x7fffffff || max_blocks_per_seq > 0x7fffffff / kBlockSize) return PKV_ERR_UNSUPPORTED;
     const size_t need = workspace_bytes(num_seqs, num_q_heads, d->head_size, max_seq_len, P);
     if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;
 

@@ -105,3 +105,14 @@ def test_selection_and_sparse_decode_refuse_elements_that_are_not_16_bits(pk, kv
             pk.paged_attention_decode_sparse(q, pool, pool, d, tables, lens, sel, 0.1, q, q_dtype="bf16")
         with pytest.raises(TypeError, match=err):
             pk.paged_key_bounds(pool, d, tables, lens, None, 64, bounds, bounds_dtype="bf16")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "int8", "int4"])
+def test_decode_refuses_positions_past_32_bits(pk, kv):
+    import ctypes
+    L = pk.lib()
+    at = 1 << 20  # never followed
+    d = ctypes.byref(pk.CacheDesc(num_blocks=8, num_kv_heads=2, head_size=128, kv_dtype=kv).c())
+    call = lambda MB, mx, P: L.pkv_paged_attention_decode(at, 1, 2, 4, at, at, d, at, MB, at, mx, 0.1, at, at, 1 << 40, P, None)
+    assert call(2 ** 27, 64, 0) == pk.ERR_UNSUPPORTED                       # 2^31 tokens of table
+    assert call(2 ** 27 - 1, 2 ** 31 - 16, 2 ** 30 + 16) == pk.ERR_UNSUPPORTED  # two partitions end past 2^31
