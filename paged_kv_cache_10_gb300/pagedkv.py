@@ -295,6 +295,8 @@ def copy_blocks(k_cache, v_cache, desc: CacheDesc, pairs, num_pairs: int | None 
     n = int(pairs.shape[0]) if num_pairs is None else int(num_pairs)
     if pairs.dtype != torch.int32:
         raise TypeError("pairs must be int32")
+    if pairs.numel() < 2 * n:
+        raise ValueError("pairs must hold num_pairs pairs")
     _int_pools(desc, k_cache, v_cache)
     st = lib().pkv_copy_blocks(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _desc(desc)[0],
                                _dev_ptr(pairs, "pairs") if n > 0 else None, n, _stream(stream))
@@ -607,6 +609,8 @@ def swap_blocks(k_cache, v_cache, desc: CacheDesc, k_host, v_host, pairs, direct
             raise ValueError(f"{n} must be a contiguous pinned CPU tensor")
     _int_pools(desc, k_cache, v_cache)
     n = int(pairs.shape[0])
+    if pairs.numel() < 2 * n or (n and pairs.dtype != torch.int32):
+        raise ValueError("pairs must be int32 [n, 2]")
     st = lib().pkv_swap_blocks(_dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _desc(desc)[0],
                                k_host.data_ptr(), v_host.data_ptr(), int(k_host.shape[0]),
                                _dev_ptr(pairs, "pairs") if n else None, n, int(direction), _stream(stream))

@@ -116,3 +116,19 @@ def test_decode_refuses_positions_past_32_bits(pk, kv):
     call = lambda MB, mx, P: L.pkv_paged_attention_decode(at, 1, 2, 4, at, at, d, at, MB, at, mx, 0.1, at, at, 1 << 40, P, None)
     assert call(2 ** 27, 64, 0) == pk.ERR_UNSUPPORTED                       # 2^31 tokens of table
     assert call(2 ** 27 - 1, 2 ** 31 - 16, 2 ** 30 + 16) == pk.ERR_UNSUPPORTED  # two partitions end past 2^31
+
+
+def test_copy_and_swap_refuse_lists_without_the_pairs(pk, monkeypatch):
+    d = pk.CacheDesc(num_blocks=4, num_kv_heads=1, head_size=64, kv_dtype="int8")
+    pool = torch.zeros(4, pk.block_bytes(d), dtype=torch.uint8)
+    for pairs, n in ((i32(6), None), (i32(2, 2), 3), (i32(3), 2)):
+        with pytest.raises(ValueError, match="pairs"):
+            pk.copy_blocks(pool, pool, d, pairs, n)
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        pk.copy_blocks(pool, pool, d, i32(6), 3)
+    monkeypatch.setattr(torch.Tensor, "is_pinned", lambda t: True)
+    for pairs in (i32(6), torch.zeros(3, 2, dtype=torch.int64)):
+        with pytest.raises(ValueError, match="pairs"):
+            pk.swap_blocks(pool, pool, d, pool, pool, pairs, pk.SWAP_OUT)
+    with pytest.raises(TypeError, match="CUDA tensor"):
+        pk.swap_blocks(pool, pool, d, pool, pool, i32(3, 2), pk.SWAP_OUT)
