@@ -17,7 +17,8 @@ bounded sample of the same workload.  ``--impl reference`` times that oracle
 alone, as the reference arm.  The default run (the Llama-7B-shaped MHA
 workload on one GPU) also times every other decode config under ``configs``
 and the chunked prefill (bf16 and fp8 pools), the host prefix cache and block
-swap under ``next``; ``--workload prefill_*`` times a prefill step instead.
+swap under ``next`` (headline figures in the line, the whole of it on standard
+error); ``--workload prefill_*`` times a prefill step instead.
 
 With ``--gpus N`` (torchrun) every rank runs its own replica of the workload
 on its own GPU (the path has no exchange step; no collective touches the
@@ -1222,6 +1223,41 @@ def run_reference(args, rank, world):
     }
 
 
+LINE_LIMIT = 2600  # characters of the printed line: readers that keep the end of the output get it whole
+
+
+def printed_line(line: dict) -> str:
+    """The JSON line for standard output.  A line longer than LINE_LIMIT is printed without its prose and with each
+    entry of ``configs`` and ``next`` as its headline figures; main() sends the whole of it to standard error."""
+    full = json.dumps(line)
+    if len(full) <= LINE_LIMIT:
+        return full
+
+    def keep(d, *names):
+        return {k: d[k] for k in names if k in d}
+
+    out = dict(line)
+    for part in ("configs", "next"):
+        if part in out:
+            out[part] = {name: {**keep(d, "us_per_step", "value", *(("unit",) if part == "next" else ())), **{k: d[k]["GB/s"] for k in d if
+                                                                              isinstance(d[k], dict) and "GB/s" in d[k]},
+                                **({"frac": d["roofline"]["frac"]} if "roofline" in d else {}),
+                                **({"ok": d["parity"]["within_tolerance"]} if "parity" in d else {})}
+                         for name, d in out[part].items()}
+    if "e2e" in out and "copies" in out["e2e"]:
+        out["e2e"] = {**out["e2e"], "copies": "every step, both ways, over its neighbours' kernels"}
+    for part, names in (("parity", ("rows", "tokens", "max_abs_err", "tol", "within_tolerance", "pools_bit_exact")),
+                        ("cpu_baseline", ("value", "unit", "cores", "kind", "sample")),
+                        ("roofline", ("bound", "achieved", "peak", "unit", "frac", "traffic", "peak_kind", "kernel",
+                                      "mean_launch_us", "algorithmic_bytes_per_launch", "algorithmic_flops_per_launch"))):
+        if part in out:
+            out[part] = keep(out[part], *names)
+    out.pop("kv_utilisation", None)
+    out["config"] = {k: v for k, v in out.get("config", {}).items() if k != "bytes_per_step"}
+    out["whole_line"] = "stderr"
+    return json.dumps(out, separators=(",", ":"))
+
+
 def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -1285,7 +1321,10 @@ def main(argv=None):
             import torch.distributed as dist
             dist.destroy_process_group()
     if line is not None:
-        print(json.dumps(line), flush=True)
+        text = printed_line(line)
+        if "whole_line" in text:
+            print(json.dumps(line), file=sys.stderr, flush=True)
+        print(text, flush=True)
 
 
 if __name__ == "__main__":
