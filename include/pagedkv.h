@@ -244,7 +244,8 @@ size_t pkv_decode_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t
  * Implemented: block_size 16; head_size 64 or 128; num_q_heads / num_kv_heads
  *   in {1, 2, 4, 8}; pools f16, bf16, fp8 E4M3, or integer-coded (q f16 or
  *   bf16; one tensor-core kernel, which pkv_set_decode_path does not change;
- *   a NaN score or value makes the rows of out that it enters NaN).
+ *   a NaN score or value makes the rows of out that it enters NaN, and so
+ *   does an element of q of 2^119 or more).
  */
 pkv_status pkv_paged_attention_decode(const void* q, int32_t q_dtype, int32_t num_seqs,
                                       int32_t num_q_heads, const void* k_cache, const void* v_cache,

@@ -301,8 +301,9 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
             amax = fmaxf(amax, v.x);
             sum += v.y;
         }
-        // 2^ex with amax * 2^ex in [2^9, 2^10), kept within 2^+-100
-        const int ex = min(max(9 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), -100), 100);
+        // 2^ex with amax * 2^ex in [2^9, 2^10); 2^(24 - ex), the scores' factor, stays in binary32's
+        // range, so that an element of 2^119 or more becomes infinite and one below 2^-118 loses bits
+        const int ex = min(max(9 + 127 - static_cast<int>(__float_as_uint(amax) >> 23), -103), 127);
         const float up = __int_as_float((ex + 127) << 23);
         const float hi = BITS == 8 ? up : up * 0.0625f;  // odd elements of 4-bit words come times 16
 #pragma unroll
@@ -316,7 +317,7 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
                                                             pack2<false>(e[m][2 * j + 1] * hi, e[m][2 * j + 1 + R] * hi));
             }
         }
-        const float sf = p.qk_scale * (__int_as_float((127 - ex) << 23) * 0x1p24f), qs = p.qk_scale * sum;
+        const float sf = p.qk_scale * __int_as_float((127 + 24 - ex) << 23), qs = p.qk_scale * sum;
         sfA = __shfl_sync(kFull, sf, 8 * qd);
         sfB = __shfl_sync(kFull, sf, 8 * qd + 4);
         qsA = __shfl_sync(kFull, qs, 8 * qd);

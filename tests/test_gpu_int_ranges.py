@@ -180,3 +180,16 @@ def test_values_near_the_ends_of_binary32(pk, kv, size):
     ks = [rng.standard_normal((L, Hkv, D)) for L in (60, 17)]
     vs = [rng.standard_normal((L, Hkv, D)) * size for L in (60, 17)]
     Rows(rng, ks, vs, kv).check(pk, q, scale, "dense")
+
+
+@pytest.mark.parametrize("way", ["dense", "sparse_split"])
+@pytest.mark.parametrize("e", [-124, -120, -105, 100, 110, 116])
+@pytest.mark.parametrize("kv", KVS)
+def test_queries_near_the_ends_of_binary32(pk, kv, e, way):
+    """Queries of 2^e against keys of 2^-e: scores of a few nats, neither lost nor overflowing."""
+    rng = np.random.default_rng(23)
+    D, Hkv, scale = 128, 2, 128 ** -0.5
+    q = (qu.queries(rng, 2, Hkv * 4, D, "f16", 0.5).double().clamp(-3, 3) * 2.0 ** e).to(torch.bfloat16)
+    ks = [rng.standard_normal((L, Hkv, D)).clip(-3, 3) * 2.0 ** -e for L in (200, 17)]
+    vs = [rng.standard_normal((L, Hkv, D)) for L in (200, 17)]
+    Rows(rng, ks, vs, kv).check(pk, q, scale, way)
