@@ -205,10 +205,10 @@ int auto_partition(int S, int Hkv, int max_seq_len, bool planned) {
 // The same for integer-coded pools.  Where one round of resident CTAs gives each
 // row ten partitions or more, that round is all: a second one costs its start
 // and its partials (one sequence of 32768 tokens, eight KV heads, int4: 608 CTAs
-// 15.0 us, 1024 CTAs 19.3; int8: 344 CTAs 17.7 us, 1024 CTAs 24.5).  With fewer
-// partitions a row, several rounds even out what a round leaves idle (8 x 32768
-// tokens, int4: 1216 CTAs 60.7 us, 576 CTAs 62.4; 16 x U[1000, 32768]: 31.8
-// against 34.4).
+// 13.9 us, 1024 CTAs 16.7; int8: 344 CTAs 13.1 us, 1024 CTAs 19.5).  With fewer
+// partitions a row, several rounds even out what a round leaves idle (16 x U[1000,
+// 32768] tokens, eight KV heads, int4: 62.4 us against 119.8 in one round, int8 91.0
+// against 96.8; 8 x 32768, where a round comes out whole, int4 59.3 against 59.4).
 int auto_partition_int(int S, int Hkv, int max_seq_len, int kv_dtype, int D) {
     const int64_t units = std::max<int64_t>(1, static_cast<int64_t>(S) * Hkv);
     const int64_t parts = num_sms() * static_cast<int64_t>(kv_dtype == PKV_INT8 && D == 128 ? 3 : 4) / units;

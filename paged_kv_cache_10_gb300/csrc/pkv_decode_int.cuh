@@ -34,7 +34,8 @@
 // the pair's steps, 22 significant bits or 2^-25, are at most 2^-31 of it): a row
 // of a wide range that the query does not attend to takes no bits of the others.
 // Two MMAs, or one for groups of up to four heads, whose tails ride in the spare
-// columns 4 .. 7 (64 x U[512, 4096] 32/32 heads, int4: 135.7 -> 128.5 us).
+// columns 4 .. 7 (64 x U[512, 4096] 32/32 heads, int4, when it was taken: 135.7 ->
+// 128.5 us).
 //
 // A warp's step is two blocks: one barrier wait, one vote and one load of Q's
 // fragments for 32 tokens, and two independent chains of MMAs.  A ring of two steps
@@ -44,12 +45,12 @@
 //
 // Measured on one GB300 (calls replayed in a graph, share of the measured HBM copy
 // bandwidth on the bytes the call cannot do without): int8 256 x U[128, 2048],
-// 32/8 heads 96.5 us (0.98); int8 64 x U[512, 4096], 32/32 heads 187 us (1.04);
-// int4 8 x 32768, 64/8 heads 57.2 us (0.78); int4 256 x U[128, 2048], 32/8 heads
-// 66.7 us (0.76).  8 bits are bound by HBM.  4 bits halve the bytes but not the
-// instructions: 237 a block and warp plus 900 a warp for its start and end (600
-// since), issued in 54 % of the cycles; with its copies left out an earlier
-// version took 55 of its 63 us.
+// 32/8 heads 96.3 us (0.98); int8 64 x U[512, 4096], 32/32 heads 187 us (1.04);
+// int4 8 x 32768, 64/8 heads 58.8 us (0.76); int4 256 x U[128, 2048], 32/8 heads
+// 66.1 us (0.72).  8 bits are bound by HBM.  4 bits halve the bytes but not the
+// instructions: 243 a block and warp plus 850 a warp for its start and end, issued
+// in 54 % of the cycles; with its copies left out an earlier version took 55 of its
+// 63 us.  Following the largest p s' costs the 4 bits 1.3 to 2.4 of these us.
 #pragma once
 
 #include "pkv_decode_mma.cuh"

@@ -8,13 +8,15 @@
 // that a row's loads and stores stay contiguous over its lanes), so a row's
 // minimum and maximum are 2 or 3 shuffle steps and no shared memory is used.
 //
-// Measured on one GB300: 8192 tokens x 8 heads x 128 at 4 bits written and read
-// back 18.1 us, 0.62 of the measured copy bandwidth on 75.8 MB (11.2 us).  Under
-// the profiler, with cold caches, the append takes 12.2 us, bound by its
-// instructions (63 % of the issue slots), the read 9.9, bound by its chain slot ->
-// codes -> store.  One round of eight resident CTAs an SM, four a pool, beats a
-// row's share a CTA (18.7 against 19.8 us), sixteen elements a lane beat eight
-// (22.2 us).  The 64 tokens of a decode step are latency: 2.5 us a launch.
+// Measured on one GB300: 8192 tokens x 8 heads x 128 at 4 bits written in 10.3 us
+// and read back in 9.8, 18.4 together, 0.61 of the measured copy bandwidth on 75.8
+// MB (11.2 us); at 8 bits 26.5 and 14.3 (7.6 each).  Neither fills a unit (append,
+// cold: 32 % of DRAM, 64 % of the issue slots; read: 10 %, 54 %): a group of lanes
+// has one row in flight an iteration and waits for its loads.  At 8 bits the append
+// waits for its stores too, value codes two bytes at a time: 2.5 M sector writes
+// for 0.56 M sectors of codes.  One round of eight resident CTAs an SM, four a pool,
+// beats a row's share a CTA (18.7 against 19.8 us), sixteen elements a lane beat
+// eight (22.2 us).  The 64 tokens of a decode step are latency: 1.6 to 2.7 us a launch.
 #include <cstdint>
 
 #include "pkv_append.cuh"

@@ -936,10 +936,10 @@ extern "C" pkv_status pkv_select_blocks(const void* q, int32_t q_dtype, int32_t 
 // a sequence of the list's length, whose least is 16 blocks, but 8 where 8 still
 // leave the launch within one CTA an SM: then a CTA's chain of loads is what the
 // call waits for, and halving it gains more than the merge's doubled rows cost.
-// 1 sequence x 8 KV heads x 128 blocks, bf16: 6.4 us against 7.4 (128 and 64
-// CTAs), int8 4.9 against 5.6; 1 x 1 x 400: 5.7 against 6.9; with more CTAs, 2 x
-// 8 x 128, int8: 6.1 against 5.7.  Four blocks: 6.7, 5.4, 6.0.  A workspace that
-// holds partitions of 16 blocks only is taken too, with those.
+// 1 sequence x 8 KV heads x 128 blocks, bf16: 5.8 us against 7.2 (128 and 64
+// CTAs), int8 5.5 against 6.3; 1 x 1 x 400, bf16: 5.9 against 7.0; with more CTAs, 2
+// x 8 x 128, int8: 6.6 against 6.3 (bf16 6.8 against 7.2).  Four blocks: 6.2, 6.1,
+// 6.1.  A workspace that holds partitions of 16 blocks only is taken too, with those.
 constexpr int kSmallPartition = 8, kSmallLaunch = 152;
 
 static bool small_lists(int64_t S, int64_t Hkv, int n) {
