@@ -193,3 +193,26 @@ def test_queries_near_the_ends_of_binary32(pk, kv, e, way):
     ks = [rng.standard_normal((L, Hkv, D)).clip(-3, 3) * 2.0 ** -e for L in (200, 17)]
     vs = [rng.standard_normal((L, Hkv, D)) for L in (200, 17)]
     Rows(rng, ks, vs, kv).check(pk, q, scale, way)
+
+
+@pytest.mark.parametrize("seed", range(16))
+@pytest.mark.parametrize("kv", KVS)
+def test_rows_of_every_size_at_any_score(pk, kv, seed):
+    """Value ranges over 2^+-40 and scores over tens of nats, row by row and at random; constant and zero rows."""
+    rng = np.random.default_rng(1000 + seed)
+    D, Hkv, G = int(rng.choice([64, 128])), int(rng.choice([1, 3])), int(rng.choice([1, 2, 4, 8]))
+    dtype, way, scale = ["bf16", "f16"][seed % 2], WAYS[seed % 4], D ** -0.5
+    spread = 40 if dtype == "bf16" else 12  # outputs within f16's range
+    lens = [int(x) for x in rng.integers(1, 600, 4)]
+    q = torch.from_numpy(np.abs(rng.standard_normal((4, Hkv * G, D))) + 0.5).to(qu.TORCH[dtype])
+    unit = float(q.double().sum(-1).mean()) * scale
+    ks, vs = [], []
+    for L in lens:
+        k = rng.standard_normal((L, Hkv, D)) * 0.1 + rng.standard_normal((L, Hkv, 1)) * 15 / unit
+        v = rng.standard_normal((L, Hkv, D)) * np.exp2(rng.uniform(-spread, spread, (L, Hkv, 1)))
+        v[rng.random(L) < 0.1] = 0.0
+        flat = rng.random(L) < 0.1
+        v[flat] = v[flat][..., :1]
+        ks.append(k)
+        vs.append(v)
+    Rows(rng, ks, vs, kv).check(pk, q, scale, way)
