@@ -506,6 +506,78 @@ pkv_status pkv_paged_attention_decode_sparse(const void* q, int32_t q_dtype, int
                                              int32_t partition_blocks, void* stream);
 
 /*
+ * Scored attention: decode and prefill whose scores are capped, fall with the
+ * distance and are masked.  The pages describe plain softmax attention only;
+ * models that cap their scores, attend through a sliding window, carry no
+ * positions but a distance bias, or pack documents into a sequence need these.
+ * The score of the query at position p with the key at position t is
+ *     x = scale * q.k
+ *     x = cap * tanh(x / cap)             (cap > 0)
+ *     x = x - slopes[i] * |p - t|         (slopes given; i the query head)
+ * for every t with t >= first, t > p - window (window > 0), and t <= p or t <
+ * prefix; other keys, whatever they and their values hold, take no part.  A row
+ * that no key is left for gives zeros.  Keys that no row of a launch's unit of work
+ * reaches (in front of a window or of the first position) are not read.
+ *
+ *   cap: 0 for none, else from 2^-20 to 2^20 (and scale / cap, times k_scale for an
+ *     fp8 pool, finite).  tanh is within 2^-22 of 1, and of itself for small scores.
+ *   window: 0 for none.
+ *   slopes: device float [num_q_heads], or NULL.
+ *   first: device int32, or NULL; a negative entry counts as 0.  Decode: [num_seqs],
+ *     the first position of each sequence (padding in front, or the start of the
+ *     last document).  Prefill: [num_tokens], of each row of q (documents packed
+ *     into a sequence).
+ *   prefix_lens: prefill only (decode: NULL): device int32 [num_seqs], or NULL.
+ *     Positions below it are visible to the rows before them too (a prefix
+ *     attended to in both directions); an entry above the length counts as the
+ *     length.
+ * Positions are places in the cache: after an eviction (pkv_paged_kv_compact)
+ * they are no longer the tokens' own, and a window or a distance bias counts
+ * cached tokens.
+ */
+typedef struct {
+    float cap;
+    int32_t window;
+    const float* slopes;
+    const int32_t* first;
+    const int32_t* prefix_lens;
+} pkv_score_mod;
+
+/* Workspace bytes of pkv_paged_attention_decode_scored (0 on invalid sizes, or
+ * when none is needed).  partition_tokens = 0 sizes for the automatic choice's
+ * largest case. */
+size_t pkv_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t head_size,
+                                         int32_t max_seq_len, int32_t window, int32_t partition_tokens,
+                                         int32_t with_weights);
+
+/*
+ * pkv_paged_attention_decode with such scores (score NULL: plain ones), over
+ * every pool type.  The query of sequence s sits at position seq_lens[s] - 1.
+ * partition_tokens divides what a row may span: max_seq_len tokens, or with a
+ * window those of the blocks it touches.  A length above max_seq_len rounded up to whole
+ * blocks sets PKV_DEVERR_SEQ_LEN, and that row may lose tokens.
+ * weights: device float [num_blocks][num_kv_heads][block_size], or NULL.  Cached
+ *   token t of sequence s receives, for each KV head, its share of the softmax
+ *   summed over that head's query heads (num_q_heads / num_kv_heads in all for a
+ *   row), the measure that pkv_select_tokens evicts by.
+ * new_lens: device int32 [num_seqs]: the entries of the last new_lens[s] tokens
+ *   are set; those of the others are added to.  NULL: every token's is set, so
+ *   that weights holds this step's shares alone.  An entry below 0 or above the length sets
+ *   PKV_DEVERR_SEQ_LEN and is clamped.  Entries outside the batch's sequences stay
+ *   as they are.  Sequences of one call that share a block race on its entries
+ *   where they are added to.  A row with a NaN score leaves its shares unspecified.
+ * workspace: pkv_decode_scored_workspace_bytes(...) bytes (may be NULL when that is
+ *   0), in use until the call's kernels have finished.
+ */
+pkv_status pkv_paged_attention_decode_scored(const void* q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
+                                             const void* k_cache, const void* v_cache, const pkv_cache_desc* desc,
+                                             const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                             const int32_t* seq_lens, int32_t max_seq_len, float scale,
+                                             const pkv_score_mod* score, float* weights, const int32_t* new_lens,
+                                             void* out, void* workspace, size_t workspace_bytes,
+                                             int32_t partition_tokens, void* stream);
+
+/*
  * Paged (chunked) prefill attention, causal, on the tensor cores.  Prefill
  * processes a prompt's tokens together; chunked prefill cuts a long prompt
  * into chunks that run in successive iterations, each attending to the KV

@@ -217,6 +217,28 @@ int auto_partition_int(int S, int Hkv, int max_seq_len, int kv_dtype, int D) {
     return static_cast<int>(std::max<int64_t>(P, kAutoMinPartition));
 }
 
+pkv_status check_score_mod(const pkv_score_mod* m, float scale, const pkv_cache_desc* d) {
+    if (!(m->cap >= 0.f) || m->window < 0 || (reinterpret_cast<uintptr_t>(m->slopes) & 3u) ||
+        (reinterpret_cast<uintptr_t>(m->first) & 3u) || (reinterpret_cast<uintptr_t>(m->prefix_lens) & 3u))
+        return PKV_ERR_INVALID;
+    if (m->cap > 0.f) {
+        if (m->cap < 0x1p-20f || m->cap > 0x1p20f) return PKV_ERR_INVALID;
+        const float y = scale * (d->kv_dtype == PKV_FP8_E4M3 ? d->k_scale : 1.f) / m->cap;
+        if (!(y < 3.0e38f && y > -3.0e38f)) return PKV_ERR_INVALID;
+    }
+    return PKV_OK;
+}
+
+void set_score_mod(DecodeParams& p, const pkv_score_mod& m, float scale, const pkv_cache_desc* d) {
+    if (m.cap > 0.f) {
+        p.qk_scale = scale * (d->kv_dtype == PKV_FP8_E4M3 ? d->k_scale : 1.f) / m.cap;
+        p.cap_out = m.cap * kLog2e;
+    }
+    p.window = m.window;
+    p.slopes = m.slopes;
+    p.first = m.first;
+}
+
 size_t partials_bytes(int64_t S, int64_t Hq, int64_t D, int64_t NP) {
     // m, l and o rows, each region 256-byte aligned
     const int64_t rows = S * Hq * NP;
@@ -278,12 +300,32 @@ struct FusedAppend {
     const int32_t* cow_src;  // [num_seqs] or null
 };
 
+// What scored decode adds to a call.
+struct Scored {
+    pkv_score_mod mod;
+    float* weights;           // [NB][Hkv][16] or null
+    const int32_t* new_lens;  // [num_seqs] or null
+};
+
+// Most tokens a row of a scored launch spans, from the start of its first block.
+int64_t scored_span(int64_t max_seq_len, int64_t window) {
+    const int64_t most = window > 0 ? std::min<int64_t>(max_seq_len, window + kBlockSize - 1) : max_seq_len;
+    return ceil_div(most, kBlockSize) * kBlockSize;
+}
+
+size_t scored_workspace(int64_t S, int64_t Hq, int64_t D, int64_t span, int64_t P, bool weights) {
+    if (span == 0) return 0;
+    const int64_t NP = std::max<int64_t>(1, ceil_div(span, P));
+    if (!weights) return NP > 1 ? partials_bytes(S, Hq, D, NP) : 0;
+    return static_cast<size_t>(ceil_div(partials_bytes(S, Hq, D, NP), 256) * 256 + S * Hq * span * 4);
+}
+
 pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32_t num_q_heads,
                          const void* k_cache, const void* v_cache, const pkv_cache_desc* d,
                          const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
                          int32_t max_seq_len, float scale, void* out, void* workspace, size_t ws_bytes,
                          int32_t partition_tokens, void* stream, const FusedAppend* app,
-                         const int32_t* work = nullptr, int32_t num_work = 0) {
+                         const int32_t* work = nullptr, int32_t num_work = 0, const Scored* sc = nullptr) {
     // ---- validation (host, before any launch)
     if (num_work < 0 || (!work && num_work > 0)) return PKV_ERR_INVALID;
     if (!d || num_seqs < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 || max_seq_len < 0 ||
@@ -306,6 +348,13 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
     const int G = num_q_heads / d->num_kv_heads;
     if (G != 1 && G != 2 && G != 4 && G != 8) return PKV_ERR_UNSUPPORTED;
     if (num_seqs > 65535 || d->num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+    if (sc) {
+        const pkv_status bad = check_score_mod(&sc->mod, scale, d);
+        if (bad != PKV_OK) return bad;
+        if (sc->mod.prefix_lens || (sc->new_lens && !sc->weights) || (reinterpret_cast<uintptr_t>(sc->weights) & 3u) ||
+            (reinterpret_cast<uintptr_t>(sc->new_lens) & 3u))
+            return PKV_ERR_INVALID;
+    }
     if (num_seqs == 0 || (work && num_work == 0)) return PKV_OK;
     if (!q || !k_cache || !v_cache || !block_tables || !seq_lens || !out) return PKV_ERR_INVALID;
     if (static_cast<int64_t>(num_work) * d->num_kv_heads > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
@@ -322,13 +371,18 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
         if (!same16 && !to_fp8) return PKV_ERR_UNSUPPORTED;
     }
 
+    // tokens that the launch's partitions divide
+    const int64_t reach = sc ? scored_span(max_seq_len, sc->mod.window) : max_seq_len;
+    if (reach > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
     const int P = partition_tokens > 0 ? partition_tokens
-                  : int_pool ? auto_partition_int(num_seqs, d->num_kv_heads, max_seq_len, d->kv_dtype, d->head_size)
-                             : auto_partition(num_seqs, d->num_kv_heads, max_seq_len, work != nullptr);
-    const int64_t NP = max_seq_len > 0 ? ceil_div(max_seq_len, P) : 1;
+                  : int_pool ? auto_partition_int(num_seqs, d->num_kv_heads, static_cast<int>(reach), d->kv_dtype, d->head_size)
+                             : auto_partition(num_seqs, d->num_kv_heads, static_cast<int>(reach), work != nullptr);
+    const int64_t NP = reach > 0 ? ceil_div(reach, P) : 1;
     // positions, and the end of a row's last partition, are 32-bit in the kernels
     if (NP * P > 0x7fffffff || max_blocks_per_seq > 0x7fffffff / kBlockSize) return PKV_ERR_UNSUPPORTED;
-    const size_t need = workspace_bytes(num_seqs, num_q_heads, d->head_size, max_seq_len, P);
+    if (sc && static_cast<int64_t>(max_blocks_per_seq) * kBlockSize + P > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+    const size_t need = sc ? scored_workspace(num_seqs, num_q_heads, d->head_size, reach, P, sc->weights != nullptr)
+                           : workspace_bytes(num_seqs, num_q_heads, d->head_size, max_seq_len, P);
     if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;
 
     unsigned int* err = error_word();
@@ -366,6 +420,17 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
         p.v_enc_scale = d->v_scale;
     }
 
+    if (sc) {
+        set_score_mod(p, sc->mod, scale, d);
+        // a launch without any token still marks itself as scored
+        p.span = static_cast<int32_t>(std::max<int64_t>(reach, kBlockSize));
+        if (sc->weights && reach > 0) {
+            p.cascade = 1;  // every row's partials are kept, and the merge writes its output
+            p.scores = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
+                                                ceil_div(partials_bytes(num_seqs, num_q_heads, d->head_size, NP), 256) * 256);
+        }
+    }
+
     // Tensor-core kernel for grouped-query heads at head_size 128; CUDA
     // cores otherwise (one query row per KV head is not a dense tile).
     const int64_t pool_rows = static_cast<int64_t>(d->num_blocks) * d->num_kv_heads * kBlockSize;
@@ -376,14 +441,26 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (int_pool) {
-        e = d->kv_dtype == PKV_INT8 ? launch_decode_int8(p, G, q_dtype, st) : launch_decode_int4(p, G, q_dtype, st);
-    } else if (use_mma) {
-        CUtensorMap tk, tv;
+    CUtensorMap tk, tv;
+    if (use_mma) {
         const int eb = d->kv_dtype == PKV_FP8_E4M3 ? 1 : 2;
         if (!encode_pool_map(&tk, k_cache, eb, pool_rows, d->head_size) ||
             !encode_pool_map(&tv, v_cache, eb, pool_rows, d->head_size))
             return PKV_ERR_CUDA;
+    }
+    if (sc) {
+        const CUtensorMap* mk = use_mma ? &tk : nullptr;
+        const CUtensorMap* mv = use_mma ? &tv : nullptr;
+        switch (d->kv_dtype) {
+        case PKV_F16: e = launch_decode_scored_f16(p, G, mk, mv, st); break;
+        case PKV_BF16: e = launch_decode_scored_bf16(p, G, mk, mv, st); break;
+        case PKV_FP8_E4M3: e = launch_decode_scored_fp8(p, G, q_dtype, mk, mv, st); break;
+        case PKV_INT8: e = launch_decode_scored_int8(p, G, q_dtype, st); break;
+        default: e = launch_decode_scored_int4(p, G, q_dtype, st); break;
+        }
+    } else if (int_pool) {
+        e = d->kv_dtype == PKV_INT8 ? launch_decode_int8(p, G, q_dtype, st) : launch_decode_int4(p, G, q_dtype, st);
+    } else if (use_mma) {
         e = launch_decode_gqa(p, G, d->kv_dtype, q_dtype, tk, tv, st);
     } else if (d->kv_dtype == PKV_F16) {
         e = launch_decode_f16(p, G, st);
@@ -395,13 +472,44 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
         e = launch_decode_fp8_f16q(p, G, st);
     }
     if (e != cudaSuccess) return PKV_ERR_CUDA;
-    if (NP > 1) {
+    if (NP > 1 || p.cascade) {
         e = launch_merge(p, q_dtype, st);
+        if (e != cudaSuccess) return PKV_ERR_CUDA;
+    }
+    if (p.scores) {
+        e = launch_weights(p, sc->new_lens, max_seq_len, sc->weights, st);
         if (e != cudaSuccess) return PKV_ERR_CUDA;
     }
     return PKV_OK;
 }
 }  // namespace
+
+extern "C" size_t pkv_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t head_size,
+                                                    int32_t max_seq_len, int32_t window, int32_t partition_tokens,
+                                                    int32_t with_weights) {
+    if (num_seqs < 0 || num_q_heads <= 0 || head_size <= 0 || max_seq_len < 0 || window < 0 || partition_tokens < 0 ||
+        partition_tokens % kBlockSize)
+        return 0;
+    const int64_t P = partition_tokens > 0 ? partition_tokens : kAutoMinPartition;
+    return scored_workspace(num_seqs, num_q_heads, head_size, scored_span(max_seq_len, window), P, with_weights != 0);
+}
+
+extern "C" pkv_status pkv_paged_attention_decode_scored(const void* q, int32_t q_dtype, int32_t num_seqs,
+                                                        int32_t num_q_heads, const void* k_cache, const void* v_cache,
+                                                        const pkv_cache_desc* d, const int32_t* block_tables,
+                                                        int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                                        int32_t max_seq_len, float scale, const pkv_score_mod* score,
+                                                        float* weights, const int32_t* new_lens, void* out,
+                                                        void* workspace, size_t ws_bytes, int32_t partition_tokens,
+                                                        void* stream) {
+    Scored sc{};
+    if (score) sc.mod = *score;
+    sc.weights = weights;
+    sc.new_lens = new_lens;
+    return decode_common(q, q_dtype, num_seqs, num_q_heads, k_cache, v_cache, d, block_tables, max_blocks_per_seq,
+                         seq_lens, max_seq_len, scale, out, workspace, ws_bytes, partition_tokens, stream, nullptr,
+                         nullptr, 0, &sc);
+}
 
 extern "C" pkv_status pkv_paged_attention_decode(const void* q, int32_t q_dtype, int32_t num_seqs,
                                                  int32_t num_q_heads, const void* k_cache, const void* v_cache,

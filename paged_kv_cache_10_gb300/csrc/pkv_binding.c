@@ -30,14 +30,18 @@ static struct {
     pkv_status (*sparse)(const void*, int32_t, int32_t, int32_t, const void*, const void*, const pkv_cache_desc*,
                          const int32_t*, int32_t, const int32_t*, const int32_t*, int32_t, float, void*, void*, size_t,
                          int32_t, void*);
+    pkv_status (*scored)(const void*, int32_t, int32_t, int32_t, const void*, const void*, const pkv_cache_desc*,
+                         const int32_t*, int32_t, const int32_t*, int32_t, float, const pkv_score_mod*, float*,
+                         const int32_t*, void*, void*, size_t, int32_t, void*);
     size_t (*block_bytes)(const pkv_cache_desc*);
 } fn;
 
 /* Objects of torch that bind() keeps. */
-static PyObject *t_i32, *t_i64, *t_f16, *t_bf16, *f_device, *f_raw_stream, *f_stream;
+static PyObject *t_i32, *t_i64, *t_f16, *t_bf16, *t_f32, *f_device, *f_raw_stream, *f_stream;
 /* Attribute and method names. */
 static PyObject *s_get_device, *s_is_contiguous, *s_data_ptr, *s_shape, *s_dtype, *s_nbytes, *s_num_blocks,
-    *s_block_size, *s_num_kv_heads, *s_head_size, *s_kv_dtype, *s_k_scale, *s_v_scale;
+    *s_block_size, *s_num_kv_heads, *s_head_size, *s_kv_dtype, *s_k_scale, *s_v_scale, *s_cap, *s_window, *s_slopes,
+    *s_first, *s_prefix_lens;
 
 static const char* const kDtypes[5] = {"f16", "bf16", "e4m3", "int8", "int4"};
 
@@ -500,6 +504,110 @@ static PyObject* py_sparse(PyObject* self, PyObject* const* a, Py_ssize_t n) {
                    (const int32_t*)selected, ss[2], (float)scale, out, ws, wn, part, st));
 }
 
+/* Pointer of an optional tensor of n elements of a type; NULL for None. */
+static int optional_vector(PyObject* t, PyObject* dtype, int32_t n, const char* name, const char* kind, long dev, void** p) {
+    int32_t got[1];
+    *p = NULL;
+    if (t == Py_None) return 0;
+    const int ok = is_type(t, dtype);
+    if (ok < 0 || dims(t, name, 1, got)) return -1;
+    if (!ok || got[0] != n) {
+        PyErr_Format(PyExc_ValueError, "%s must be %s with %d entries", name, kind, n);
+        return -1;
+    }
+    return ptr_of(t, name, dev, p);
+}
+
+/* A ScoreMod (None: plain scores): heads slopes, n first positions, S prefix lengths. */
+static int get_score(PyObject* o, int32_t heads, int32_t n, int32_t S, long dev, pkv_score_mod* m) {
+    memset(m, 0, sizeof *m);
+    if (o == Py_None) return 0;
+    if (attr_float(o, s_cap, &m->cap) || attr_i32(o, s_window, &m->window)) return -1;
+    PyObject* const names[3] = {s_slopes, s_first, s_prefix_lens};
+    void* p[3];
+    for (int i = 0; i < 3; ++i) {
+        PyObject* a = PyObject_GetAttr(o, names[i]);
+        if (!a) return -1;
+        const int r = i == 0   ? optional_vector(a, t_f32, heads, "slopes", "float32", dev, &p[0])
+                      : i == 1 ? optional_vector(a, t_i32, n, "first", "int32", dev, &p[1])
+                               : optional_vector(a, t_i32, S, "prefix_lens", "int32", dev, &p[2]);
+        Py_DECREF(a);
+        if (r) return -1;
+    }
+    m->slopes = (const float*)p[0];
+    m->first = (const int32_t*)p[1];
+    m->prefix_lens = (const int32_t*)p[2];
+    return 0;
+}
+
+/* Weights of cached tokens, float32 [num_blocks, num_kv_heads, block_size]. */
+static int weights_of(PyObject* t, const pkv_cache_desc* c, long dev, void** p) {
+    int32_t ws[3];
+    *p = NULL;
+    if (t == Py_None) return 0;
+    const int ok = is_type(t, t_f32);
+    if (ok < 0 || dims(t, "weights", 3, ws)) return -1;
+    if (!ok || ws[0] != c->num_blocks || ws[1] != c->num_kv_heads || ws[2] != c->block_size) {
+        PyErr_SetString(PyExc_ValueError, "weights must be float32 [num_blocks, num_kv_heads, block_size]");
+        return -1;
+    }
+    return ptr_of(t, "weights", dev, p);
+}
+
+/* q [S, Hq, D] with a table row and a length for each sequence. */
+static int batch_ok(PyObject* q, PyObject* tables, PyObject* lens, const pkv_cache_desc* c, int32_t* qs, int32_t* ts) {
+    int32_t S[1];
+    if (want_i32(tables, "block_tables and seq_lens") || want_i32(lens, "block_tables and seq_lens") ||
+        dims(q, "q", 3, qs) || dims(tables, "block_tables", 2, ts) || dims(lens, "seq_lens", 1, S) ||
+        same(qs[2], c->head_size, "q must have the cache's head_size") ||
+        same(ts[0], qs[0], "block_tables and seq_lens must have one row per sequence") ||
+        same(S[0], qs[0], "block_tables and seq_lens must have one row per sequence"))
+        return -1;
+    return bytes16(q, (size_t)qs[0] * qs[1] * qs[2], "q");
+}
+
+/* 0 if y has x's shape (three sizes) and type. */
+static int alike3(PyObject* x, const int32_t* xs, PyObject* y, const char* name, const char* what) {
+    int32_t ys[3];
+    if (dims(y, name, 3, ys)) return -1;
+    PyObject* d = PyObject_GetAttr(x, s_dtype);
+    if (!d) return -1;
+    const int ok = is_type(y, d);
+    Py_DECREF(d);
+    if (ok < 0) return -1;
+    if (ok && ys[0] == xs[0] && ys[1] == xs[1] && ys[2] == xs[2]) return 0;
+    PyErr_SetString(PyExc_ValueError, what);
+    return -1;
+}
+
+/* scored(q, k_cache, v_cache, desc, block_tables, seq_lens, max_seq_len, scale, out, score, weights, new_lens, workspace,
+ *        partition_tokens, q_dtype, stream) */
+static PyObject* py_scored(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    pkv_cache_desc c;
+    pkv_score_mod m;
+    int32_t type, qs[3], ts[2], max_len, part;
+    void *q, *kc, *vc, *tables, *lens, *out, *w, *fresh, *ws, *st;
+    size_t wn;
+    long dev;
+    if (!nargs_ok(n, 16)) return NULL;
+    if (get_desc(a[3], &c) || batch_ok(a[0], a[4], a[5], &c, qs, ts) ||
+        alike3(a[0], qs, a[8], "out", "out must have q's shape and type"))
+        return NULL;
+    const double scale = PyFloat_AsDouble(a[7]);
+    if (scale == -1.0 && PyErr_Occurred()) return NULL;
+    if (as_i32(a[6], &max_len) || as_i32(a[13], &part) || element_type(a[0], a[14], &type) || ptr_of(a[0], "q", -1, &q) ||
+        current_device(&dev) || ptr_of(a[0], "q", dev, &q) || pool_size(a[1], &c, "k_cache") ||
+        pool_size(a[2], &c, "v_cache") || ptr_of(a[1], "k_cache", dev, &kc) || ptr_of(a[2], "v_cache", dev, &vc) ||
+        ptr_of(a[4], "block_tables", dev, &tables) || ptr_of(a[5], "seq_lens", dev, &lens) ||
+        ptr_of(a[8], "out", dev, &out) || get_score(a[9], qs[1], qs[0], qs[0], dev, &m) ||
+        weights_of(a[10], &c, dev, &w) || optional_vector(a[11], t_i32, qs[0], "new_lens", "int32", dev, &fresh) ||
+        workspace_of(a[12], dev, &ws, &wn) || stream_of(a[15], &st))
+        return NULL;
+    DONE(fn.scored(q, type, qs[0], qs[1], kc, vc, &c, (const int32_t*)tables, ts[1], (const int32_t*)lens, max_len,
+                   (float)scale, &m, (float*)w, (const int32_t*)fresh, out, ws, wn, part, st));
+}
+
 static int address(PyObject* map, const char* name, void* slot) {
     PyObject* a = PyDict_GetItemString(map, name);
     void* p = a ? PyLong_AsVoidPtr(a) : NULL;
@@ -522,7 +630,7 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         PyObject* from;
         const char* name;
     } keep[] = {{&t_i32, a[0], "int32"},    {&t_i64, a[0], "int64"},          {&t_f16, a[0], "float16"},
-                {&t_bf16, a[0], "bfloat16"}, {&f_device, c, "_cuda_getDevice"}, {&f_raw_stream, c, "_cuda_getCurrentRawStream"}};
+                {&t_bf16, a[0], "bfloat16"}, {&t_f32, a[0], "float32"}, {&f_device, c, "_cuda_getDevice"}, {&f_raw_stream, c, "_cuda_getCurrentRawStream"}};
     for (size_t i = 0; i < sizeof keep / sizeof keep[0]; ++i) {
         PyObject* v = PyObject_GetAttrString(keep[i].from, keep[i].name);
         if (!v && keep[i].from == c) {  /* a torch without CUDA: no call gets as far as needing it */
@@ -541,6 +649,7 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         address(a[1], "pkv_paged_attention_decode", &fn.decode) || address(a[1], "pkv_paged_key_bounds", &fn.bounds) ||
         address(a[1], "pkv_select_blocks", &fn.select) ||
         address(a[1], "pkv_paged_attention_decode_sparse", &fn.sparse) ||
+        address(a[1], "pkv_paged_attention_decode_scored", &fn.scored) ||
         address(a[1], "pkv_cache_block_bytes", &fn.block_bytes))
         return NULL;
     Py_RETURN_NONE;
@@ -548,7 +657,8 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(bind),   METHOD(append), METHOD(read),   METHOD(decode),
-                                METHOD(bounds), METHOD(select), METHOD(sparse), {NULL, NULL, 0, NULL}};
+                                METHOD(bounds), METHOD(select), METHOD(sparse), METHOD(scored),
+                                {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkv_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
 PyMODINIT_FUNC PyInit__pkv_binding(void) {
@@ -559,7 +669,8 @@ PyMODINIT_FUNC PyInit__pkv_binding(void) {
                  {&s_shape, "shape"},           {&s_dtype, "dtype"},                 {&s_nbytes, "nbytes"},
                  {&s_num_blocks, "num_blocks"}, {&s_block_size, "block_size"},       {&s_num_kv_heads, "num_kv_heads"},
                  {&s_head_size, "head_size"},   {&s_kv_dtype, "kv_dtype"},           {&s_k_scale, "k_scale"},
-                 {&s_v_scale, "v_scale"}};
+                 {&s_v_scale, "v_scale"},       {&s_cap, "cap"},                     {&s_window, "window"},
+                 {&s_slopes, "slopes"},         {&s_first, "first"},                 {&s_prefix_lens, "prefix_lens"}};
     for (size_t i = 0; i < sizeof names / sizeof names[0]; ++i)
         if (!(*names[i].to = PyUnicode_InternFromString(names[i].name))) return NULL;
     return PyModule_Create(&module);

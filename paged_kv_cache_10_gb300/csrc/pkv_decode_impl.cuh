@@ -36,6 +36,7 @@
 
 #include "pkv_append.cuh"
 #include "pkv_device.cuh"
+#include "pkv_score.cuh"
 
 namespace pkv {
 
@@ -130,7 +131,7 @@ __device__ __forceinline__ int sparse_block(const DecodeParams& p, int s, int lo
     return load_live(p.block_tables + static_cast<int64_t>(s) * p.MB + logical);
 }
 
-template <int D, int G, typename KT, typename QT, int NW, int NST, bool SPARSE>
+template <int D, int G, typename KT, typename QT, int NW, int NST, bool SPARSE, bool SCORED>
 __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
     constexpr int VEC = D / 16;               // elements of a row per lane
     constexpr int VBYTES = VEC * KT::bytes;   // bytes of a row slice per lane
@@ -144,9 +145,9 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
     extern __shared__ __align__(128) unsigned char smem[];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // sparse: a programmatic dependent of the kernel before it on the stream, which it
-    // waits for before it lets its own dependent (the merge) start
-    if constexpr (SPARSE) wait_primary_grid();
+    // sparse, scored: a programmatic dependent of the kernel before it on the stream, which
+    // it waits for before it lets its own dependent (the merge) start
+    if constexpr (SPARSE || SCORED) wait_primary_grid();
     allow_dependent_launch();  // the merge may stage its CTAs behind this grid's last wave
     const int hf = lane >> 4, li = lane & 15;
     int part, h, s;
@@ -160,11 +161,22 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
     bool bad = L < 0 || L > Lcap;
     L = L < 0 ? 0 : (L > Lcap ? Lcap : L);
     int nparts, t1, j0, nblk;
+    ScoredRow row;  // scored: the row's range and its head's slope
     if constexpr (SPARSE) {
         if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
         nparts = p.NP;
         t1 = L;
         nblk = sparse_range(p, part, j0);
+    } else if constexpr (SCORED) {
+        row = scored_row(p, s, L, bad);
+        if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        L = row.end;
+        nparts = scored_parts(p, row);
+        if (part >= nparts) return;
+        const int t0 = row.start + part * p.P;
+        t1 = min(L, t0 + p.P);
+        j0 = t0 / kBlockSize;
+        nblk = row.lo < L ? (t1 + kBlockSize - 1) / kBlockSize - j0 : 0;
     } else {
         const int start = own_start(p.seq_group, p.group_blocks, s, L, &bad);
         int Lown = L - start;
@@ -184,7 +196,7 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
     const int nb_w = warp < nblk ? (nblk - warp + NW - 1) / NW : 0;
     // fused append: the warp that streams the partition's last block writes
     // the new token's row just before copying that block
-    const bool append_here = !SPARSE && p.slots && t1 == L && !bad && nblk > 0 && warp == (nblk - 1) % NW;
+    const bool append_here = !SPARSE && !SCORED && p.slots && t1 == L && !bad && nblk > 0 && warp == (nblk - 1) % NW;
     const FusedRow frow = fused_prefetch(p, s, h, L, append_here);
 
     unsigned char* wbase = smem + warp * NST * STAGE;
@@ -262,7 +274,7 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
     float lsum = 0.f;  // this lane's share of the softmax denominator of head g_h
 #pragma unroll
     for (int g = 0; g < G; ++g) {
-        m[g] = -INFINITY;
+        m[g] = SCORED ? kNoScore : -INFINITY;
 #pragma unroll
         for (int e = 0; e < VEC; ++e) acc[g][e] = 0.f;
     }
@@ -270,6 +282,8 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
     const int off = N >= 16 ? li * (N / 16) : (li >> 1);
     const int g_h = off / 8;
     const bool owner = N >= 16 || (li & 1) == 0;  // G = 1: lanes li, li^1 hold the same score
+    float slope = 0.f;
+    if constexpr (SCORED) slope = scored_slope(p, h * G + g_h);
 
     bool aborted = false;
     for (int k = 0; k < nb_w; ++k) {
@@ -303,6 +317,17 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
                 }
             }
             reduce_scatter<N, 8>(sc, li);
+            const int lead = SCORED ? row.lo - tok0 : 0;  // tokens of the block in front of the row's first
+            if constexpr (SCORED) {
+#pragma unroll
+                for (int r = 0; r < NR; ++r) {
+                    const int t = 2 * ((off + r) & 7) + hf;
+                    sc[r] = scored(p, sc[r], slope, row.end - 1 - tok0 - t);
+                    if (t < lead) sc[r] = -INFINITY;
+                    if (p.scores && owner)
+                        p.scores[((static_cast<int64_t>(s) * p.Hkv + h) * p.span + (tok0 - row.start + t)) * G + g_h] = sc[r];
+                }
+            }
             if (nvalid < kBlockSize) {
 #pragma unroll
                 for (int r = 0; r < NR; ++r) {
@@ -351,7 +376,7 @@ __global__ void __launch_bounds__(NW * 32) decode_kernel(const DecodeParams p) {
 #pragma unroll
             for (int jj = 0; jj < 8; ++jj) {
                 const int t = 2 * jj + hf;
-                if (t < nvalid) {
+                if (t < nvalid && (!SCORED || t >= lead)) {
                     uint32_t w[VBYTES / 4];
                     load_words<VBYTES>(vt + (t * D + li * VEC) * KT::bytes, w);
                     float vf[VEC];
@@ -449,12 +474,12 @@ constexpr int decode_stages() {
     return st < 2 ? 2 : (st > 8 ? 8 : st);
 }
 
-template <int D, int G, typename KT, typename QT, bool SPARSE>
+template <int D, int G, typename KT, typename QT, bool SPARSE, bool SCORED>
 cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t st) {
     constexpr int NW = kDecodeWarps;
     constexpr int NST = decode_stages<D, KT>();
     constexpr int SMEM = DecodeSmem<D, KT, NW, NST>::template bytes<G>() + (SPARSE ? NW * NST * 4 : 0);
-    auto kern = decode_kernel<D, G, KT, QT, NW, NST, SPARSE>;
+    auto kern = decode_kernel<D, G, KT, QT, NW, NST, SPARSE, SCORED>;
     static bool configured[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -467,24 +492,24 @@ cudaError_t launch_decode_t(const DecodeParams& p, cudaStream_t st) {
     }
     const dim3 grid = p.work ? dim3(static_cast<unsigned>(static_cast<int64_t>(p.num_work) * p.Hkv))
                              : dim3(p.NP - p.part_base, p.Hkv, p.S + (p.join_primary ? 1 : 0));  // this launch's partitions
-    return launch_maybe_pdl(SPARSE || (p.join_primary != 0 && !p.work), kern, grid, dim3(NW * 32), SMEM, st, p);
+    return launch_maybe_pdl(SPARSE || SCORED || (p.join_primary != 0 && !p.work), kern, grid, dim3(NW * 32), SMEM, st, p);
 }
 
-template <typename KT, typename QT, bool SPARSE = false>
+template <typename KT, typename QT, bool SPARSE = false, bool SCORED = false>
 cudaError_t launch_decode_family(const DecodeParams& p, int G, cudaStream_t st) {
     if (p.D == 128) {
         switch (G) {
-        case 1: return launch_decode_t<128, 1, KT, QT, SPARSE>(p, st);
-        case 2: return launch_decode_t<128, 2, KT, QT, SPARSE>(p, st);
-        case 4: return launch_decode_t<128, 4, KT, QT, SPARSE>(p, st);
-        case 8: return launch_decode_t<128, 8, KT, QT, SPARSE>(p, st);
+        case 1: return launch_decode_t<128, 1, KT, QT, SPARSE, SCORED>(p, st);
+        case 2: return launch_decode_t<128, 2, KT, QT, SPARSE, SCORED>(p, st);
+        case 4: return launch_decode_t<128, 4, KT, QT, SPARSE, SCORED>(p, st);
+        case 8: return launch_decode_t<128, 8, KT, QT, SPARSE, SCORED>(p, st);
         }
     } else if (p.D == 64) {
         switch (G) {
-        case 1: return launch_decode_t<64, 1, KT, QT, SPARSE>(p, st);
-        case 2: return launch_decode_t<64, 2, KT, QT, SPARSE>(p, st);
-        case 4: return launch_decode_t<64, 4, KT, QT, SPARSE>(p, st);
-        case 8: return launch_decode_t<64, 8, KT, QT, SPARSE>(p, st);
+        case 1: return launch_decode_t<64, 1, KT, QT, SPARSE, SCORED>(p, st);
+        case 2: return launch_decode_t<64, 2, KT, QT, SPARSE, SCORED>(p, st);
+        case 4: return launch_decode_t<64, 4, KT, QT, SPARSE, SCORED>(p, st);
+        case 8: return launch_decode_t<64, 8, KT, QT, SPARSE, SCORED>(p, st);
         }
     }
     return cudaErrorInvalidValue;

@@ -121,8 +121,6 @@ __device__ __forceinline__ void code_pairs(uint32_t w, int j, uint32_t& lo, uint
     }
 }
 
-constexpr float kNoScore = -3e38f;  // softmax reference before the first score
-
 // 2^e / c for a power of two c, the quotient within binary32's normal range.
 __device__ __forceinline__ float pow2_over(int e, float c) {
     return __uint_as_float((static_cast<uint32_t>(254 + e) << 23) - __float_as_uint(c));
@@ -144,7 +142,7 @@ __device__ __forceinline__ float move_weights(float& c, float& lim, float a, flo
     return a * __int_as_float((127 + half) << 23) * __int_as_float((127 + d - half) << 23);
 }
 
-template <int D, int BITS, bool FOLD, bool SPARSE>
+template <int D, int BITS, bool FOLD, bool SPARSE, bool SCORED>
 __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, BITS, FOLD>::kCtasPerSm)
     decode_int_kernel(const DecodeParams p, const int G, const int q_bf16) {
     using C = IntCfg<D, BITS, FOLD>;
@@ -175,7 +173,24 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     allow_dependent_launch();
     // the first window's table (or list) entries, loaded beside the length
     const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.MB;
-    const int j0 = part * (p.P / kBlockSize);  // first block (or list entry) of this partition
+    int len;
+    bool bad;
+    const auto load_len = [&] {
+        len = load_live(p.seq_lens + s);
+        const int cap = p.MB * kBlockSize;
+        bad = len < 0 || len > cap;
+        len = len < 0 ? 0 : (len > cap ? cap : len);
+    };
+    ScoredRow row{};  // scored: the row's range, which its table entries wait for
+    if constexpr (SCORED) {
+        load_len();
+        row = scored_row(p, s, len, bad);
+        len = row.end;
+        if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        if (part >= scored_parts(p, row)) return;
+    }
+    // first block (or list entry) of this partition
+    const int j0 = part * (p.P / kBlockSize) + (SCORED ? row.start / kBlockSize : 0);
     const int32_t* list = SPARSE ? p.selected + (static_cast<int64_t>(s) * p.Hkv + h) * p.nsel + j0 : table + j0;
     const int list_len = (SPARSE ? p.nsel : p.MB) - j0;
     const auto entry = [&](int k) {  // lane 2i + u: block u of this warp's step k + i
@@ -183,14 +198,13 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
         return j < list_len ? load_live(list + j) : -1;
     };
     int next = entry(0);
-    int len = load_live(p.seq_lens + s);
-    const int cap = p.MB * kBlockSize;
-    bool bad = len < 0 || len > cap;
-    len = len < 0 ? 0 : (len > cap ? cap : len);
+    if constexpr (!SCORED) load_len();
     int nblk;  // blocks (or list entries) of this partition
     if constexpr (SPARSE) {
         nblk = min(p.P / kBlockSize, list_len);
         if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+    } else if constexpr (SCORED) {
+        nblk = row.lo < len ? (min(len, row.start + (part + 1) * p.P) + kBlockSize - 1) / kBlockSize - j0 : 0;
     } else {
         if (len > p.NP * p.P) {
             bad = true;
@@ -332,6 +346,13 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     float mA = kNoScore, mB = kNoScore, lA = 0.f, lB = 0.f, zA = 0.f, zB = 0.f;
     float cA = 0x1p118f, cB = 0x1p118f, limA = 0x1p-103f, limB = 0x1p-103f;  // scales of the weights p s'
 
+    float slopeA = 0.f, slopeB = 0.f;
+    const int colA = FOLD ? 2 * qd & 3 : 2 * qd;  // the lane's heads in the group
+    if constexpr (SCORED) {
+        if (colA < G) slopeA = scored_slope(p, h * G + colA);
+        if (colA + 1 < G) slopeB = scored_slope(p, h * G + colA + 1);
+    }
+
     // the lane's fragment offsets in a tile
     const uint32_t koff = g8 * L::KW + qd * (L::KW / 4);
     const uint32_t voff = WORDS == 2 ? (g8 >> 2) * 256 + qd * 32 + (g8 & 3) * 8
@@ -349,6 +370,9 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
                 break;
             }
             const uint32_t nvs = *reinterpret_cast<const volatile uint16_t*>(info + 2 * st);
+            // scored: first token of the step, tokens in front of the row's first
+            const int tok0 = SCORED ? (j0 + 2 * (warp + (k0 + st) * NW)) * kBlockSize : 0;
+            const int lead = SCORED ? row.lo - tok0 : 0;
             if (nvs != 0u) {
                 const uint32_t base = smem_addr(ring + st * STAGE);
                 const bool whole = nvs == (kBlockSize << 8 | kBlockSize);
@@ -392,6 +416,26 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
                         sv[b][1] = fmaf(ks0 * sa[b][1], sfB, kz0 * qsB);
                         sv[b][2] = fmaf(ks1 * sa[b][2], sfA, kz1 * qsA);
                         sv[b][3] = fmaf(ks1 * sa[b][3], sfB, kz1 * qsB);
+                        if constexpr (SCORED) {
+                            const int t0 = b * kBlockSize + g8, t1 = t0 + 8;
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                sv[b][c] = scored(p, sv[b][c], (c & 1) ? slopeB : slopeA, row.end - 1 - tok0 - (c < 2 ? t0 : t1));
+                            if (t0 < lead) sv[b][0] = sv[b][1] = -INFINITY;
+                            if (t1 < lead) sv[b][2] = sv[b][3] = -INFINITY;
+                            if (p.scores && (FOLD ? qd < 2 : true)) {
+                                // past the row's last block (an odd step) there is no room
+                                float* out = p.scores + ((static_cast<int64_t>(s) * p.Hkv + h) * p.span + (tok0 - row.start)) * G;
+                                if (t0 < b * kBlockSize + nv[b]) {
+                                    if (colA < G) out[t0 * G + colA] = sv[b][0];
+                                    if (colA + 1 < G) out[t0 * G + colA + 1] = sv[b][1];
+                                }
+                                if (t1 < b * kBlockSize + nv[b]) {
+                                    if (colA < G) out[t1 * G + colA] = sv[b][2];
+                                    if (colA + 1 < G) out[t1 * G + colA + 1] = sv[b][3];
+                                }
+                            }
+                        }
                         if (!whole) {  // tokens past the end: stale parameters must not get through
                             if (g8 >= nv[b]) sv[b][0] = sv[b][1] = -INFINITY;
                             if (g8 + 8 >= nv[b]) sv[b][2] = sv[b][3] = -INFINITY;
@@ -410,6 +454,10 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
                     if (!whole) {
                         if (g8 >= nv[b]) vs[b][0] = vz[b][0] = 0.f;
                         if (g8 + 8 >= nv[b]) vs[b][1] = vz[b][1] = 0.f;
+                    }
+                    if constexpr (SCORED) {
+                        if (b * kBlockSize + g8 < lead) vs[b][0] = vz[b][0] = 0.f;
+                        if (b * kBlockSize + g8 + 8 < lead) vs[b][1] = vz[b][1] = 0.f;
                     }
                 }
                 // Lazy references, checked lane by lane: the probabilities' maximum moves when a
@@ -565,7 +613,7 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     __syncthreads();
 
     // ---- output: four dimensions of a head a thread
-    const bool direct = SPARSE ? p.NP == 1 : len <= p.P;
+    const bool direct = SPARSE ? p.NP == 1 : SCORED ? !p.cascade && len - row.start <= p.P : len <= p.P;
     for (int i4 = threadIdx.x; i4 < G * (D / 4); i4 += NW * 32) {
         const int g = i4 / (D / 4), d = 4 * (i4 % (D / 4));
         float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -603,10 +651,10 @@ __global__ void __launch_bounds__(IntCfg<D, BITS, FOLD>::kWarps * 32, IntCfg<D, 
     }
 }
 
-template <int D, int BITS, bool FOLD, bool SPARSE>
+template <int D, int BITS, bool FOLD, bool SPARSE, bool SCORED>
 cudaError_t launch_decode_int_t(const DecodeParams& p, int G, int q_dtype, cudaStream_t st) {
     constexpr int SMEM = IntCfg<D, BITS, FOLD>::kBytes;
-    auto kern = decode_int_kernel<D, BITS, FOLD, SPARSE>;
+    auto kern = decode_int_kernel<D, BITS, FOLD, SPARSE, SCORED>;
     static bool configured[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -621,15 +669,20 @@ cudaError_t launch_decode_int_t(const DecodeParams& p, int G, int q_dtype, cudaS
                             q_dtype == PKV_BF16 ? 1 : 0);
 }
 
-template <int BITS>
+template <int BITS, bool SCORED = false>
 cudaError_t launch_decode_int(const DecodeParams& p, int G, int q_dtype, cudaStream_t st) {
     const auto run = [&](auto fold) {
         constexpr bool F = decltype(fold)::value;
-        if (p.selected)
-            return p.D == 128 ? launch_decode_int_t<128, BITS, F, true>(p, G, q_dtype, st)
-                              : launch_decode_int_t<64, BITS, F, true>(p, G, q_dtype, st);
-        return p.D == 128 ? launch_decode_int_t<128, BITS, F, false>(p, G, q_dtype, st)
-                          : launch_decode_int_t<64, BITS, F, false>(p, G, q_dtype, st);
+        if constexpr (SCORED) {
+            return p.D == 128 ? launch_decode_int_t<128, BITS, F, false, true>(p, G, q_dtype, st)
+                              : launch_decode_int_t<64, BITS, F, false, true>(p, G, q_dtype, st);
+        } else {
+            if (p.selected)
+                return p.D == 128 ? launch_decode_int_t<128, BITS, F, true, false>(p, G, q_dtype, st)
+                                  : launch_decode_int_t<64, BITS, F, true, false>(p, G, q_dtype, st);
+            return p.D == 128 ? launch_decode_int_t<128, BITS, F, false, false>(p, G, q_dtype, st)
+                              : launch_decode_int_t<64, BITS, F, false, false>(p, G, q_dtype, st);
+        }
     };
     return G <= 4 ? run(std::true_type{}) : run(std::false_type{});
 }

@@ -85,13 +85,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     return y;
 }
 
-// 2^x with the hardware approximation (relative error ~2^-22; -inf -> 0).
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // Splits a 32-bit word of four E4M3 bytes into two f16x2 words (bytes 0,1
 // and bytes 2,3), with the hardware conversion.
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -224,10 +217,19 @@ __device__ __forceinline__ void load_qb(const void* q, int Hq, int s, int h, uin
 // TILE bytes after it) in the 128-byte-swizzled layout the TMA lands;
 // nvalid: tokens of the block inside the sequence (value rows past it are
 // zeroed first).  Warp-uniform call.
-template <int G, typename KT, typename QT>
+// Scored decode: sb says what the scores become, how many tokens of the block
+// lie in front of the row's first (their value rows are zeroed too) and where
+// the scores go; p holds the cap.
+struct ScoredBlock {
+    float slopeA, slopeB;  // of heads 2 qd, 2 qd + 1
+    int dist, lead;        // distance of the block's first token; tokens in front
+    float* scores;         // the block's scores [16][G], or null
+};
+template <int G, typename KT, typename QT, bool SCORED = false>
 __device__ __forceinline__ void mma_block(unsigned char* kt, int nvalid, const uint32_t (&qb)[8][2],
                                           const uint2* qsm, float (&o)[8][4], float& mA, float& mB, float& lA,
-                                          float& lB, float qk_scale, uint32_t koff, uint32_t voff) {
+                                          float& lB, float qk_scale, uint32_t koff, uint32_t voff,
+                                          const DecodeParams& p, const ScoredBlock& sb) {
     constexpr bool kFP8 = KT::bytes == 1;
     constexpr bool kBF = std::is_same<KT, BF16>::value;
     constexpr int TILE = kBlockSize * 128 * KT::bytes;
@@ -246,6 +248,16 @@ __device__ __forceinline__ void mma_block(unsigned char* kt, int nvalid, const u
                 make_uint4(0u, 0u, 0u, 0u);
         }
         __syncwarp();
+    }
+    if constexpr (SCORED) {
+        if (sb.lead > 0) {
+            constexpr int kChunksPerRow = kFP8 ? 8 : 16;
+            for (int i = lane; i < sb.lead * kChunksPerRow; i += 32) {
+                const int row = i / kChunksPerRow, c = i % kChunksPerRow;
+                *reinterpret_cast<uint4*>(vt + (c >> 3) * 2048 + row * 128 + (c & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            __syncwarp();
+        }
     }
     // ---- S = K Q^T, two accumulators (even / odd k-steps) to halve the chain
     float sa[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -285,6 +297,17 @@ __device__ __forceinline__ void mma_block(unsigned char* kt, int nvalid, const u
     float sv[4];
 #pragma unroll
     for (int c = 0; c < 4; ++c) sv[c] = (sa[0][c] + sa[1][c]) * qk_scale;
+    if constexpr (SCORED) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            sv[c] = scored(p, sv[c], (c & 1) ? sb.slopeB : sb.slopeA, sb.dist - g8 - 8 * (c >> 1));
+        if (g8 < sb.lead) sv[0] = sv[1] = -INFINITY;
+        if (g8 + 8 < sb.lead) sv[2] = sv[3] = -INFINITY;
+        if (sb.scores && 2 * (lane & 3) < G) {
+            *reinterpret_cast<float2*>(sb.scores + g8 * G + 2 * (lane & 3)) = make_float2(sv[0], sv[1]);
+            *reinterpret_cast<float2*>(sb.scores + (g8 + 8) * G + 2 * (lane & 3)) = make_float2(sv[2], sv[3]);
+        }
+    }
     if (nvalid < kBlockSize) {
         if (g8 >= nvalid) sv[0] = sv[1] = -INFINITY;
         if (g8 + 8 >= nvalid) sv[2] = sv[3] = -INFINITY;
@@ -369,7 +392,7 @@ __device__ __forceinline__ void mma_block(unsigned char* kt, int nvalid, const u
     }
 }
 
-template <int G, typename KT, typename QT, int NW, int NST, bool SPARSE>
+template <int G, typename KT, typename QT, int NW, int NST, bool SPARSE, bool SCORED>
 __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     decode_mma_kernel(const DecodeParams p, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv) {
@@ -386,9 +409,9 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     unsigned char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    // sparse: a programmatic dependent of the kernel before it on the stream, which it
-    // waits for before it lets its own dependent (the merge) start
-    if constexpr (SPARSE) wait_primary_grid();
+    // sparse, scored: a programmatic dependent of the kernel before it on the stream, which
+    // it waits for before it lets its own dependent (the merge) start
+    if constexpr (SPARSE || SCORED) wait_primary_grid();
     allow_dependent_launch();  // the merge may stage its CTAs behind this grid's last wave
     const int g8 = lane >> 2, qd = lane & 3;  // fragment row group / quad member
     int part, h, s;
@@ -402,11 +425,22 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     bool bad = L < 0 || L > Lcap;
     L = L < 0 ? 0 : (L > Lcap ? Lcap : L);
     int nparts, t1, j0, nblk;
+    ScoredRow srow;  // scored: the row's range
     if constexpr (SPARSE) {
         if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
         nparts = p.NP;
         t1 = L;
         nblk = sparse_range(p, part, j0);
+    } else if constexpr (SCORED) {
+        srow = scored_row(p, s, L, bad);
+        if (bad && threadIdx.x == 0 && part == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        L = srow.end;
+        nparts = scored_parts(p, srow);
+        if (part >= nparts) return;
+        const int t0 = srow.start + part * p.P;
+        t1 = min(L, t0 + p.P);
+        j0 = t0 / kBlockSize;
+        nblk = srow.lo < L ? (t1 + kBlockSize - 1) / kBlockSize - j0 : 0;
     } else {
         const int start = own_start(p.seq_group, p.group_blocks, s, L, &bad);
         int Lown = L - start;
@@ -426,7 +460,7 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     const int nb_w = warp < nblk ? (nblk - warp + NW - 1) / NW : 0;
     // fused append: the warp that streams the partition's last block writes
     // the new token's row just before copying that block
-    const bool append_here = !SPARSE && p.slots && t1 == L && !bad && nblk > 0 && warp == (nblk - 1) % NW;
+    const bool append_here = !SPARSE && !SCORED && p.slots && t1 == L && !bad && nblk > 0 && warp == (nblk - 1) % NW;
     const FusedRow frow = fused_prefetch(p, s, h, L, append_here);
 
     unsigned char* wbase = smem + warp * NST * STAGE;
@@ -510,7 +544,13 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
     float o[8][4];
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    float mA = -INFINITY, mB = -INFINITY, lA = 0.f, lB = 0.f;  // heads 2qd (A), 2qd+1 (B)
+    // heads 2qd (A), 2qd+1 (B); scored: a block's scores may all be -inf
+    float mA = SCORED ? kNoScore : -INFINITY, mB = mA, lA = 0.f, lB = 0.f;
+    ScoredBlock sb{};
+    if constexpr (SCORED) {
+        sb.slopeA = 2 * qd < G ? scored_slope(p, h * G + 2 * qd) : 0.f;
+        sb.slopeB = 2 * qd < G ? scored_slope(p, h * G + 2 * qd + 1) : 0.f;
+    }
 
     // fp8 fragment offsets in a stage's tiles: K chunk 2qd of row g8, V chunk
     // g8 of row 2qd (the stage bases are 1024-byte aligned)
@@ -530,9 +570,16 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
             }
             const int phys = stage_phys[st];
             const int nvalid = SPARSE ? stage_val[st] : min(kBlockSize, t1 - tok0);
+            if constexpr (SCORED) {
+                sb.dist = srow.end - 1 - tok0;
+                sb.lead = srow.lo - tok0;
+                sb.scores = p.scores ? p.scores + ((static_cast<int64_t>(s) * p.Hkv + h) * p.span + (tok0 - srow.start)) * G
+                                     : nullptr;
+            }
             tok0 += NW * kBlockSize;
             if (phys >= 0 && phys < p.NB) {
-                mma_block<G, KT, QT>(wbase + st * STAGE, nvalid, qb, qsm, o, mA, mB, lA, lB, p.qk_scale, koff, voff);
+                mma_block<G, KT, QT, SCORED>(wbase + st * STAGE, nvalid, qb, qsm, o, mA, mB, lA, lB, p.qk_scale, koff, voff,
+                                             p, sb);
             }
             __syncwarp();
             if (k_issue < nb_w) issue_next(st);
@@ -658,13 +705,13 @@ __global__ void __launch_bounds__(NW * 32, MmaCfg<KT>::kCtasPerSm)
 }
 
 // ------------------------------------------------------------- launchers
-template <int G, typename KT, typename QT, bool SPARSE>
+template <int G, typename KT, typename QT, bool SPARSE, bool SCORED>
 cudaError_t launch_decode_mma_t(const DecodeParams& p, const CUtensorMap& tk, const CUtensorMap& tv,
                                 cudaStream_t st) {
     constexpr int NW = MmaCfg<KT>::kWarps;
     constexpr int NST = MmaCfg<KT>::kStages;
     constexpr int SMEM = MmaSmem<KT, NW, NST>::kBytes + (SPARSE ? NW * NST * 4 : 0);
-    auto kern = decode_mma_kernel<G, KT, QT, NW, NST, SPARSE>;
+    auto kern = decode_mma_kernel<G, KT, QT, NW, NST, SPARSE, SCORED>;
     static bool configured[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -677,16 +724,17 @@ cudaError_t launch_decode_mma_t(const DecodeParams& p, const CUtensorMap& tk, co
     }
     const dim3 grid = p.work ? dim3(static_cast<unsigned>(static_cast<int64_t>(p.num_work) * p.Hkv))
                              : dim3(p.NP - p.part_base, p.Hkv, p.S + (p.join_primary ? 1 : 0));  // this launch's partitions
-    return launch_maybe_pdl(SPARSE || (p.join_primary != 0 && !p.work), kern, grid, dim3(NW * 32), SMEM, st, p, tk, tv);
+    return launch_maybe_pdl(SPARSE || SCORED || (p.join_primary != 0 && !p.work), kern, grid, dim3(NW * 32), SMEM, st, p, tk,
+                            tv);
 }
 
-template <typename KT, typename QT, bool SPARSE = false>
+template <typename KT, typename QT, bool SPARSE = false, bool SCORED = false>
 cudaError_t launch_decode_mma_family(const DecodeParams& p, int G, const CUtensorMap& tk, const CUtensorMap& tv,
                                      cudaStream_t st) {
     switch (G) {
-    case 2: return launch_decode_mma_t<2, KT, QT, SPARSE>(p, tk, tv, st);
-    case 4: return launch_decode_mma_t<4, KT, QT, SPARSE>(p, tk, tv, st);
-    case 8: return launch_decode_mma_t<8, KT, QT, SPARSE>(p, tk, tv, st);
+    case 2: return launch_decode_mma_t<2, KT, QT, SPARSE, SCORED>(p, tk, tv, st);
+    case 4: return launch_decode_mma_t<4, KT, QT, SPARSE, SCORED>(p, tk, tv, st);
+    case 8: return launch_decode_mma_t<8, KT, QT, SPARSE, SCORED>(p, tk, tv, st);
     }
     return cudaErrorInvalidValue;
 }

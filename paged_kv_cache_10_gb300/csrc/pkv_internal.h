@@ -81,6 +81,16 @@ struct DecodeParams {
     // of them in a partition), and every row has NP partitions.  Null: dense.
     const int32_t* selected = nullptr;
     int32_t nsel = 0;
+    // Scored decode (pkv_score_mod).  With a cap, qk_scale is scale * k_scale / cap
+    // and a score is cap_out * tanh(q.k * qk_scale), cap_out = cap * log2(e); 0: no cap.
+    float cap_out = 0.f;
+    int32_t window = 0;               // > 0: the last `window` positions only
+    const float* slopes = nullptr;    // [Hq] or null
+    const int32_t* first = nullptr;   // [S] or null
+    int32_t span = 0;                 // > 0 marks a scored launch: most tokens of a row, in whole blocks
+    // Scores in log2 units for pkv_paged_attention_decode_scored's weights, [S][Hkv][span][G], a row's
+    // first token being that of scored_range; null: none kept.
+    float* scores = nullptr;
 };
 
 // Launches kern on st, as a programmatic dependent of the kernel before it
@@ -121,6 +131,14 @@ __host__ __device__ inline int own_start(const int32_t* seq_group, const int32_t
         start = start < 0 ? 0 : (L / kBlockSize) * kBlockSize;
     }
     return start;
+}
+
+// Scored decode: the first token a row of L tokens attends to, through its
+// window and its first position (L where nothing is left).
+__host__ __device__ inline int scored_first(int window, const int32_t* first, int s, int L) {
+    int lo = first ? first[s] : 0;
+    if (window > 0 && lo < L - window) lo = L - window;
+    return lo < 0 ? 0 : (lo > L ? L : lo);
 }
 
 // Device address of the error word on the current device (cached).
@@ -164,6 +182,20 @@ cudaError_t launch_decode_sparse_bf16(const DecodeParams& p, int G, const CUtens
                                       cudaStream_t st);
 cudaError_t launch_decode_sparse_fp8(const DecodeParams& p, int G, int q_dtype, const CUtensorMap* tk,
                                      const CUtensorMap* tv, cudaStream_t st);
+// Scored decode over each pool type: the dense kernels with capped, biased and
+// masked scores.
+cudaError_t launch_decode_scored_f16(const DecodeParams& p, int G, const CUtensorMap* tk, const CUtensorMap* tv,
+                                     cudaStream_t st);
+cudaError_t launch_decode_scored_bf16(const DecodeParams& p, int G, const CUtensorMap* tk, const CUtensorMap* tv,
+                                      cudaStream_t st);
+cudaError_t launch_decode_scored_fp8(const DecodeParams& p, int G, int q_dtype, const CUtensorMap* tk,
+                                     const CUtensorMap* tv, cudaStream_t st);
+cudaError_t launch_decode_scored_int8(const DecodeParams& p, int G, int q_dtype, cudaStream_t st);
+cudaError_t launch_decode_scored_int4(const DecodeParams& p, int G, int q_dtype, cudaStream_t st);
+// Each cached token's share of the softmax into weights [NB][Hkv][16], from the
+// launch's scores and partials (pkv_weights.cu).
+cudaError_t launch_weights(const DecodeParams& p, const int32_t* new_lens, int max_seq_len, float* weights,
+                           cudaStream_t st);
 // Copies the blocks a batch reaches out of an integer-coded pool into 16-bit
 // blocks of q's type (prefill): copy block s * MB + j holds sequence s's
 // logical block j, and table_copy says so.
@@ -222,6 +254,9 @@ bool encode_pool_map(CUtensorMap* map, const void* base, int elem_bytes, int64_t
 bool encode_token_head_map(CUtensorMap* map, const void* base, int D, int H, int64_t T, int box_h, int box_t);
 // Partials of S*Hq rows x NP partitions: m, l (256-byte aligned regions), o.
 size_t partials_bytes(int64_t S, int64_t Hq, int64_t D, int64_t NP);
+// What scored attention asks for: a status, and its fields of the launch (qk_scale with a cap included).
+pkv_status check_score_mod(const pkv_score_mod* m, float scale, const pkv_cache_desc* d);
+void set_score_mod(DecodeParams& p, const pkv_score_mod& m, float scale, const pkv_cache_desc* d);
 void partials_layout(DecodeParams& p, void* workspace);  // sets part_m/l/o from S, Hq, NP
 
 int num_sms();

@@ -7,6 +7,7 @@
 #pragma once
 
 #include "pkv_device.cuh"
+#include "pkv_score.cuh"
 
 namespace pkv {
 
@@ -27,6 +28,11 @@ __device__ __forceinline__ void merge_row_range(const DecodeParams& p, int64_t r
     const int Lcap = p.MB * kBlockSize;
     L = L < 0 ? 0 : (L > Lcap ? Lcap : L);
     bool bad = false;
+    if (p.span > 0) {  // scored decode
+        first = 0;
+        nparts = scored_parts(p, scored_row(p, s, L, bad));
+        return;
+    }
     const int start = own_start(p.seq_group, p.group_blocks, s, L, &bad);
     const int Lown = min(L - start, (p.NP - p.part_base) * p.P);
     const int nown = Lown > 0 ? (Lown + p.P - 1) / p.P : 0;

@@ -44,7 +44,7 @@ EXPORTED = [
     "pkv_prefill_plan", "pkv_decode_plan", "pkv_prefill_workspace_bytes", "pkv_check_wait_timeout",
     "pkv_decode_cascade_staging_bytes", "pkv_cache_block_bytes", "pkv_paged_kv_read", "pkv_paged_key_bounds",
     "pkv_select_blocks_workspace_bytes", "pkv_select_blocks", "pkv_decode_sparse_workspace_bytes",
-    "pkv_paged_attention_decode_sparse",
+    "pkv_paged_attention_decode_sparse", "pkv_decode_scored_workspace_bytes", "pkv_paged_attention_decode_scored",
 ]
 
 
@@ -79,6 +79,23 @@ class CacheDesc:
                           DTYPE_CODE[self.kv_dtype], self.k_scale, self.v_scale)
 
 
+class _ScoreMod(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("window", ctypes.c_int32), ("slopes", ctypes.c_void_p),
+                ("first", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p)]
+
+
+@dataclass
+class ScoreMod:
+    """What scored attention does to its scores: x = cap * tanh(x / cap) (cap > 0), minus slopes[head] * |p - t|
+    (float32 [Hq]), over the keys t > p - window (window > 0), t >= first (int32 [S] in decode, [T] in prefill) and
+    t <= p or, in prefill, t < prefix_lens (int32 [S])."""
+    cap: float = 0.0
+    window: int = 0
+    slopes: torch.Tensor | None = None
+    first: torch.Tensor | None = None
+    prefix_lens: torch.Tensor | None = None
+
+
 _lib = None
 
 
@@ -91,7 +108,7 @@ def lib():
         raise RuntimeError(f"{LIB_PATH} is missing: build it with paged_kv_cache_10_gb300.build.build()")
     L = ctypes.CDLL(LIB_PATH)
     P, i32, i64, u32p = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.POINTER(ctypes.c_uint32)
-    D = ctypes.POINTER(_CacheDesc)
+    D, M = ctypes.POINTER(_CacheDesc), ctypes.POINTER(_ScoreMod)
     sig = {
         "pkv_paged_kv_append": (i32, [P, P, i32, i32, P, P, P, D, P]),
         "pkv_copy_blocks": (i32, [P, P, D, P, i32, P]),
@@ -154,6 +171,9 @@ def lib():
         "pkv_decode_sparse_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32]),
         "pkv_paged_attention_decode_sparse": (i32, [P, i32, i32, i32, P, P, D, P, i32, P, P, i32, ctypes.c_float, P,
                                                     P, ctypes.c_size_t, i32, P]),
+        "pkv_decode_scored_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
+        "pkv_paged_attention_decode_scored": (i32, [P, i32, i32, i32, P, P, D, P, i32, P, i32, ctypes.c_float, M, P, P,
+                                                    P, P, ctypes.c_size_t, i32, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -179,7 +199,8 @@ def _calls():
     m = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(m)
     names = ("pkv_paged_kv_append", "pkv_paged_kv_read", "pkv_paged_attention_decode", "pkv_paged_key_bounds",
-             "pkv_select_blocks", "pkv_paged_attention_decode_sparse", "pkv_cache_block_bytes")
+             "pkv_select_blocks", "pkv_paged_attention_decode_sparse", "pkv_paged_attention_decode_scored",
+             "pkv_cache_block_bytes")
     m.bind(torch, {n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _stream)
     _native = m
     return m
@@ -476,6 +497,25 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, desc: CacheDesc, block_ta
                          partition_blocks, q_dtype, stream)
     if st:
         _check(st, "paged_attention_decode_sparse")
+
+
+def decode_scored_workspace_bytes(num_seqs: int, num_q_heads: int, head_size: int, max_seq_len: int, window: int = 0,
+                                  partition_tokens: int = 0, with_weights: bool = False) -> int:
+    return int(lib().pkv_decode_scored_workspace_bytes(num_seqs, num_q_heads, head_size, max_seq_len, window,
+                                                       partition_tokens, 1 if with_weights else 0))
+
+
+def paged_attention_decode_scored(q, k_cache, v_cache, desc: CacheDesc, block_tables, seq_lens, max_seq_len: int,
+                                  scale: float, out, score: ScoreMod | None = None, weights=None, new_lens=None,
+                                  workspace=None, partition_tokens: int = 0, q_dtype: str | None = None,
+                                  stream=None) -> None:
+    """Decode attention with capped, biased and masked scores: q, out [S, Hq, D].  weights (float32 [NB, Hkv, 16], or
+    None) receives each cached token's share of the softmax, summed over its KV head's query heads: set for the last
+    new_lens[s] tokens (int32 [S]; None: all of them), added to for the others."""
+    st = _calls().scored(q, k_cache, v_cache, desc, block_tables, seq_lens, max_seq_len, scale, out, score, weights,
+                         new_lens, workspace, partition_tokens, q_dtype, stream)
+    if st:
+        _check(st, "paged_attention_decode_scored")
 
 
 def decode_plan(seq_lens, num_kv_heads: int, max_seq_len: int, partition_tokens: int = 0) -> np.ndarray:
