@@ -141,6 +141,60 @@ pkv_status pkv_paged_kv_append(const void* k, const void* v, int32_t in_dtype, i
                                const int64_t* slot_mapping, void* k_cache, void* v_cache,
                                const pkv_cache_desc* desc, void* stream);
 
+/*
+ * Rotary positions.  The pages take queries and keys as given; models that
+ * rotate them by their positions do it between the projection and the append,
+ * and this call is that step and the append in one pass.
+ *
+ * pkv_rope_frequencies (host, plain C++, 64 bits): the turns per position of
+ * each of the rotary_dim / 2 rotated pairs, f_i / 2 pi with f_i = base^(-2 i /
+ * rotary_dim) scaled for contexts `factor` times the original one:
+ *   PKV_ROPE_NONE    f_i
+ *   PKV_ROPE_LINEAR  f_i / factor (position interpolation)
+ *   PKV_ROPE_NTK     f_i of the base base * factor^(rotary_dim / (rotary_dim - 2))
+ *   PKV_ROPE_PARTS   (1 - g) f_i / factor + g f_i, g = (r - low) / (high - low) clamped
+ *                    to [0, 1], r = original_len * f_i / 2 pi the turns over the
+ *                    original context (low 1, high 32 with a magnitude of 0.1 ln(factor)
+ *                    + 1, or low 1, high 4 with none, are in use)
+ * freqs (host, [rotary_dim / 2][2]) receives pairs of binary32 whose sum is the
+ * frequency to 2^-48.  factor >= 1, base > 1; low < high and original_len > 0 for
+ * PKV_ROPE_PARTS, rotary_dim >= 4 for PKV_ROPE_NTK, else PKV_ERR_INVALID.
+ */
+typedef enum { PKV_ROPE_NONE = 0, PKV_ROPE_LINEAR = 1, PKV_ROPE_NTK = 2, PKV_ROPE_PARTS = 3 } pkv_rope_scaling;
+pkv_status pkv_rope_frequencies(int32_t rotary_dim, double base, int32_t scaling, double factor, int32_t original_len,
+                                double low, double high, float* freqs);
+
+/*
+ * Rotates the step's queries and keys and appends its keys and values:
+ * pair i of each head's first rotary_dim elements, (a, b), becomes
+ *     magnitude * (a cos - b sin, b cos + a sin),  angle = 2 pi positions[t] f_i
+ * in binary32 (the angle within 2^-23 of a turn, plus |positions[t]| 2^-51 of
+ * one), rounded once to in_dtype; the other elements stay as they are.  Pair i is
+ * elements i and i + rotary_dim / 2, or with interleaved != 0 elements 2 i and 2 i + 1.
+ * Queries go to q_out, keys and values to the cache as pkv_paged_kv_append
+ * writes rows of in_dtype (to every pool type).
+ *
+ * q [num_tokens][num_q_heads][head_size], k, v [num_tokens][num_kv_heads]
+ *   [head_size], in_dtype (PKV_F16 or PKV_BF16, a 16-bit pool's own type): a token's heads
+ *   lie side by side, tokens are q_stride, k_stride, v_stride elements apart
+ *   (multiples of 8, at least a row for more than one token), so the three
+ *   can be parts of one projection's rows.  num_q_heads == 0: no queries.
+ * q_out: like q, tokens q_out_stride elements apart; q itself (with its stride), or memory
+ *   that overlaps no input.
+ * positions: device int32 [num_tokens], any values.  slot_mapping: device int64
+ *   [num_tokens]; a negative slot appends nothing (the token's query is rotated
+ *   all the same), a slot outside the pool sets PKV_DEVERR_SLOT and is skipped.
+ * freqs: device float [rotary_dim / 2][2], as pkv_rope_frequencies writes them (8-byte
+ *   aligned).  rotary_dim: a multiple of 16 up to head_size.
+ * num_tokens == 0 is a no-op.
+ */
+pkv_status pkv_paged_rope_append(const void* q, int64_t q_stride, int32_t num_q_heads, const void* k,
+                                 int64_t k_stride, const void* v, int64_t v_stride, int32_t in_dtype,
+                                 int32_t num_tokens, const int32_t* positions, const int64_t* slot_mapping,
+                                 const float* freqs, int32_t rotary_dim, int32_t interleaved, float magnitude,
+                                 void* k_cache, void* v_cache, const pkv_cache_desc* desc, void* q_out,
+                                 int64_t q_out_stride, void* stream);
+
 /* Bytes of one block (all KV heads) of one pool of this description; 0 for a
  * description that is not supported. */
 size_t pkv_cache_block_bytes(const pkv_cache_desc* desc);

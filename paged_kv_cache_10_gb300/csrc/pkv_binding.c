@@ -33,13 +33,16 @@ static struct {
     pkv_status (*scored)(const void*, int32_t, int32_t, int32_t, const void*, const void*, const pkv_cache_desc*,
                          const int32_t*, int32_t, const int32_t*, int32_t, float, const pkv_score_mod*, float*,
                          const int32_t*, void*, void*, size_t, int32_t, void*);
+    pkv_status (*rope)(const void*, int64_t, int32_t, const void*, int64_t, const void*, int64_t, int32_t, int32_t,
+                       const int32_t*, const int64_t*, const float*, int32_t, int32_t, float, void*, void*,
+                       const pkv_cache_desc*, void*, int64_t, void*);
     size_t (*block_bytes)(const pkv_cache_desc*);
 } fn;
 
 /* Objects of torch that bind() keeps. */
 static PyObject *t_i32, *t_i64, *t_f16, *t_bf16, *t_f32, *f_device, *f_raw_stream, *f_stream;
 /* Attribute and method names. */
-static PyObject *s_get_device, *s_is_contiguous, *s_data_ptr, *s_shape, *s_dtype, *s_nbytes, *s_num_blocks,
+static PyObject *s_get_device, *s_is_contiguous, *s_stride, *s_data_ptr, *s_shape, *s_dtype, *s_nbytes, *s_num_blocks,
     *s_block_size, *s_num_kv_heads, *s_head_size, *s_kv_dtype, *s_k_scale, *s_v_scale, *s_cap, *s_window, *s_slopes,
     *s_first, *s_prefix_lens;
 
@@ -608,6 +611,116 @@ static PyObject* py_scored(PyObject* self, PyObject* const* a, Py_ssize_t n) {
                    (float)scale, &m, (float*)w, (const int32_t*)fresh, out, ws, wn, part, st));
 }
 
+/* A 16-bit tensor [n, heads, D] (heads < 0: any number, returned) whose tokens may lie apart: pointer and elements from
+ * one token to the next. */
+static int token_rows(PyObject* t, const char* name, PyObject* type_of, int32_t n, int32_t D, long dev, int32_t* heads,
+                      void** p, int64_t* step) {
+    int32_t ts[3];
+    if (dims(t, name, 3, ts)) return -1;
+    PyObject* d = PyObject_GetAttr(type_of, s_dtype);
+    if (!d) return -1;
+    const int ok = is_type(t, d);
+    Py_DECREF(d);
+    if (ok < 0) return -1;
+    if (!ok || ts[0] != n || ts[2] != D || (*heads >= 0 && ts[1] != *heads)) {
+        PyErr_Format(PyExc_ValueError, "%s must have one type with k and a row of heads of %d elements for each of %d tokens",
+                     name, D, n);
+        return -1;
+    }
+    *heads = ts[1];
+    PyObject* r = PyObject_CallMethodNoArgs(t, s_stride);
+    if (!r) return -1;
+    long long at[3] = {0, 0, 0};
+    int good = PyTuple_Check(r) && PyTuple_GET_SIZE(r) == 3;
+    for (int i = 0; i < 3 && good; ++i) {
+        at[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(r, i));
+        good = !(at[i] == -1 && PyErr_Occurred());
+    }
+    Py_DECREF(r);
+    if (PyErr_Occurred()) return -1;
+    /* sizes of one have any stride */
+    if (!good || (at[2] != 1 && ts[2] > 1) || (at[1] != D && ts[1] > 1)) {
+        PyErr_Format(PyExc_ValueError, "%s must have a token's heads side by side", name);
+        return -1;
+    }
+    *step = ts[0] > 1 ? at[0] : (int64_t)ts[1] * D;
+    r = PyObject_CallMethodNoArgs(t, s_get_device);
+    const long on = r ? PyLong_AsLong(r) : -1;
+    Py_XDECREF(r);
+    if (on < 0) {
+        PyErr_Clear();
+        PyErr_Format(PyExc_TypeError, "%s must be a CUDA tensor", name);
+        return -1;
+    }
+    if (dev >= 0 && on != dev) {
+        PyErr_Format(PyExc_ValueError, "%s is on cuda:%ld, the current device is cuda:%ld", name, on, dev);
+        return -1;
+    }
+    r = PyObject_CallMethodNoArgs(t, s_data_ptr);
+    if (!r) return -1;
+    *p = PyLong_AsVoidPtr(r);
+    Py_DECREF(r);
+    return PyErr_Occurred() ? -1 : 0;
+}
+
+/* rope(q, k, v, positions, slot_mapping, freqs, k_cache, v_cache, desc, q_out, interleaved, magnitude, stream) */
+static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    pkv_cache_desc c;
+    int32_t type, T[1], fs[2], Hq = 0, Hk, Hv;
+    void *q = NULL, *k, *v, *pos, *slots, *freqs, *kc, *vc, *o = NULL, *st;
+    int64_t qstep = 0, kstep, vstep, ostep = 0;
+    long dev;
+    if (!nargs_ok(n, 13)) return NULL;
+    if (get_desc(a[8], &c) || dims(a[4], "slot_mapping", 1, T) || dims(a[5], "freqs", 2, fs)) return NULL;
+    int ok = is_type(a[4], t_i64);
+    if (ok < 0) return NULL;
+    if (!ok) {
+        PyErr_SetString(PyExc_TypeError, "slot_mapping must be int64");
+        return NULL;
+    }
+    ok = is_type(a[5], t_f32);
+    if (ok < 0) return NULL;
+    if (!ok || fs[1] != 2) {
+        PyErr_SetString(PyExc_ValueError, "freqs must be float32 [rotary_dim / 2, 2]");
+        return NULL;
+    }
+    const double magnitude = PyFloat_AsDouble(a[11]);
+    if (magnitude == -1.0 && PyErr_Occurred()) return NULL;
+    const int inter = PyObject_IsTrue(a[10]);
+    if (inter < 0 || element_type(a[1], Py_None, &type)) return NULL;
+    if ((a[0] == Py_None) != (a[9] == Py_None)) {
+        PyErr_SetString(PyExc_ValueError, "q and q_out go together");
+        return NULL;
+    }
+    if (a[3] == Py_None) {
+        PyErr_SetString(PyExc_TypeError, "positions must be int32");
+        return NULL;
+    }
+    Hk = Hv = c.num_kv_heads;
+    if (Hk < 0 || fs[0] > INT32_MAX / 2) {
+        PyErr_SetString(PyExc_ValueError, "sizes out of range");
+        return NULL;
+    }
+    if (token_rows(a[1], "k", a[1], T[0], c.head_size, -1, &Hk, &k, &kstep) || current_device(&dev) ||
+        token_rows(a[1], "k", a[1], T[0], c.head_size, dev, &Hk, &k, &kstep) ||
+        token_rows(a[2], "v", a[1], T[0], c.head_size, dev, &Hv, &v, &vstep))
+        return NULL;
+    if (a[0] != Py_None) {
+        Hq = -1;
+        if (token_rows(a[0], "q", a[1], T[0], c.head_size, dev, &Hq, &q, &qstep) ||
+            token_rows(a[9], "q_out", a[1], T[0], c.head_size, dev, &Hq, &o, &ostep))
+            return NULL;
+    }
+    if (optional_vector(a[3], t_i32, T[0], "positions", "int32", dev, &pos) ||
+        ptr_of(a[4], "slot_mapping", dev, &slots) || ptr_of(a[5], "freqs", dev, &freqs) ||
+        pool_size(a[6], &c, "k_cache") || pool_size(a[7], &c, "v_cache") || ptr_of(a[6], "k_cache", dev, &kc) ||
+        ptr_of(a[7], "v_cache", dev, &vc) || stream_of(a[12], &st))
+        return NULL;
+    DONE(fn.rope(q, qstep, Hq, k, kstep, v, vstep, type, T[0], (const int32_t*)pos, (const int64_t*)slots,
+                 (const float*)freqs, 2 * fs[0], inter, (float)magnitude, kc, vc, &c, o, ostep, st));
+}
+
 static int address(PyObject* map, const char* name, void* slot) {
     PyObject* a = PyDict_GetItemString(map, name);
     void* p = a ? PyLong_AsVoidPtr(a) : NULL;
@@ -650,6 +763,7 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         address(a[1], "pkv_select_blocks", &fn.select) ||
         address(a[1], "pkv_paged_attention_decode_sparse", &fn.sparse) ||
         address(a[1], "pkv_paged_attention_decode_scored", &fn.scored) ||
+        address(a[1], "pkv_paged_rope_append", &fn.rope) ||
         address(a[1], "pkv_cache_block_bytes", &fn.block_bytes))
         return NULL;
     Py_RETURN_NONE;
@@ -657,7 +771,7 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(bind),   METHOD(append), METHOD(read),   METHOD(decode),
-                                METHOD(bounds), METHOD(select), METHOD(sparse), METHOD(scored),
+                                METHOD(bounds), METHOD(select), METHOD(sparse), METHOD(scored), METHOD(rope),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkv_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
@@ -670,7 +784,8 @@ PyMODINIT_FUNC PyInit__pkv_binding(void) {
                  {&s_num_blocks, "num_blocks"}, {&s_block_size, "block_size"},       {&s_num_kv_heads, "num_kv_heads"},
                  {&s_head_size, "head_size"},   {&s_kv_dtype, "kv_dtype"},           {&s_k_scale, "k_scale"},
                  {&s_v_scale, "v_scale"},       {&s_cap, "cap"},                     {&s_window, "window"},
-                 {&s_slopes, "slopes"},         {&s_first, "first"},                 {&s_prefix_lens, "prefix_lens"}};
+                 {&s_slopes, "slopes"},         {&s_first, "first"},                 {&s_prefix_lens, "prefix_lens"},
+                 {&s_stride, "stride"}};
     for (size_t i = 0; i < sizeof names / sizeof names[0]; ++i)
         if (!(*names[i].to = PyUnicode_InternFromString(names[i].name))) return NULL;
     return PyModule_Create(&module);

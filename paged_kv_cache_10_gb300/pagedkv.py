@@ -45,6 +45,7 @@ EXPORTED = [
     "pkv_decode_cascade_staging_bytes", "pkv_cache_block_bytes", "pkv_paged_kv_read", "pkv_paged_key_bounds",
     "pkv_select_blocks_workspace_bytes", "pkv_select_blocks", "pkv_decode_sparse_workspace_bytes",
     "pkv_paged_attention_decode_sparse", "pkv_decode_scored_workspace_bytes", "pkv_paged_attention_decode_scored",
+    "pkv_rope_frequencies", "pkv_paged_rope_append",
 ]
 
 
@@ -174,6 +175,9 @@ def lib():
         "pkv_decode_scored_workspace_bytes": (ctypes.c_size_t, [i32, i32, i32, i32, i32, i32, i32]),
         "pkv_paged_attention_decode_scored": (i32, [P, i32, i32, i32, P, P, D, P, i32, P, i32, ctypes.c_float, M, P, P,
                                                     P, P, ctypes.c_size_t, i32, P]),
+        "pkv_rope_frequencies": (i32, [i32, ctypes.c_double, i32, ctypes.c_double, i32, ctypes.c_double, ctypes.c_double, P]),
+        "pkv_paged_rope_append": (i32, [P, i64, i32, P, i64, P, i64, i32, i32, P, P, P, i32, i32, ctypes.c_float, P, P, D,
+                                        P, i64, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(L, name)
@@ -200,7 +204,7 @@ def _calls():
     spec.loader.exec_module(m)
     names = ("pkv_paged_kv_append", "pkv_paged_kv_read", "pkv_paged_attention_decode", "pkv_paged_key_bounds",
              "pkv_select_blocks", "pkv_paged_attention_decode_sparse", "pkv_paged_attention_decode_scored",
-             "pkv_cache_block_bytes")
+             "pkv_paged_rope_append", "pkv_cache_block_bytes")
     m.bind(torch, {n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _stream)
     _native = m
     return m
@@ -300,6 +304,31 @@ def paged_kv_append(k, v, slot_mapping, k_cache, v_cache, desc: CacheDesc, in_dt
     st = _calls().append(k, v, slot_mapping, k_cache, v_cache, desc, in_dtype, stream)
     if st:
         _check(st, "paged_kv_append")
+
+
+ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                     original_len: int = 0, low: float = 1.0, high: float = 32.0) -> np.ndarray:
+    """Turns per position of the rotated pairs, float32 [rotary_dim / 2, 2] (pairs that add up to 48 bits), for
+    paged_rope_append; scaling: "none", "linear", "ntk" or "parts" (by turns over original_len positions)."""
+    if rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("rotary_dim must be positive and even")
+    out = np.empty((rotary_dim // 2, 2), np.float32)
+    _check(lib().pkv_rope_frequencies(int(rotary_dim), float(base), ROPE_SCALING[scaling], float(factor), int(original_len),
+                                      float(low), float(high), _np_ptr(out)), "rope_frequencies")
+    return out
+
+
+def paged_rope_append(q, k, v, positions, slot_mapping, freqs, k_cache, v_cache, desc: CacheDesc, q_out,
+                      interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
+    """Rotates queries and keys by positions (int32 [T]) and appends keys and values: q, q_out [T, Hq, D] (both None:
+    no queries; q_out may be q), k, v [T, Hkv, D], all of one 16-bit type, tokens any multiple of 8 elements apart;
+    slot_mapping int64 [T]; freqs float32 [rotary_dim / 2, 2] from rope_frequencies (device tensors)."""
+    st = _calls().rope(q, k, v, positions, slot_mapping, freqs, k_cache, v_cache, desc, q_out, interleaved, magnitude, stream)
+    if st:
+        _check(st, "paged_rope_append")
 
 
 def paged_kv_read(slot_mapping, k_cache, v_cache, desc: CacheDesc, k_out, v_out, out_dtype: str | None = None,
