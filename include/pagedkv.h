@@ -571,7 +571,9 @@ pkv_status pkv_paged_attention_decode_sparse(const void* q, int32_t q_dtype, int
  * for every t with t >= first, t > p - window (window > 0), and t <= p or t <
  * prefix; other keys, whatever they and their values hold, take no part.  A row
  * that no key is left for gives zeros.  Keys that no row of a launch's unit of work
- * reaches (in front of a window or of the first position) are not read.
+ * reaches (in front of a window or of the first position) are not read, but by the
+ * first kernel of a prefill over fp8 or integer-coded pools, which copies
+ * whole sequences.
  *
  *   cap: 0 for none, else from 2^-20 to 2^20 (and scale / cap, times k_scale for an
  *     fp8 pool, finite).  tanh is within 2^-22 of 1, and of itself for small scores.
@@ -699,6 +701,25 @@ pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype, int32_t n
                                        const int32_t* seq_lens, const int32_t* work_units,
                                        int32_t num_work_units, float scale, void* out, void* workspace,
                                        size_t workspace_bytes, void* stream);
+
+/*
+ * pkv_paged_attention_prefill with scores capped, biased and masked as
+ * pkv_score_mod says (score NULL: plain causal ones): row j of sequence s sits at
+ * position p = seq_lens[s] - n_s + j, and key t is visible to it when t <= p or t <
+ * prefix_lens[s], inside its window and not in front of first[query_start[s] + j].
+ * Arguments, pools, workspace, plan and errors as for pkv_paged_attention_prefill.
+ * Keys and values that a row does not see do not reach it, whatever they hold.
+ * A value that is not finite makes the rows that see it, in a 128-key tile where
+ * some row of the same 256 does not see every key, NaN in whole; elsewhere it
+ * makes them what the products give.
+ */
+pkv_status pkv_paged_attention_prefill_scored(const void* q, int32_t q_dtype, int32_t num_tokens, int32_t num_q_heads,
+                                              int32_t num_seqs, const int32_t* query_start, int32_t max_query_len,
+                                              const void* k_cache, const void* v_cache, const pkv_cache_desc* desc,
+                                              const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                              const int32_t* seq_lens, const int32_t* work_units,
+                                              int32_t num_work_units, float scale, const pkv_score_mod* score,
+                                              void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Workspace bytes pkv_paged_attention_prefill needs: 0 for an f16 / bf16

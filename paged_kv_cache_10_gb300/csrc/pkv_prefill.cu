@@ -64,6 +64,10 @@ constexpr float kRebase = 8.0f;   // log2 units
 constexpr int kUnitSlots = 4;
 constexpr int kUnitReaders = 11;
 
+// Scored prefill: the mask of a value tile's tokens with a value that is not
+// finite, for the last kBadSlots tiles.
+constexpr int kBadSlots = 8;
+
 // q_full, q_empty, k_full[3], k_empty[3], v_full[2], v_empty[2], v_zero[2], s_full[2 tiles],
 // p_full[2 tiles], o_done[2 tiles], drain, u_full[4], u_empty[4]
 constexpr int kNumBars = 2 + 2 * kKStages + 3 * kVStages + 2 + 2 + 2 + 1 + 2 * kUnitSlots;
@@ -80,9 +84,11 @@ struct Tile {
     static constexpr int kOffV = kOffK + kKStages * kOp;
     static constexpr int kOffBar = kOffV + kVStages * kOp;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
-    static constexpr int kUnitBytes = 48;  // one published unit (sizeof(Unit) rounded up)
-    static constexpr int kSmemBytes = kOffMisc + 8 + kUnitSlots * kUnitBytes + 1024;  // tmem slot, abort flag,
-                                                                                       // unit ring; alignment slack
+    static constexpr int kUnitBytes = 64;  // one published unit (sizeof(Unit) rounded up)
+    static constexpr int kOffBad = kOffMisc + 8 + kUnitSlots * kUnitBytes;  // scored: tokens with values to poison
+    static_assert(kOffBad % 16 == 0, "token masks are read as vectors");
+    static constexpr int kSmemBytes = kOffBad + kBadSlots * 16 + 1024;  // tmem slot, abort flag, unit ring, token
+                                                                         // masks; alignment slack
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
@@ -111,6 +117,12 @@ struct PrefillParams {
     int32_t NP, row_chunks;
     // prefill: the launch's scheduling counters (g_prefill_sched slot)
     int32_t sched_slot;
+    // scored prefill (pkv_score_mod): with a cap, qk_scale is scale / cap (* k_scale)
+    float cap_out = 0.f;                  // cap * log2(e), or 0
+    int32_t window = 0;
+    const float* slopes = nullptr;        // [Hq]
+    const int32_t* first = nullptr;       // [T]
+    const int32_t* prefix_lens = nullptr; // [S]
 };
 
 // Unit-claim counters of the persistent prefill, one pair (next unit, CTAs
@@ -217,14 +229,174 @@ struct Unit {
     int h;              // KV head
     int q0, n, ctx, t0;  // prefill: the sequence's first row in q / out, its new tokens, the
                          // tokens before them, the first token of Q tile A
+    // scored prefill: keys count from position k0 (kv_end and bt too), the first of a block
+    int k0, prefix;      // prefix: positions below it are visible to every row
+    int lead;            // keys in front of the lowest that any row attends to
+    int lo_max, hi_min;  // highest first and lowest last key of the rows: tiles inside are whole
 };
+static_assert(sizeof(Unit) <= Tile<128>::kUnitBytes, "unit ring");
+
+// Keys [lo, hi] that the row of token tok of the unit's sequence attends to; none where lo > hi.
+__device__ __forceinline__ void row_range(const PrefillParams& p, const Unit& u, int tok, int& lo, int& hi) {
+    const int pos = u.ctx + tok;
+    lo = p.first ? max(load_live(p.first + u.q0 + tok), 0) : 0;
+    if (p.window > 0) lo = max(lo, pos - p.window + 1);
+    hi = max(pos, u.prefix - 1);
+}
+
+// Scored prefill: the unit's key range from its rows'.  Whole warp; every lane
+// gets the same result.  A Q tile whose rows are all empty keeps one masked tile,
+// whose softmax threads write the zeros.
+__device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int RQ, int lane, Unit& u) {
+    u.prefix = p.prefix_lens ? min(load_live(p.prefix_lens + s), u.ctx + u.n) : 0;
+    int lo_min = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff, end[2] = {0, 0};
+    for (int i = lane; i < 2 * RQ && u.t0 + i < u.n; i += 32) {
+        int lo, hi;
+        row_range(p, u, u.t0 + i, lo, hi);
+        if (lo <= hi) {
+            lo_min = min(lo_min, lo);
+            end[i >= RQ] = max(end[i >= RQ], hi + 1);
+        }
+        lo_max = max(lo_max, lo <= hi ? lo : 0x7fffffff);
+        hi_min = min(hi_min, hi);
+    }
+    lo_min = __reduce_min_sync(0xffffffffu, lo_min);
+    lo_max = __reduce_max_sync(0xffffffffu, lo_max);
+    hi_min = __reduce_min_sync(0xffffffffu, hi_min);
+    const bool any = lo_min != 0x7fffffff;
+    u.k0 = any ? lo_min / kBlockSize * kBlockSize : 0;
+    u.lead = any ? lo_min - u.k0 : 1;
+    for (int X = 0; X < 2; ++X) {
+        const int e = __reduce_max_sync(0xffffffffu, end[X]);
+        u.kv_end[X] = u.t0 + X * RQ < u.n ? max(e - u.k0, 1) : 0;
+    }
+    u.lo_max = lo_max == 0x7fffffff ? lo_max : lo_max - u.k0;
+    u.hi_min = hi_min - u.k0;
+    u.bt += u.k0 / kBlockSize;
+}
+
+// Scores of a row's tile in log2 units, in place: x = q.k.  Returns the factor that
+// is left to apply (qk_scale where neither a cap nor a bias was).
+// tanh within |y| <= 1 is y P(y^2) with the polynomial of degree 6 of the least
+// relative error, 2^-23.5, fitted at the Chebyshev points of [0, 1]: twelve
+// multiply-adds and products on the FMA pipe for two elements instead of two
+// special-function operations each, which would triple the pipe that the
+// exponentials use.  A warp whose tile has a larger y takes those.
+__device__ __forceinline__ float score_tile(const PrefillParams& p, uint32_t (&x)[4][32], float slope, int dist0) {
+    const auto get = [&](int q, int i) { return make_float2(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])); };
+    const auto put = [&](int q, int i, float2 v) {
+        x[q][2 * i] = __float_as_uint(v.x);
+        x[q][2 * i + 1] = __float_as_uint(v.y);
+    };
+    float left = p.qk_scale;
+    if (p.cap_out > 0.f) {
+        float mx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+                mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], fabsf(__uint_as_float(x[q][i])), fabsf(__uint_as_float(x[q][i + 1])));
+        const float amax = fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], 0.f) * left;
+        const float2 c2 = make_float2(left, left), o2 = make_float2(p.cap_out, p.cap_out);
+        if (warp_all(amax <= 1.f)) {
+            const auto k = [](float v) { return make_float2(v, v); };
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float2 y = fmul2(get(q, i), c2), u = fmul2(y, y);
+                    float2 t = ffma2(u, k(0.0010455536f), k(-0.00621706992f));
+                    t = ffma2(u, t, k(0.0203055199f));
+                    t = ffma2(u, t, k(-0.0534651764f));
+                    t = ffma2(u, t, k(0.133253977f));
+                    t = ffma2(u, t, k(-0.333328575f));
+                    t = ffma2(u, t, k(0.99999994f));
+                    put(q, i, fmul2(fmul2(y, o2), t));
+                }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    x[q][i] = __float_as_uint(tanh_score(__uint_as_float(x[q][i]) * left) * p.cap_out);
+        }
+        left = 1.f;
+    }
+    if (p.slopes) {
+        const float2 l2 = make_float2(left, left);
+        const float d0 = static_cast<float>(dist0);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float j = static_cast<float>(q * 32 + 2 * i);
+                const float2 v = fmul2(get(q, i), l2);
+                put(q, i, make_float2(fmaf(-slope, fabsf(d0 - j), v.x), fmaf(-slope, fabsf(d0 - (j + 1.f)), v.y)));
+            }
+        left = 1.f;
+    }
+    return left;
+}
+
+// Whether a token of the mask lies in keys [lo, hi] counted from the tile's first.
+__device__ __forceinline__ bool any_token(uint4 m, int lo, int hi) {
+    const uint32_t w[4] = {m.x, m.y, m.z, m.w};
+    bool any = false;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const int a = max(lo - 32 * q, 0), b = min(hi - 32 * q, 31);
+        if (a <= b) any |= (w[q] & (0xffffffffu << a) & (0xffffffffu >> (31 - b))) != 0u;
+    }
+    return any;
+}
+
+// Scored prefill, a landed value tile that some row sees in part: clears the 16-byte
+// chunks with a value that is not finite, which would turn every row's output
+// into NaN through 0 * NaN, and returns the mask of their tokens; rows that
+// attend to one of those become NaN at the end.  Whole warp; one pass over the
+// tile where all is finite.
+template <typename T, int D>
+__device__ uint4 clear_not_finite(unsigned char* vb, int lane) {
+    constexpr int kRowChunks = D / 8, kPerStep = 32 / kRowChunks;  // rows a step covers
+    constexpr uint32_t kInf = std::is_same<T, BF16>::value ? 0x7f80u : 0x7c00u;
+    const auto chunk = [&](int step) {
+        const int idx = step * 32 + lane, r = idx / kRowChunks, c = idx % kRowChunks;
+        return reinterpret_cast<uint4*>(vb + (c >> 3) * kColBlock + swz128(r, c & 7));
+    };
+    const auto top = [](uint4 v) {  // largest magnitude bits of the eight elements, two lanes
+        const uint32_t m = 0x7fff7fffu;
+        return __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+    };
+    uint32_t acc[2] = {0u, 0u};
+#pragma unroll 8
+    for (int step = 0; step < kTileN / kPerStep; ++step) acc[step & 1] = __vmaxu2(acc[step & 1], top(*chunk(step)));
+    const uint32_t a = __vmaxu2(acc[0], acc[1]);
+    uint32_t mask[4] = {0u, 0u, 0u, 0u};
+    if (__any_sync(0xffffffffu, (a & 0xffffu) >= kInf || (a >> 16) >= kInf)) {
+        for (int step = 0; step < kTileN / kPerStep; ++step) {
+            const uint32_t t = top(*chunk(step));
+            const bool bad = (t & 0xffffu) >= kInf || (t >> 16) >= kInf;
+            if (bad) *chunk(step) = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t b = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+            for (int r = 0; r < kPerStep; ++r)
+                if ((b >> (r * kRowChunks)) & ((1u << kRowChunks) - 1u)) {
+                    const int row = step * kPerStep + r;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (row >> 5 == q) mask[q] |= 1u << (row & 31);
+                }
+        }
+    }
+    return make_uint4(mask[0], mask[1], mask[2], mask[3]);
+}
 
 // Prefill unit number lin: unit work[lin / Hkv] of the host plan (or of the
 // default order: each (sequence, KV head) from its last query tiles down)
 // for KV head lin % Hkv.  False when the unit has no rows or its sequence's
 // bounds are inconsistent (reported when rep).
-__device__ bool prefill_unit(const PrefillParams& p, int64_t lin, int RQ, bool rep, Unit& u) {
-    int s, qt;
+__device__ bool prefill_unit(const PrefillParams& p, int64_t lin, int RQ, bool rep, Unit& u, int& s) {
+    int qt;
     if (p.work) {
         const int w = load_live(p.work + lin / p.Hkv);
         u.h = static_cast<int>(lin % p.Hkv);
@@ -288,7 +460,9 @@ __device__ __forceinline__ bool take_unit(uint64_t* u_full, uint64_t* u_empty, c
 // Q tile X holds 128 / G members x G heads of one (group, KV head); keys =
 // one partition of the group's shared blocks (no causal mask); split-K
 // partials.
-template <typename T, int D, bool kPrefix>
+// kScored (prefill only): capped, biased and masked scores; keys count from the
+// first block that some row of the unit attends to.
+template <typename T, int D, bool kPrefix, bool kScored>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
@@ -317,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kOffMisc + 4);
     Unit* unit_ring = reinterpret_cast<Unit*>(sm + kOffMisc + 8);  // [kUnitSlots]
+    uint4* bad_ring = reinterpret_cast<uint4*>(sm + TL::kOffBad);   // [kBadSlots]
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.G;
@@ -458,7 +633,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (lane == 0) c = atomicAdd(sched, 1u);
                         c = __shfl_sync(0xffffffffu, c, 0);
                         if (c >= total) break;
-                        if (prefill_unit(p, c, RQ, lane == 0, u)) {
+                        int seq;
+                        if (prefill_unit(p, c, RQ, lane == 0, u, seq)) {
+                            if constexpr (kScored) scored_unit(p, seq, RQ, lane, u);
                             found = true;
                             break;
                         }
@@ -608,7 +785,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // then completes v_zero of its stage.
                     const int r0 = kv_max - j * kTileN;
                     bool okv = true;
-                    if (j == nkt - 1 && r0 < kTileN) {
+                    if constexpr (kScored) {
+                        // rows in front of the lowest key too, and the tokens with values
+                        // that are not finite in tiles that some row sees in part
+                        uint4 bad = make_uint4(0u, 0u, 0u, 0u);
+                        if (j * kTileN < u.lo_max || j * kTileN + kTileN - 1 > u.hi_min) {
+                            okv = warp_all(mbar_wait(v_full + st, (g / nst) & 1));
+                            if (okv) {
+                                unsigned char* vb = sm + kOffV + st * kOpBytes;
+                                constexpr int kRowChunks = D / 8;
+                                const int head = j == 0 ? u.lead : 0, tail = max(kTileN - r0, 0);
+                                for (int idx = lane; idx < (head + tail) * kRowChunks; idx += 32) {
+                                    const int i = idx / kRowChunks, c = idx % kRowChunks;
+                                    const int r = i < head ? i : r0 + i - head;
+                                    *reinterpret_cast<uint4*>(vb + (c >> 3) * kColBlock + swz128(r, c & 7)) =
+                                        make_uint4(0u, 0u, 0u, 0u);
+                                }
+                                __syncwarp();
+                                bad = clear_not_finite<T, D>(vb, lane);
+                                fence_proxy_async_smem();
+                            }
+                        }
+                        if (lane == 0) bad_ring[g % kBadSlots] = bad;
+                    } else if (j == nkt - 1 && r0 < kTileN) {
                         okv = warp_all(mbar_wait(v_full + st, (g / nst) & 1));
                         if (okv) {
                             unsigned char* vb = sm + kOffV + st * kOpBytes;
@@ -721,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // ahead here (it waits for v_empty of this tile), so the
                     // last tile's phase is the one this parity names.
                     ok = tc::wait_spin(v_full + g % kVStages, (g / kVStages) & 1);
-                    if (ok && j == nkt - 1) ok = tc::wait_spin(v_zero + g % kVStages, (g / kVStages) & 1);
+                    if (ok && (kScored || j == nkt - 1)) ok = tc::wait_spin(v_zero + g % kVStages, (g / kVStages) & 1);
                     if (!ok) break;
                     bool kn = false;  // keys of tile j + 1 waited for
                     // Q tile A, then B: P V_X(j), then S_X(j + 1)
@@ -786,6 +985,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float2 c2 = make_float2(c, c);
         bool ok = true;
         int tp = 0;  // tiles of this Q tile in the finished units
+        int gt = 0;  // scored: value tiles of the finished units
         for (int k = 0;; ++k) {
             Unit u;
             const int r = next_unit(k, true, u);
@@ -795,7 +995,17 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ntx = ((X ? u.kv_end[1] : u.kv_end[0]) + kTileN - 1) / kTileN;
             bool row_valid;
             int pos;  // last key this row attends to
-            if constexpr (!kPrefix) {
+            int lo = 0;       // scored: the first; none where it is above pos
+            float slope = 0.f;
+            bool poisoned = false;  // scored: the row attends to a value that is not finite
+            if constexpr (kScored) {
+                const int tx = u.t0 + X * RQ;
+                row_valid = tx + rq < u.n;
+                row_range(p, u, min(tx + rq, u.n - 1), lo, pos);
+                lo -= u.k0;
+                pos -= u.k0;
+                if (p.slopes) slope = load_live(p.slopes + h * G + g) * kLog2e;
+            } else if constexpr (!kPrefix) {
                 const int tx = u.t0 + X * RQ;
                 row_valid = tx + rq < u.n;
                 pos = u.ctx + tx + min(rq, max(u.n - 1 - tx, 0));  // padding rows reuse the last position
@@ -807,7 +1017,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             // does not wait for it
             const int member_row =
                 kPrefix && row_valid ? load_live(p.group_members + m0 + mrow0 + X * RQ + rq) : -1;
-            float m_ref = -INFINITY, l = 0.f;
+            // scored: this row's place counted from the first key; a tile may leave it nothing
+            const int place = kScored ? u.ctx + min(u.t0 + X * RQ + rq, u.n - 1) - u.k0 : 0;
+            float m_ref = kScored ? kNoScore : -INFINITY, l = 0.f;
+            const auto check_values = [&](int j) {  // the value tile's scan is done once P V of it is
+                const uint4 m = bad_ring[(gt + j) % kBadSlots];
+                if ((m.x | m.y | m.z | m.w) != 0u) poisoned |= any_token(m, lo - j * kTileN, pos - j * kTileN);
+            };
             for (int j = 0; j < ntx; ++j) {
                 ok = warp_all(tc::wait_spin(s_full + X, (tp + j) & 1));
                 if (!ok || !warp_all(*abort_flag == 0)) break;
@@ -815,6 +1031,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P V_X(j - 1) is complete (it precedes S_X(j)): take its phase
                 if (j > 0) ok = warp_all(tc::wait_spin(o_done + X, (tp + j - 1) & 1));
                 if (!ok) break;
+                if constexpr (kScored) {
+                    if (j > 0) check_values(j - 1);
+                }
                 uint32_t x[4][32];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tc::ld32(tS + q * 32, x[q]);
@@ -823,7 +1042,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // masked keys -inf; row maximum of the raw scores (scale > 0
                 // keeps the order)
                 const int key0 = j * kTileN;
-                if (key0 + kTileN - 1 > pos) {
+                float ce = c;  // factor that is left on x
+                if constexpr (kScored) {
+                    ce = score_tile(p, x, slope, place - key0);
+                    if (key0 + kTileN - 1 > pos || key0 < lo) {
+                        const int a = lo - key0, b = pos - key0;
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                if (q * 32 + i > b || q * 32 + i < a) x[q][i] = __float_as_uint(-INFINITY);
+                    }
+                } else if (key0 + kTileN - 1 > pos) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -836,7 +1066,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int i = 0; i < 32; i += 2)
                         mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], __uint_as_float(x[q][i]), __uint_as_float(x[q][i + 1]));
-                const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], -INFINITY) * c;
+                const float mt = fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], -INFINITY) * ce;
+                const float2 ce2 = kScored ? make_float2(ce, ce) : c2;
                 const float m_new = fmaxf(m_ref, mt);
                 const bool rebase = m_new > m_ref + kRebase;
                 float alpha = 1.f;
@@ -855,7 +1086,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     uint32_t pk[16], pl[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float2 a = ffma2(make_float2(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])), c2, nm2);
+                        float2 a = ffma2(make_float2(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])), ce2, nm2);
                         a.x = ex2(a.x);
                         a.y = ex2(a.y);
                         ls[i & 3] = fadd2(ls[i & 3], a);
@@ -891,7 +1122,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (live) ok = warp_all(tc::wait_spin(o_done + X, (tp + ntx - 1) & 1));
             if (live && ok) {
                 tc::fence_after();
-                const float inv = p.o_scale / l;
+                float inv = p.o_scale / l;
+                if constexpr (kScored) {
+                    check_values(ntx - 1);
+                    if (l == 0.f) inv = 0.f;  // a row with nothing to attend to
+                    if (poisoned) inv = __int_as_float(0x7fffffff);
+                }
                 if constexpr (!kPrefix) {
                     typename T::storage* orow =
                         reinterpret_cast<typename T::storage*>(p.out) +
@@ -954,6 +1190,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tp += ntx;
+            gt += (max(u.kv_end[0], u.kv_end[1]) + kTileN - 1) / kTileN;
             if (!ok || *abort_flag) break;
         }
     }
@@ -974,7 +1211,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <typename T, int D, bool kPrefix>
+template <typename T, int D, bool kPrefix, bool kScored = false>
 cudaError_t launch_tile(const PrefillParams& p, dim3 grid, const CUtensorMap& tq, const CUtensorMap& tk,
                         const CUtensorMap& tv, cudaStream_t st) {
     constexpr int kSmemBytes = Tile<D>::kSmemBytes;
@@ -985,7 +1222,7 @@ cudaError_t launch_tile(const PrefillParams& p, dim3 grid, const CUtensorMap& tq
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     cudaError_t attr = cudaSuccess;
     std::call_once(once[dev], [&] {
-        attr = cudaFuncSetAttribute(prefill_tc_kernel<T, D, kPrefix>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr = cudaFuncSetAttribute(prefill_tc_kernel<T, D, kPrefix, kScored>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kSmemBytes);
     });
     if (attr != cudaSuccess) return attr;
@@ -1001,11 +1238,11 @@ cudaError_t launch_tile(const PrefillParams& p, dim3 grid, const CUtensorMap& tq
         la[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = la;
         cfg.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_tc_kernel<T, D, kPrefix>, p, tq, tk, tv);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_tc_kernel<T, D, kPrefix, kScored>, p, tq, tk, tv);
         if (e != cudaErrorNotSupported && e != cudaErrorInvalidValue) return e;
         (void)cudaGetLastError();  // a driver that refuses the attribute gets a plain launch
     }
-    prefill_tc_kernel<T, D, kPrefix><<<grid, kThreads, kSmemBytes, st>>>(p, tq, tk, tv);
+    prefill_tc_kernel<T, D, kPrefix, kScored><<<grid, kThreads, kSmemBytes, st>>>(p, tq, tk, tv);
     return cudaGetLastError();
 }
 
@@ -1013,11 +1250,14 @@ cudaError_t launch_tile(const PrefillParams& p, dim3 grid, const CUtensorMap& tq
 // when there are fewer; the launch takes the next counter slot.
 template <typename T>
 cudaError_t launch_prefill(PrefillParams p, int D, const CUtensorMap& tq, const CUtensorMap& tk,
-                           const CUtensorMap& tv, cudaStream_t st) {
+                           const CUtensorMap& tv, bool scored, cudaStream_t st) {
     static std::atomic<uint32_t> next_slot{0};
     p.sched_slot = static_cast<int32_t>(next_slot.fetch_add(1u, std::memory_order_relaxed) % kSchedSlots);
     const int64_t units = p.work ? p.num_work : static_cast<int64_t>(p.num_qtiles) * p.S;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units * p.Hkv, num_sms())));
+    if (scored)
+        return D == 64 ? launch_tile<T, 64, false, true>(p, grid, tq, tk, tv, st)
+                       : launch_tile<T, 128, false, true>(p, grid, tq, tk, tv, st);
     return D == 64 ? launch_tile<T, 64, false>(p, grid, tq, tk, tv, st)
                    : launch_tile<T, 128, false>(p, grid, tq, tk, tv, st);
 }
@@ -1204,14 +1444,12 @@ cudaError_t launch_cascade_stage_fp8(const CascadeParams& cp, int num_groups, in
 
 using namespace pkv;
 
-extern "C" pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype, int32_t num_tokens,
-                                                  int32_t num_q_heads, int32_t num_seqs, const int32_t* query_start,
-                                                  int32_t max_query_len, const void* k_cache, const void* v_cache,
-                                                  const pkv_cache_desc* desc, const int32_t* block_tables,
-                                                  int32_t max_blocks_per_seq, const int32_t* seq_lens,
-                                                  const int32_t* work_units, int32_t num_work_units, float scale,
-                                                  void* out, void* workspace, size_t workspace_bytes,
-                                                  void* stream) {
+namespace {
+pkv_status prefill_common(const void* q, int32_t q_dtype, int32_t num_tokens, int32_t num_q_heads, int32_t num_seqs,
+                          const int32_t* query_start, int32_t max_query_len, const void* k_cache, const void* v_cache,
+                          const pkv_cache_desc* desc, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                          const int32_t* seq_lens, const int32_t* work_units, int32_t num_work_units, float scale,
+                          const pkv_score_mod* mod, void* out, void* workspace, size_t workspace_bytes, void* stream) {
     if (!desc || num_tokens < 0 || num_seqs < 0 || max_query_len < 0 || num_q_heads <= 0) return PKV_ERR_INVALID;
     if (num_work_units < 0 || (!work_units && num_work_units > 0)) return PKV_ERR_INVALID;
     if (desc->block_size != kBlockSize || desc->num_kv_heads <= 0 || desc->num_blocks <= 0) return PKV_ERR_INVALID;
@@ -1228,6 +1466,10 @@ extern "C" pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype
     if (fp8 && !(desc->k_scale > 0.f && desc->k_scale < 3.0e38f && desc->v_scale > 0.f && desc->v_scale < 3.0e38f))
         return PKV_ERR_INVALID;
     if (fp8 && !(scale * desc->k_scale < 3.0e38f)) return PKV_ERR_INVALID;
+    if (mod) {
+        const pkv_status bad = check_score_mod(mod, scale, desc);
+        if (bad != PKV_OK) return bad;
+    }
     if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0 || (work_units && num_work_units == 0)) return PKV_OK;
     if (!q || !out || !k_cache || !v_cache || !block_tables || !seq_lens || !query_start) return PKV_ERR_INVALID;
     if (max_blocks_per_seq <= 0 || !aligned16(q) || !aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache))
@@ -1302,14 +1544,51 @@ extern "C" pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype
     p.out_v8 = (reinterpret_cast<uintptr_t>(out) & 31u) == 0;  // rows are multiples of 128 bytes
     p.err = err;
 
+    if (mod) {
+        if (mod->cap > 0.f) {
+            p.qk_scale = scale * (fp8 ? desc->k_scale : 1.f) / mod->cap;
+            p.cap_out = mod->cap * kLog2e;
+        }
+        p.window = mod->window;
+        p.slopes = mod->slopes;
+        p.first = mod->first;
+        p.prefix_lens = mod->prefix_lens;
+    }
+
     CUtensorMap tq, tk, tv;
     const int64_t pool_rows = static_cast<int64_t>(pool_blocks) * desc->num_kv_heads * kBlockSize;
     if (!encode_token_head_map(&tq, q, D, num_q_heads, num_tokens, G, kTileM / G) ||
         !encode_pool_map(&tk, k_pool, 2, pool_rows, D) || !encode_pool_map(&tv, v_pool, 2, pool_rows, D))
         return PKV_ERR_CUDA;
-    const cudaError_t e = q_dtype == PKV_BF16 ? launch_prefill<BF16>(p, D, tq, tk, tv, st)
-                                              : launch_prefill<F16>(p, D, tq, tk, tv, st);
+    const cudaError_t e = q_dtype == PKV_BF16 ? launch_prefill<BF16>(p, D, tq, tk, tv, mod != nullptr, st)
+                                              : launch_prefill<F16>(p, D, tq, tk, tv, mod != nullptr, st);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+}  // namespace
+
+extern "C" pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype, int32_t num_tokens,
+                                                  int32_t num_q_heads, int32_t num_seqs, const int32_t* query_start,
+                                                  int32_t max_query_len, const void* k_cache, const void* v_cache,
+                                                  const pkv_cache_desc* desc, const int32_t* block_tables,
+                                                  int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                                  const int32_t* work_units, int32_t num_work_units, float scale,
+                                                  void* out, void* workspace, size_t workspace_bytes,
+                                                  void* stream) {
+    return prefill_common(q, q_dtype, num_tokens, num_q_heads, num_seqs, query_start, max_query_len, k_cache, v_cache,
+                          desc, block_tables, max_blocks_per_seq, seq_lens, work_units, num_work_units, scale, nullptr,
+                          out, workspace, workspace_bytes, stream);
+}
+
+extern "C" pkv_status pkv_paged_attention_prefill_scored(
+    const void* q, int32_t q_dtype, int32_t num_tokens, int32_t num_q_heads, int32_t num_seqs,
+    const int32_t* query_start, int32_t max_query_len, const void* k_cache, const void* v_cache,
+    const pkv_cache_desc* desc, const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+    const int32_t* work_units, int32_t num_work_units, float scale, const pkv_score_mod* score, void* out,
+    void* workspace, size_t workspace_bytes, void* stream) {
+    const pkv_score_mod none{};
+    return prefill_common(q, q_dtype, num_tokens, num_q_heads, num_seqs, query_start, max_query_len, k_cache, v_cache,
+                          desc, block_tables, max_blocks_per_seq, seq_lens, work_units, num_work_units, scale,
+                          score ? score : &none, out, workspace, workspace_bytes, stream);
 }
 
 extern "C" size_t pkv_prefill_workspace_bytes(int32_t kv_dtype, int32_t num_seqs, int32_t num_kv_heads,
