@@ -634,6 +634,53 @@ pkv_status pkv_paged_attention_decode_scored(const void* q, int32_t q_dtype, int
                                              int32_t partition_tokens, void* stream);
 
 /*
+ * Eviction by weight: a cache that holds a fixed number of tokens keeps those
+ * that attention goes to.  The pages know preemption and block eviction (whole
+ * sequences, whole prefixes), not this.  The weights are what
+ * pkv_paged_attention_decode_scored leaves (or any other measure);
+ * pkv_select_tokens chooses, for each sequence and KV head, the tokens to keep;
+ * pkv_alloc_evict_batch shortens the sequences on the host; pkv_paged_kv_compact
+ * moves the rows together.  Heads keep different tokens, in their order.  Keys
+ * rotated by their positions stay as they are; the next token's position is the
+ * caller's to count.
+ *
+ * pkv_select_tokens
+ * kept: device int32 [num_seqs][num_kv_heads][num_kept]: positions, ascending: the first
+ *   sink_tokens and the last recent_tokens of the sequence and, of the others, those of
+ *   the largest weights (equal ones, -0 and 0 among them: the lowest positions first;
+ *   NaN below every number); every token where there are at most num_kept; the
+ *   rest -1.  sink_tokens + recent_tokens <= num_kept, num_kept > 0.
+ * weights: device float [num_blocks][num_kv_heads][block_size].
+ * max_seq_len (host, up to 2^30) must be >= every length; a length below 0, above it (rounded
+ *   up to whole blocks) or above the block table sets PKV_DEVERR_SEQ_LEN and is clamped.  A
+ *   block id outside the pool sets PKV_DEVERR_BLOCK_ID; its tokens count lowest.
+ */
+pkv_status pkv_select_tokens(const float* weights, const pkv_cache_desc* desc, const int32_t* block_tables,
+                             int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len,
+                             int32_t num_seqs, int32_t num_kept, int32_t sink_tokens, int32_t recent_tokens,
+                             int32_t* kept, void* stream);
+
+/*
+ * Moves rows together: for every sequence s, KV head h and entry i, key, value and
+ * (weights not NULL) weight of position kept[s][h][i] go to position i of the
+ * sequence, whose blocks block_tables (before) and dst_tables (after) name; pools of
+ * every type, codes with their parameters.  What lies behind the last row of a
+ * list stays as it was.  seq_lens: the lengths before.
+ * A list's entries ascend and are followed by -1.  A block of dst_tables is either none
+ * of the call's source blocks, or stands at the same place of the same sequence's row
+ * of block_tables, where no other sequence of the call holds it; so the two tables may be
+ * one, and pkv_alloc_evict_batch's are such.  An entry at or above the sequence's length sets
+ * PKV_DEVERR_SEQ_LEN, a block id outside the pool PKV_DEVERR_BLOCK_ID, and the row is
+ * skipped; more entries than dst_tables has room for set PKV_DEVERR_SEQ_LEN and are dropped.
+ * Key bounds of the blocks (pkv_paged_key_bounds) have to be made anew, and so do the
+ * groups of a cascade.
+ */
+pkv_status pkv_paged_kv_compact(const int32_t* kept, int32_t num_kept, void* k_cache, void* v_cache, float* weights,
+                                const pkv_cache_desc* desc, const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                const int32_t* seq_lens, int32_t num_seqs, const int32_t* dst_tables,
+                                int32_t dst_blocks_per_seq, void* stream);
+
+/*
  * Paged (chunked) prefill attention, causal, on the tensor cores.  Prefill
  * processes a prompt's tokens together; chunked prefill cuts a long prompt
  * into chunks that run in successive iterations, each attending to the KV
@@ -864,6 +911,17 @@ pkv_status pkv_alloc_append_batch(pkv_alloc* a, const int64_t* seq_ids, int32_t 
 pkv_status pkv_alloc_append_tokens(pkv_alloc* a, const int64_t* seq_ids, const int32_t* counts, int32_t n,
                                    int64_t* slots, int64_t slots_cap, int32_t* pairs, int32_t pairs_cap,
                                    int32_t* num_pairs);
+/* Eviction (pkv_paged_kv_compact): sequence seq_ids[i] keeps counts[i] tokens (a
+ * sequence at most once; negative ids are padding; a sequence that holds no more than its
+ * count stays as it is).  Of the blocks that hold them, one that another sequence
+ * shares is replaced by a fresh one, and one that is cached under a hash, its
+ * content about to change, loses the hash; the other blocks are released.  Every fresh block is taken
+ * before any is released, so that no block of the batch's tables before is one of another
+ * sequence's after.  Export the tables before and after, and enqueue the
+ * compaction before any call that writes to blocks taken later.  The sequence's blocks
+ * can no longer be committed under hashes (pkv_alloc_commit gives PKV_ERR_INVALID), nor
+ * those of its forks.  All or nothing; PKV_ERR_OOM if the fresh blocks are not there. */
+pkv_status pkv_alloc_evict_batch(pkv_alloc* a, const int64_t* seq_ids, const int32_t* counts, int32_t n);
 /* Export padded block tables and lengths for a batch: tables is
  * [n][max_blocks] (unused entries -1), seq_lens [n]; a row whose seq_id is
  * negative gets length 0.  PKV_ERR_INVALID if a table does not fit. */

@@ -160,6 +160,29 @@ class AllocatorModel:
         for blk in reversed(table):
             self._release(blk)
 
+    def evict_batch(self, seqs, counts) -> None:
+        """Sequence seqs[i] keeps counts[i] tokens in blocks of its own, uncached; the others are released."""
+        short = [(s, c) for s, c in zip(seqs, counts) if s >= 0 and self.lens[s] > c]
+        places = [(s, b) for s, c in short for b in range(-(-c // self.block_size)) if self.ref[self.tables[s][b]] > 1]
+        if len(places) > self.num_free():
+            raise OutOfBlocks()
+        fresh = {place: self._take() for place in places}
+        gone = []
+        for s, c in short:
+            table = self.tables[s]
+            nb = -(-c // self.block_size)
+            gone += reversed(table[nb:])
+            del table[nb:]
+            for b in range(nb):
+                if (s, b) in fresh:
+                    gone.append(table[b])
+                    table[b] = fresh[s, b]
+                elif table[b] in self.hash_of:
+                    del self.cached[self.hash_of.pop(table[b])]
+            self.lens[s] = c
+        for blk in gone:
+            self._release(blk)
+
     def move_to(self, other: "AllocatorModel", seq: int):
         """Moves seq into another pool (swap out / in): one new block per
         block, all held by this sequence alone; returns (old, new) pairs."""

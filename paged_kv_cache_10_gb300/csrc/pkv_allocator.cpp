@@ -43,6 +43,7 @@ namespace {
 struct Seq {
     std::vector<int32_t> blocks;
     int64_t len = 0;
+    bool evicted = false;  // rows were dropped: its blocks hold no prefix of its tokens
 };
 
 }  // namespace
@@ -286,6 +287,71 @@ pkv_status pkv_alloc_free(pkv_alloc* a, int64_t seq_id) {
     return PKV_OK;
 }
 
+pkv_status pkv_alloc_evict_batch(pkv_alloc* a, const int64_t* seq_ids, const int32_t* counts, int32_t n) {
+    if (!a || n < 0 || (n > 0 && (!seq_ids || !counts))) return PKV_ERR_INVALID;
+    try {
+        std::unordered_map<int64_t, int> seen;
+        for (int32_t i = 0; i < n; ++i) {
+            if (seq_ids[i] < 0) continue;
+            if (counts[i] < 0 || seen[seq_ids[i]]++) return PKV_ERR_INVALID;
+            if (!a->seqs.count(seq_ids[i])) return PKV_ERR_NOT_FOUND;
+        }
+        struct Swap {
+            int32_t row, at, fresh;
+        };
+        std::vector<Swap> swaps;
+        std::vector<int32_t> gone;
+        size_t most = 0;
+        const auto blocks = [&](int32_t i) { return (static_cast<int64_t>(counts[i]) + a->block_size - 1) / a->block_size; };
+        const auto undo = [&] {
+            for (auto r = swaps.rbegin(); r != swaps.rend(); ++r) a->untake(r->fresh);
+        };
+        for (int32_t i = 0; i < n; ++i) {
+            if (seq_ids[i] < 0) continue;
+            const Seq& s = a->seqs.find(seq_ids[i])->second;
+            if (s.len <= counts[i]) continue;
+            most += s.blocks.size();
+            for (int64_t b = 0; b < blocks(i); ++b)
+                if (a->ref[s.blocks[b]] > 1) swaps.push_back({i, static_cast<int32_t>(b), -1});
+        }
+        gone.reserve(most);
+        for (size_t k = 0; k < swaps.size(); ++k) {
+            if (!a->can_take()) {
+                swaps.resize(k);
+                undo();
+                return PKV_ERR_OOM;
+            }
+            swaps[k].fresh = a->take();
+        }
+        // nothing fails from here on
+        size_t k = 0;
+        for (int32_t i = 0; i < n; ++i) {
+            if (seq_ids[i] < 0) continue;
+            Seq& s = a->seqs.find(seq_ids[i])->second;
+            if (s.len <= counts[i]) continue;
+            const int64_t nb = blocks(i);
+            for (int64_t b = static_cast<int64_t>(s.blocks.size()) - 1; b >= nb; --b) gone.push_back(s.blocks[b]);
+            for (int64_t b = 0; b < nb; ++b) {
+                int32_t& id = s.blocks[b];
+                if (k < swaps.size() && swaps[k].row == i && swaps[k].at == b) {
+                    gone.push_back(id);
+                    id = swaps[k++].fresh;
+                } else if (a->hashed[id]) {
+                    a->table.erase(a->bhash[id]);
+                    a->hashed[id] = 0;
+                }
+            }
+            s.blocks.resize(nb);
+            s.len = counts[i];
+            s.evicted = true;
+        }
+        for (int32_t id : gone) a->release(id);
+    } catch (const std::bad_alloc&) {
+        return PKV_ERR_OOM;
+    }
+    return PKV_OK;
+}
+
 pkv_status pkv_alloc_append_batch(pkv_alloc* a, const int64_t* seq_ids, int32_t n, int64_t* slots,
                                   int32_t* pairs, int32_t pairs_cap, int32_t* num_pairs) {
     if (!a || n < 0 || (n > 0 && (!seq_ids || !slots)) || !num_pairs) return PKV_ERR_INVALID;
@@ -493,6 +559,7 @@ pkv_status move_seq(pkv_alloc* from, pkv_alloc* to, int64_t seq_id, int32_t* pai
     if (nb > to->available()) return PKV_ERR_OOM;
     Seq moved;
     moved.len = s.len;
+    moved.evicted = s.evicted;
     for (int32_t i = 0; i < nb; ++i) {
         if (!to->can_take()) {
             for (auto r = moved.blocks.rbegin(); r != moved.blocks.rend(); ++r) to->untake(*r);
@@ -622,6 +689,7 @@ pkv_status pkv_alloc_commit(pkv_alloc* a, int64_t seq_id, const uint64_t* hashes
     auto it = a->seqs.find(seq_id);
     if (it == a->seqs.end()) return PKV_ERR_NOT_FOUND;
     const Seq& s = it->second;
+    if (s.evicted && num_hashes > 0) return PKV_ERR_INVALID;
     if (static_cast<int64_t>(num_hashes) * a->block_size > s.len) return PKV_ERR_INVALID;  // full blocks only
     for (int32_t i = 0; i < num_hashes; ++i) {
         const int32_t id = s.blocks[i];

@@ -36,6 +36,10 @@ static struct {
     pkv_status (*rope)(const void*, int64_t, int32_t, const void*, int64_t, const void*, int64_t, int32_t, int32_t,
                        const int32_t*, const int64_t*, const float*, int32_t, int32_t, float, void*, void*,
                        const pkv_cache_desc*, void*, int64_t, void*);
+    pkv_status (*select_tokens)(const float*, const pkv_cache_desc*, const int32_t*, int32_t, const int32_t*, int32_t,
+                                int32_t, int32_t, int32_t, int32_t, int32_t*, void*);
+    pkv_status (*compact)(const int32_t*, int32_t, void*, void*, float*, const pkv_cache_desc*, const int32_t*, int32_t,
+                          const int32_t*, int32_t, const int32_t*, int32_t, void*);
     size_t (*block_bytes)(const pkv_cache_desc*);
 } fn;
 
@@ -721,6 +725,63 @@ static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
                  (const float*)freqs, 2 * fs[0], inter, (float)magnitude, kc, vc, &c, o, ostep, st));
 }
 
+/* kept [S, Hkv, n], block_tables [S, MB] and seq_lens [S] of an eviction. */
+static int kept_ok(PyObject* kept, PyObject* tables, PyObject* lens, const pkv_cache_desc* c, int32_t* ks, int32_t* ts) {
+    int32_t S[1];
+    if (want_i32(kept, "kept, block_tables and seq_lens") || want_i32(tables, "kept, block_tables and seq_lens") ||
+        want_i32(lens, "kept, block_tables and seq_lens") || dims(kept, "kept", 3, ks) ||
+        dims(tables, "block_tables", 2, ts) || dims(lens, "seq_lens", 1, S) ||
+        same(ks[1], c->num_kv_heads, "kept must have shape [num_seqs, num_kv_heads, n]") ||
+        same(ks[0], S[0], "kept must have shape [num_seqs, num_kv_heads, n]") ||
+        same(ts[0], S[0], "block_tables must have one row per sequence"))
+        return -1;
+    return 0;
+}
+
+/* select_tokens(weights, desc, block_tables, seq_lens, max_seq_len, kept, sink_tokens, recent_tokens, stream) */
+static PyObject* py_select_tokens(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    pkv_cache_desc c;
+    int32_t ks[3], ts[2], max_len, sink, recent;
+    void *w, *tables, *lens, *kept, *st;
+    long dev;
+    if (!nargs_ok(n, 9)) return NULL;
+    if (get_desc(a[1], &c) || kept_ok(a[5], a[2], a[3], &c, ks, ts) || as_i32(a[4], &max_len) || as_i32(a[6], &sink) ||
+        as_i32(a[7], &recent))
+        return NULL;
+    if (a[0] == Py_None) {
+        PyErr_SetString(PyExc_TypeError, "weights must be a CUDA tensor");
+        return NULL;
+    }
+    if (ptr_of(a[5], "kept", -1, &kept) || current_device(&dev) || ptr_of(a[5], "kept", dev, &kept) ||
+        weights_of(a[0], &c, dev, &w) || ptr_of(a[2], "block_tables", dev, &tables) ||
+        ptr_of(a[3], "seq_lens", dev, &lens) || stream_of(a[8], &st))
+        return NULL;
+    DONE(fn.select_tokens((const float*)w, &c, (const int32_t*)tables, ts[1], (const int32_t*)lens, max_len, ks[0], ks[2],
+                          sink, recent, (int32_t*)kept, st));
+}
+
+/* compact(kept, k_cache, v_cache, desc, block_tables, seq_lens, dst_tables, weights, stream) */
+static PyObject* py_compact(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    pkv_cache_desc c;
+    int32_t ks[3], ts[2], ds[2];
+    void *w, *tables, *lens, *kept, *dst, *kc, *vc, *st;
+    long dev;
+    if (!nargs_ok(n, 9)) return NULL;
+    if (get_desc(a[3], &c) || kept_ok(a[0], a[4], a[5], &c, ks, ts) || want_i32(a[6], "dst_tables") ||
+        dims(a[6], "dst_tables", 2, ds) || same(ds[0], ks[0], "dst_tables must have one row per sequence"))
+        return NULL;
+    if (ptr_of(a[0], "kept", -1, &kept) || current_device(&dev) || ptr_of(a[0], "kept", dev, &kept) ||
+        pool_size(a[1], &c, "k_cache") || pool_size(a[2], &c, "v_cache") || ptr_of(a[1], "k_cache", dev, &kc) ||
+        ptr_of(a[2], "v_cache", dev, &vc) || ptr_of(a[4], "block_tables", dev, &tables) ||
+        ptr_of(a[5], "seq_lens", dev, &lens) || ptr_of(a[6], "dst_tables", dev, &dst) ||
+        weights_of(a[7], &c, dev, &w) || stream_of(a[8], &st))
+        return NULL;
+    DONE(fn.compact((const int32_t*)kept, ks[2], kc, vc, (float*)w, &c, (const int32_t*)tables, ts[1], (const int32_t*)lens,
+                    ks[0], (const int32_t*)dst, ds[1], st));
+}
+
 static int address(PyObject* map, const char* name, void* slot) {
     PyObject* a = PyDict_GetItemString(map, name);
     void* p = a ? PyLong_AsVoidPtr(a) : NULL;
@@ -763,7 +824,8 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         address(a[1], "pkv_select_blocks", &fn.select) ||
         address(a[1], "pkv_paged_attention_decode_sparse", &fn.sparse) ||
         address(a[1], "pkv_paged_attention_decode_scored", &fn.scored) ||
-        address(a[1], "pkv_paged_rope_append", &fn.rope) ||
+        address(a[1], "pkv_paged_rope_append", &fn.rope) || address(a[1], "pkv_select_tokens", &fn.select_tokens) ||
+        address(a[1], "pkv_paged_kv_compact", &fn.compact) ||
         address(a[1], "pkv_cache_block_bytes", &fn.block_bytes))
         return NULL;
     Py_RETURN_NONE;
@@ -772,6 +834,7 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(bind),   METHOD(append), METHOD(read),   METHOD(decode),
                                 METHOD(bounds), METHOD(select), METHOD(sparse), METHOD(scored), METHOD(rope),
+                                METHOD(select_tokens), METHOD(compact),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkv_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

@@ -1,0 +1,372 @@
+// pkv_evict.cu -- eviction from the cache by accumulated attention weight: the
+// tokens that each (sequence, KV head) keeps, and their rows moved together.
+//
+// Selection: of a row's L tokens the first `sink`, the last `recent` and those of
+// the largest weights among the others, n in all, ascending.  Weights become
+// 32-bit keys that order like them; a radix selection over 11, 11 and 10 bits
+// finds the key of the last one kept, exactly, and ties go to the lowest position.
+// One CTA a row keeps its keys in shared memory (up to kCachedTokens; a longer row
+// reads its weights again in each pass).
+//
+// Compaction: row kept[i] moves to position i.  kept ascends, so kept[i] >= i: a
+// chunk of entries [a, b) writes positions below b and every later entry reads at b
+// or above.  So one CTA that takes its entries chunk by chunk, all of a chunk's
+// loads before its first store, may write the blocks it reads from, with one
+// barrier a chunk.  Columns of a row never meet: they are split over CTAs where
+// there are few rows of sequences and heads.
+#include <algorithm>
+#include <cstdint>
+
+#include "pkv_int.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kCachedTokens = 40960;  // 160 KB of keys
+constexpr int kBins = 2048;
+
+struct SelectTokens {
+    const float* weights;
+    const int32_t *block_tables, *seq_lens;
+    int32_t* kept;
+    int32_t MB, NB, Hkv, n, sink, recent, max_len, cached;
+    unsigned int* err;
+};
+
+// Larger weights have larger keys; -0 equals 0, NaN is below everything.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+    if (!(w == w)) return 0u;
+    const uint32_t u = w == 0.f ? 0u : __float_as_uint(w);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+__device__ __forceinline__ uint32_t load_key(const SelectTokens& p, const int32_t* table, int h, int t, bool rep) {
+    const int blk = load_live(table + t / kBlockSize);
+    if (blk < 0 || blk >= p.NB) {
+        if (rep) report(p.err, PKV_DEVERR_BLOCK_ID);
+        return 0u;
+    }
+    return weight_key(load_live(p.weights + (static_cast<int64_t>(blk) * p.Hkv + h) * kBlockSize + t % kBlockSize));
+}
+
+// CTA (KV head x, sequence y).
+__global__ void __launch_bounds__(kSelThreads) select_tokens_kernel(const SelectTokens p) {
+    extern __shared__ uint32_t keys[];  // [p.cached]
+    __shared__ uint32_t hist[kBins];
+    __shared__ uint32_t wsum[kSelWarps], wtie[kSelWarps];
+    __shared__ uint32_t found_digit, found_left, found_count;
+    wait_primary_grid();
+    allow_dependent_launch();
+    const int h = blockIdx.x, s = blockIdx.y;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int L = load_live(p.seq_lens + s);
+    const int cap = min(p.MB * kBlockSize, p.max_len);
+    if (L < 0 || L > cap) {
+        if (tid == 0 && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        L = L < 0 ? 0 : cap;
+    }
+    int32_t* out = p.kept + (static_cast<int64_t>(s) * p.Hkv + h) * p.n;
+    if (L <= p.n) {
+        for (int i = tid; i < p.n; i += kSelThreads) out[i] = i < L ? i : -1;
+        return;
+    }
+    for (int i = tid; i < p.sink; i += kSelThreads) out[i] = i;
+    for (int i = tid; i < p.recent; i += kSelThreads) out[p.n - p.recent + i] = L - p.recent + i;
+    const int M = L - p.sink - p.recent;                // tokens to choose from, from position sink on
+    const uint32_t k = p.n - p.sink - p.recent;         // as many of them
+    if (k == 0) return;
+    const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.MB;
+    const bool cached = M <= p.cached;
+    for (int i = tid; i < M; i += kSelThreads) {
+        const uint32_t key = load_key(p, table, h, p.sink + i, true);
+        if (cached) keys[i] = key;
+    }
+    const auto key_of = [&](int i) { return cached ? keys[i] : load_key(p, table, h, p.sink + i, false); };
+
+    // keys at or above `from` are kept, and `ties` of those equal to `tie`
+    uint32_t prefix = 0u, left = k;
+    bool whole = false;  // the last digit's bin is kept in whole
+    int shift = 32;
+#pragma unroll 1
+    for (int pass = 0; pass < 3 && !whole; ++pass) {
+        const int bits = pass < 2 ? 11 : 10;
+        const int high = shift;  // bits [high, 32) are known
+        shift -= bits;
+        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0u;
+        __syncthreads();
+        for (int i = tid; i < M; i += kSelThreads) {
+            const uint32_t key = key_of(i);
+            if (high == 32 || (key >> high) == (prefix >> high)) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+        }
+        __syncthreads();
+        // bins from the top: thread i has the pair 2i, 2i + 1 counted from there
+        const uint32_t hi = hist[kBins - 1 - 2 * tid], lo = hist[kBins - 2 - 2 * tid];
+        uint32_t sum = hi + lo;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(kAll, sum, d);
+            if (lane >= d) sum += o;
+        }
+        if (lane == 31) wsum[warp] = sum;
+        __syncthreads();
+        uint32_t before = lane < warp ? wsum[lane] : 0u;
+        before = __reduce_add_sync(kAll, before);
+        const uint32_t end = before + sum, mid = end - lo, begin = mid - hi;  // counts above each bin
+        if (begin < left && left <= mid) {
+            found_digit = kBins - 1 - 2 * tid;
+            found_left = left - begin;
+            found_count = hi;
+        } else if (mid < left && left <= end) {
+            found_digit = kBins - 2 - 2 * tid;
+            found_left = left - mid;
+            found_count = lo;
+        }
+        __syncthreads();
+        prefix |= found_digit << shift;
+        left = found_left;
+        whole = found_count == found_left;
+    }
+    const uint32_t from = whole ? prefix : prefix + 1u;  // keys end at 0xff800000 (+infinity)
+    const uint32_t tie = prefix, ties = whole ? 0u : left;
+
+    // ---- ascending output: a warp's positions are consecutive
+    const int seg = (M + kSelThreads - 1) / kSelThreads * 32;
+    const int i0 = warp * seg, i1 = min(M, i0 + seg);
+    uint32_t sel = 0u, eq = 0u;
+    for (int i = i0; i < i1; i += 32) {
+        const uint32_t key = i + lane < i1 ? key_of(i + lane) : 0u;
+        const bool in = i + lane < i1;
+        sel += __popc(__ballot_sync(kAll, in && key >= from));
+        eq += __popc(__ballot_sync(kAll, in && ties > 0u && key == tie));
+    }
+    if (lane == 0) {
+        wsum[warp] = sel;
+        wtie[warp] = eq;
+    }
+    __syncthreads();
+    sel = __reduce_add_sync(kAll, lane < warp ? wsum[lane] : 0u);
+    eq = __reduce_add_sync(kAll, lane < warp ? wtie[lane] : 0u);
+    for (int i = i0; i < i1; i += 32) {
+        const uint32_t key = i + lane < i1 ? key_of(i + lane) : 0u;
+        const bool in = i + lane < i1;
+        const bool above = in && key >= from, equal = in && ties > 0u && key == tie;
+        const uint32_t ba = __ballot_sync(kAll, above), be = __ballot_sync(kAll, equal), below = (1u << lane) - 1u;
+        const uint32_t ra = sel + __popc(ba & below), re = eq + __popc(be & below);
+        if (above || (equal && re < ties)) out[p.sink + ra + min(re, ties)] = p.sink + i + lane;
+        sel += __popc(ba);
+        eq += __popc(be);
+    }
+}
+
+constexpr int kMoveThreads = 256;
+
+struct Compact {
+    const int32_t* kept;
+    unsigned char *k_cache, *v_cache;
+    float* weights;
+    const int32_t *src_tables, *dst_tables, *seq_lens;
+    int32_t n, Hkv, NB, src_mb, dst_mb, slices;
+    unsigned int* err;
+};
+
+// Moves one head's rows of one pool: `units` pieces of type T a row, from piece u0
+// on; off(t, u) is piece u of token t in a tile of tile_bytes.
+template <typename T, int PER, typename Off>
+__device__ __forceinline__ void move_rows(const Compact& p, unsigned char* pool, int64_t tile_bytes, int units, int u0,
+                                          int h, int s, int count, int L, bool rep, Off off) {
+    const int32_t* kept = p.kept + (static_cast<int64_t>(s) * p.Hkv + h) * p.n;
+    const int32_t* src_table = p.src_tables + static_cast<int64_t>(s) * p.src_mb;
+    const int32_t* dst_table = p.dst_tables + static_cast<int64_t>(s) * p.dst_mb;
+    const int rows = kMoveThreads * PER / units;  // units divides 256
+    for (int base = 0; base < count; base += rows) {
+        T x[PER];
+        unsigned char* to[PER];
+#pragma unroll
+        for (int e = 0; e < PER; ++e) {
+            const int at = e * kMoveThreads + threadIdx.x;
+            const int i = base + at / units, u = u0 + at % units;
+            to[e] = nullptr;
+            if (i >= count) continue;
+            const int t = load_live(kept + i);
+            if (t < 0) continue;
+            if (t >= L) {
+                if (rep) report(p.err, PKV_DEVERR_SEQ_LEN);
+                continue;
+            }
+            const int a = load_live(src_table + t / kBlockSize), b = load_live(dst_table + i / kBlockSize);
+            if (a < 0 || a >= p.NB || b < 0 || b >= p.NB) {
+                if (rep) report(p.err, PKV_DEVERR_BLOCK_ID);
+                continue;
+            }
+            if (a == b && t % kBlockSize == i % kBlockSize) continue;  // already there
+            x[e] = load_live(reinterpret_cast<const T*>(pool + (static_cast<int64_t>(a) * p.Hkv + h) * tile_bytes +
+                                                        off(t % kBlockSize, u)));
+            to[e] = pool + (static_cast<int64_t>(b) * p.Hkv + h) * tile_bytes + off(i % kBlockSize, u);
+        }
+        __syncthreads();  // a chunk's loads before its stores; later chunks read above what it writes
+#pragma unroll
+        for (int e = 0; e < PER; ++e)
+            if (to[e]) *reinterpret_cast<T*>(to[e]) = x[e];
+    }
+}
+
+// CTA (column slice x, plane and KV head y, sequence z).  Planes: keys, values, then for
+// integer-coded pools their rows' parameters, and the weights last.
+template <int D, int KV>
+__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const Compact p) {
+    constexpr bool kInt = KV == PKV_INT8 || KV == PKV_INT4;
+    wait_primary_grid();
+    const int plane = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv, s = blockIdx.z;
+    int L = load_live(p.seq_lens + s);
+    const bool first = blockIdx.x == 0 && plane == 0;
+    if (L < 0 || L > p.src_mb * kBlockSize) {
+        if (threadIdx.x == 0 && first && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        L = L < 0 ? 0 : p.src_mb * kBlockSize;
+    }
+    int count = min(p.n, L);
+    if (count > p.dst_mb * kBlockSize) {
+        if (threadIdx.x == 0 && first && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        count = p.dst_mb * kBlockSize;
+    }
+    if constexpr (!kInt) {
+        if (plane == 2) {
+            if (blockIdx.x == 0)
+                move_rows<float, 4>(p, reinterpret_cast<unsigned char*>(p.weights), kBlockSize * 4, 1, 0, h, s, count, L,
+                                    false, [](int t, int) { return t * 4; });
+            return;
+        }
+        constexpr int ROW = D * (KV == PKV_FP8_E4M3 ? 1 : 2);
+        const int units = ROW / 16 / p.slices;
+        move_rows<uint4, 4>(p, plane ? p.v_cache : p.k_cache, kBlockSize * ROW, units, blockIdx.x * units, h, s, count, L,
+                            first, [](int t, int u) { return t * ROW + u * 16; });
+    } else {
+        using L_ = IntTile<D, KV == PKV_INT8 ? 8 : 4>;
+        if (blockIdx.x != 0 && plane != 1) return;  // the value codes alone are split
+        if (plane == 0)
+            move_rows<uint4, 4>(p, p.k_cache, L_::kBytes, L_::RB / 16, 0, h, s, count, L, first,
+                                [](int t, int u) { return L_::key(t, u * 16); });
+        else if (plane == 1) {
+            const int units = L_::RB / 2 / p.slices;
+            move_rows<uint16_t, 8>(p, p.v_cache, L_::kBytes, units, blockIdx.x * units, h, s, count, L, false,
+                                   [](int t, int u) { return L_::val(t, u * 2); });
+        } else if (plane == 4)
+            move_rows<float, 4>(p, reinterpret_cast<unsigned char*>(p.weights), kBlockSize * 4, 1, 0, h, s, count, L, false,
+                                [](int t, int) { return t * 4; });
+        else
+            move_rows<uint2, 4>(p, plane == 3 ? p.v_cache : p.k_cache, L_::kBytes, 1, 0, h, s, count, L, false,
+                                [](int t, int) { return L_::param(t); });
+    }
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+pkv_status check_desc(const pkv_cache_desc* d) {
+    if (!d || d->num_blocks <= 0 || d->num_kv_heads <= 0 || d->head_size <= 0 || d->block_size <= 0 ||
+        !known_kv_dtype(d->kv_dtype))
+        return PKV_ERR_INVALID;
+    if (d->block_size != kBlockSize || (d->head_size != 64 && d->head_size != 128)) return PKV_ERR_UNSUPPORTED;
+    return PKV_OK;
+}
+
+template <int D>
+void (*compact_of(int kv))(Compact) {
+    switch (kv) {
+    case PKV_INT8: return compact_kernel<D, PKV_INT8>;
+    case PKV_INT4: return compact_kernel<D, PKV_INT4>;
+    case PKV_FP8_E4M3: return compact_kernel<D, PKV_FP8_E4M3>;
+    default: return compact_kernel<D, PKV_BF16>;  // 16-bit rows alike
+    }
+}
+
+}  // namespace
+}  // namespace pkv
+
+using namespace pkv;
+
+extern "C" pkv_status pkv_select_tokens(const float* weights, const pkv_cache_desc* d, const int32_t* block_tables,
+                                        int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t max_seq_len,
+                                        int32_t num_seqs, int32_t num_kept, int32_t sink_tokens, int32_t recent_tokens,
+                                        int32_t* kept, void* stream) {
+    const pkv_status bad = check_desc(d);
+    if (bad != PKV_OK) return bad;
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || max_seq_len < 0 || num_kept <= 0 || sink_tokens < 0 ||
+        recent_tokens < 0 || sink_tokens > num_kept || recent_tokens > num_kept - sink_tokens)
+        return PKV_ERR_INVALID;
+    if (max_blocks_per_seq > 0x7fffffff / kBlockSize || max_seq_len > max_blocks_per_seq * kBlockSize)
+        return max_blocks_per_seq > 0x7fffffff / kBlockSize ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID;
+    if (num_seqs > 65535 || max_seq_len > 0x40000000) return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!weights || !block_tables || !seq_lens || !kept || !aligned4(weights) || !aligned4(block_tables) ||
+        !aligned4(seq_lens) || !aligned4(kept))
+        return PKV_ERR_INVALID;
+    SelectTokens p{};
+    p.err = error_word();
+    if (!p.err) return PKV_ERR_CUDA;
+    p.weights = weights;
+    p.block_tables = block_tables;
+    p.seq_lens = seq_lens;
+    p.kept = kept;
+    p.MB = max_blocks_per_seq;
+    p.NB = d->num_blocks;
+    p.Hkv = d->num_kv_heads;
+    p.n = num_kept;
+    p.sink = sink_tokens;
+    p.recent = recent_tokens;
+    p.max_len = static_cast<int32_t>(std::min<int64_t>((static_cast<int64_t>(max_seq_len) + kBlockSize - 1) / kBlockSize * kBlockSize,
+                                                       static_cast<int64_t>(max_blocks_per_seq) * kBlockSize));
+    p.cached = std::min(p.max_len, kCachedTokens);
+    static bool configured[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PKV_ERR_CUDA;
+    if (!configured[dev]) {
+        if (cudaFuncSetAttribute(select_tokens_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCachedTokens * 4) !=
+            cudaSuccess)
+            return PKV_ERR_CUDA;
+        configured[dev] = true;
+    }
+    const cudaError_t e = launch_maybe_pdl(true, select_tokens_kernel, dim3(p.Hkv, num_seqs), dim3(kSelThreads),
+                                           static_cast<size_t>(p.cached) * 4, static_cast<cudaStream_t>(stream), p);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+extern "C" pkv_status pkv_paged_kv_compact(const int32_t* kept, int32_t num_kept, void* k_cache, void* v_cache,
+                                           float* weights, const pkv_cache_desc* d, const int32_t* block_tables,
+                                           int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+                                           const int32_t* dst_tables, int32_t dst_blocks_per_seq, void* stream) {
+    const pkv_status bad = check_desc(d);
+    if (bad != PKV_OK) return bad;
+    if (num_seqs < 0 || num_kept <= 0 || max_blocks_per_seq <= 0 || dst_blocks_per_seq <= 0) return PKV_ERR_INVALID;
+    if (max_blocks_per_seq > 0x7fffffff / kBlockSize || dst_blocks_per_seq > 0x7fffffff / kBlockSize ||
+        num_kept > 0x7fffffff - 4096 || num_seqs > 65535 || d->num_kv_heads > 65535 / 5)
+        return PKV_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PKV_OK;
+    if (!kept || !k_cache || !v_cache || !block_tables || !seq_lens || !dst_tables || !aligned4(kept) ||
+        !aligned4(block_tables) || !aligned4(seq_lens) || !aligned4(dst_tables) || !aligned4(weights) ||
+        !aligned16(k_cache) || !aligned16(v_cache))
+        return PKV_ERR_INVALID;
+    Compact p{};
+    p.err = error_word();
+    if (!p.err) return PKV_ERR_CUDA;
+    p.kept = kept;
+    p.k_cache = static_cast<unsigned char*>(k_cache);
+    p.v_cache = static_cast<unsigned char*>(v_cache);
+    p.weights = weights;
+    p.src_tables = block_tables;
+    p.dst_tables = dst_tables;
+    p.seq_lens = seq_lens;
+    p.n = num_kept;
+    p.Hkv = d->num_kv_heads;
+    p.NB = d->num_blocks;
+    p.src_mb = max_blocks_per_seq;
+    p.dst_mb = dst_blocks_per_seq;
+    // rows of few sequences and heads are split over four CTAs each
+    p.slices = static_cast<int64_t>(num_seqs) * p.Hkv * 2 <= num_sms() ? 4 : 1;
+    const int planes = (is_int_pool(d->kv_dtype) ? 4 : 2) + (weights ? 1 : 0);
+    auto kern = d->head_size == 128 ? compact_of<128>(d->kv_dtype) : compact_of<64>(d->kv_dtype);
+    const cudaError_t e = launch_maybe_pdl(true, kern, dim3(p.slices, planes * p.Hkv, num_seqs), dim3(kMoveThreads), 0,
+                                           static_cast<cudaStream_t>(stream), p);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}

@@ -46,6 +46,7 @@ EXPORTED = [
     "pkv_select_blocks_workspace_bytes", "pkv_select_blocks", "pkv_decode_sparse_workspace_bytes",
     "pkv_paged_attention_decode_sparse", "pkv_decode_scored_workspace_bytes", "pkv_paged_attention_decode_scored",
     "pkv_rope_frequencies", "pkv_paged_rope_append", "pkv_paged_attention_prefill_scored",
+    "pkv_select_tokens", "pkv_paged_kv_compact", "pkv_alloc_evict_batch",
 ]
 
 
@@ -177,6 +178,9 @@ def lib():
                                                     P, P, ctypes.c_size_t, i32, P]),
         "pkv_paged_attention_prefill_scored": (i32, [P, i32, i32, i32, i32, P, i32, P, P, D, P, i32, P, P, i32,
                                                      ctypes.c_float, M, P, P, ctypes.c_size_t, P]),
+        "pkv_select_tokens": (i32, [P, D, P, i32, P, i32, i32, i32, i32, i32, P, P]),
+        "pkv_paged_kv_compact": (i32, [P, i32, P, P, P, D, P, i32, P, i32, P, i32, P]),
+        "pkv_alloc_evict_batch": (i32, [P, P, P, i32]),
         "pkv_rope_frequencies": (i32, [i32, ctypes.c_double, i32, ctypes.c_double, i32, ctypes.c_double, ctypes.c_double, P]),
         "pkv_paged_rope_append": (i32, [P, i64, i32, P, i64, P, i64, i32, i32, P, P, P, i32, i32, ctypes.c_float, P, P, D,
                                         P, i64, P]),
@@ -206,7 +210,8 @@ def _calls():
     spec.loader.exec_module(m)
     names = ("pkv_paged_kv_append", "pkv_paged_kv_read", "pkv_paged_attention_decode", "pkv_paged_key_bounds",
              "pkv_select_blocks", "pkv_paged_attention_decode_sparse", "pkv_paged_attention_decode_scored",
-             "pkv_paged_rope_append", "pkv_cache_block_bytes")
+             "pkv_paged_rope_append", "pkv_select_tokens",
+             "pkv_paged_kv_compact", "pkv_cache_block_bytes")
     m.bind(torch, {n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _stream)
     _native = m
     return m
@@ -549,6 +554,24 @@ def paged_attention_decode_scored(q, k_cache, v_cache, desc: CacheDesc, block_ta
         _check(st, "paged_attention_decode_scored")
 
 
+def select_tokens(weights, desc: CacheDesc, block_tables, seq_lens, max_seq_len: int, kept, sink_tokens: int = 0,
+                  recent_tokens: int = 0, stream=None) -> None:
+    """The tokens each (sequence, KV head) keeps: weights float32 [NB, Hkv, 16], kept int32 [S, Hkv, n] (positions,
+    ascending, then -1): the first sink_tokens, the last recent_tokens and the largest weights among the others."""
+    st = _calls().select_tokens(weights, desc, block_tables, seq_lens, max_seq_len, kept, sink_tokens, recent_tokens, stream)
+    if st:
+        _check(st, "select_tokens")
+
+
+def paged_kv_compact(kept, k_cache, v_cache, desc: CacheDesc, block_tables, seq_lens, dst_tables, weights=None,
+                     stream=None) -> None:
+    """Moves the kept rows (int32 [S, Hkv, n], as select_tokens writes them) of every sequence and KV head together:
+    entry i to position i of the blocks that dst_tables (int32 [S, MB']) names, which may be those of block_tables."""
+    st = _calls().compact(kept, k_cache, v_cache, desc, block_tables, seq_lens, dst_tables, weights, stream)
+    if st:
+        _check(st, "paged_kv_compact")
+
+
 def decode_plan(seq_lens, num_kv_heads: int, max_seq_len: int, partition_tokens: int = 0) -> np.ndarray:
     """Host work plan for paged_attention_decode_append: every (sequence,
     partition) unit, longest first (int32)."""
@@ -825,6 +848,15 @@ class Allocator:
         _check(lib().pkv_alloc_append_tokens(self._h, _np_ptr(ids), _np_ptr(cnt), n, _np_ptr(slots), total,
                                              _np_ptr(pairs), max(n, 1), ctypes.byref(npairs)), "alloc_append_tokens")
         return slots[:total].copy(), pairs[: npairs.value].copy()
+
+    def evict_batch(self, seq_ids, counts) -> None:
+        """Sequence seq_ids[i] keeps counts[i] tokens, in blocks that no other sequence or hash holds (export the
+        tables before and after; the rows are moved by paged_kv_compact)."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        cnt = np.ascontiguousarray(counts, dtype=np.int32)
+        if ids.ndim != 1 or cnt.shape != ids.shape:
+            raise ValueError("seq_ids and counts differ in length")
+        _check(lib().pkv_alloc_evict_batch(self._h, _np_ptr(ids), _np_ptr(cnt), ids.shape[0]), "alloc_evict_batch")
 
     # -- automatic prefix caching
     def lookup(self, hashes) -> int:

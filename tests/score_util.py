@@ -88,8 +88,8 @@ def ref_select_tokens(weights, tables, lens, n, sink, recent):
         t = np.arange(L)
         for h in range(Hkv):
             w = weights[np.asarray(tables[s])[t // B], h, t % B].astype(np.float64)
-            w = np.where(np.isnan(w), -np.inf, w)
+            nan = np.isnan(w)  # below every number, -inf too
             forced = (t < sink) | (t >= L - recent)
-            order = np.lexsort((t, -w, ~forced))[:n]
+            order = np.lexsort((t, np.where(nan, 0.0, -w), nan, ~forced))[:n]
             kept[s, h, :len(order)] = np.sort(order)
     return kept
