@@ -119,6 +119,8 @@ struct PrefillParams {
     int32_t sched_slot;
     // scored prefill (pkv_score_mod): with a cap, qk_scale is scale / cap (* k_scale)
     float cap_out = 0.f;                  // cap * log2(e), or 0
+    float2 tanh_low[4];                   // coefficients of score_tile's short polynomial, twice
+    float tanh_low_max = 0.f;             // ... and the largest |q.k| that it takes
     int32_t window = 0;
     const float* slopes = nullptr;        // [Hq]
     const int32_t* first = nullptr;       // [T]
@@ -249,13 +251,16 @@ __device__ __forceinline__ void row_range(const PrefillParams& p, const Unit& u,
 // whose softmax threads write the zeros.
 __device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int RQ, int lane, Unit& u) {
     u.prefix = p.prefix_lens ? min(load_live(p.prefix_lens + s), u.ctx + u.n) : 0;
-    int lo_min = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff, end[2] = {0, 0};
+    int lo_min = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff, end0 = 0, end1 = 0;
     for (int i = lane; i < 2 * RQ && u.t0 + i < u.n; i += 32) {
         int lo, hi;
         row_range(p, u, u.t0 + i, lo, hi);
         if (lo <= hi) {
             lo_min = min(lo_min, lo);
-            end[i >= RQ] = max(end[i >= RQ], hi + 1);
+            if (i < RQ)
+                end0 = max(end0, hi + 1);
+            else
+                end1 = max(end1, hi + 1);
         }
         lo_max = max(lo_max, lo <= hi ? lo : 0x7fffffff);
         hi_min = min(hi_min, hi);
@@ -266,10 +271,8 @@ __device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int R
     const bool any = lo_min != 0x7fffffff;
     u.k0 = any ? lo_min / kBlockSize * kBlockSize : 0;
     u.lead = any ? lo_min - u.k0 : 1;
-    for (int X = 0; X < 2; ++X) {
-        const int e = __reduce_max_sync(0xffffffffu, end[X]);
-        u.kv_end[X] = u.t0 + X * RQ < u.n ? max(e - u.k0, 1) : 0;
-    }
+    u.kv_end[0] = max(__reduce_max_sync(0xffffffffu, end0) - u.k0, 1);
+    u.kv_end[1] = u.t0 + RQ < u.n ? max(__reduce_max_sync(0xffffffffu, end1) - u.k0, 1) : 0;
     u.lo_max = lo_max == 0x7fffffff ? lo_max : lo_max - u.k0;
     u.hi_min = hi_min - u.k0;
     u.bt += u.k0 / kBlockSize;
@@ -277,17 +280,20 @@ __device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int R
 
 // Scores of a row's tile in log2 units, in place: x = q.k.  Returns the factor that
 // is left to apply (qk_scale where neither a cap nor a bias was).
-// tanh within |y| <= 1 is y P(y^2) with the polynomial of degree 6 of the least
-// relative error, 2^-23.5, fitted at the Chebyshev points of [0, 1]: twelve
-// multiply-adds and products on the FMA pipe for two elements instead of two
-// special-function operations each, which would triple the pipe that the
-// exponentials use.  A warp whose tile has a larger y takes those.
-__device__ __forceinline__ float score_tile(const PrefillParams& p, uint32_t (&x)[4][32], float slope, int dist0) {
-    const auto get = [&](int q, int i) { return make_float2(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])); };
-    const auto put = [&](int q, int i, float2 v) {
-        x[q][2 * i] = __float_as_uint(v.x);
-        x[q][2 * i + 1] = __float_as_uint(v.y);
-    };
+//
+// tanh(y) is y P(y^2), P the polynomial of the least relative error fitted at the
+// Chebyshev points: degree 3 for |y| <= 0.375 (2^-23.9), degree 6 for |y| <= 1
+// (2^-23.5).  The first's coefficients take qk_scale and the cap in, which leaves five
+// packed products and multiply-adds for two elements (a packed one takes the FMA
+// pipe two cycles, and nothing hides it: 0.2 us of 185 an operation and chunk batch);
+// the second's seven coefficients are immediates of scalar ones, since packed they
+// would need registers that the 128 scores leave no room for.  A special-function
+// form takes two operations an element beside the softmax's one, and that pipe would
+// be the limit; a warp whose tile has a larger y takes it.
+constexpr float kTanhLow[4] = {0.99999994f, -0.333319813f, 0.132846266f, -0.0482781753f};
+
+__device__ __forceinline__ float score_tile(const PrefillParams& p, uint32_t (&x)[4][32], float slope, int dist0,
+                                            bool both_sides) {
     float left = p.qk_scale;
     if (p.cap_out > 0.f) {
         float mx[4] = {0.f, 0.f, 0.f, 0.f};
@@ -296,22 +302,31 @@ __device__ __forceinline__ float score_tile(const PrefillParams& p, uint32_t (&x
 #pragma unroll
             for (int i = 0; i < 32; i += 2)
                 mx[(i >> 1) & 3] = fmax3(mx[(i >> 1) & 3], fabsf(__uint_as_float(x[q][i])), fabsf(__uint_as_float(x[q][i + 1])));
-        const float amax = fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], 0.f) * left;
-        const float2 c2 = make_float2(left, left), o2 = make_float2(p.cap_out, p.cap_out);
-        if (warp_all(amax <= 1.f)) {
-            const auto k = [](float v) { return make_float2(v, v); };
+        const float amax = fmax3(fmax3(mx[0], mx[1], mx[2]), mx[3], 0.f);
+        if (warp_all(amax <= p.tanh_low_max)) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float2 y = fmul2(get(q, i), c2), u = fmul2(y, y);
-                    float2 t = ffma2(u, k(0.0010455536f), k(-0.00621706992f));
-                    t = ffma2(u, t, k(0.0203055199f));
-                    t = ffma2(u, t, k(-0.0534651764f));
-                    t = ffma2(u, t, k(0.133253977f));
-                    t = ffma2(u, t, k(-0.333328575f));
-                    t = ffma2(u, t, k(0.99999994f));
-                    put(q, i, fmul2(fmul2(y, o2), t));
+                    const float2 v = make_float2(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1]));
+                    const float2 u = fmul2(v, v);
+                    const float2 t = fmul2(v, ffma2(u, ffma2(u, ffma2(u, p.tanh_low[3], p.tanh_low[2]), p.tanh_low[1]), p.tanh_low[0]));
+                    x[q][2 * i] = __float_as_uint(t.x);
+                    x[q][2 * i + 1] = __float_as_uint(t.y);
+                }
+        } else if (warp_all(amax * left <= 1.f)) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const float y = __uint_as_float(x[q][i]) * left, u = y * y;
+                    float t = fmaf(u, 0.0010455536f, -0.00621706992f);
+                    t = fmaf(u, t, 0.0203055199f);
+                    t = fmaf(u, t, -0.0534651764f);
+                    t = fmaf(u, t, 0.133253977f);
+                    t = fmaf(u, t, -0.333328575f);
+                    t = fmaf(u, t, 0.99999994f);
+                    x[q][i] = __float_as_uint(y * p.cap_out * t);
                 }
         } else {
 #pragma unroll
@@ -325,14 +340,32 @@ __device__ __forceinline__ float score_tile(const PrefillParams& p, uint32_t (&x
     if (p.slopes) {
         const float2 l2 = make_float2(left, left);
         const float d0 = static_cast<float>(dist0);
+        if (!both_sides) {
+            // keys behind the row's place are masked: the distance is dist0 - j, and its
+            // constant part joins the scores' multiply-add (it is large only where the
+            // whole tile is far)
+            const float base = -slope * d0;
+            const float2 b2 = make_float2(base, base);
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const float j = static_cast<float>(q * 32 + 2 * i);
-                const float2 v = fmul2(get(q, i), l2);
-                put(q, i, make_float2(fmaf(-slope, fabsf(d0 - j), v.x), fmaf(-slope, fabsf(d0 - (j + 1.f)), v.y)));
-            }
+                for (int i = 0; i < 16; ++i) {
+                    const float j = static_cast<float>(q * 32 + 2 * i);
+                    const float2 v = ffma2(make_float2(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])), l2, b2);
+                    x[q][2 * i] = __float_as_uint(fmaf(slope, j, v.x));
+                    x[q][2 * i + 1] = __float_as_uint(fmaf(slope, j + 1.f, v.y));
+                }
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float j = static_cast<float>(q * 32 + 2 * i);
+                    const float2 v = fmul2(make_float2(__uint_as_float(x[q][2 * i]), __uint_as_float(x[q][2 * i + 1])), l2);
+                    x[q][2 * i] = __float_as_uint(fmaf(-slope, fabsf(d0 - j), v.x));
+                    x[q][2 * i + 1] = __float_as_uint(fmaf(-slope, fabsf(d0 - (j + 1.f)), v.y));
+                }
+        }
         left = 1.f;
     }
     return left;
@@ -391,13 +424,78 @@ __device__ uint4 clear_not_finite(unsigned char* vb, int lane) {
     return make_uint4(mask[0], mask[1], mask[2], mask[3]);
 }
 
+// Scored prefill without a host plan, up to 32 sequences: lane i of the claiming warp
+// holds sequence i, and the units are taken longest causal range first, as a
+// plan would order them (8 x 512 new tokens behind 0 to 3584, capped: 272 us in the
+// order of the grid, 241 so).
+struct Ranks {
+    int n, ctx, units;  // new tokens, tokens before them, units of the lane's sequence
+    int total;          // units of the batch
+    int reach;          // what the last ranked unit reaches to: later ones reach no further
+    int shift;          // log2 of a unit's tokens
+};
+__device__ __forceinline__ Ranks load_ranks(const PrefillParams& p, int r, int lane) {
+    Ranks k{0, 0, 0, 0, 0, 31 - __clz(r)};
+    if (lane < p.S) {
+        const int q0 = load_live(p.query_start + lane), q1 = load_live(p.query_start + lane + 1);
+        const int L = load_live(p.seq_lens + lane);
+        const int64_t n = static_cast<int64_t>(q1) - q0;
+        if (q0 >= 0 && n >= 0 && q1 <= p.T && L >= n && L <= p.MB * kBlockSize) {
+            k.n = static_cast<int>(n);
+            k.ctx = L - k.n;
+            k.units = min((k.n + r - 1) / r, p.num_qtiles);
+        } else if (blockIdx.x == 0) {
+            report(p.err, PKV_DEVERR_SEQ_LEN);
+        }
+    }
+    k.total = __reduce_add_sync(0xffffffffu, k.units);
+    k.reach = __reduce_max_sync(0xffffffffu, k.ctx + k.n);
+    return k;
+}
+// The unit of rank `rank` < total: unit qt of a sequence reaches to key ctx + min(n, (qt
+// + 1) r), and the keys of one sequence differ.  Ranks ascend from call to call.
+// Whole warp.
+__device__ __forceinline__ void ranked_unit(Ranks& k, int rank, int lane, int& s, int& qt) {
+    const int r = 1 << k.shift;
+    const auto above = [&](int T) {  // units that reach past T
+        const int d = T - k.ctx;
+        const int mine = d < 0 ? k.units : (d >= k.n ? 0 : max(k.units - (d >> k.shift), 0));
+        return __reduce_add_sync(0xffffffffu, mine);
+    };
+    // above(lo) > rank >= above(hi), from the last unit's reach down in growing steps
+    int hi = k.reach, step = r, lo = max(hi - step, -1);
+    while (above(lo) <= rank) {  // above(-1) is all units
+        hi = lo;
+        step *= 2;
+        lo = max(hi - step, -1);
+    }
+    while (hi - lo > 1) {
+        const int mid = lo + ((hi - lo) >> 1);
+        if (above(mid) > rank)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    const int at = rank - above(hi);  // among the units that reach to hi, by sequence
+    k.reach = hi;
+    const int d = hi - k.ctx, t = (d - 1) >> k.shift;
+    const bool has = d > 0 && t < k.units && min(k.n, (t + 1) * r) == d;
+    const uint32_t b = __ballot_sync(0xffffffffu, has);
+    const bool pick = has && __popc(b & ((1u << lane) - 1u)) == at;
+    s = __ffs(__ballot_sync(0xffffffffu, pick)) - 1;
+    qt = __shfl_sync(0xffffffffu, t, s);
+}
+
 // Prefill unit number lin: unit work[lin / Hkv] of the host plan (or of the
 // default order: each (sequence, KV head) from its last query tiles down)
 // for KV head lin % Hkv.  False when the unit has no rows or its sequence's
 // bounds are inconsistent (reported when rep).
-__device__ bool prefill_unit(const PrefillParams& p, int64_t lin, int RQ, bool rep, Unit& u, int& s) {
-    int qt;
-    if (p.work) {
+// ranked: s and qt are given.
+__device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int64_t lin, int RQ, bool rep, bool ranked, Unit& u,
+                                             int& s, int& qt) {
+    if (ranked) {
+        u.h = static_cast<int>(lin % p.Hkv);
+    } else if (p.work) {
         const int w = load_live(p.work + lin / p.Hkv);
         u.h = static_cast<int>(lin % p.Hkv);
         if (w < 0 || w >= p.S * p.num_qtiles) {
@@ -610,6 +708,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t pol_q = policy_evict_first();
         int k = 0, qloads = 0;
         bool done = false;
+        const bool ranked = kScored && !p.work && p.S <= 32;
+        Ranks ranks{0, 0, 0, 0, 0, 0};
+        if (ranked) ranks = load_ranks(p, 2 * RQ, lane);
         for (;; ++k) {
             // unit k is claimed once the S MMAs of unit k - 1 are issued (that
             // unit is in its last key tile), so a CTA holds at most one unit
@@ -632,9 +733,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                         unsigned int c = 0;
                         if (lane == 0) c = atomicAdd(sched, 1u);
                         c = __shfl_sync(0xffffffffu, c, 0);
-                        if (c >= total) break;
-                        int seq;
-                        if (prefill_unit(p, c, RQ, lane == 0, u, seq)) {
+                        int seq = 0, qt = 0;
+                        if (ranked) {
+                            if (c / p.Hkv >= ranks.total) break;
+                            ranked_unit(ranks, c / p.Hkv, lane, seq, qt);
+                        } else if (c >= total) {
+                            break;
+                        }
+                        if (prefill_unit(p, c, RQ, lane == 0, ranked, u, seq, qt)) {
                             if constexpr (kScored) scored_unit(p, seq, RQ, lane, u);
                             found = true;
                             break;
@@ -995,15 +1101,20 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int ntx = ((X ? u.kv_end[1] : u.kv_end[0]) + kTileN - 1) / kTileN;
             bool row_valid;
             int pos;  // last key this row attends to
-            int lo = 0;       // scored: the first; none where it is above pos
+            // scored: keys lo to max(place, shared), counted from the unit's first
+            int lo = 0, place = 0, shared = 0;
             float slope = 0.f;
-            bool poisoned = false;  // scored: the row attends to a value that is not finite
+            int64_t out_row = 0;  // scored: the row of out
+            int nvt = 0;       // scored: value tiles of the unit
             if constexpr (kScored) {
-                const int tx = u.t0 + X * RQ;
+                out_row = static_cast<int64_t>(u.q0 + u.t0 + X * RQ + rq) * p.Hq + h * G + g;
+                nvt = (max(u.kv_end[0], u.kv_end[1]) + kTileN - 1) / kTileN;
+                const int tx = u.t0 + X * RQ, tok = min(tx + rq, u.n - 1);
                 row_valid = tx + rq < u.n;
-                row_range(p, u, min(tx + rq, u.n - 1), lo, pos);
+                row_range(p, u, tok, lo, pos);
                 lo -= u.k0;
-                pos -= u.k0;
+                place = u.ctx + tok - u.k0;
+                shared = u.prefix - 1 - u.k0;
                 if (p.slopes) slope = load_live(p.slopes + h * G + g) * kLog2e;
             } else if constexpr (!kPrefix) {
                 const int tx = u.t0 + X * RQ;
@@ -1017,12 +1128,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             // does not wait for it
             const int member_row =
                 kPrefix && row_valid ? load_live(p.group_members + m0 + mrow0 + X * RQ + rq) : -1;
-            // scored: this row's place counted from the first key; a tile may leave it nothing
-            const int place = kScored ? u.ctx + min(u.t0 + X * RQ + rq, u.n - 1) - u.k0 : 0;
+            // scored: a tile may leave the row nothing
             float m_ref = kScored ? kNoScore : -INFINITY, l = 0.f;
-            const auto check_values = [&](int j) {  // the value tile's scan is done once P V of it is
+            // scored: a row that attends to a value that is not finite becomes NaN (the value
+            // tile's scan is done once P V of it is)
+            const auto check_values = [&](int j) {
                 const uint4 m = bad_ring[(gt + j) % kBadSlots];
-                if ((m.x | m.y | m.z | m.w) != 0u) poisoned |= any_token(m, lo - j * kTileN, pos - j * kTileN);
+                if (__builtin_expect((m.x | m.y | m.z | m.w) != 0u, 0))
+                    if (any_token(m, lo - j * kTileN, max(place, shared) - j * kTileN)) l = __int_as_float(0x7fffffff);
             };
             for (int j = 0; j < ntx; ++j) {
                 ok = warp_all(tc::wait_spin(s_full + X, (tp + j) & 1));
@@ -1044,9 +1157,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int key0 = j * kTileN;
                 float ce = c;  // factor that is left on x
                 if constexpr (kScored) {
-                    ce = score_tile(p, x, slope, place - key0);
-                    if (key0 + kTileN - 1 > pos || key0 < lo) {
-                        const int a = lo - key0, b = pos - key0;
+                    ce = score_tile(p, x, slope, place - key0, shared > place);
+                    const int a = lo - key0, b = max(place, shared) - key0;
+                    if (b < kTileN - 1 || a > 0) {
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
 #pragma unroll
@@ -1125,13 +1238,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float inv = p.o_scale / l;
                 if constexpr (kScored) {
                     check_values(ntx - 1);
-                    if (l == 0.f) inv = 0.f;  // a row with nothing to attend to
-                    if (poisoned) inv = __int_as_float(0x7fffffff);
+                    inv = l == 0.f ? 0.f : p.o_scale / l;  // 0: a row with nothing to attend to
                 }
                 if constexpr (!kPrefix) {
                     typename T::storage* orow =
                         reinterpret_cast<typename T::storage*>(p.out) +
-                        (static_cast<int64_t>(u.q0 + u.t0 + X * RQ + rq) * p.Hq + h * G + g) * D;
+                        (kScored ? out_row : (static_cast<int64_t>(u.q0 + u.t0 + X * RQ + rq) * p.Hq + h * G + g)) * D;
 #pragma unroll
                     for (int q = 0; q < D / 32; ++q) {
                         uint32_t o[32];
@@ -1190,7 +1302,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tp += ntx;
-            gt += (max(u.kv_end[0], u.kv_end[1]) + kTileN - 1) / kTileN;
+            gt += nvt;
             if (!ok || *abort_flag) break;
         }
     }
@@ -1548,6 +1660,16 @@ pkv_status prefill_common(const void* q, int32_t q_dtype, int32_t num_tokens, in
         if (mod->cap > 0.f) {
             p.qk_scale = scale * (fp8 ? desc->k_scale : 1.f) / mod->cap;
             p.cap_out = mod->cap * kLog2e;
+            // x tanh_low(x^2) = cap_out y kTanhLow(y^2), y = qk_scale x; not where a coefficient
+            // leaves binary32's normal range (a cap of 10^5 times the scores)
+            double k = static_cast<double>(p.cap_out) * p.qk_scale;
+            bool normal = true;
+            for (int i = 0; i < 4; ++i) {
+                p.tanh_low[i].x = p.tanh_low[i].y = static_cast<float>(k * kTanhLow[i]);
+                normal &= k > 1e-30 && k < 1e30;
+                k *= static_cast<double>(p.qk_scale) * p.qk_scale;
+            }
+            p.tanh_low_max = normal ? 0.375f / p.qk_scale : -1.f;
         }
         p.window = mod->window;
         p.slopes = mod->slopes;

@@ -209,3 +209,30 @@ def test_captured_and_replayed_after_its_masks_changed(pk):
         torch.cuda.synchronize()
         c.check(out)
     assert pk.get_device_error() == 0
+
+
+@pytest.mark.parametrize("S", [1, 31, 32, 33, 70])
+def test_many_sequences_in_the_order_of_their_reach(pk, S):
+    """Without a plan, batches of up to 32 sequences are taken by their reach, larger ones in the order of the grid."""
+    rng = np.random.default_rng(S)
+    chunks = [(int(rng.integers(0, 200)), int(rng.choice([0, 1, 40, 64, 65, 130]))) for _ in range(S)]
+    chunks[0] = (77, 133)
+    c = Case(pk, "bf16", 64, 1, 4, "bf16", dict(window=90, cap=30.0), chunks=chunks, seed=S)
+    c.check(c.run())
+    c.check(c.run(plan=True))
+    assert pk.get_device_error() == 0
+
+
+def test_inconsistent_sequences_are_reported_and_skipped(pk):
+    c = Case(pk, "bf16", 128, 1, 4, "bf16", {}, chunks=[(10, 40), (0, 70), (5, 30)])
+    q, out = c.q.cuda(), torch.full_like(c.q, 7.0, device="cuda")
+    lens = i32([50, 69, 35])  # the second holds fewer tokens than its chunk
+    pk.paged_attention_prefill_scored(q, c.kd, c.vd, c.pools.desc, i32(c.start), 70, i32(c.tables), lens, c.scale, out)
+    assert pk.get_device_error() == pk.DEVERR_SEQ_LEN
+    assert bool((out[40:110] == 7).all())
+    c.check(out, np.r_[0:40, 110:140])
+    # chunks past max_query_len lose rows, and say so; the first rows are there
+    out.fill_(7.0)
+    pk.paged_attention_prefill_scored(q, c.kd, c.vd, c.pools.desc, i32(c.start), 40, i32(c.tables), i32(c.lens), c.scale, out)
+    assert pk.get_device_error() == pk.DEVERR_SEQ_LEN
+    c.check(out, np.r_[0:40, 110:140])
