@@ -612,7 +612,7 @@ size_t pkv_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, 
  * partition_tokens divides what a row may span: max_seq_len tokens, or with a
  * window those of the blocks it touches.  A length above max_seq_len rounded up to whole
  * blocks sets PKV_DEVERR_SEQ_LEN, and that row may lose tokens.
- * weights: device float [num_blocks][num_kv_heads][block_size], or NULL.  Cached
+ * weights: device float [num_blocks][num_kv_heads][block_size] (16-byte aligned), or NULL.  Cached
  *   token t of sequence s receives, for each KV head, its share of the softmax
  *   summed over that head's query heads (num_q_heads / num_kv_heads in all for a
  *   row), the measure that pkv_select_tokens evicts by.
@@ -650,7 +650,7 @@ pkv_status pkv_paged_attention_decode_scored(const void* q, int32_t q_dtype, int
  *   the largest weights (equal ones, -0 and 0 among them: the lowest positions first;
  *   NaN below every number); every token where there are at most num_kept; the
  *   rest -1.  sink_tokens + recent_tokens <= num_kept, num_kept > 0.
- * weights: device float [num_blocks][num_kv_heads][block_size].
+ * weights: device float [num_blocks][num_kv_heads][block_size], 16-byte aligned.
  * max_seq_len (host, up to 2^30) must be >= every length; a length below 0, above it (rounded
  *   up to whole blocks) or above the block table sets PKV_DEVERR_SEQ_LEN and is clamped.  A
  *   block id outside the pool sets PKV_DEVERR_BLOCK_ID; its tokens count lowest.

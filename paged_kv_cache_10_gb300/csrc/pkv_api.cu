@@ -351,7 +351,7 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
     if (sc) {
         const pkv_status bad = check_score_mod(&sc->mod, scale, d);
         if (bad != PKV_OK) return bad;
-        if (sc->mod.prefix_lens || (sc->new_lens && !sc->weights) || (reinterpret_cast<uintptr_t>(sc->weights) & 3u) ||
+        if (sc->mod.prefix_lens || (sc->new_lens && !sc->weights) || !aligned16(sc->weights) ||
             (reinterpret_cast<uintptr_t>(sc->new_lens) & 3u))
             return PKV_ERR_INVALID;
     }
@@ -425,7 +425,7 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
         // a launch without any token still marks itself as scored
         p.span = static_cast<int32_t>(std::max<int64_t>(reach, kBlockSize));
         if (sc->weights && reach > 0) {
-            p.cascade = 1;  // every row's partials are kept, and the merge writes its output
+            p.cascade = 1;  // every row's partials are kept, and the last kernel writes its output
             p.scores = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
                                                 ceil_div(partials_bytes(num_seqs, num_q_heads, d->head_size, NP), 256) * 256);
         }
@@ -472,12 +472,11 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
         e = launch_decode_fp8_f16q(p, G, st);
     }
     if (e != cudaSuccess) return PKV_ERR_CUDA;
-    if (NP > 1 || p.cascade) {
-        e = launch_merge(p, q_dtype, st);
-        if (e != cudaSuccess) return PKV_ERR_CUDA;
-    }
     if (p.scores) {
-        e = launch_weights(p, sc->new_lens, max_seq_len, sc->weights, st);
+        e = launch_weights(p, sc->new_lens, max_seq_len, q_dtype, sc->weights, st);
+        if (e != cudaSuccess) return PKV_ERR_CUDA;
+    } else if (NP > 1) {
+        e = launch_merge(p, q_dtype, st);
         if (e != cudaSuccess) return PKV_ERR_CUDA;
     }
     return PKV_OK;

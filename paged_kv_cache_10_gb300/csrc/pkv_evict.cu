@@ -42,19 +42,17 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__device__ __forceinline__ uint32_t load_key(const SelectTokens& p, const int32_t* table, int h, int t, bool rep) {
+// Key of position t of a row that does not fit shared memory.
+__device__ __forceinline__ uint32_t load_key(const SelectTokens& p, const int32_t* table, int h, int t) {
     const int blk = load_live(table + t / kBlockSize);
-    if (blk < 0 || blk >= p.NB) {
-        if (rep) report(p.err, PKV_DEVERR_BLOCK_ID);
-        return 0u;
-    }
+    if (blk < 0 || blk >= p.NB) return 0u;
     return weight_key(load_live(p.weights + (static_cast<int64_t>(blk) * p.Hkv + h) * kBlockSize + t % kBlockSize));
 }
 
 // CTA (KV head x, sequence y).
 __global__ void __launch_bounds__(kSelThreads) select_tokens_kernel(const SelectTokens p) {
     extern __shared__ uint32_t keys[];  // [p.cached]
-    __shared__ uint32_t hist[kBins];
+    __shared__ uint32_t hists[3][kBins];  // one a pass, all cleared before the first
     __shared__ uint32_t wsum[kSelWarps], wtie[kSelWarps];
     __shared__ uint32_t found_digit, found_left, found_count;
     wait_primary_grid();
@@ -79,11 +77,31 @@ __global__ void __launch_bounds__(kSelThreads) select_tokens_kernel(const Select
     if (k == 0) return;
     const int32_t* table = p.block_tables + static_cast<int64_t>(s) * p.MB;
     const bool cached = M <= p.cached;
-    for (int i = tid; i < M; i += kSelThreads) {
-        const uint32_t key = load_key(p, table, h, p.sink + i, true);
-        if (cached) keys[i] = key;
+    for (int i = tid; i < 3 * kBins; i += kSelThreads) hists[0][i] = 0u;
+    __syncthreads();
+    // the keys, four of a block a lane, and with them the first digits' counts
+    const int from4 = p.sink & ~3, to = p.sink + M;
+#pragma unroll 2
+    for (int t = from4 + 4 * tid; t < to; t += 4 * kSelThreads) {
+        const int blk = load_live(table + t / kBlockSize);
+        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+        const bool ok = blk >= 0 && blk < p.NB;
+        if (ok)
+            w = load_live(reinterpret_cast<const float4*>(p.weights + (static_cast<int64_t>(blk) * p.Hkv + h) * kBlockSize +
+                                                          t % kBlockSize));
+        else
+            report(p.err, PKV_DEVERR_BLOCK_ID);
+        const float v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = t + e - p.sink;
+            if (i < 0 || i >= M) continue;
+            const uint32_t key = ok ? weight_key(v[e]) : 0u;
+            if (cached) keys[i] = key;
+            atomicAdd(&hists[0][key >> 21], 1u);
+        }
     }
-    const auto key_of = [&](int i) { return cached ? keys[i] : load_key(p, table, h, p.sink + i, false); };
+    const auto key_of = [&](int i) { return cached ? keys[i] : load_key(p, table, h, p.sink + i); };
 
     // keys at or above `from` are kept, and `ties` of those equal to `tie`
     uint32_t prefix = 0u, left = k;
@@ -94,11 +112,12 @@ __global__ void __launch_bounds__(kSelThreads) select_tokens_kernel(const Select
         const int bits = pass < 2 ? 11 : 10;
         const int high = shift;  // bits [high, 32) are known
         shift -= bits;
-        for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0u;
-        __syncthreads();
-        for (int i = tid; i < M; i += kSelThreads) {
-            const uint32_t key = key_of(i);
-            if (high == 32 || (key >> high) == (prefix >> high)) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+        uint32_t* hist = hists[pass];
+        if (pass > 0) {
+            for (int i = tid; i < M; i += kSelThreads) {
+                const uint32_t key = key_of(i);
+                if ((key >> high) == (prefix >> high)) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1u)], 1u);
+            }
         }
         __syncthreads();
         // bins from the top: thread i has the pair 2i, 2i + 1 counted from there
@@ -160,8 +179,6 @@ __global__ void __launch_bounds__(kSelThreads) select_tokens_kernel(const Select
     }
 }
 
-constexpr int kMoveThreads = 256;
-
 struct Compact {
     const int32_t* kept;
     unsigned char *k_cache, *v_cache;
@@ -171,51 +188,90 @@ struct Compact {
     unsigned int* err;
 };
 
-// Moves one head's rows of one pool: `units` pieces of type T a row, from piece u0
-// on; off(t, u) is piece u of token t in a tile of tile_bytes.
-template <typename T, int PER, typename Off>
-__device__ __forceinline__ void move_rows(const Compact& p, unsigned char* pool, int64_t tile_bytes, int units, int u0,
-                                          int h, int s, int count, int L, bool rep, Off off) {
+// One entry of a list: the bytes from the pool's start to where its row comes from
+// and goes to; src < 0: it stays.
+struct __align__(16) Move {
+    int64_t src, dst;
+};
+
+// Moves one head's rows of one pool: 2^lg pieces of type T a row, row(t) + col(u) the
+// place of piece u of token t in a tile of tile_bytes, u from u0 on.  The entries of a
+// window (one a thread of the CTA) are translated through the tables once, the next window's loads under
+// way meanwhile; within it a thread holds PER pieces, and as many of the chunk
+// behind them, in registers.  A thread's pieces are all of one column.
+template <int THREADS, typename T, int PER, typename Row, typename Col>
+__device__ __forceinline__ void move_rows(const Compact& p, Move* win, unsigned char* pool, int64_t tile_bytes, int lg,
+                                          int u0, int h, int s, int count, int L, bool rep, Row row, Col col) {
     const int32_t* kept = p.kept + (static_cast<int64_t>(s) * p.Hkv + h) * p.n;
     const int32_t* src_table = p.src_tables + static_cast<int64_t>(s) * p.src_mb;
     const int32_t* dst_table = p.dst_tables + static_cast<int64_t>(s) * p.dst_mb;
-    const int rows = kMoveThreads * PER / units;  // units divides 256
-    for (int base = 0; base < count; base += rows) {
-        T x[PER];
-        unsigned char* to[PER];
-#pragma unroll
-        for (int e = 0; e < PER; ++e) {
-            const int at = e * kMoveThreads + threadIdx.x;
-            const int i = base + at / units, u = u0 + at % units;
-            to[e] = nullptr;
-            if (i >= count) continue;
-            const int t = load_live(kept + i);
-            if (t < 0) continue;
-            if (t >= L) {
-                if (rep) report(p.err, PKV_DEVERR_SEQ_LEN);
-                continue;
-            }
-            const int a = load_live(src_table + t / kBlockSize), b = load_live(dst_table + i / kBlockSize);
-            if (a < 0 || a >= p.NB || b < 0 || b >= p.NB) {
-                if (rep) report(p.err, PKV_DEVERR_BLOCK_ID);
-                continue;
-            }
-            if (a == b && t % kBlockSize == i % kBlockSize) continue;  // already there
-            x[e] = load_live(reinterpret_cast<const T*>(pool + (static_cast<int64_t>(a) * p.Hkv + h) * tile_bytes +
-                                                        off(t % kBlockSize, u)));
-            to[e] = pool + (static_cast<int64_t>(b) * p.Hkv + h) * tile_bytes + off(i % kBlockSize, u);
+    const auto translate = [&](int i) {
+        Move m{-1, 0};
+        if (i >= count) return m;
+        const int b = load_live(dst_table + i / kBlockSize);
+        const int t = load_live(kept + i);
+        if (t < 0) return m;
+        if (t >= L) {
+            if (rep) report(p.err, PKV_DEVERR_SEQ_LEN);
+            return m;
         }
-        __syncthreads();  // a chunk's loads before its stores; later chunks read above what it writes
+        const int a = load_live(src_table + t / kBlockSize);
+        if (a < 0 || a >= p.NB || b < 0 || b >= p.NB) {
+            if (rep) report(p.err, PKV_DEVERR_BLOCK_ID);
+            return m;
+        }
+        if (a == b && t % kBlockSize == i % kBlockSize) return m;  // already there
+        m.src = (static_cast<int64_t>(a) * p.Hkv + h) * tile_bytes + row(t % kBlockSize);
+        m.dst = (static_cast<int64_t>(b) * p.Hkv + h) * tile_bytes + row(i % kBlockSize);
+        return m;
+    };
+    unsigned char* column = pool + col(u0 + (threadIdx.x & ((1 << lg) - 1)));
+    const int first = threadIdx.x >> lg, step = THREADS >> lg;  // this thread's rows of a window
+    Move next = translate(threadIdx.x);
+    for (int w0 = 0; w0 < count; w0 += THREADS) {
+        __syncthreads();  // the window before is through
+        win[threadIdx.x] = next;
+        __syncthreads();
+        next = translate(w0 + THREADS + threadIdx.x);
+        const int rows = min(THREADS, count - w0);
+        const auto load = [&](int at, T (&x)[PER]) {
 #pragma unroll
-        for (int e = 0; e < PER; ++e)
-            if (to[e]) *reinterpret_cast<T*>(to[e]) = x[e];
+            for (int e = 0; e < PER; ++e) {
+                const int i = at + e * step + first;
+                const int64_t src = i < rows ? win[i].src : -1;
+                if (src >= 0) x[e] = load_live(reinterpret_cast<const T*>(column + src));
+            }
+        };
+        const auto store = [&](int at, const T (&x)[PER]) {
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int i = at + e * step + first;
+                if (i < rows) {
+                    const Move m = win[i];
+                    if (m.src >= 0) *reinterpret_cast<T*>(column + m.dst) = x[e];
+                }
+            }
+        };
+        // a chunk's loads before its stores; the loads of chunks behind it read above what it writes
+        const int chunk = PER * step;
+        T x[PER], y[PER];
+        load(0, x);
+        for (int at = 0; at < rows; at += 2 * chunk) {
+            if (at + chunk < rows) load(at + chunk, y);
+            __syncthreads();
+            store(at, x);
+            if (at + chunk >= rows) break;
+            if (at + 2 * chunk < rows) load(at + 2 * chunk, x);
+            __syncthreads();
+            store(at + chunk, y);
+        }
     }
 }
 
 // CTA (column slice x, plane and KV head y, sequence z).  Planes: keys, values, then for
 // integer-coded pools their rows' parameters, and the weights last.
-template <int D, int KV>
-__global__ void __launch_bounds__(kMoveThreads) compact_kernel(const Compact p) {
+template <int THREADS, int D, int KV>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kernel(const Compact p) {
     constexpr bool kInt = KV == PKV_INT8 || KV == PKV_INT4;
     wait_primary_grid();
     const int plane = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv, s = blockIdx.z;
@@ -230,33 +286,40 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const Compact p) 
         if (threadIdx.x == 0 && first && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
         count = p.dst_mb * kBlockSize;
     }
+    __shared__ Move win[THREADS];
+    const int cut = __ffs(p.slices) - 1;  // log2 of the column slices
+    const auto none = [](int) { return 0; };
+    const auto one = [&](unsigned char* pool, int64_t tile_bytes, auto type, auto row) {
+        using T = decltype(type);
+        if (blockIdx.x == 0) move_rows<THREADS, T, 1>(p, win, pool, tile_bytes, 0, 0, h, s, count, L, false, row, none);
+    };
+    const auto weights = [&] {
+        one(reinterpret_cast<unsigned char*>(p.weights), kBlockSize * 4, float{}, [](int t) { return t * 4; });
+    };
     if constexpr (!kInt) {
         if (plane == 2) {
-            if (blockIdx.x == 0)
-                move_rows<float, 4>(p, reinterpret_cast<unsigned char*>(p.weights), kBlockSize * 4, 1, 0, h, s, count, L,
-                                    false, [](int t, int) { return t * 4; });
+            weights();
             return;
         }
-        constexpr int ROW = D * (KV == PKV_FP8_E4M3 ? 1 : 2);
-        const int units = ROW / 16 / p.slices;
-        move_rows<uint4, 4>(p, plane ? p.v_cache : p.k_cache, kBlockSize * ROW, units, blockIdx.x * units, h, s, count, L,
-                            first, [](int t, int u) { return t * ROW + u * 16; });
+        constexpr int ROW = D * (KV == PKV_FP8_E4M3 ? 1 : 2), LG = ROW == 256 ? 4 : (ROW == 128 ? 3 : 2);
+        move_rows<THREADS, uint4, 4>(p, win, plane ? p.v_cache : p.k_cache, kBlockSize * ROW, LG - cut, blockIdx.x << (LG - cut), h, s,
+                            count, L, first, [](int t) { return t * ROW; }, [](int u) { return u * 16; });
     } else {
         using L_ = IntTile<D, KV == PKV_INT8 ? 8 : 4>;
-        if (blockIdx.x != 0 && plane != 1) return;  // the value codes alone are split
-        if (plane == 0)
-            move_rows<uint4, 4>(p, p.k_cache, L_::kBytes, L_::RB / 16, 0, h, s, count, L, first,
-                                [](int t, int u) { return L_::key(t, u * 16); });
-        else if (plane == 1) {
-            const int units = L_::RB / 2 / p.slices;
-            move_rows<uint16_t, 8>(p, p.v_cache, L_::kBytes, units, blockIdx.x * units, h, s, count, L, false,
-                                   [](int t, int u) { return L_::val(t, u * 2); });
-        } else if (plane == 4)
-            move_rows<float, 4>(p, reinterpret_cast<unsigned char*>(p.weights), kBlockSize * 4, 1, 0, h, s, count, L, false,
-                                [](int t, int) { return t * 4; });
-        else
-            move_rows<uint2, 4>(p, plane == 3 ? p.v_cache : p.k_cache, L_::kBytes, 1, 0, h, s, count, L, false,
-                                [](int t, int) { return L_::param(t); });
+        constexpr int LG = L_::RB == 128 ? 3 : (L_::RB == 64 ? 2 : 1);  // 16-byte pieces of a key row
+        // both places are a token's plus a byte's
+        if (plane == 0) {
+            if (blockIdx.x == 0)
+                move_rows<THREADS, uint4, 4>(p, win, p.k_cache, L_::kBytes, LG, 0, h, s, count, L, first,
+                                    [](int t) { return L_::key(t, 0); }, [](int u) { return L_::key(0, u * 16); });
+        } else if (plane == 1) {  // two bytes lie together in a value tile: the codes that are split
+            move_rows<THREADS, uint16_t, 8>(p, win, p.v_cache, L_::kBytes, LG + 3 - cut, blockIdx.x << (LG + 3 - cut), h, s, count, L,
+                                   false, [](int t) { return L_::val(t, 0); }, [](int u) { return L_::val(0, u * 2); });
+        } else if (plane == 4) {
+            weights();
+        } else {
+            one(plane == 3 ? p.v_cache : p.k_cache, L_::kBytes, uint2{}, [](int t) { return L_::param(t); });
+        }
     }
 }
 
@@ -271,13 +334,13 @@ pkv_status check_desc(const pkv_cache_desc* d) {
     return PKV_OK;
 }
 
-template <int D>
+template <int THREADS, int D>
 void (*compact_of(int kv))(Compact) {
     switch (kv) {
-    case PKV_INT8: return compact_kernel<D, PKV_INT8>;
-    case PKV_INT4: return compact_kernel<D, PKV_INT4>;
-    case PKV_FP8_E4M3: return compact_kernel<D, PKV_FP8_E4M3>;
-    default: return compact_kernel<D, PKV_BF16>;  // 16-bit rows alike
+    case PKV_INT8: return compact_kernel<THREADS, D, PKV_INT8>;
+    case PKV_INT4: return compact_kernel<THREADS, D, PKV_INT4>;
+    case PKV_FP8_E4M3: return compact_kernel<THREADS, D, PKV_FP8_E4M3>;
+    default: return compact_kernel<THREADS, D, PKV_BF16>;  // 16-bit rows alike
     }
 }
 
@@ -299,7 +362,7 @@ extern "C" pkv_status pkv_select_tokens(const float* weights, const pkv_cache_de
         return max_blocks_per_seq > 0x7fffffff / kBlockSize ? PKV_ERR_UNSUPPORTED : PKV_ERR_INVALID;
     if (num_seqs > 65535 || max_seq_len > 0x40000000) return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PKV_OK;
-    if (!weights || !block_tables || !seq_lens || !kept || !aligned4(weights) || !aligned4(block_tables) ||
+    if (!weights || !block_tables || !seq_lens || !kept || !aligned16(weights) || !aligned4(block_tables) ||
         !aligned4(seq_lens) || !aligned4(kept))
         return PKV_ERR_INVALID;
     SelectTokens p{};
@@ -362,11 +425,17 @@ extern "C" pkv_status pkv_paged_kv_compact(const int32_t* kept, int32_t num_kept
     p.NB = d->num_blocks;
     p.src_mb = max_blocks_per_seq;
     p.dst_mb = dst_blocks_per_seq;
-    // rows of few sequences and heads are split over four CTAs each
-    p.slices = static_cast<int64_t>(num_seqs) * p.Hkv * 2 <= num_sms() ? 4 : 1;
+    // Columns split over up to four CTAs until there are six an SM.  Where that is not
+    // reached by far, what one CTA has under way limits the rate, and CTAs of four times the
+    // threads take over (2048 of 8190 tokens, 8 heads: 6.6 us against 11.0; with twice the
+    // threads 7.9, where 32 sequences of 1000 tokens take 51.8 against 50.3).
+    const int64_t rows = static_cast<int64_t>(num_seqs) * p.Hkv * 2;
+    p.slices = rows >= 6 * num_sms() ? 1 : (2 * rows >= 6 * num_sms() ? 2 : 4);
+    const bool few = rows < num_sms();
     const int planes = (is_int_pool(d->kv_dtype) ? 4 : 2) + (weights ? 1 : 0);
-    auto kern = d->head_size == 128 ? compact_of<128>(d->kv_dtype) : compact_of<64>(d->kv_dtype);
-    const cudaError_t e = launch_maybe_pdl(true, kern, dim3(p.slices, planes * p.Hkv, num_seqs), dim3(kMoveThreads), 0,
+    auto kern = d->head_size == 128 ? (few ? compact_of<1024, 128>(d->kv_dtype) : compact_of<256, 128>(d->kv_dtype))
+                                    : (few ? compact_of<1024, 64>(d->kv_dtype) : compact_of<256, 64>(d->kv_dtype));
+    const cudaError_t e = launch_maybe_pdl(true, kern, dim3(p.slices, planes * p.Hkv, num_seqs), dim3(few ? 1024 : 256), 0,
                                            static_cast<cudaStream_t>(stream), p);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

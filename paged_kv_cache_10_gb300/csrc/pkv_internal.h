@@ -193,8 +193,8 @@ cudaError_t launch_decode_scored_fp8(const DecodeParams& p, int G, int q_dtype, 
 cudaError_t launch_decode_scored_int8(const DecodeParams& p, int G, int q_dtype, cudaStream_t st);
 cudaError_t launch_decode_scored_int4(const DecodeParams& p, int G, int q_dtype, cudaStream_t st);
 // Each cached token's share of the softmax into weights [NB][Hkv][16], from the
-// launch's scores and partials (pkv_weights.cu).
-cudaError_t launch_weights(const DecodeParams& p, const int32_t* new_lens, int max_seq_len, float* weights,
+// launch's scores and partials, and the merge of those into out (pkv_weights.cu).
+cudaError_t launch_weights(const DecodeParams& p, const int32_t* new_lens, int max_seq_len, int q_dtype, float* weights,
                            cudaStream_t st);
 // Copies the blocks a batch reaches out of an integer-coded pool into 16-bit
 // blocks of q's type (prefill): copy block s * MB + j holds sequence s's
