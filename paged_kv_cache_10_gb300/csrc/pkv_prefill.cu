@@ -69,8 +69,8 @@ constexpr int kUnitReaders = 11;
 constexpr int kBadSlots = 8;
 
 // q_full, q_empty, k_full[3], k_empty[3], v_full[2], v_empty[2], v_zero[2], s_full[2 tiles],
-// p_full[2 tiles], o_done[2 tiles], drain, u_full[4], u_empty[4]
-constexpr int kNumBars = 2 + 2 * kKStages + 3 * kVStages + 2 + 2 + 2 + 1 + 2 * kUnitSlots;
+// p_full[2 tiles], o_done[2 tiles], drain, u_full[4], u_empty[4], u_near
+constexpr int kNumBars = 2 + 2 * kKStages + 3 * kVStages + 2 + 2 + 2 + 1 + 2 * kUnitSlots + 1;
 
 // Shared-memory layout for head_size D (64 or 128): operands are 128 rows x
 // D 16-bit elements in D / 64 column blocks of 128-byte rows.
@@ -85,8 +85,8 @@ struct Tile {
     static constexpr int kOffBar = kOffV + kVStages * kOp;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;
     static constexpr int kUnitBytes = 64;  // one published unit (sizeof(Unit) rounded up)
-    static constexpr int kOffBad = kOffMisc + 8 + kUnitSlots * kUnitBytes;  // scored: tokens with values to poison
-    static_assert(kOffBad % 16 == 0, "token masks are read as vectors");
+    // scored: tokens with values to poison, read as vectors
+    static constexpr int kOffBad = (kOffMisc + 8 + kUnitSlots * kUnitBytes + 15) / 16 * 16;
     static constexpr int kSmemBytes = kOffBad + kBadSlots * 16 + 1024;  // tmem slot, abort flag, unit ring, token
                                                                          // masks; alignment slack
     static_assert(kSmemBytes <= 227 * 1024, "shared memory");
@@ -371,15 +371,19 @@ __device__ __forceinline__ float score_tile(const PrefillParams& p, uint32_t (&x
     return left;
 }
 
+// Bits lo to hi of 32; none where hi < lo.
+__device__ __forceinline__ uint32_t key_bits(int lo, int hi) {
+    lo = max(lo, 0);
+    hi = min(hi, 31);
+    return lo > hi ? 0u : (0xffffffffu << lo) & (0xffffffffu >> (31 - hi));
+}
+
 // Whether a token of the mask lies in keys [lo, hi] counted from the tile's first.
 __device__ __forceinline__ bool any_token(uint4 m, int lo, int hi) {
     const uint32_t w[4] = {m.x, m.y, m.z, m.w};
     bool any = false;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int a = max(lo - 32 * q, 0), b = min(hi - 32 * q, 31);
-        if (a <= b) any |= (w[q] & (0xffffffffu << a) & (0xffffffffu >> (31 - b))) != 0u;
-    }
+    for (int q = 0; q < 4; ++q) any |= (w[q] & key_bits(lo - 32 * q, hi - 32 * q)) != 0u;
     return any;
 }
 
@@ -396,19 +400,30 @@ __device__ uint4 clear_not_finite(unsigned char* vb, int lane) {
         const int idx = step * 32 + lane, r = idx / kRowChunks, c = idx % kRowChunks;
         return reinterpret_cast<uint4*>(vb + (c >> 3) * kColBlock + swz128(r, c & 7));
     };
-    const auto top = [](uint4 v) {  // largest magnitude bits of the eight elements, two lanes
-        const uint32_t m = 0x7fff7fffu;
-        return __vmaxu2(__vmaxu2(v.x & m, v.y & m), __vmaxu2(v.z & m, v.w & m));
+    // 0 x is NaN where x is not finite, and stays so in a sum
+    using P2 = typename std::conditional<std::is_same<T, BF16>::value, __nv_bfloat162, __half2>::type;
+    constexpr uint32_t kZeroPair = 0u;
+    const P2 zero = *reinterpret_cast<const P2*>(&kZeroPair);
+    const auto pair = [](const uint32_t& w) { return *reinterpret_cast<const P2*>(&w); };
+    const auto is_nan = [](P2 a) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&a) & 0x7fff7fffu;
+        return (w & 0xffffu) > kInf || (w >> 16) > kInf;
     };
-    uint32_t acc[2] = {0u, 0u};
+    P2 acc[4] = {zero, zero, zero, zero};
 #pragma unroll 8
-    for (int step = 0; step < kTileN / kPerStep; ++step) acc[step & 1] = __vmaxu2(acc[step & 1], top(*chunk(step)));
-    const uint32_t a = __vmaxu2(acc[0], acc[1]);
+    for (int step = 0; step < kTileN / kPerStep; ++step) {
+        const uint4 v = *chunk(step);
+        acc[0] = __hfma2(pair(v.x), zero, acc[0]);
+        acc[1] = __hfma2(pair(v.y), zero, acc[1]);
+        acc[2] = __hfma2(pair(v.z), zero, acc[2]);
+        acc[3] = __hfma2(pair(v.w), zero, acc[3]);
+    }
     uint32_t mask[4] = {0u, 0u, 0u, 0u};
-    if (__any_sync(0xffffffffu, (a & 0xffffu) >= kInf || (a >> 16) >= kInf)) {
+    if (__any_sync(0xffffffffu, is_nan(__hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]))))) {
         for (int step = 0; step < kTileN / kPerStep; ++step) {
-            const uint32_t t = top(*chunk(step));
-            const bool bad = (t & 0xffffu) >= kInf || (t >> 16) >= kInf;
+            const uint4 v = *chunk(step);
+            const P2 t = __hfma2(pair(v.x), zero, __hfma2(pair(v.y), zero, __hfma2(pair(v.z), zero, __hmul2(pair(v.w), zero))));
+            const bool bad = is_nan(t);
             if (bad) *chunk(step) = make_uint4(0u, 0u, 0u, 0u);
             const uint32_t b = __ballot_sync(0xffffffffu, bad);
 #pragma unroll
@@ -586,6 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* drain = o_done + 2;
     uint64_t* u_full = drain + 1;            // [kUnitSlots]
     uint64_t* u_empty = u_full + kUnitSlots; // [kUnitSlots]
+    uint64_t* u_near = u_empty + kUnitSlots; // scored: the unit's end is near
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sm + kOffMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + kOffMisc + 4);
     Unit* unit_ring = reinterpret_cast<Unit*>(sm + kOffMisc + 8);  // [kUnitSlots]
@@ -677,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(u_full + i, 1);
             mbar_init(u_empty + i, kUnitReaders);
         }
+        mbar_init(u_near, 1);
         *abort_flag = 0;
         mbar_init_fence();
     }
@@ -715,7 +732,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             // unit k is claimed once the S MMAs of unit k - 1 are issued (that
             // unit is in its last key tile), so a CTA holds at most one unit
             // ahead and the list stays longest first across the SMs
-            if (!kPrefix && k > 0 && !done && !__all_sync(0xffffffffu, mbar_wait(q_empty, (k - 1) & 1))) {
+            // (scored: a tile sooner, since behind a window or of a short document a unit is
+            // no longer than a claim and its loads)
+            if (!kPrefix && k > 0 && !done &&
+                !__all_sync(0xffffffffu, mbar_wait(kScored ? u_near : q_empty, (k - 1) & 1))) {
                 if (lane == 0) {
                     report(p.err, PKV_DEVERR_TIMEOUT);
                     *abort_flag = 1;
@@ -766,6 +786,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             __syncwarp();
             if (u.h < 0) break;
+            if constexpr (kScored) {
+                // the Q buffers are free once the S MMAs of unit k - 1 are complete
+                if (k > 0 && !__all_sync(0xffffffffu, mbar_wait(q_empty, (k - 1) & 1))) {
+                    if (lane == 0) {
+                        report(p.err, PKV_DEVERR_TIMEOUT);
+                        *abort_flag = 1;
+                    }
+                    break;
+                }
+            }
             const int ntiles = u.kv_end[1] > 0 ? 2 : 1;
             if constexpr (!kPrefix) {
                 if (lane == 0) {
@@ -1020,6 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         break;
                     }
                     const int g = gt + j;
+                    if (kScored && j == max(nkt - 2, 0)) tc::arrive(u_near);
                     // values of tile j; in the unit's last tile, with the rows
                     // past its keys cleared.  v_zero of a stage completes once
                     // per value tile, and the producer cannot be a stage round
@@ -1160,11 +1191,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ce = score_tile(p, x, slope, place - key0, shared > place);
                     const int a = lo - key0, b = max(place, shared) - key0;
                     if (b < kTileN - 1 || a > 0) {
+                        // as bits of 32 keys each, which become predicates several at a time
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t seen = key_bits(a - 32 * q, b - 32 * q);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (q * 32 + i > b || q * 32 + i < a) x[q][i] = __float_as_uint(-INFINITY);
+                                if (!(seen & (1u << i))) x[q][i] = __float_as_uint(-INFINITY);
+                        }
                     }
                 } else if (key0 + kTileN - 1 > pos) {
 #pragma unroll

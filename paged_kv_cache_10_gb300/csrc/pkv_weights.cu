@@ -22,6 +22,7 @@ namespace pkv {
 namespace {
 
 constexpr int kWeightThreads = 256, kWeightWarps = kWeightThreads / 32;
+static_assert(kWeightWarps >= 8, "a warp for each head of a group");
 constexpr int kWeightTokens = 4 * kWeightThreads;  // tokens of a CTA
 constexpr int kMergeAlone = 8;                     // partitions of a launch up to which a warp merges a row alone
 
