@@ -1394,11 +1394,13 @@ cudaError_t launch_tile(const PrefillParams& p, dim3 grid, const CUtensorMap& tq
 
 // Persistent prefill: one CTA per SM (one CTA fits an SM), or one per unit
 // when there are fewer; the launch takes the next counter slot.
+// One sequence of slots for calls of every type: they share the counters.
+std::atomic<uint32_t> g_next_sched_slot{0};
+
 template <typename T>
 cudaError_t launch_prefill(PrefillParams p, int D, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, bool scored, cudaStream_t st) {
-    static std::atomic<uint32_t> next_slot{0};
-    p.sched_slot = static_cast<int32_t>(next_slot.fetch_add(1u, std::memory_order_relaxed) % kSchedSlots);
+    p.sched_slot = static_cast<int32_t>(g_next_sched_slot.fetch_add(1u, std::memory_order_relaxed) % kSchedSlots);
     const int64_t units = p.work ? p.num_work : static_cast<int64_t>(p.num_qtiles) * p.S;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units * p.Hkv, num_sms())));
     if (scored)
