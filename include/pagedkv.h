@@ -610,8 +610,8 @@ size_t pkv_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, 
  * pkv_paged_attention_decode with such scores (score NULL: plain ones), over
  * every pool type.  The query of sequence s sits at position seq_lens[s] - 1.
  * partition_tokens divides what a row may span: max_seq_len tokens, or with a
- * window those of the blocks it touches.  A length above max_seq_len rounded up to whole
- * blocks sets PKV_DEVERR_SEQ_LEN, and that row may lose tokens.
+ * window those of the blocks it touches.  max_seq_len must be >= every length; a row that
+ * does not fit the launch sets PKV_DEVERR_SEQ_LEN and loses its last tokens.
  * weights: device float [num_blocks][num_kv_heads][block_size] (16-byte aligned), or NULL.  Cached
  *   token t of sequence s receives, for each KV head, its share of the softmax
  *   summed over that head's query heads (num_q_heads / num_kv_heads in all for a
@@ -620,8 +620,8 @@ size_t pkv_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, 
  *   are set; those of the others are added to.  NULL: every token's is set, so
  *   that weights holds this step's shares alone.  An entry below 0 or above the length sets
  *   PKV_DEVERR_SEQ_LEN and is clamped.  Entries outside the batch's sequences stay
- *   as they are.  Sequences of one call that share a block race on its entries
- *   where they are added to.  A row with a NaN score leaves its shares unspecified.
+ *   as they are.  Sequences of one call that share a block race on its
+ *   entries (one's shares are lost).  A row with a NaN score leaves its shares unspecified.
  * workspace: pkv_decode_scored_workspace_bytes(...) bytes (may be NULL when that is
  *   0), in use until the call's kernels have finished.
  */
@@ -666,7 +666,7 @@ pkv_status pkv_select_tokens(const float* weights, const pkv_cache_desc* desc, c
  * sequence, whose blocks block_tables (before) and dst_tables (after) name; pools of
  * every type, codes with their parameters.  What lies behind the last row of a
  * list stays as it was.  seq_lens: the lengths before.
- * A list's entries ascend and are followed by -1.  A block of dst_tables is either none
+ * A list's entries are distinct, ascend and are followed by -1.  A block of dst_tables is either none
  * of the call's source blocks, or stands at the same place of the same sequence's row
  * of block_tables, where no other sequence of the call holds it; so the two tables may be
  * one, and pkv_alloc_evict_batch's are such.  An entry at or above the sequence's length sets
