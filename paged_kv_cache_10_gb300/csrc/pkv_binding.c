@@ -616,8 +616,8 @@ static PyObject* py_scored(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 }
 
 /* A 16-bit tensor [n, heads, D] (heads < 0: any number, returned) whose tokens may lie apart: pointer and elements from
- * one token to the next. */
-static int token_rows(PyObject* t, const char* name, PyObject* type_of, int32_t n, int32_t D, long dev, int32_t* heads,
+ * one token to the next.  dev: its device, set by the first call (-1) and demanded by later ones. */
+static int token_rows(PyObject* t, const char* name, PyObject* type_of, int32_t n, int32_t D, long* dev, int32_t* heads,
                       void** p, int64_t* step) {
     int32_t ts[3];
     if (dims(t, name, 3, ts)) return -1;
@@ -656,8 +656,11 @@ static int token_rows(PyObject* t, const char* name, PyObject* type_of, int32_t 
         PyErr_Format(PyExc_TypeError, "%s must be a CUDA tensor", name);
         return -1;
     }
-    if (dev >= 0 && on != dev) {
-        PyErr_Format(PyExc_ValueError, "%s is on cuda:%ld, the current device is cuda:%ld", name, on, dev);
+    if (*dev < 0) {
+        if (current_device(dev)) return -1;
+    }
+    if (on != *dev) {
+        PyErr_Format(PyExc_ValueError, "%s is on cuda:%ld, the current device is cuda:%ld", name, on, *dev);
         return -1;
     }
     r = PyObject_CallMethodNoArgs(t, s_data_ptr);
@@ -674,7 +677,7 @@ static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
     int32_t type, T[1], fs[2], Hq = 0, Hk, Hv;
     void *q = NULL, *k, *v, *pos, *slots, *freqs, *kc, *vc, *o = NULL, *st;
     int64_t qstep = 0, kstep, vstep, ostep = 0;
-    long dev;
+    long dev = -1;
     if (!nargs_ok(n, 13)) return NULL;
     if (get_desc(a[8], &c) || dims(a[4], "slot_mapping", 1, T) || dims(a[5], "freqs", 2, fs)) return NULL;
     int ok = is_type(a[4], t_i64);
@@ -706,14 +709,13 @@ static PyObject* py_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         PyErr_SetString(PyExc_ValueError, "sizes out of range");
         return NULL;
     }
-    if (token_rows(a[1], "k", a[1], T[0], c.head_size, -1, &Hk, &k, &kstep) || current_device(&dev) ||
-        token_rows(a[1], "k", a[1], T[0], c.head_size, dev, &Hk, &k, &kstep) ||
-        token_rows(a[2], "v", a[1], T[0], c.head_size, dev, &Hv, &v, &vstep))
+    if (token_rows(a[1], "k", a[1], T[0], c.head_size, &dev, &Hk, &k, &kstep) ||
+        token_rows(a[2], "v", a[1], T[0], c.head_size, &dev, &Hv, &v, &vstep))
         return NULL;
     if (a[0] != Py_None) {
         Hq = -1;
-        if (token_rows(a[0], "q", a[1], T[0], c.head_size, dev, &Hq, &q, &qstep) ||
-            token_rows(a[9], "q_out", a[1], T[0], c.head_size, dev, &Hq, &o, &ostep))
+        if (token_rows(a[0], "q", a[1], T[0], c.head_size, &dev, &Hq, &q, &qstep) ||
+            token_rows(a[9], "q_out", a[1], T[0], c.head_size, &dev, &Hq, &o, &ostep))
             return NULL;
     }
     if (optional_vector(a[3], t_i32, T[0], "positions", "int32", dev, &pos) ||
