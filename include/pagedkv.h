@@ -576,7 +576,7 @@ pkv_status pkv_paged_attention_decode_sparse(const void* q, int32_t q_dtype, int
  * whole sequences.
  *
  *   cap: 0 for none, else from 2^-20 to 2^20 (and scale / cap, times k_scale for an
- *     fp8 pool, finite).  tanh is within 2^-22 of 1, and of itself for small scores.
+ *     fp8 pool, finite).  tanh is within 2^-22 of the exact one.
  *   window: 0 for none.
  *   slopes: device float [num_q_heads], or NULL.
  *   first: device int32, or NULL; a negative entry counts as 0.  Decode: [num_seqs],

@@ -18,6 +18,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// 1 / x with the hardware approximation (one unit in the last place).
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 constexpr float kNoScore = -3e38f;  // softmax reference before the first score
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -26,9 +33,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // series (the sixth is 2^-26.8 of y at 1/4).
 __device__ __forceinline__ float tanh_score(float y) {
     const float a = fabsf(y), y2 = y * y;
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(ex2(a * (2.f * kLog2e)) + 1.f));
-    const float big = copysignf(fmaf(-2.f, r, 1.f), y);
+    const float big = copysignf(fmaf(-2.f, rcp(ex2(a * (2.f * kLog2e)) + 1.f), 1.f), y);
     const float c = fmaf(y2, fmaf(y2, fmaf(y2, 62.f / 2835.f, -17.f / 315.f), 2.f / 15.f), -1.f / 3.f);
     const float small = fmaf(y * y2, c, y);
     return a < 0.25f ? small : big;
