@@ -33,6 +33,9 @@ static struct {
     pkv_status (*scored)(const void*, int32_t, int32_t, int32_t, const void*, const void*, const pkv_cache_desc*,
                          const int32_t*, int32_t, const int32_t*, int32_t, float, const pkv_score_mod*, float*,
                          const int32_t*, void*, void*, size_t, int32_t, void*);
+    pkv_status (*prefill)(const void*, int32_t, int32_t, int32_t, int32_t, const int32_t*, int32_t, const void*, const void*,
+                          const pkv_cache_desc*, const int32_t*, int32_t, const int32_t*, const int32_t*, int32_t, float,
+                          const pkv_score_mod*, void*, void*, size_t, void*);
     pkv_status (*rope)(const void*, int64_t, int32_t, const void*, int64_t, const void*, int64_t, int32_t, int32_t,
                        const int32_t*, const int64_t*, const float*, int32_t, int32_t, float, void*, void*,
                        const pkv_cache_desc*, void*, int64_t, void*);
@@ -511,10 +514,10 @@ static PyObject* py_sparse(PyObject* self, PyObject* const* a, Py_ssize_t n) {
                    (const int32_t*)selected, ss[2], (float)scale, out, ws, wn, part, st));
 }
 
-/* Pointer of an optional tensor of n elements of a type; NULL for None. */
+/* Pointer of an optional tensor of n elements of a type; NULL for None.  p NULL: its type and size alone. */
 static int optional_vector(PyObject* t, PyObject* dtype, int32_t n, const char* name, const char* kind, long dev, void** p) {
     int32_t got[1];
-    *p = NULL;
+    if (p) *p = NULL;
     if (t == Py_None) return 0;
     const int ok = is_type(t, dtype);
     if (ok < 0 || dims(t, name, 1, got)) return -1;
@@ -522,22 +525,24 @@ static int optional_vector(PyObject* t, PyObject* dtype, int32_t n, const char* 
         PyErr_Format(PyExc_ValueError, "%s must be %s with %d entries", name, kind, n);
         return -1;
     }
-    return ptr_of(t, name, dev, p);
+    return p ? ptr_of(t, name, dev, p) : 0;
 }
 
-/* A ScoreMod (None: plain scores): heads slopes, n first positions, S prefix lengths. */
-static int get_score(PyObject* o, int32_t heads, int32_t n, int32_t S, long dev, pkv_score_mod* m) {
+/* A ScoreMod (None: plain scores): heads slopes, n first positions, S prefix lengths.  pointers 0: their types and
+ * sizes alone. */
+static int get_score(PyObject* o, int32_t heads, int32_t n, int32_t S, long dev, int pointers, pkv_score_mod* m) {
     memset(m, 0, sizeof *m);
     if (o == Py_None) return 0;
     if (attr_float(o, s_cap, &m->cap) || attr_i32(o, s_window, &m->window)) return -1;
     PyObject* const names[3] = {s_slopes, s_first, s_prefix_lens};
-    void* p[3];
+    void* p[3] = {NULL, NULL, NULL};
     for (int i = 0; i < 3; ++i) {
         PyObject* a = PyObject_GetAttr(o, names[i]);
         if (!a) return -1;
-        const int r = i == 0   ? optional_vector(a, t_f32, heads, "slopes", "float32", dev, &p[0])
-                      : i == 1 ? optional_vector(a, t_i32, n, "first", "int32", dev, &p[1])
-                               : optional_vector(a, t_i32, S, "prefix_lens", "int32", dev, &p[2]);
+        void** at = pointers ? &p[i] : NULL;
+        const int r = i == 0   ? optional_vector(a, t_f32, heads, "slopes", "float32", dev, at)
+                      : i == 1 ? optional_vector(a, t_i32, n, "first", "int32", dev, at)
+                               : optional_vector(a, t_i32, S, "prefix_lens", "int32", dev, at);
         Py_DECREF(a);
         if (r) return -1;
     }
@@ -607,12 +612,47 @@ static PyObject* py_scored(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         current_device(&dev) || ptr_of(a[0], "q", dev, &q) || pool_size(a[1], &c, "k_cache") ||
         pool_size(a[2], &c, "v_cache") || ptr_of(a[1], "k_cache", dev, &kc) || ptr_of(a[2], "v_cache", dev, &vc) ||
         ptr_of(a[4], "block_tables", dev, &tables) || ptr_of(a[5], "seq_lens", dev, &lens) ||
-        ptr_of(a[8], "out", dev, &out) || get_score(a[9], qs[1], qs[0], qs[0], dev, &m) ||
+        ptr_of(a[8], "out", dev, &out) || get_score(a[9], qs[1], qs[0], qs[0], dev, 1, &m) ||
         weights_of(a[10], &c, dev, &w) || optional_vector(a[11], t_i32, qs[0], "new_lens", "int32", dev, &fresh) ||
         workspace_of(a[12], dev, &ws, &wn) || stream_of(a[15], &st))
         return NULL;
     DONE(fn.scored(q, type, qs[0], qs[1], kc, vc, &c, (const int32_t*)tables, ts[1], (const int32_t*)lens, max_len,
                    (float)scale, &m, (float*)w, (const int32_t*)fresh, out, ws, wn, part, st));
+}
+
+/* prefill_scored(q, k_cache, v_cache, desc, query_start, max_query_len, block_tables, seq_lens, scale, out, score,
+ *                work_units, workspace, q_dtype, stream) */
+static PyObject* py_prefill_scored(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+    (void)self;
+    pkv_cache_desc c;
+    pkv_score_mod m;
+    int32_t type, qs[3], ts[2], S[1], starts[1], most, units[1] = {0};
+    void *q, *kc, *vc, *start, *tables, *lens, *out, *work = NULL, *ws, *st;
+    size_t wn;
+    long dev;
+    if (!nargs_ok(n, 15)) return NULL;
+    static const char ints[] = "query_start, block_tables, seq_lens and work_units";
+    if (get_desc(a[3], &c) || want_i32(a[4], ints) || want_i32(a[6], ints) || want_i32(a[7], ints) ||
+        (a[11] != Py_None && (want_i32(a[11], ints) || dims(a[11], "work_units", 1, units))) || dims(a[0], "q", 3, qs) ||
+        same(qs[2], c.head_size, "q must have the cache's head_size") || bytes16(a[0], (size_t)qs[0] * qs[1] * qs[2], "q") ||
+        alike3(a[0], qs, a[9], "out", "out must have q's shape and type") || dims(a[7], "seq_lens", 1, S) ||
+        dims(a[4], "query_start", 1, starts) ||
+        same(starts[0] - 1, S[0], "query_start must have num_seqs + 1 entries") || dims(a[6], "block_tables", 2, ts) ||
+        same(ts[0], S[0], "block_tables and seq_lens must have one row per sequence") || as_i32(a[5], &most) ||
+        pool_size(a[1], &c, "k_cache") || pool_size(a[2], &c, "v_cache") || element_type(a[0], a[13], &type) ||
+        get_score(a[10], qs[1], qs[0], S[0], -1, 0, &m))
+        return NULL;
+    const double scale = PyFloat_AsDouble(a[8]);
+    if (scale == -1.0 && PyErr_Occurred()) return NULL;
+    if (ptr_of(a[0], "q", -1, &q) || current_device(&dev) || ptr_of(a[0], "q", dev, &q) ||
+        ptr_of(a[1], "k_cache", dev, &kc) || ptr_of(a[2], "v_cache", dev, &vc) || ptr_of(a[4], "query_start", dev, &start) ||
+        ptr_of(a[6], "block_tables", dev, &tables) || ptr_of(a[7], "seq_lens", dev, &lens) ||
+        ptr_of(a[9], "out", dev, &out) || get_score(a[10], qs[1], qs[0], S[0], dev, 1, &m) ||
+        (units[0] > 0 && ptr_of(a[11], "work_units", dev, &work)) || workspace_of(a[12], dev, &ws, &wn) ||
+        stream_of(a[14], &st))
+        return NULL;
+    DONE(fn.prefill(q, type, qs[0], qs[1], S[0], (const int32_t*)start, most, kc, vc, &c, (const int32_t*)tables, ts[1],
+                    (const int32_t*)lens, (const int32_t*)work, units[0], (float)scale, &m, out, ws, wn, st));
 }
 
 /* A 16-bit tensor [n, heads, D] (heads < 0: any number, returned) whose tokens may lie apart: pointer and elements from
@@ -826,6 +866,7 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
         address(a[1], "pkv_select_blocks", &fn.select) ||
         address(a[1], "pkv_paged_attention_decode_sparse", &fn.sparse) ||
         address(a[1], "pkv_paged_attention_decode_scored", &fn.scored) ||
+        address(a[1], "pkv_paged_attention_prefill_scored", &fn.prefill) ||
         address(a[1], "pkv_paged_rope_append", &fn.rope) || address(a[1], "pkv_select_tokens", &fn.select_tokens) ||
         address(a[1], "pkv_paged_kv_compact", &fn.compact) ||
         address(a[1], "pkv_cache_block_bytes", &fn.block_bytes))
@@ -836,7 +877,7 @@ static PyObject* py_bind(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 #define METHOD(name) {#name, (PyCFunction)(void (*)(void))py_##name, METH_FASTCALL, NULL}
 static PyMethodDef methods[] = {METHOD(bind),   METHOD(append), METHOD(read),   METHOD(decode),
                                 METHOD(bounds), METHOD(select), METHOD(sparse), METHOD(scored), METHOD(rope),
-                                METHOD(select_tokens), METHOD(compact),
+                                METHOD(select_tokens), METHOD(compact), METHOD(prefill_scored),
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_pkv_binding", NULL, -1, methods, NULL, NULL, NULL, NULL};
 

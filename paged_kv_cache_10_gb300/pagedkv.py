@@ -210,7 +210,7 @@ def _calls():
     spec.loader.exec_module(m)
     names = ("pkv_paged_kv_append", "pkv_paged_kv_read", "pkv_paged_attention_decode", "pkv_paged_key_bounds",
              "pkv_select_blocks", "pkv_paged_attention_decode_sparse", "pkv_paged_attention_decode_scored",
-             "pkv_paged_rope_append", "pkv_select_tokens",
+             "pkv_paged_attention_prefill_scored", "pkv_paged_rope_append", "pkv_select_tokens",
              "pkv_paged_kv_compact", "pkv_cache_block_bytes")
     m.bind(torch, {n: ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in names}, _stream)
     _native = m
@@ -639,51 +639,15 @@ def paged_attention_prefill(q, k_cache, v_cache, desc: CacheDesc, query_start, m
     _check(st, "paged_attention_prefill")
 
 
-def _vector(t, name: str, dtype, n: int):
-    """Pointer of an optional device tensor of n elements of a type (None: NULL)."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.dim() != 1 or t.numel() != n:
-        raise ValueError(f"{name} must be {str(dtype).split('.')[-1]} with {n} entries")
-    return _dev_ptr(t, name)
-
-
 def paged_attention_prefill_scored(q, k_cache, v_cache, desc: CacheDesc, query_start, max_query_len: int, block_tables,
                                    seq_lens, scale: float, out, score: ScoreMod | None = None, q_dtype: str | None = None,
                                    stream=None, work_units=None, workspace=None) -> None:
     """Paged prefill with capped, biased and masked scores (ScoreMod, first [T] and prefix_lens [S]); everything else
     as for paged_attention_prefill."""
-    if q.dim() != 3 or q.shape[2] != desc.head_size or q.element_size() != 2:
-        raise ValueError("q must be [T, Hq, head_size] of a 16-bit type")
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError("out must have q's shape and type")
-    T, Hq, S = int(q.shape[0]), int(q.shape[1]), int(seq_lens.numel())
-    if any(t is not None and t.dtype != torch.int32 for t in (query_start, block_tables, seq_lens, work_units)):
-        raise TypeError("query_start, block_tables, seq_lens and work_units must be int32")
-    if seq_lens.dim() != 1 or query_start.dim() != 1 or query_start.numel() != S + 1:
-        raise ValueError("query_start must have num_seqs + 1 entries")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S:
-        raise ValueError("block_tables and seq_lens must have one row per sequence")
-    nbytes = _desc(desc)[1]
-    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if nbytes and t.nbytes != nbytes:
-            raise ValueError(f"{n} must hold {desc.num_blocks} blocks of {block_bytes(desc)} bytes")
-    mod = score or ScoreMod()
-    for t, n in ((q, "q"), (out, "out"), (k_cache, "k_cache"), (v_cache, "v_cache"), (query_start, "query_start"),
-                 (block_tables, "block_tables"), (seq_lens, "seq_lens"), (work_units, "work_units"), (workspace, "workspace"),
-                 (mod.slopes, "slopes"), (mod.first, "first"), (mod.prefix_lens, "prefix_lens")):
-        if t is not None and t.is_cuda and t.get_device() != torch.cuda.current_device():
-            raise ValueError(f"{n} is on cuda:{t.get_device()}, the current device is cuda:{torch.cuda.current_device()}")
-    c = _ScoreMod(mod.cap, mod.window, _vector(mod.slopes, "slopes", torch.float32, Hq),
-                  _vector(mod.first, "first", torch.int32, T), _vector(mod.prefix_lens, "prefix_lens", torch.int32, S))
-    nw = 0 if work_units is None else int(work_units.numel())
-    st = lib().pkv_paged_attention_prefill_scored(
-        _dev_ptr(q, "q"), _dtype_code(q, q_dtype), T, Hq, S, _dev_ptr(query_start, "query_start"), int(max_query_len),
-        _dev_ptr(k_cache, "k_cache"), _dev_ptr(v_cache, "v_cache"), _desc(desc)[0], _dev_ptr(block_tables, "block_tables"),
-        int(block_tables.shape[1]), _dev_ptr(seq_lens, "seq_lens"), _dev_ptr(work_units, "work_units") if nw else None, nw,
-        float(scale), ctypes.byref(c), _dev_ptr(out, "out"), None if workspace is None else _dev_ptr(workspace, "workspace"),
-        0 if workspace is None else workspace.nbytes, _stream(stream))
-    _check(st, "paged_attention_prefill_scored")
+    st = _calls().prefill_scored(q, k_cache, v_cache, desc, query_start, max_query_len, block_tables, seq_lens, scale, out,
+                                 score, work_units, workspace, q_dtype, stream)
+    if st:
+        _check(st, "paged_attention_prefill_scored")
 
 
 def prefill_workspace_bytes(kv_dtype: str, num_seqs: int, num_kv_heads: int, head_size: int,
