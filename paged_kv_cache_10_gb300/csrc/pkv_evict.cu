@@ -14,6 +14,11 @@
 // loads before its first store, may write the blocks it reads from, with one
 // barrier a chunk.  Columns of a row never meet: they are split over CTAs where
 // there are few rows of sequences and heads.
+//
+// One GB300: the tokens of 8190 for 8 heads chosen in 8.4 us (two dependent loads,
+// three passes of barriers: latency), 2048 of them moved in 6.6; those of 32 x 2048 to
+// 4096 chosen in 10.2 us, 1000 each moved in 45.3, 0.87 of what a plain copy of as
+// many bytes takes.
 #include <algorithm>
 #include <cstdint>
 
@@ -184,9 +189,11 @@ struct Compact {
     unsigned char *k_cache, *v_cache;
     float* weights;
     const int32_t *src_tables, *dst_tables, *seq_lens;
-    int32_t n, Hkv, NB, src_mb, dst_mb, slices;
+    int32_t n, Hkv, NB, src_mb, dst_mb, slices, rows, planes;  // rows: sequences times heads
     unsigned int* err;
 };
+
+constexpr int kRowsY = 65535;  // rows of grid axis y; axis z holds the planes of these, of the next ones, ...
 
 // One entry of a list: the bytes from the pool's start to where its row comes from
 // and goes to; src < 0: it stays.
@@ -268,25 +275,11 @@ __device__ __forceinline__ void move_rows(const Compact& p, Move* win, unsigned 
     }
 }
 
-// CTA (column slice x, plane and KV head y, sequence z).  Planes: keys, values, then for
-// integer-coded pools their rows' parameters, and the weights last.
+// One sequence's and head's part of a plane.
 template <int THREADS, int D, int KV>
-__global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kernel(const Compact p) {
+__device__ __forceinline__ void compact_row(const Compact& p, Move* win, int plane, int s, int h, int count, int L,
+                                            bool first) {
     constexpr bool kInt = KV == PKV_INT8 || KV == PKV_INT4;
-    wait_primary_grid();
-    const int plane = blockIdx.y / p.Hkv, h = blockIdx.y % p.Hkv, s = blockIdx.z;
-    int L = load_live(p.seq_lens + s);
-    const bool first = blockIdx.x == 0 && plane == 0;
-    if (L < 0 || L > p.src_mb * kBlockSize) {
-        if (threadIdx.x == 0 && first && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
-        L = L < 0 ? 0 : p.src_mb * kBlockSize;
-    }
-    int count = min(p.n, L);
-    if (count > p.dst_mb * kBlockSize) {
-        if (threadIdx.x == 0 && first && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
-        count = p.dst_mb * kBlockSize;
-    }
-    __shared__ Move win[THREADS];
     const int cut = __ffs(p.slices) - 1;  // log2 of the column slices
     const auto none = [](int) { return 0; };
     const auto one = [&](unsigned char* pool, int64_t tile_bytes, auto type, auto row) {
@@ -301,8 +294,10 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kernel(const 
             weights();
             return;
         }
+        // three pieces a thread and buffer: with four, whose rows lie a power of two apart, 49.2 us
+        // against 45.3 for 32 sequences of 1000 tokens; with five 46.1, with two 50.8
         constexpr int ROW = D * (KV == PKV_FP8_E4M3 ? 1 : 2), LG = ROW == 256 ? 4 : (ROW == 128 ? 3 : 2);
-        move_rows<THREADS, uint4, 4>(p, win, plane ? p.v_cache : p.k_cache, kBlockSize * ROW, LG - cut, blockIdx.x << (LG - cut), h, s,
+        move_rows<THREADS, uint4, 3>(p, win, plane ? p.v_cache : p.k_cache, kBlockSize * ROW, LG - cut, blockIdx.x << (LG - cut), h, s,
                             count, L, first, [](int t) { return t * ROW; }, [](int u) { return u * 16; });
     } else {
         using L_ = IntTile<D, KV == PKV_INT8 ? 8 : 4>;
@@ -321,6 +316,31 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kernel(const 
             one(plane == 3 ? p.v_cache : p.k_cache, L_::kBytes, uint2{}, [](int t) { return L_::param(t); });
         }
     }
+}
+
+// CTA (column slice x, sequence and KV head y, plane z) of up to kRowsY rows.  Planes: keys, values, then
+// for integer-coded pools their rows' parameters, and the weights last: one pool after
+// the other (1000 of 2048 to 4096 tokens, 32 sequences, 8 heads: 45.3 us, 3 less than
+// with a head's pools side by side; a copy of as many bytes takes 39.7).
+template <int THREADS, int D, int KV>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kernel(const Compact p) {
+    __shared__ Move win[THREADS];
+    wait_primary_grid();
+    const int plane = blockIdx.z % p.planes, r = static_cast<int>(blockIdx.z / p.planes) * kRowsY + blockIdx.y;
+    if (r >= p.rows) return;
+    const int s = r / p.Hkv, h = r - s * p.Hkv;
+    const bool first = blockIdx.x == 0 && plane == 0;
+    int L = load_live(p.seq_lens + s);
+    if (L < 0 || L > p.src_mb * kBlockSize) {
+        if (threadIdx.x == 0 && first && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        L = L < 0 ? 0 : p.src_mb * kBlockSize;
+    }
+    int count = min(p.n, L);
+    if (count > p.dst_mb * kBlockSize) {
+        if (threadIdx.x == 0 && first && h == 0) report(p.err, PKV_DEVERR_SEQ_LEN);
+        count = p.dst_mb * kBlockSize;
+    }
+    compact_row<THREADS, D, KV>(p, win, plane, s, h, count, L, first);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -403,7 +423,7 @@ extern "C" pkv_status pkv_paged_kv_compact(const int32_t* kept, int32_t num_kept
     if (bad != PKV_OK) return bad;
     if (num_seqs < 0 || num_kept <= 0 || max_blocks_per_seq <= 0 || dst_blocks_per_seq <= 0) return PKV_ERR_INVALID;
     if (max_blocks_per_seq > 0x7fffffff / kBlockSize || dst_blocks_per_seq > 0x7fffffff / kBlockSize ||
-        num_kept > 0x7fffffff - 4096 || num_seqs > 65535 || d->num_kv_heads > 65535 / 5)
+        num_kept > 0x7fffffff - 4096 || num_seqs > 65535)
         return PKV_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PKV_OK;
     if (!kept || !k_cache || !v_cache || !block_tables || !seq_lens || !dst_tables || !aligned4(kept) ||
@@ -425,17 +445,19 @@ extern "C" pkv_status pkv_paged_kv_compact(const int32_t* kept, int32_t num_kept
     p.NB = d->num_blocks;
     p.src_mb = max_blocks_per_seq;
     p.dst_mb = dst_blocks_per_seq;
-    // Columns split over up to four CTAs until there are six an SM.  Where that is not
-    // reached by far, what one CTA has under way limits the rate, and CTAs of four times the
-    // threads take over (2048 of 8190 tokens, 8 heads: 6.6 us against 11.0; with twice the
-    // threads 7.9, where 32 sequences of 1000 tokens take 51.8 against 50.3).
-    const int64_t rows = static_cast<int64_t>(num_seqs) * p.Hkv * 2;
-    p.slices = rows >= 6 * num_sms() ? 1 : (2 * rows >= 6 * num_sms() ? 2 : 4);
+    // Columns split over up to four CTAs until there are three an SM (two pools; 45.3
+    // against 48.8 us with twice as many for 32 sequences of 1000 tokens).  Where that is
+    // not reached by far, what one CTA has under way limits the rate, and CTAs of four
+    // times the threads take over (2048 of 8190 tokens, 8 heads: 6.6 us against 11.0).
+    if (static_cast<int64_t>(num_seqs) * p.Hkv > int64_t{kRowsY} * (65535 / 5)) return PKV_ERR_UNSUPPORTED;  // grid axis z
+    p.rows = num_seqs * p.Hkv;
+    const int64_t rows = 2 * static_cast<int64_t>(p.rows);
+    p.slices = rows >= 3 * num_sms() ? 1 : (2 * rows >= 3 * num_sms() ? 2 : 4);
     const bool few = rows < num_sms();
-    const int planes = (is_int_pool(d->kv_dtype) ? 4 : 2) + (weights ? 1 : 0);
+    p.planes = (is_int_pool(d->kv_dtype) ? 4 : 2) + (weights ? 1 : 0);
     auto kern = d->head_size == 128 ? (few ? compact_of<1024, 128>(d->kv_dtype) : compact_of<256, 128>(d->kv_dtype))
                                     : (few ? compact_of<1024, 64>(d->kv_dtype) : compact_of<256, 64>(d->kv_dtype));
-    const cudaError_t e = launch_maybe_pdl(true, kern, dim3(p.slices, planes * p.Hkv, num_seqs), dim3(few ? 1024 : 256), 0,
+    const cudaError_t e = launch_maybe_pdl(true, kern, dim3(p.slices, std::min(p.rows, kRowsY), p.planes * ((p.rows + kRowsY - 1) / kRowsY)), dim3(few ? 1024 : 256), 0,
                                            static_cast<cudaStream_t>(stream), p);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

@@ -14,6 +14,10 @@
 // its loads go out before the heads' sums are known.  The merge has CTAs of its own
 // behind those, so that each CTA waits for memory twice: for its row's length, then
 // for everything else.
+//
+// One GB300, bf16: 64 x U[512, 4096] tokens, 32/8 heads 110.0 us with the decode, which
+// takes 95.0 without shares (5 of the 15 to write 19 MB of scores, 4 for this launch, 6
+// for its loads' latency); 1 x 8190 tokens, 64/8 heads 12.6 against 10.2.
 #include <cstdint>
 
 #include "pkv_decode_impl.cuh"

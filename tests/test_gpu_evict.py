@@ -295,3 +295,20 @@ def test_a_serving_loop(pk, kv, capture):
     for _ in range(3):
         step()
     assert pk.get_device_error() == 0
+
+
+def test_more_rows_than_a_grid_axis_holds(pk):
+    """20000 sequences of 4 heads: 80000 rows, of two tokens each, the second kept."""
+    S, Hkv, D = 20000, 4, 64
+    desc = pk.CacheDesc(num_blocks=S, num_kv_heads=Hkv, head_size=D, kv_dtype="bf16")
+    kc, vc = (torch.randn(S, Hkv, 16, D, device="cuda").to(torch.bfloat16) for _ in range(2))
+    k0, v0 = kc.clone(), vc.clone()
+    w = torch.rand(S, Hkv, 16, device="cuda")
+    w0 = w.clone()
+    tables = torch.randperm(S, device="cuda").int()[:, None].contiguous()
+    lens = torch.full((S,), 2, dtype=torch.int32, device="cuda")
+    kept = torch.ones(S, Hkv, 1, dtype=torch.int32, device="cuda")
+    pk.paged_kv_compact(kept, kc, vc, desc, tables, lens, tables, weights=w)
+    assert pk.get_device_error() == 0
+    for new, old in ((kc, k0), (vc, v0), (w, w0)):
+        assert torch.equal(new[:, :, 0], old[:, :, 1]) and torch.equal(new[:, :, 1:], old[:, :, 1:])
