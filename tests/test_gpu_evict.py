@@ -312,3 +312,18 @@ def test_more_rows_than_a_grid_axis_holds(pk):
     assert pk.get_device_error() == 0
     for new, old in ((kc, k0), (vc, v0), (w, w0)):
         assert torch.equal(new[:, :, 0], old[:, :, 1]) and torch.equal(new[:, :, 1:], old[:, :, 1:])
+
+
+def test_readme_example_of_an_eviction_runs():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    code = [c for c in re.findall(r"```python\n(.*?)```", text, re.S) if "paged_kv_compact" in c]
+    assert len(code) == 1
+    e = {}
+    exec(compile(code[0], "README.md example", "exec"), e)
+    first, k, D = e["kept"][0], e["k_cache"], e["D"]
+    assert bool((first[:, 1:] > first[:, :-1]).all()) and first[:, :4].tolist() == [list(range(4))] * e["Hkv"]
+    shares = e["weights"][e["dev"](e["fewer"])[0, : e["keep"] // 16].long()]
+    # four steps leave Hq each; besides 68 fixed tokens the 444 largest of 1936 stay, which hold at least 444/1936
+    assert bool(torch.isfinite(k.float()).all()) and float(shares.sum()) > 0.999 * 4 * e["Hq"] * 444 / 1936
