@@ -615,7 +615,7 @@ size_t pkv_decode_scored_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, 
  * weights: device float [num_blocks][num_kv_heads][block_size] (16-byte aligned), or NULL.  Cached
  *   token t of sequence s receives, for each KV head, its share of the softmax
  *   summed over that head's query heads (num_q_heads / num_kv_heads in all for a
- *   row), the measure that pkv_select_tokens evicts by.
+ *   row), the measure that pkv_select_tokens evicts by.  Rows of up to 2^30 tokens.
  * new_lens: device int32 [num_seqs]: the entries of the last new_lens[s] tokens
  *   are set; those of the others are added to.  NULL: every token's is set, so
  *   that weights holds this step's shares alone.  An entry below 0 or above the length sets

@@ -381,6 +381,7 @@ pkv_status decode_common(const void* q, int32_t q_dtype, int32_t num_seqs, int32
     // positions, and the end of a row's last partition, are 32-bit in the kernels
     if (NP * P > 0x7fffffff || max_blocks_per_seq > 0x7fffffff / kBlockSize) return PKV_ERR_UNSUPPORTED;
     if (sc && static_cast<int64_t>(max_blocks_per_seq) * kBlockSize + P > 0x7fffffff) return PKV_ERR_UNSUPPORTED;
+    if (sc && sc->weights && max_seq_len > 0x40000000) return PKV_ERR_UNSUPPORTED;  // 32-bit tiles of tokens
     const size_t need = sc ? scored_workspace(num_seqs, num_q_heads, d->head_size, reach, P, sc->weights != nullptr)
                            : workspace_bytes(num_seqs, num_q_heads, d->head_size, max_seq_len, P);
     if (need > 0 && (!workspace || ws_bytes < need || !aligned16(workspace))) return PKV_ERR_WORKSPACE;

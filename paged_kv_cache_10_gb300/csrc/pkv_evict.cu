@@ -297,8 +297,9 @@ __device__ __forceinline__ void compact_row(const Compact& p, Move* win, int pla
         // three pieces a thread and buffer: with four, whose rows lie a power of two apart, 49.2 us
         // against 45.3 for 32 sequences of 1000 tokens; with five 46.1, with two 50.8
         constexpr int ROW = D * (KV == PKV_FP8_E4M3 ? 1 : 2), LG = ROW == 256 ? 4 : (ROW == 128 ? 3 : 2);
-        move_rows<THREADS, uint4, 3>(p, win, plane ? p.v_cache : p.k_cache, kBlockSize * ROW, LG - cut, blockIdx.x << (LG - cut), h, s,
-                            count, L, first, [](int t) { return t * ROW; }, [](int u) { return u * 16; });
+        move_rows<THREADS, uint4, 3>(p, win, plane ? p.v_cache : p.k_cache, kBlockSize * ROW, LG - cut,
+                                     blockIdx.x << (LG - cut), h, s, count, L, first, [](int t) { return t * ROW; },
+                                     [](int u) { return u * 16; });
     } else {
         using L_ = IntTile<D, KV == PKV_INT8 ? 8 : 4>;
         constexpr int LG = L_::RB == 128 ? 3 : (L_::RB == 64 ? 2 : 1);  // 16-byte pieces of a key row
@@ -306,10 +307,10 @@ __device__ __forceinline__ void compact_row(const Compact& p, Move* win, int pla
         if (plane == 0) {
             if (blockIdx.x == 0)
                 move_rows<THREADS, uint4, 4>(p, win, p.k_cache, L_::kBytes, LG, 0, h, s, count, L, first,
-                                    [](int t) { return L_::key(t, 0); }, [](int u) { return L_::key(0, u * 16); });
+                                             [](int t) { return L_::key(t, 0); }, [](int u) { return L_::key(0, u * 16); });
         } else if (plane == 1) {  // two bytes lie together in a value tile: the codes that are split
-            move_rows<THREADS, uint16_t, 8>(p, win, p.v_cache, L_::kBytes, LG + 3 - cut, blockIdx.x << (LG + 3 - cut), h, s, count, L,
-                                   false, [](int t) { return L_::val(t, 0); }, [](int u) { return L_::val(0, u * 2); });
+            move_rows<THREADS, uint16_t, 8>(p, win, p.v_cache, L_::kBytes, LG + 3 - cut, blockIdx.x << (LG + 3 - cut), h, s,
+                                        count, L, false, [](int t) { return L_::val(t, 0); }, [](int u) { return L_::val(0, u * 2); });
         } else if (plane == 4) {
             weights();
         } else {
@@ -457,7 +458,8 @@ extern "C" pkv_status pkv_paged_kv_compact(const int32_t* kept, int32_t num_kept
     p.planes = (is_int_pool(d->kv_dtype) ? 4 : 2) + (weights ? 1 : 0);
     auto kern = d->head_size == 128 ? (few ? compact_of<1024, 128>(d->kv_dtype) : compact_of<256, 128>(d->kv_dtype))
                                     : (few ? compact_of<1024, 64>(d->kv_dtype) : compact_of<256, 64>(d->kv_dtype));
-    const cudaError_t e = launch_maybe_pdl(true, kern, dim3(p.slices, std::min(p.rows, kRowsY), p.planes * ((p.rows + kRowsY - 1) / kRowsY)), dim3(few ? 1024 : 256), 0,
+    const dim3 grid(p.slices, std::min(p.rows, kRowsY), p.planes * ((p.rows + kRowsY - 1) / kRowsY));
+    const cudaError_t e = launch_maybe_pdl(true, kern, grid, dim3(few ? 1024 : 256), 0,
                                            static_cast<cudaStream_t>(stream), p);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

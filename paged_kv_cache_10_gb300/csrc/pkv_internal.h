@@ -89,7 +89,7 @@ struct DecodeParams {
     const int32_t* first = nullptr;   // [S] or null
     int32_t span = 0;                 // > 0 marks a scored launch: most tokens of a row, in whole blocks
     // Scores in log2 units for pkv_paged_attention_decode_scored's weights, [S][Hkv][span][G], a row's
-    // first token being that of scored_range; null: none kept.
+    // first token being the first of the block that its range starts in; null: none kept.
     float* scores = nullptr;
 };
 
@@ -131,14 +131,6 @@ __host__ __device__ inline int own_start(const int32_t* seq_group, const int32_t
         start = start < 0 ? 0 : (L / kBlockSize) * kBlockSize;
     }
     return start;
-}
-
-// Scored decode: the first token a row of L tokens attends to, through its
-// window and its first position (L where nothing is left).
-__host__ __device__ inline int scored_first(int window, const int32_t* first, int s, int L) {
-    int lo = first ? first[s] : 0;
-    if (window > 0 && lo < L - window) lo = L - window;
-    return lo < 0 ? 0 : (lo > L ? L : lo);
 }
 
 // Device address of the error word on the current device (cached).

@@ -65,8 +65,13 @@ constexpr int kUnitSlots = 4;
 constexpr int kUnitReaders = 11;
 
 // Scored prefill: the mask of a value tile's tokens with a value that is not
-// finite, for the last kBadSlots tiles.
-constexpr int kBadSlots = 8;
+// finite, for the last kBadSlots tiles.  A softmax warp reads a tile's mask before it
+// hands on P of its Q tile's next one, or, the last of a unit, before it takes the next
+// unit.  By then the value warp is at most kBadLag tiles further in that unit (its
+// Q tiles end that close to each other), and in the up to kUnitSlots units behind it, each
+// of which it enters no further than kBadWait tiles before every warp has taken it.
+constexpr int kBadSlots = 32, kBadLag = 4, kBadWait = 5;
+static_assert(kBadLag + kUnitSlots * kBadWait < kBadSlots, "masks");
 
 // q_full, q_empty, k_full[3], k_empty[3], v_full[2], v_empty[2], v_zero[2], s_full[2 tiles],
 // p_full[2 tiles], o_done[2 tiles], drain, u_full[4], u_empty[4], u_near
@@ -273,6 +278,10 @@ __device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int R
     u.lead = any ? lo_min - u.k0 : 1;
     u.kv_end[0] = max(__reduce_max_sync(0xffffffffu, end0) - u.k0, 1);
     u.kv_end[1] = u.t0 + RQ < u.n ? max(__reduce_max_sync(0xffffffffu, end1) - u.k0, 1) : 0;
+    // a Q tile whose rows see nothing goes along to kBadLag tiles before the other's end
+    const int most = max(u.kv_end[0], u.kv_end[1]) - kBadLag * kTileN;
+    u.kv_end[0] = max(u.kv_end[0], most);
+    if (u.kv_end[1] > 0) u.kv_end[1] = max(u.kv_end[1], most);
     u.lo_max = lo_max == 0x7fffffff ? lo_max : lo_max - u.k0;
     u.hi_min = hi_min - u.k0;
     u.bt += u.k0 / kBlockSize;
@@ -921,7 +930,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // rows in front of the lowest key too, and the tokens with values
                         // that are not finite in tiles that some row sees in part
                         uint4 bad = make_uint4(0u, 0u, 0u, 0u);
-                        if (j * kTileN < u.lo_max || j * kTileN + kTileN - 1 > u.hi_min) {
+                        if (j == kBadWait) okv = warp_all(mbar_wait(u_empty + k % kUnitSlots, (k / kUnitSlots) & 1));
+                        if (!okv) {
+                            // reported below
+                        } else if (j * kTileN < u.lo_max || j * kTileN + kTileN - 1 > u.hi_min) {
                             okv = warp_all(mbar_wait(v_full + st, (g / nst) & 1));
                             if (okv) {
                                 unsigned char* vb = sm + kOffV + st * kOpBytes;
@@ -1158,7 +1170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // scored: a tile may leave the row nothing
             float m_ref = kScored ? kNoScore : -INFINITY, l = 0.f;
             // scored: a row that attends to a value that is not finite becomes NaN (the value
-            // tile's scan is done once P V of it is)
+            // tile's scan is done once P V of it is, and its mask stays until it is read)
             const auto check_values = [&](int j) {
                 const uint4 m = bad_ring[(gt + j) % kBadSlots];
                 if (__builtin_expect((m.x | m.y | m.z | m.w) != 0u, 0))
@@ -1388,11 +1400,11 @@ cudaError_t launch_tile(const PrefillParams& p, dim3 grid, const CUtensorMap& tq
     return cudaGetLastError();
 }
 
-// Persistent prefill: one CTA per SM (one CTA fits an SM), or one per unit
-// when there are fewer; the launch takes the next counter slot.
 // One sequence of slots for calls of every type: they share the counters.
 std::atomic<uint32_t> g_next_sched_slot{0};
 
+// Persistent prefill: one CTA per SM (one CTA fits an SM), or one per unit
+// when there are fewer; the launch takes the next counter slot.
 template <typename T>
 cudaError_t launch_prefill(PrefillParams p, int D, const CUtensorMap& tq, const CUtensorMap& tk,
                            const CUtensorMap& tv, bool scored, cudaStream_t st) {

@@ -39,6 +39,14 @@ __device__ __forceinline__ float tanh_score(float y) {
     return a < 0.25f ? small : big;
 }
 
+// Scored decode: the first token a row of L tokens attends to, through its
+// window and its first position (L where nothing is left).
+__device__ __forceinline__ int scored_first(int window, const int32_t* first, int s, int L) {
+    int lo = first ? load_live(first + s) : 0;
+    if (window > 0 && lo < L - window) lo = L - window;
+    return lo < 0 ? 0 : (lo > L ? L : lo);
+}
+
 // A row's tokens [lo, end) and the first one of the block that lo lies in.
 struct ScoredRow {
     int lo, start, end;

@@ -254,7 +254,6 @@ cudaError_t launch_weights_t(const DecodeParams& p, const int32_t* new_lens, int
 cudaError_t launch_weights(const DecodeParams& p, const int32_t* new_lens, int max_seq_len, int q_dtype, float* weights,
                            cudaStream_t st) {
     const int max_len = (max_seq_len + kBlockSize - 1) / kBlockSize * kBlockSize;
-    if (max_len == 0) return cudaSuccess;
     if (q_dtype == PKV_BF16)
         return p.D == 128 ? launch_weights_t<128, BF16>(p, new_lens, max_len, weights, st)
                           : launch_weights_t<64, BF16>(p, new_lens, max_len, weights, st);

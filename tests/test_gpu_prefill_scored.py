@@ -159,6 +159,28 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them(pk, D, G, bad):
     assert pk.get_device_error() == 0
 
 
+@pytest.mark.parametrize("short", [0, 1])
+@pytest.mark.parametrize("D,G", [(64, 1), (128, 1), (128, 8)])
+def test_one_half_of_a_unit_is_through_long_before_the_other(pk, D, G, short):
+    """Rows of one Q tile see nothing, those of the other a long context; then the next unit, and the other way round."""
+    RQ, ctx = 128 // G, 2600
+    n = 4 * RQ
+    c = Case(pk, "f16", D, 1, G, "f16", {}, chunks=[(ctx, n), (0, 40)], seed=9)
+    first = np.zeros(n + 40, np.int32)
+    half = np.arange(n) // RQ % 2 == short
+    first[:n][half] = ctx + 4 * RQ  # nothing to see: the unit's one tile
+    c.first = first
+    c.ref, c.shares = su.ref_scored(c.q, c.where, c.pools, c.tables, c.lens, c.scale, 0.0, 0, None, first, None)
+    c.check(c.run())
+    for t in (3, 127, ctx - 1, ctx + n - 1):  # seen by the other half alone; the last by its last row
+        c.vd[int(c.tables[0][t // 16]), 0, t % 16, 1 + t % 60] = float("nan")
+    out = c.run()
+    c.check(out, np.append(half, np.ones(40, bool)))
+    got = out.double().cpu().numpy()[:n][~half]
+    assert np.all((~np.isfinite(got)).any(-1))
+    assert pk.get_device_error() == 0
+
+
 def test_long_context_behind_a_window(pk):
     """Many tiles in front of the window, a ring of value masks gone round many times."""
     c = Case(pk, "bf16", 128, 1, 4, "bf16", dict(window=3000, cap=40.0, docs=40), chunks=[(9000, 200)], seed=8)

@@ -42,6 +42,7 @@ def test_scored_decode_refused(pk):
     assert call(dt=0) == pk.ERR_UNSUPPORTED and call(mx=65) == pk.ERR_INVALID and call(part=24) == pk.ERR_INVALID
     assert call(q=AT + 8) == pk.ERR_INVALID and call(kv="e4m3", k_scale=0.0) == pk.ERR_INVALID
     assert call(MB=1 << 27) == pk.ERR_UNSUPPORTED and call(MB=(1 << 27) - 1, part=64, n=1 << 40, mx=64) == pk.ERR_UNSUPPORTED
+    assert call(MB=1 << 26, mx=1 << 30, w=AT) == pk.ERR_WORKSPACE and call(MB=1 << 27 >> 1 | 1, mx=(1 << 30) + 1, w=AT) == pk.ERR_UNSUPPORTED
     # the workspace: partials of split rows, and with weights those of every row and the scores
     assert call(part=16, ws=None) == pk.ERR_WORKSPACE and call(w=AT, ws=None) == pk.ERR_WORKSPACE
     for window, part, weights in ((0, 16, 0), (0, 16, 1), (0, 0, 1), (20, 16, 1)):
