@@ -296,7 +296,7 @@ __device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int R
 // elements.  A warp whose tile has a larger y takes 1 - 2 / (e^2y + 1), within 2^-22 of
 // 1: two special-function operations an element beside the softmax's own.  Nothing
 // hides either from the tile's chain: 8 x 512 new tokens behind 0 to 3584, 32/8
-// heads, take 175 us uncapped, 222 with the polynomial, 265 with the other (degree
+// heads, take 177 us uncapped, 226 with the polynomial, 265 with the other (degree
 // 4 up to 0.5: 238; degree 6 up to 1 on scalars: 340).
 constexpr float kTanhLow[4] = {0.99999994f, -0.333319813f, 0.132846266f, -0.0482781753f};
 
