@@ -757,7 +757,7 @@ pkv_status pkv_paged_attention_prefill(const void* q, int32_t q_dtype, int32_t n
  * Arguments, pools, workspace, plan and errors as for pkv_paged_attention_prefill.
  * Keys and values that a row does not see do not reach it, whatever they hold.
  * A value that is not finite makes the rows that see it, in a 128-key tile where
- * some row of the same 256 does not see every key, NaN in whole; elsewhere it
+ * some row of the same up to 256 does not see every key, NaN in whole; elsewhere it
  * makes them what the products give.
  */
 pkv_status pkv_paged_attention_prefill_scored(const void* q, int32_t q_dtype, int32_t num_tokens, int32_t num_q_heads,

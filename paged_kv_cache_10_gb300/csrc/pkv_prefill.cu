@@ -104,7 +104,8 @@ struct PrefillParams {
     void* out;                   // [T][Hq][D]
     int32_t S, T, Hq, Hkv, MB, NB;
     int32_t G, TT;               // heads per KV head, tokens per CTA (128 / G)
-    int32_t num_qtiles;          // CTAs per (sequence, KV head) along the queries
+    int32_t num_qtiles;          // units per (sequence, KV head) along the queries
+    int32_t unit_tiles = 2;      // Q tiles of a unit (1: tile B stays empty)
     int32_t max_query_len;       // the caller's bound on every chunk
     const int32_t* work;         // [num_work] units s * num_qtiles + qt in start order, or null
     int32_t num_work;
@@ -257,7 +258,7 @@ __device__ __forceinline__ void row_range(const PrefillParams& p, const Unit& u,
 __device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int RQ, int lane, Unit& u) {
     u.prefix = p.prefix_lens ? min(load_live(p.prefix_lens + s), u.ctx + u.n) : 0;
     int lo_min = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff, end0 = 0, end1 = 0;
-    for (int i = lane; i < 2 * RQ && u.t0 + i < u.n; i += 32) {
+    for (int i = lane; i < p.unit_tiles * RQ && u.t0 + i < u.n; i += 32) {
         int lo, hi;
         row_range(p, u, u.t0 + i, lo, hi);
         if (lo <= hi) {
@@ -277,7 +278,7 @@ __device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int R
     u.k0 = any ? lo_min / kBlockSize * kBlockSize : 0;
     u.lead = any ? lo_min - u.k0 : 1;
     u.kv_end[0] = max(__reduce_max_sync(0xffffffffu, end0) - u.k0, 1);
-    u.kv_end[1] = u.t0 + RQ < u.n ? max(__reduce_max_sync(0xffffffffu, end1) - u.k0, 1) : 0;
+    u.kv_end[1] = u.kv_end[1] > 0 ? max(__reduce_max_sync(0xffffffffu, end1) - u.k0, 1) : 0;
     // a Q tile whose rows see nothing goes along to kBadLag tiles before the other's end
     const int most = max(u.kv_end[0], u.kv_end[1]) - kBadLag * kTileN;
     u.kv_end[0] = max(u.kv_end[0], most);
@@ -538,12 +539,12 @@ __device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int64_t lin
         return false;
     }
     if (u.n > p.max_query_len && rep) report(p.err, PKV_DEVERR_SEQ_LEN);
-    u.t0 = qt * 2 * RQ;
+    u.t0 = qt * p.unit_tiles * RQ;
     if (u.t0 >= u.n) return false;
     u.ctx = L - u.n;  // tokens before this chunk
     for (int X = 0; X < 2; ++X) {
         const int tx = u.t0 + X * RQ;
-        u.kv_end[X] = tx < u.n ? u.ctx + tx + min(RQ, u.n - tx) : 0;
+        u.kv_end[X] = X < p.unit_tiles && tx < u.n ? u.ctx + tx + min(RQ, u.n - tx) : 0;
     }
     u.bt = p.block_tables + static_cast<int64_t>(s) * p.MB;
     return true;
@@ -732,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool done = false;
         const bool ranked = kScored && !p.work && p.S <= 32;
         Ranks ranks{0, 0, 0, 0, 0, 0};
-        if (ranked) ranks = load_ranks(p, 2 * RQ, lane);
+        if (ranked) ranks = load_ranks(p, p.unit_tiles * RQ, lane);
         for (;; ++k) {
             // unit k is claimed once the S MMAs of unit k - 1 are issued (that
             // unit is in its last key tile), so a CTA holds at most one unit
@@ -1689,7 +1690,14 @@ pkv_status prefill_common(const void* q, int32_t q_dtype, int32_t num_tokens, in
     p.NB = pool_blocks;
     p.G = G;
     p.TT = kTileM / G;
-    p.num_qtiles = (max_query_len + 2 * p.TT - 1) / (2 * p.TT);  // CTAs of two Q tiles
+    p.num_qtiles = (max_query_len + 2 * p.TT - 1) / (2 * p.TT);  // units of two Q tiles
+    // Scored, without a plan: units of one Q tile while all of them fit the SMs at once, since
+    // a unit's chain from tile to tile is shorter so (512 new tokens behind 4000, 32/8 heads: 128
+    // units of one 79.4 us, 64 of two 92.8; 64 tokens, 16/4 heads: 73.7 against 84.3).
+    if (mod && !work_units && 2 * static_cast<int64_t>(p.num_qtiles) * p.Hkv * p.S <= num_sms()) {
+        p.unit_tiles = 1;
+        p.num_qtiles = (max_query_len + p.TT - 1) / p.TT;
+    }
     if (static_cast<int64_t>(p.num_qtiles) * p.Hkv * p.S > INT32_MAX) return PKV_ERR_UNSUPPORTED;  // one grid axis
     p.work = work_units;
     p.num_work = num_work_units;

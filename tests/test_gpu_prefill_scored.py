@@ -160,24 +160,27 @@ def test_values_that_are_not_finite_reach_the_rows_that_see_them(pk, D, G, bad):
 
 
 @pytest.mark.parametrize("short", [0, 1])
-@pytest.mark.parametrize("D,G", [(64, 1), (128, 1), (128, 8)])
-def test_one_half_of_a_unit_is_through_long_before_the_other(pk, D, G, short):
-    """Rows of one Q tile see nothing, those of the other a long context; then the next unit, and the other way round."""
+@pytest.mark.parametrize("D,Hkv,G", [(64, 1, 1), (128, 1, 1), (128, 1, 8), (64, 20, 1)])
+def test_one_half_of_a_unit_is_through_long_before_the_other(pk, D, Hkv, G, short):
+    """Rows of one Q tile see nothing, those of the other a long context; then the next unit, and the other way round.
+    Few units have one Q tile each, unless a plan names them; 20 heads' have two."""
     RQ, ctx = 128 // G, 2600
     n = 4 * RQ
-    c = Case(pk, "f16", D, 1, G, "f16", {}, chunks=[(ctx, n), (0, 40)], seed=9)
+    c = Case(pk, "f16", D, Hkv, G, "f16", {}, chunks=[(ctx, n), (0, 40)], seed=9)
     first = np.zeros(n + 40, np.int32)
     half = np.arange(n) // RQ % 2 == short
     first[:n][half] = ctx + 4 * RQ  # nothing to see: the unit's one tile
     c.first = first
     c.ref, c.shares = su.ref_scored(c.q, c.where, c.pools, c.tables, c.lens, c.scale, 0.0, 0, None, first, None)
     c.check(c.run())
-    for t in (3, 127, ctx - 1, ctx + n - 1):  # seen by the other half alone; the last by its last row
-        c.vd[int(c.tables[0][t // 16]), 0, t % 16, 1 + t % 60] = float("nan")
-    out = c.run()
-    c.check(out, np.append(half, np.ones(40, bool)))
-    got = out.double().cpu().numpy()[:n][~half]
-    assert np.all((~np.isfinite(got)).any(-1))
+    c.check(c.run(plan=True))
+    for t in (3, 127, ctx - 1):  # seen by the other half alone
+        c.vd[int(c.tables[0][t // 16]), :, t % 16, 1 + t % 60] = float("nan")
+    for plan in (False, True):
+        out = c.run(plan)
+        c.check(out, np.append(half, np.ones(40, bool)))
+        got = out.double().cpu().numpy()[:n][~half]
+        assert np.all((~np.isfinite(got)).any(-1))
     assert pk.get_device_error() == 0
 
 
