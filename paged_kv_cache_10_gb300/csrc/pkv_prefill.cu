@@ -105,7 +105,6 @@ struct PrefillParams {
     int32_t S, T, Hq, Hkv, MB, NB;
     int32_t G, TT;               // heads per KV head, tokens per CTA (128 / G)
     int32_t num_qtiles;          // units per (sequence, KV head) along the queries
-    int32_t unit_tiles = 2;      // Q tiles of a unit (1: tile B stays empty)
     int32_t max_query_len;       // the caller's bound on every chunk
     const int32_t* work;         // [num_work] units s * num_qtiles + qt in start order, or null
     int32_t num_work;
@@ -255,10 +254,10 @@ __device__ __forceinline__ void row_range(const PrefillParams& p, const Unit& u,
 // Scored prefill: the unit's key range from its rows'.  Whole warp; every lane
 // gets the same result.  A Q tile whose rows are all empty keeps one masked tile,
 // whose softmax threads write the zeros.
-__device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int RQ, int lane, Unit& u) {
+__device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int RQ, int tiles, int lane, Unit& u) {
     u.prefix = p.prefix_lens ? min(load_live(p.prefix_lens + s), u.ctx + u.n) : 0;
     int lo_min = 0x7fffffff, lo_max = 0, hi_min = 0x7fffffff, end0 = 0, end1 = 0;
-    for (int i = lane; i < p.unit_tiles * RQ && u.t0 + i < u.n; i += 32) {
+    for (int i = lane; i < tiles * RQ && u.t0 + i < u.n; i += 32) {
         int lo, hi;
         row_range(p, u, u.t0 + i, lo, hi);
         if (lo <= hi) {
@@ -278,7 +277,7 @@ __device__ __forceinline__ void scored_unit(const PrefillParams& p, int s, int R
     u.k0 = any ? lo_min / kBlockSize * kBlockSize : 0;
     u.lead = any ? lo_min - u.k0 : 1;
     u.kv_end[0] = max(__reduce_max_sync(0xffffffffu, end0) - u.k0, 1);
-    u.kv_end[1] = u.kv_end[1] > 0 ? max(__reduce_max_sync(0xffffffffu, end1) - u.k0, 1) : 0;
+    u.kv_end[1] = tiles > 1 && u.t0 + RQ < u.n ? max(__reduce_max_sync(0xffffffffu, end1) - u.k0, 1) : 0;
     // a Q tile whose rows see nothing goes along to kBadLag tiles before the other's end
     const int most = max(u.kv_end[0], u.kv_end[1]) - kBadLag * kTileN;
     u.kv_end[0] = max(u.kv_end[0], most);
@@ -512,8 +511,8 @@ __device__ __forceinline__ void ranked_unit(Ranks& k, int rank, int lane, int& s
 // for KV head lin % Hkv.  False when the unit has no rows or its sequence's
 // bounds are inconsistent (reported when rep).
 // ranked: s and qt are given.
-__device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int64_t lin, int RQ, bool rep, bool ranked, Unit& u,
-                                             int& s, int& qt) {
+__device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int64_t lin, int RQ, int tiles, bool rep, bool ranked,
+                                             Unit& u, int& s, int& qt) {
     if (ranked) {
         u.h = static_cast<int>(lin % p.Hkv);
     } else if (p.work) {
@@ -539,12 +538,12 @@ __device__ __forceinline__ bool prefill_unit(const PrefillParams& p, int64_t lin
         return false;
     }
     if (u.n > p.max_query_len && rep) report(p.err, PKV_DEVERR_SEQ_LEN);
-    u.t0 = qt * p.unit_tiles * RQ;
+    u.t0 = qt * tiles * RQ;
     if (u.t0 >= u.n) return false;
     u.ctx = L - u.n;  // tokens before this chunk
     for (int X = 0; X < 2; ++X) {
         const int tx = u.t0 + X * RQ;
-        u.kv_end[X] = X < p.unit_tiles && tx < u.n ? u.ctx + tx + min(RQ, u.n - tx) : 0;
+        u.kv_end[X] = X < tiles && tx < u.n ? u.ctx + tx + min(RQ, u.n - tx) : 0;
     }
     u.bt = p.block_tables + static_cast<int64_t>(s) * p.MB;
     return true;
@@ -580,8 +579,9 @@ __device__ __forceinline__ bool take_unit(uint64_t* u_full, uint64_t* u_empty, c
 // one partition of the group's shared blocks (no causal mask); split-K
 // partials.
 // kScored (prefill only): capped, biased and masked scores; keys count from the
-// first block that some row of the unit attends to.
-template <typename T, int D, bool kPrefix, bool kScored>
+// first block that some row of the unit attends to.  kTiles: Q tiles of a unit (1, scored
+// only: tile B stays empty); as a number of the launch, it cost the large batches 2 to 3 %.
+template <typename T, int D, bool kPrefix, bool kScored, int kTiles>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const PrefillParams p, const __grid_constant__ CUtensorMap tmq,
                       const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
@@ -733,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool done = false;
         const bool ranked = kScored && !p.work && p.S <= 32;
         Ranks ranks{0, 0, 0, 0, 0, 0};
-        if (ranked) ranks = load_ranks(p, p.unit_tiles * RQ, lane);
+        if (ranked) ranks = load_ranks(p, kTiles * RQ, lane);
         for (;; ++k) {
             // unit k is claimed once the S MMAs of unit k - 1 are issued (that
             // unit is in its last key tile), so a CTA holds at most one unit
@@ -766,8 +766,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else if (c >= total) {
                             break;
                         }
-                        if (prefill_unit(p, c, RQ, lane == 0, ranked, u, seq, qt)) {
-                            if constexpr (kScored) scored_unit(p, seq, RQ, lane, u);
+                        if (prefill_unit(p, c, RQ, kTiles, lane == 0, ranked, u, seq, qt)) {
+                            if constexpr (kScored) scored_unit(p, seq, RQ, kTiles, lane, u);
                             found = true;
                             break;
                         }
@@ -1366,7 +1366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <typename T, int D, bool kPrefix, bool kScored = false>
+template <typename T, int D, bool kPrefix, bool kScored = false, int kTiles = 2>
 cudaError_t launch_tile(const PrefillParams& p, dim3 grid, const CUtensorMap& tq, const CUtensorMap& tk,
                         const CUtensorMap& tv, cudaStream_t st) {
     constexpr int kSmemBytes = Tile<D>::kSmemBytes;
@@ -1377,7 +1377,7 @@ cudaError_t launch_tile(const PrefillParams& p, dim3 grid, const CUtensorMap& tq
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     cudaError_t attr = cudaSuccess;
     std::call_once(once[dev], [&] {
-        attr = cudaFuncSetAttribute(prefill_tc_kernel<T, D, kPrefix, kScored>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        attr = cudaFuncSetAttribute(prefill_tc_kernel<T, D, kPrefix, kScored, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kSmemBytes);
     });
     if (attr != cudaSuccess) return attr;
@@ -1393,11 +1393,11 @@ cudaError_t launch_tile(const PrefillParams& p, dim3 grid, const CUtensorMap& tq
         la[0].val.programmaticStreamSerializationAllowed = 1;
         cfg.attrs = la;
         cfg.numAttrs = 1;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_tc_kernel<T, D, kPrefix, kScored>, p, tq, tk, tv);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, prefill_tc_kernel<T, D, kPrefix, kScored, kTiles>, p, tq, tk, tv);
         if (e != cudaErrorNotSupported && e != cudaErrorInvalidValue) return e;
         (void)cudaGetLastError();  // a driver that refuses the attribute gets a plain launch
     }
-    prefill_tc_kernel<T, D, kPrefix, kScored><<<grid, kThreads, kSmemBytes, st>>>(p, tq, tk, tv);
+    prefill_tc_kernel<T, D, kPrefix, kScored, kTiles><<<grid, kThreads, kSmemBytes, st>>>(p, tq, tk, tv);
     return cudaGetLastError();
 }
 
@@ -1408,10 +1408,13 @@ std::atomic<uint32_t> g_next_sched_slot{0};
 // when there are fewer; the launch takes the next counter slot.
 template <typename T>
 cudaError_t launch_prefill(PrefillParams p, int D, const CUtensorMap& tq, const CUtensorMap& tk,
-                           const CUtensorMap& tv, bool scored, cudaStream_t st) {
+                           const CUtensorMap& tv, bool scored, int tiles, cudaStream_t st) {
     p.sched_slot = static_cast<int32_t>(g_next_sched_slot.fetch_add(1u, std::memory_order_relaxed) % kSchedSlots);
     const int64_t units = p.work ? p.num_work : static_cast<int64_t>(p.num_qtiles) * p.S;
     const dim3 grid(static_cast<unsigned>(std::min<int64_t>(units * p.Hkv, num_sms())));
+    if (scored && tiles == 1)
+        return D == 64 ? launch_tile<T, 64, false, true, 1>(p, grid, tq, tk, tv, st)
+                       : launch_tile<T, 128, false, true, 1>(p, grid, tq, tk, tv, st);
     if (scored)
         return D == 64 ? launch_tile<T, 64, false, true>(p, grid, tq, tk, tv, st)
                        : launch_tile<T, 128, false, true>(p, grid, tq, tk, tv, st);
@@ -1691,11 +1694,12 @@ pkv_status prefill_common(const void* q, int32_t q_dtype, int32_t num_tokens, in
     p.G = G;
     p.TT = kTileM / G;
     p.num_qtiles = (max_query_len + 2 * p.TT - 1) / (2 * p.TT);  // units of two Q tiles
+    int tiles = 2;
     // Scored, without a plan: units of one Q tile while all of them fit the SMs at once, since
     // a unit's chain from tile to tile is shorter so (512 new tokens behind 4000, 32/8 heads: 128
-    // units of one 79.4 us, 64 of two 92.8; 64 tokens, 16/4 heads: 73.7 against 84.3).
+    // units of one 79.1 us, 64 of two 93.2; 64 tokens, 16/4 heads: 71.1 against 84.2).
     if (mod && !work_units && 2 * static_cast<int64_t>(p.num_qtiles) * p.Hkv * p.S <= num_sms()) {
-        p.unit_tiles = 1;
+        tiles = 1;
         p.num_qtiles = (max_query_len + p.TT - 1) / p.TT;
     }
     if (static_cast<int64_t>(p.num_qtiles) * p.Hkv * p.S > INT32_MAX) return PKV_ERR_UNSUPPORTED;  // one grid axis
@@ -1734,8 +1738,8 @@ pkv_status prefill_common(const void* q, int32_t q_dtype, int32_t num_tokens, in
     if (!encode_token_head_map(&tq, q, D, num_q_heads, num_tokens, G, kTileM / G) ||
         !encode_pool_map(&tk, k_pool, 2, pool_rows, D) || !encode_pool_map(&tv, v_pool, 2, pool_rows, D))
         return PKV_ERR_CUDA;
-    const cudaError_t e = q_dtype == PKV_BF16 ? launch_prefill<BF16>(p, D, tq, tk, tv, mod != nullptr, st)
-                                              : launch_prefill<F16>(p, D, tq, tk, tv, mod != nullptr, st);
+    const cudaError_t e = q_dtype == PKV_BF16 ? launch_prefill<BF16>(p, D, tq, tk, tv, mod != nullptr, tiles, st)
+                                              : launch_prefill<F16>(p, D, tq, tk, tv, mod != nullptr, tiles, st);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 }  // namespace
